@@ -312,6 +312,182 @@ def csa_layer_prefill(params, B, Q, pos0, Ca, Za, Cb, Zb, Cb_prev, Zb_prev, Ba, 
                                   _stream(stream)), "csa_layer_prefill")
 
 
+# ---- grouped-query attention layers --------------------------------------------
+# These calls take their sizes and strides from the tensors and refuse, as
+# CSA_ERR_INVALID_ARG, tensors of another type, shape or device than theirs
+# (the device: the current one).
+
+(CSA_ROPE_INTERLEAVED, CSA_ROPE_HALF) = range(2)
+(CSA_ROPE_UNSCALED, CSA_ROPE_LINEAR, CSA_ROPE_BY_PARTS) = range(3)
+
+
+class CsaRopeParams(ctypes.Structure):
+    """Mirror of ``csa_rope_params``."""
+    _fields_ = [("rope_dim", ctypes.c_int32), ("offset", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_float), ("factor", ctypes.c_float),
+                ("orig_len", ctypes.c_int32), ("beta_fast", ctypes.c_float), ("beta_slow", ctypes.c_float),
+                ("mscale", ctypes.c_float)]
+
+
+class CsaPagedCache(ctypes.Structure):
+    """Mirror of ``csa_paged_cache`` (device pointers; see paged_cache)."""
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)]
+
+
+_R, _C = ctypes.POINTER(CsaRopeParams), ctypes.POINTER(CsaPagedCache)
+_lib.csa_default_rope.argtypes = [_R]
+_lib.csa_default_rope.restype = None
+_lib.csa_rope_table.argtypes = [_R, _vp]
+_lib.csa_rope.argtypes = [_R, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp]
+_lib.csa_kv_append.argtypes = [_C, _R, _vp, _i32, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp]
+_lib.csa_paged_attn_workspace_size.argtypes = [_C, _i32, _i32]
+_lib.csa_paged_attn_workspace_size.restype = _sz
+_lib.csa_paged_attn.argtypes = [_C, _i32, _i32, _vp, _vp, _i64, _i64, ctypes.c_float, _i32, _vp, _vp, _vp, _vp, _sz,
+                                _vp]
+_lib.csa_prompt_attn.argtypes = ([_i32] * 4 + [_i64] * 2 + [_vp] * 2 + [_vp, _i64, _i64] * 3 +
+                                 [ctypes.c_float, _i32, _i32] + [_vp] * 4)
+for _f in ("csa_rope_table", "csa_rope", "csa_kv_append", "csa_paged_attn", "csa_prompt_attn"):
+    getattr(_lib, _f).restype = ctypes.c_int
+
+
+def _need(ok: bool, where: str, what: str):
+    if not ok:
+        raise CsaError(1, "%s (%s)" % (where, what))
+
+
+def _arg(where, name, t, dtypes, shape, contiguous=True):
+    """Checks one tensor; shape entries of None are free.  Returns the tensor."""
+    _need(torch.is_tensor(t), where, "%s: no tensor" % name)
+    _need(t.dtype in dtypes, where, "%s: %s" % (name, t.dtype))
+    _need(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), where,
+          "%s: shape %s, expected %s" % (name, tuple(t.shape), tuple("any" if n is None else n for n in shape)))
+    _need(t.is_cuda and t.device.index == torch.cuda.current_device(), where, "%s: on %s" % (name, t.device))
+    _need(t.is_contiguous() if contiguous else t.shape[-1] <= 1 or t.stride(-1) == 1, where, "%s: strides" % name)
+    return t
+
+
+def _strides(t):
+    """Row and head strides of a [rows][heads][channels] tensor; of a dimension of size one, whose stride has no
+    meaning, a valid one."""
+    rows, heads, dim = t.shape
+    h = t.stride(1) if heads > 1 else dim
+    return (t.stride(0) if rows > 1 else max(h * heads, dim)), h
+
+
+def rope_params(**fields) -> CsaRopeParams:
+    """csa_default_rope with any field overridden."""
+    r = CsaRopeParams()
+    _lib.csa_default_rope(ctypes.byref(r))
+    for k, v in fields.items():
+        _need(k in dict(CsaRopeParams._fields_), "rope_params", "no field %s" % k)
+        setattr(r, k, v)
+    return r
+
+
+def rope_table(r: CsaRopeParams, device=None) -> torch.Tensor:
+    """csa_rope_table's array in device memory (int64 bits), for csa_rope and csa_kv_append."""
+    host = torch.empty(max(r.rope_dim // 2, 1), dtype=torch.int64)
+    _check(_lib.csa_rope_table(ctypes.byref(r), host.data_ptr()), "csa_rope_table")
+    return host.to(device or "cuda")
+
+
+def csa_rope(r, turns, pos, x, out=None, inverse=False, stream=None):
+    """Rotates x [rows][heads][channels] by pos [rows] (int32) into out, a new tensor where it is None; returns it."""
+    w = "csa_rope"
+    bf16 = (torch.bfloat16,)
+    _arg(w, "x", x, bf16, (None, None, None), contiguous=False)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _arg(w, "out", out, bf16, tuple(x.shape), contiguous=False)
+    _arg(w, "pos", pos, (torch.int32,), (x.shape[0],))
+    _arg(w, "turns", turns, (torch.int64,), (r.rope_dim // 2,))
+    _check(_lib.csa_rope(ctypes.byref(r), _ptr(turns), *x.shape, _ptr(pos), _ptr(x), *_strides(x), _ptr(out),
+                         *_strides(out), int(inverse), _stream(stream)), w)
+    return out
+
+
+def paged_cache(k, v, k_scale, v_scale, table) -> CsaPagedCache:
+    """A ``csa_paged_cache`` over device tensors: k, v [pages][kv heads][page size][channels] E4M3 (or uint8 codes),
+    k_scale, v_scale [pages][kv heads] fp32, table [sequences][pages] int32.  It keeps the tensors."""
+    w, f8 = "paged_cache", (torch.float8_e4m3fn, torch.uint8)
+    n, heads, page, dim = _arg(w, "k", k, f8, (None,) * 4).shape
+    _arg(w, "v", v, f8, (n, heads, page, dim))
+    _arg(w, "k_scale", k_scale, (torch.float32,), (n, heads))
+    _arg(w, "v_scale", v_scale, (torch.float32,), (n, heads))
+    _arg(w, "table", table, (torch.int32,), (None, None))
+    c = CsaPagedCache(heads, dim, page, n, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(table),
+                      table.shape[1])
+    c.tensors = (k, v, k_scale, v_scale, table)
+    return c
+
+
+def csa_kv_append(cache, r, turns, cu_rows, pos0, k, v, stream=None):
+    """Appends rows of k and v [rows][kv heads][channels] to the cache from positions pos0 [B] on; sequence b's rows
+    are cu_rows[b] .. cu_rows[b+1]-1 (cu_rows [B+1], or None: one row each).  r and turns None: keys as they are."""
+    w = "csa_kv_append"
+    bf16, i32 = (torch.bfloat16,), (torch.int32,)
+    B = _arg(w, "pos0", pos0, i32, (None,)).shape[0]
+    _need(B <= cache.tensors[4].shape[0], w, "pos0: more sequences than the table has")
+    _arg(w, "k", k, bf16, (None if cu_rows is not None else B, cache.n_kv_heads, cache.head_dim), contiguous=False)
+    _arg(w, "v", v, bf16, tuple(k.shape), contiguous=False)
+    if cu_rows is not None:
+        _arg(w, "cu_rows", cu_rows, i32, (B + 1,))
+    if r is not None:
+        _arg(w, "turns", turns, (torch.int64,), (r.rope_dim // 2,))
+    _check(_lib.csa_kv_append(ctypes.byref(cache), None if r is None else ctypes.byref(r),
+                              None if r is None else _ptr(turns), B, k.shape[0], _ptr(cu_rows), _ptr(pos0), _ptr(k),
+                              *_strides(k), _ptr(v), *_strides(v), _stream(stream)), w)
+
+
+def paged_attn_workspace(cache, B: int, n_heads: int) -> torch.Tensor:
+    """Allocates (through torch) a workspace for csa_paged_attn."""
+    n = int(_lib.csa_paged_attn_workspace_size(ctypes.byref(cache), B, n_heads))
+    if n == 0:
+        raise CsaError(2, "csa_paged_attn_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def csa_paged_attn(cache, lens, q, sm_scale, window, sink, out, lse, ws, stream=None):
+    """q [B][heads][channels] over the cached tokens 0 .. lens[b]-1 into out [B][heads][channels] (and lse
+    [B][heads] fp32, or None)."""
+    w, f32 = "csa_paged_attn", (torch.float32,)
+    B, heads, dim = _arg(w, "q", q, (torch.bfloat16,), (None, None, cache.head_dim), contiguous=False).shape
+    _need(B <= cache.tensors[4].shape[0], w, "q: more sequences than the table has")
+    _arg(w, "lens", lens, (torch.int32,), (B,))
+    _arg(w, "out", out, (torch.bfloat16,), (B, heads, dim))
+    if sink is not None:
+        _arg(w, "sink", sink, f32, (heads,))
+    if lse is not None:
+        _arg(w, "lse", lse, f32, (B, heads))
+    if ws is not None:
+        _arg(w, "ws", ws, (torch.uint8,), (None,))
+    _check(_lib.csa_paged_attn(ctypes.byref(cache), B, heads, _ptr(lens), _ptr(q), *_strides(q), sm_scale, window,
+                               _ptr(sink), _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(),
+                               _stream(stream)), w)
+
+
+def csa_prompt_attn(cu_q, cu_k, q, k, v, sm_scale, causal, window, sink, out, lse=None, stream=None):
+    """Packed sequences: q [rows][heads][channels] by cu_q [B+1], k and v [rows][kv heads][channels] by cu_k [B+1],
+    into out (like q, contiguous) and lse [rows][heads] fp32 or None."""
+    w, bf16, i32, f32 = "csa_prompt_attn", (torch.bfloat16,), (torch.int32,), (torch.float32,)
+    n_q, heads, dim = _arg(w, "q", q, bf16, (None, None, None), contiguous=False).shape
+    n_k, kv_heads, _ = _arg(w, "k", k, bf16, (None, None, dim), contiguous=False).shape
+    _arg(w, "v", v, bf16, (n_k, kv_heads, dim), contiguous=False)
+    n = _arg(w, "cu_q", cu_q, i32, (None,)).shape[0]
+    _need(n >= 1, w, "cu_q: empty")
+    _arg(w, "cu_k", cu_k, i32, (n,))
+    _arg(w, "out", out, bf16, (n_q, heads, dim))
+    if sink is not None:
+        _arg(w, "sink", sink, f32, (heads,))
+    if lse is not None:
+        _arg(w, "lse", lse, f32, (n_q, heads))
+    _check(_lib.csa_prompt_attn(n - 1, heads, kv_heads, dim, n_q, n_k, _ptr(cu_q), _ptr(cu_k), _ptr(q), *_strides(q),
+                                _ptr(k), *_strides(k), _ptr(v), *_strides(v), sm_scale, int(bool(causal)), window,
+                                _ptr(sink), _ptr(out), _ptr(lse), _stream(stream)), w)
+
+
 CSA_TEST_FAULT_INDEXER, CSA_TEST_FAULT_TOPK, CSA_TEST_FAULT_ATTN = 1, 2, 4
 _lib.csa_test_set_wait_fault.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
 _lib.csa_test_set_wait_fault.restype = ctypes.c_int

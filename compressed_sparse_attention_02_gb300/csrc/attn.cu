@@ -231,24 +231,6 @@ __device__ __forceinline__ TileLoad tile_load(const RowSet& s, int r0, int r_hi,
   return t;
 }
 
-// A bounded wait that also ends when another thread of the CTA has raised
-// the abort flag; a wait that runs out records kErrTimeout and raises it.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                              unsigned* status) {
-  constexpr uint32_t kSleepNs = 20000;  // the thread wakes when the phase completes
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns(), limit = wait_limit_ns(status);
-  while (true) {
-    if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > limit) {
-      record_error(status, kErrTimeout);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
 // The query's 64 x 512 bf16 rows into eight 128-byte-swizzled 64-channel
 // blocks, on q_full (one thread).
 __device__ __forceinline__ void load_q(const CUtensorMap& tm_q, uint8_t* q_s, int64_t row_q, uint64_t* q_full) {

@@ -61,6 +61,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return g_encode;
 }
 
+}  // namespace
+
+namespace csa {
+unsigned* device_status() { return status_ptr(); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder(); }
+}  // namespace csa
+
+namespace {
+
 // Stage tracing (csa_set_trace_events): events recorded between the stages
 // of the layer calls.
 cudaEvent_t g_trace[5] = {};

@@ -1,0 +1,120 @@
+// Shared pieces of the grouped-query layer's kernels: the rotation of an item
+// of 16 channels, bf16 unpacking, and the search of a work item among
+// sequences of different lengths.
+#pragma once
+
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace csa {
+
+// Sine and cosine of position p at the frequency whose table entry is turns
+// (2^-64 turns a position): the angle's fraction of a turn is the low 64 bits
+// of p * turns, exact.  The nearest quarter turn is taken off as an integer,
+// so the remainder, at most an eighth of a turn, keeps 24 bits of its own:
+// the angle is right to 2e-8 rad whatever p is (a quarter of what rounding
+// the whole fraction to binary32 would leave).
+__device__ __forceinline__ void rope_sincos_exact(int64_t p, uint64_t turns, float* s, float* c) {
+  const uint64_t frac = static_cast<uint64_t>(p) * turns;
+  const uint32_t quarter = static_cast<uint32_t>((frac + (1ull << 61)) >> 62);
+  const int64_t rest = static_cast<int64_t>(frac - (static_cast<uint64_t>(quarter) << 62));
+  float sr, cr;  // of half-turns in [-1/4, 1/4]
+  sincospif(static_cast<float>(static_cast<int32_t>(rest >> 32)) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31
+  const float a = (quarter & 1u) ? cr : sr, b = (quarter & 1u) ? sr : cr;
+  *s = (quarter & 2u) ? -a : a;
+  *c = ((quarter + 1u) & 2u) ? -b : b;
+}
+
+// The two 8-channel chunks of item i of a row: the rotated items first, then
+// the channels that stay, in order.
+__device__ __forceinline__ void item_chunks(const RopeArgs& r, int i, int* lo, int* hi) {
+  const int n = r.rope_dim >> 4;
+  if (i < n) {
+    *lo = r.offset + (r.half ? 8 * i : 16 * i);
+    *hi = r.half ? *lo + (r.rope_dim >> 1) : *lo + 8;
+  } else {
+    int ch = 16 * (i - n);
+    if (ch >= r.offset) ch += r.rope_dim;
+    *lo = ch;
+    *hi = ch + 8;
+  }
+}
+
+__device__ __forceinline__ void unpack_bf16(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+// Rotates the item's 8 pairs by (sin, cos) sc[0..7]: with half-split pairs
+// pair j is (lo[j], hi[j]), with interleaved ones pairs 0..3 are neighbours in
+// lo and 4..7 in hi.
+__device__ __forceinline__ void rotate_item(bool half, const float2 (&sc)[8], float (&lo)[8], float (&hi)[8]) {
+  if (half) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = lo[j], y = hi[j];
+      lo[j] = fmaf(x, sc[j].y, -y * sc[j].x);
+      hi[j] = fmaf(x, sc[j].x, y * sc[j].y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = lo[2 * j], y = lo[2 * j + 1], z = hi[2 * j], w = hi[2 * j + 1];
+      lo[2 * j] = fmaf(x, sc[j].y, -y * sc[j].x);
+      lo[2 * j + 1] = fmaf(x, sc[j].x, y * sc[j].y);
+      hi[2 * j] = fmaf(z, sc[4 + j].y, -w * sc[4 + j].x);
+      hi[2 * j + 1] = fmaf(z, sc[4 + j].x, w * sc[4 + j].y);
+    }
+  }
+}
+
+// Finds the sequence that work item w belongs to, where sequence b has
+// count(b) >= 0 items: returns b and the item's index in it, or -1 when w is
+// past the last; *total, if asked for, gets the sum of all counts (a search
+// for w < 0 gives the sum alone).  Every thread of the CTA calls it (THREADS
+// threads, a multiple of 32); sh holds THREADS / 32 + 2 values.
+template <int THREADS, typename Count>
+__device__ __forceinline__ int find_item(int B, int64_t w, Count count, int64_t* sh, int64_t* index, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = THREADS / 32;
+  if (threadIdx.x == 0) sh[kWarps] = -1;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    const int64_t n = b < B ? count(b) : 0;
+    int64_t x = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    int64_t before = base, all = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const int64_t t = sh[k];
+      if (k < warp) before += t;
+      all += t;
+    }
+    before += x - n;
+    if (w >= before && w < before + n) {  // one thread at most
+      sh[kWarps] = b;
+      sh[kWarps + 1] = w - before;
+    }
+    base += all;
+    __syncthreads();
+    if (!total && sh[kWarps] >= 0) break;
+  }
+  if (B <= 0) __syncthreads();
+  if (total) *total = base;
+  *index = sh[kWarps + 1];
+  return static_cast<int>(sh[kWarps]);
+}
+
+}  // namespace csa

@@ -292,4 +292,87 @@ cudaError_t launch_quantize_index_fp4(const IndexFp4Rows& a, cudaStream_t stream
 cudaError_t launch_quantize_kv_fp4(int64_t n_rows, const uint16_t* in, int64_t in_stride, uint8_t* out,
                                    int64_t out_stride, cudaStream_t stream);
 
+// ---- grouped-query layer: rotary positions, paged 8-bit cache, prompt attention ------
+// The rotation of a row: item c (16 channels) of the rope_dim/16 rotated ones
+// holds the pairs 8c .. 8c+7; the other items hold 16 channels that stay.
+struct RopeArgs {
+  const uint64_t* turns;    // [rope_dim / 2] turns a position, times 2^64 (csa_rope_table); null: no rotation
+  int rope_dim, offset;     // multiples of 16 (rope_dim 0 with turns null)
+  int half;                 // 1: pairs (j, j + rope_dim/2); 0: pairs (2j, 2j + 1)
+  float mscale;
+};
+struct RopeRowsArgs {
+  RopeArgs rope;
+  int64_t n_rows;
+  int n_heads, head_dim;
+  const int32_t* pos;       // [n_rows]
+  const uint16_t* in;
+  int64_t in_stride, in_stride_h;    // elements
+  uint16_t* out;
+  int64_t out_stride, out_stride_h;
+  int inverse;
+};
+cudaError_t launch_rope(const RopeRowsArgs& a, cudaStream_t stream);
+
+// A pool of pages, [n_pages][n_kv_heads][page][head_dim] E4M3 codes with one
+// scale per page and head, and the sequences' page tables.
+struct PagedCache {
+  int n_kv_heads, head_dim, page, page_shift;
+  int64_t n_pages;
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;  // [n_pages][n_kv_heads]
+  const int32_t* table;      // [B][table_stride]
+  int64_t table_stride;      // pages a sequence can have
+};
+struct KvAppendArgs {
+  PagedCache cache;
+  RopeArgs rope;
+  int B;
+  int64_t n_rows;
+  const int32_t* cu_rows;    // [B+1] or null: one row a sequence
+  const int32_t* pos0;       // [B]
+  const uint16_t *k, *v;
+  int64_t k_stride, k_stride_h, v_stride, v_stride_h;
+  unsigned* status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+
+struct PagedAttnArgs {
+  PagedCache cache;
+  int B, n_heads;
+  const int32_t* lens;       // [B]
+  const uint16_t* q;
+  int64_t q_stride, q_stride_h;
+  float sm_scale;
+  int window;                // 0: none
+  const float* sink;         // [n_heads] or null
+  uint16_t* out;             // [B][n_heads][head_dim]
+  float* lse;                // [B][n_heads] or null
+  float* part;               // partial results (paged_attn_bytes)
+  unsigned* status;
+};
+// Bytes of partial results for the given SM count.
+size_t paged_attn_bytes(int head_dim, int sms);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int sms, cudaStream_t stream);
+
+struct PromptAttnArgs {
+  int B, n_heads, n_kv_heads, head_dim;
+  int64_t n_q, n_k;          // rows of q and of k / v
+  const int32_t *cu_q, *cu_k;  // [B+1]
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, q_stride_h, k_stride, k_stride_h, v_stride, v_stride_h;
+  float sm_scale;
+  int causal, window;
+  const float* sink;
+  uint16_t* out;             // [n_q][n_heads][head_dim]
+  float* lse;                // [n_q][n_heads] or null
+  unsigned* status;
+};
+cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream);
+
+// The device status word of the current device and the tensor-map encoder
+// (null when the CUDA runtime does not give them).
+unsigned* device_status();
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 }  // namespace csa

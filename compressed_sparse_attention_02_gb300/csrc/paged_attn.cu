@@ -1,0 +1,586 @@
+// Single-token attention of grouped query heads over a paged E4M3 cache with
+// one scale per page and head.
+//
+//   l_j = sm_scale * k_scale(page) * q . codes_j,   p_j = e^(l_j - m)
+//   out = sum_j p_j v_scale(page) codes^v_j / (sum_j p_j + e^(sink - m))
+//
+// Bound by memory: each cached row is read once (2 D bytes a token and head)
+// for 4 D * group operations, so the products run on tensor cores at the
+// group's size, up to 16 query heads as the 16 rows of one m16n8k16 product
+// (a 128-row tcgen05 tile would be at least 7/8 empty).  The codes become
+// f16 exactly; queries become f16 after scaling each row by a power of two to
+// [2^14, 2^15), exact but for values 2^-28 below the row's largest.
+//
+// The tokens of all (sequence, head) pairs form one line of 128-token units
+// that is cut into equal shares, one per resident CTA, whatever the lengths
+// are; a pair that a cut divides is finished by the merge kernel from fp32
+// partial results in a fixed order.  A warp takes 32 tokens of each unit with
+// its own asynchronous copies, running maximum and accumulators, so warps
+// never wait for one another inside a share.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <float.h>
+
+#include "gqa.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 2;
+constexpr int kUnitShift = 7;             // tokens a unit: 32 a warp
+constexpr int kUnit = 1 << kUnitShift;
+constexpr int kWarpTokens = kUnit / kWarps;
+constexpr int kRows = 16;                 // query heads a CTA
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A maximum may lag behind by this much (in log2) before the accumulators are
+// rescaled: weights are then at most 2^4 times 1, and as f16 they carry 2^11
+// more, so weights down to 2^-25 of the largest keep f16's full precision.
+constexpr float kLag = 4.f;
+constexpr float kWeightExp = 11.f;
+constexpr float kNone = -1e30f;           // running maximum before the first token
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = 3;
+  static constexpr int kTileBytes = kWarpTokens * D;        // K or V of one warp's 32 tokens
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kRecord = kRows * (D + 2);           // floats of a partial result
+  // A warp's accumulators in its ring at the end: one float of padding after
+  // every 32, so that the 32 lanes' channels fall into different banks.
+  static constexpr int kRowFloats = D + D / 32;
+  static_assert(kWarpBytes >= kRows * kRowFloats * 4, "a warp's accumulators fit its ring");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes, or zeros without reading.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Two E4M3 codes (low byte first) as f16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Where 16-byte chunk c of row r of a 32-row tile lies: rows of 128 bytes
+// with the chunk number XORed by the row, or two rows of 64 bytes a line with
+// it XORed by twice the line, so that both the rows that a K fragment reads
+// (8 neighbours) and those of a V fragment (every second one) fall into
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (D == 128) return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+  return static_cast<uint32_t>((r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4));
+}
+
+// A sequence's visible tokens [lo, len) and its units.
+struct Span {
+  int len, lo;
+  __device__ __forceinline__ int unit0() const { return lo >> kUnitShift; }
+  __device__ __forceinline__ int units() const { return ((len + kUnit - 1) >> kUnitShift) - unit0(); }
+};
+__device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int b) {
+  Span s;
+  const int64_t n = __ldg(a.lens + b), cap = a.cache.table_stride << a.cache.page_shift;
+  if (n > cap) record_error(a.status, kErrIndexRange);
+  s.len = static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
+  s.lo = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
+  return s;
+}
+
+// Sum over the CTA of two values.
+__device__ __forceinline__ void block_sum2(int64_t& x, int64_t& y, int64_t* sh, int threads) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, off);
+    y += __shfl_xor_sync(0xffffffffu, y, off);
+  }
+  if (lane == 0) {
+    sh[2 * warp] = x;
+    sh[2 * warp + 1] = y;
+  }
+  __syncthreads();
+  x = y = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    x += sh[2 * w];
+    y += sh[2 * w + 1];
+  }
+  __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const PagedAttnArgs a) {
+  using C = Cfg<D>;
+  constexpr int kK = D / 16;       // 16-channel steps of q . k
+  constexpr int kN = D / 8;        // 8-channel tiles of the output
+  constexpr int kChunks = D / 16;  // 16-byte chunks a row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t sh[2 * kWarps];
+  __shared__ float scale_s[kWarps][C::kStages][4];  // k, k, v, v scales of the tile's two halves
+  __shared__ int bad_s[kWarps][C::kStages];         // halves whose page is outside the cache
+  __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, cq = lane & 3;
+  const PagedCache& cache = a.cache;
+  const int group = a.n_heads / cache.n_kv_heads;
+  const int blocks = (group + kRows - 1) / kRows;   // 16-row blocks a KV head
+  const int pairs = cache.n_kv_heads * blocks;
+
+  // this CTA's share [at, end) of the line of units
+  int64_t total = 0, unused = 0;
+  for (int s = tid; s < a.B; s += kThreads) total += span_of(a, s).units();
+  block_sum2(total, unused, sh, kThreads);
+  total *= pairs;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t begin = blockIdx.x * per;
+  int64_t at = begin;
+  const int64_t end = min(total, begin + per);
+  if (at >= end) return;
+  int64_t index;
+  int b = find_item<kThreads>(
+      a.B, at, [&](int s) { return static_cast<int64_t>(span_of(a, s).units()) * pairs; }, sh, &index, nullptr);
+  Span sp = span_of(a, b);
+  int pair = static_cast<int>(index / sp.units());
+  int u = static_cast<int>(index - static_cast<int64_t>(pair) * sp.units());
+
+  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
+  while (at < end) {
+    const int nt = sp.units();
+    const int take = static_cast<int>(min(static_cast<int64_t>(nt - u), end - at));
+    const int hk = pair / blocks, row0 = (pair - hk * blocks) * kRows;
+    const int rows = min(kRows, group - row0);
+    const int head0 = hk * group + row0;
+    const int32_t* table = cache.table + static_cast<int64_t>(b) * cache.table_stride;
+
+    // copies of iteration it's 32 tokens into its stage; page ids are read an
+    // iteration ahead (next_page: of the 16 tokens of the lane's half)
+    auto tokens_at = [&](int it) { return ((sp.unit0() + u + it) << kUnitShift) + warp * kWarpTokens; };
+    auto page_at = [&](int it) -> int32_t {
+      const int t = tokens_at(it) + (lane & 16);
+      return it < take && t < sp.len && t + 16 > sp.lo ? __ldg(table + (t >> cache.page_shift)) : -1;
+    };
+    int32_t next_page = page_at(0);
+    auto issue = [&](int it) {
+      const int32_t mine = next_page;
+      next_page = page_at(it + 1);
+      const int t0 = tokens_at(it);
+      const int st = it % C::kStages;
+      if (it < take && t0 < sp.len && t0 + kWarpTokens > sp.lo) {
+        const uint32_t ks = ring + st * C::kStageBytes, vs = ks + C::kTileBytes;
+        const bool ok = mine >= 0 && mine < cache.n_pages;
+        const int th = t0 + (lane & 16);
+        const bool bad = !ok && th < sp.len && th + 16 > sp.lo;
+        if (bad) record_error(a.status, kErrIndexRange);
+        const unsigned bads = __ballot_sync(0xffffffffu, bad), oks = __ballot_sync(0xffffffffu, ok);
+        const int32_t page_a = __shfl_sync(0xffffffffu, mine, 0), page_b = __shfl_sync(0xffffffffu, mine, 16);
+        const bool ok_a = oks & 1u, ok_b = oks >> 31;
+        const int in_page = cache.page - 1;
+        const int64_t slab_a = ok_a ? static_cast<int64_t>(page_a) * cache.n_kv_heads + hk : 0;
+        const int64_t slab_b = ok_b ? static_cast<int64_t>(page_b) * cache.n_kv_heads + hk : 0;
+        const int64_t off_a = ((slab_a << cache.page_shift) + (t0 & in_page)) * D;
+        const int64_t off_b = ((slab_b << cache.page_shift) + ((t0 + 16) & in_page)) * D - 16 * D;
+        constexpr int kRowsAtOnce = 32 / kChunks;
+        const int r0 = lane / kChunks, c = lane % kChunks;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = r0 + i * kRowsAtOnce;
+          const bool first = i < kChunks / 2;  // rows below 16
+          const int t = t0 + r;
+          const bool there = (first ? ok_a : ok_b) && t >= sp.lo && t < sp.len;
+          const int64_t off = (first ? off_a : off_b) + r * D + c * 16;
+          const uint32_t dst = chunk_at<D>(r, c);
+          cp_async_16_or_zero(ks + dst, there ? cache.k + off : cache.k, there);
+          cp_async_16_or_zero(vs + dst, there ? cache.v + off : cache.v, there);
+        }
+        if (lane < 4) {
+          const bool there = (lane & 1) ? ok_b : ok_a;
+          const float* from = ((lane & 2) ? cache.v_scale : cache.k_scale) + ((lane & 1) ? slab_b : slab_a);
+          cp_async_4_or_zero(smem_u32(&scale_s[warp][st][lane]), from, there);
+        }
+        if (lane == 0) bad_s[warp][st] = (bads & 1u) | ((bads >> 31) << 1);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+
+    // the query rows g and g + 8 as fragments: lane cq holds channels
+    // cq * D/4 .. of each, in the order in which it reads the keys' bytes
+    uint32_t qf[kK][4];
+    float fac[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = g + 8 * half;
+      float x[D / 4];
+      if (r < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_stride + (head0 + r) * a.q_stride_h + cq * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float y[8];
+          unpack_bf16(__ldg(src + i), y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[8 * i + j] = y[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]) <= FLT_MAX ? fabsf(x[i]) : 0.f);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 126);
+      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      fac[half] = a.sm_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int s = 0; s < kK; ++s) {
+        qf[s][half] = pack_f16(x[4 * s] * up, x[4 * s + 1] * up);
+        qf[s][2 + half] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
+      }
+    }
+
+    float o[kN][4];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m[2] = {kNone, kNone}, mv[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+
+    for (int it = 0; it < take; ++it) {
+      cp_async_wait_pending(C::kStages - 2);
+      __syncwarp();
+      const int t0 = tokens_at(it);
+      const int st = it % C::kStages;
+      if (t0 < sp.len && t0 + kWarpTokens > sp.lo) {
+        const uint32_t ks = ring + st * C::kStageBytes, vs = ks + C::kTileBytes;
+        // logits of 32 tokens: 4 tiles of 8
+        float x[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+          const int r = 8 * n + g;
+          uint32_t w[D / 16];
+          if constexpr (D == 128) {
+            const uint4 v0 = lds128(ks + chunk_at<D>(r, 2 * cq)), v1 = lds128(ks + chunk_at<D>(r, 2 * cq + 1));
+            w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
+            w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
+          } else {
+            const uint4 v0 = lds128(ks + chunk_at<D>(r, cq));
+            w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
+          }
+#pragma unroll
+          for (int s = 0; s < kK; ++s) mma_f16_16816(x[n], qf[s], e4m3x2_to_f16x2(w[s]), e4m3x2_to_f16x2(w[s] >> 16));
+        }
+        const float4 sc = *reinterpret_cast<const float4*>(scale_s[warp][st]);
+        const int bad = bad_s[warp][st];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float k = n < 2 ? sc.x : sc.y;
+          x[n][0] *= fac[0] * k;
+          x[n][1] *= fac[0] * k;
+          x[n][2] *= fac[1] * k;
+          x[n][3] *= fac[1] * k;
+        }
+        if (t0 < sp.lo || t0 + kWarpTokens > sp.len || bad) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int t = t0 + 8 * n + 2 * cq + e;
+              if (t < sp.lo || t >= sp.len || ((bad >> (n >> 1)) & 1)) x[n][e] = x[n][2 + e] = -INFINITY;
+            }
+        }
+        // maxima of the logits, and of logit + log2(v_scale), the weights' exponents
+        const float lv[2] = {__log2f(sc.z), __log2f(sc.w)};
+        float top[2], topv[2];
+        bool grown = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a0 = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+          const float a1 = fmaxf(fmaxf(x[2][2 * h], x[2][2 * h + 1]), fmaxf(x[3][2 * h], x[3][2 * h + 1]));
+          top[h] = fmaxf(a0, a1);
+          topv[h] = fmaxf(a0 + lv[0], a1 + lv[1]);
+          grown |= top[h] > m[h] + kLag || topv[h] > mv[h] + kLag;
+        }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+              top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
+              topv[h] = fmaxf(topv[h], __shfl_xor_sync(0xffffffffu, topv[h], off));
+            }
+            const float m1 = fmaxf(m[h], top[h]), mv1 = fmaxf(mv[h], topv[h]);
+            l[h] *= ex2(m[h] - m1);
+            const float f = ex2(mv[h] - mv1);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              o[j][2 * h] *= f;
+              o[j][2 * h + 1] *= f;
+            }
+            m[h] = m1;
+            mv[h] = mv1;
+          }
+        }
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float w = ex2(lv[s] + (m[h] - mv[h]) + kWeightExp);
+            const float p0 = ex2(x[2 * s][2 * h] - m[h]), p1 = ex2(x[2 * s][2 * h + 1] - m[h]);
+            const float p2 = ex2(x[2 * s + 1][2 * h] - m[h]), p3 = ex2(x[2 * s + 1][2 * h + 1] - m[h]);
+            l[h] += (p0 + p1) + (p2 + p3);
+            pf[s][h] = pack_f16(p0 * w, p1 * w);
+            pf[s][2 + h] = pack_f16(p2 * w, p3 * w);
+          }
+        // out += weights . V: tokens 2cq, 2cq+1, 2cq+8, 2cq+9 of each 16, the
+        // bytes of two tokens paired by channel; lane group g holds channels
+        // g * D/8 .. + D/8
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t v[4][D / 32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 16 * s + 2 * cq + (i & 1) + 8 * (i >> 1);
+            if constexpr (D == 128) {
+              const uint4 q4 = lds128(vs + chunk_at<D>(r, g));
+              v[i][0] = q4.x; v[i][1] = q4.y; v[i][2] = q4.z; v[i][3] = q4.w;
+            } else {
+              const uint2 q2 = lds64(vs + chunk_at<D>(r, g >> 1) + 8 * (g & 1));
+              v[i][0] = q2.x; v[i][1] = q2.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {
+            const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), a23 = __byte_perm(v[0][w], v[1][w], 0x7362);
+            const uint32_t b01 = __byte_perm(v[2][w], v[3][w], 0x5140), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+            mma_f16_16816(o[4 * w], pf[s], e4m3x2_to_f16x2(a01), e4m3x2_to_f16x2(b01));
+            mma_f16_16816(o[4 * w + 1], pf[s], e4m3x2_to_f16x2(a01 >> 16), e4m3x2_to_f16x2(b01 >> 16));
+            mma_f16_16816(o[4 * w + 2], pf[s], e4m3x2_to_f16x2(a23), e4m3x2_to_f16x2(b23));
+            mma_f16_16816(o[4 * w + 3], pf[s], e4m3x2_to_f16x2(a23 >> 16), e4m3x2_to_f16x2(b23 >> 16));
+          }
+        }
+      }
+      __syncwarp();
+      issue(it + C::kStages - 1);
+    }
+    cp_async_wait_pending(0);
+    __syncwarp();
+
+    // the warps' results, in units of 2^m, into their rings; then one sum
+    float* mine = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);  // [16][kRowFloats]
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const float f = ex2(mv[h] - m[h] - kWeightExp);
+      // accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int d = 2 * cq * kN + j;
+        mine[r * C::kRowFloats + d + (d >> 5)] = o[j][2 * h] * f;
+        mine[r * C::kRowFloats + d + kN + ((d + kN) >> 5)] = o[j][2 * h + 1] * f;
+      }
+      if (cq == 0) {
+        m_s[warp][r] = m[h];
+        l_s[warp][r] = l[h];
+      }
+    }
+    __syncthreads();
+    const bool whole = take == nt;
+    float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (at == begin ? 0 : 1)) * C::kRecord;
+    for (int i = tid; i < rows * D; i += kThreads) {
+      const int r = i / D, d = i % D;
+      float mt = m_s[0][r];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mt = fmaxf(mt, m_s[w][r]);
+      float lt = 0.f, n = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(m_s[w][r] - mt);
+        lt += l_s[w][r] * f;
+        n += reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[r * C::kRowFloats + d + (d >> 5)] * f;
+      }
+      if (whole) {
+        if (a.sink) {
+          const float s2 = __ldg(a.sink + head0 + r) * kLog2e, m1 = fmaxf(mt, s2);
+          lt = lt * ex2(mt - m1) + ex2(s2 - m1);
+          n *= ex2(mt - m1);
+          mt = m1;
+        }
+        const int64_t row = static_cast<int64_t>(b) * a.n_heads + head0 + r;
+        const __nv_bfloat16 y = __float2bfloat16_rn(lt == 0.f ? 0.f : n / lt);
+        a.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&y);
+        if (a.lse && d == 0) a.lse[row] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+      } else {
+        part[r * D + d] = n;
+        if (d == 0) {
+          part[kRows * D + r] = mt;
+          part[kRows * D + kRows + r] = lt;
+        }
+      }
+    }
+    __syncthreads();
+    at += take;
+    u = 0;
+    if (++pair == pairs && at < end) {
+      pair = 0;
+      do {
+        sp = span_of(a, ++b);
+      } while (sp.units() == 0);
+    }
+  }
+}
+
+// Finishes the pairs that the shares' borders divide (from their CTAs'
+// records, first to last), and the rows of empty sequences.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnArgs a, const int ctas) {
+  using C = Cfg<D>;
+  constexpr int kMergeWarps = kMergeThreads / 32;
+  __shared__ int64_t sh[2 * kMergeWarps];
+  __shared__ float m_s[kMergeWarps], l_s[kMergeWarps];
+  __shared__ float n_s[kMergeWarps][D];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.n_heads / a.cache.n_kv_heads;
+  const int blocks = (group + kRows - 1) / kRows;
+  const int pairs = a.cache.n_kv_heads * blocks;
+  const int b = blockIdx.x / pairs, pair = blockIdx.x - b * pairs;
+  const int hk = pair / blocks, row0 = (pair - hk * blocks) * kRows;
+  const int r = blockIdx.y;
+  if (r >= min(kRows, group - row0)) return;
+  const int head = hk * group + row0 + r;
+  const int64_t row = static_cast<int64_t>(b) * a.n_heads + head;
+  const float sink2 = a.sink ? __ldg(a.sink + head) * kLog2e : -INFINITY;
+
+  int64_t total = 0, before = 0;
+  for (int s = tid; s < a.B; s += kMergeThreads) {
+    const int n = span_of(a, s).units();
+    total += n;
+    before += s < b ? n : 0;
+  }
+  block_sum2(total, before, sh, kMergeThreads);
+  const int nt = span_of(a, b).units();
+  if (nt == 0) {
+    if (tid < D) a.out[row * D + tid] = 0;
+    if (a.lse && tid == 0) a.lse[row] = a.sink ? __ldg(a.sink + head) : -INFINITY;
+    return;
+  }
+  const int64_t per = (total * pairs + ctas - 1) / ctas;
+  const int64_t first = before * pairs + static_cast<int64_t>(pair) * nt;
+  const int c0 = static_cast<int>(first / per), c1 = static_cast<int>((first + nt - 1) / per);
+  if (c0 == c1) return;
+  // a CTA's record 0 is that of its first segment, 1 that of a later one
+  auto record = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c * per < first ? 1 : 0)) * C::kRecord; };
+  float m = kNone;
+  for (int c = c0 + tid; c <= c1; c += kMergeThreads) m = fmaxf(m, record(c)[kRows * D + r]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) m_s[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, m_s[w]);
+  m = fmaxf(m, sink2);
+  constexpr int kPer = D / 32;  // channels a lane
+  float n[kPer], l = 0.f;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) n[j] = 0.f;
+#pragma unroll 2
+  for (int c = c0 + warp; c <= c1; c += kMergeWarps) {
+    const float* p = record(c);
+    const float f = ex2(p[kRows * D + r] - m);
+    l += p[kRows * D + kRows + r] * f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) n[j] += p[r * D + lane + 32 * j] * f;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) n_s[warp][lane + 32 * j] = n[j];
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  if (tid >= D) return;
+  float nt_sum = 0.f, lt = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    nt_sum += n_s[w][tid];
+    lt += l_s[w];
+  }
+  if (a.sink) lt += ex2(sink2 - m);
+  const __nv_bfloat16 y = __float2bfloat16_rn(lt == 0.f ? 0.f : nt_sum / lt);
+  a.out[row * D + tid] = *reinterpret_cast<const uint16_t*>(&y);
+  if (a.lse && tid == 0) a.lse[row] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
+  using C = Cfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int ctas = sms * kCtasPerSm;
+  e = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kThreads), C::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
+  const int group = a.n_heads / a.cache.n_kv_heads;
+  const int64_t pairs = static_cast<int64_t>(a.B) * a.cache.n_kv_heads * ((group + kRows - 1) / kRows);
+  if (pairs > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl(paged_merge_kernel<D>, dim3(static_cast<unsigned>(pairs), group < kRows ? group : kRows),
+                    dim3(kMergeThreads), 0, stream, a, ctas);
+}
+
+}  // namespace
+
+size_t paged_attn_bytes(int head_dim, int sms) {
+  return static_cast<size_t>(sms) * kCtasPerSm * 2 * kRows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
+  if (a.B <= 0) return cudaSuccess;
+  return a.cache.head_dim == 128 ? launch_dim<128>(a, sms, stream) : launch_dim<64>(a, sms, stream);
+}
+
+}  // namespace csa

@@ -1,0 +1,507 @@
+// Attention over packed prompts of different lengths, grouped heads, causal
+// (aligned at the sequences' ends), optionally windowed, with an optional
+// attention sink.  For query row i of a sequence of nq queries and nk keys
+//   keys j <= i + nk - nq (causal), j > i + nk - nq - W (window), j < nk
+//   out_i = sum_j e^{l_ij} v_j / (sum_j e^{l_ij} + e^{sink}),  l = sm_scale q.k
+// in one pass over the keys with a running maximum and sum.
+//
+// Bound by the tensor cores from a few hundred keys on (4 D operations a
+// query, key and head against 4 D bytes a key and head read once a tile of
+// 128 queries).  One CTA per QT tiles of 128 queries of one head: one warp
+// loads Q and a ring of 128-key K and V tiles by TMA, one thread issues the
+// tcgen05 products S = Q K^T and O += P V (S and O in tensor memory, P
+// written over S as bf16 and read from there), four warps a tile do the
+// softmax with one thread a row, so no value crosses threads.  Keys are
+// walked from the diagonal down: the masked tiles come first.
+//
+// P is rounded to bf16 (the products take one type for both operands, and V
+// is bf16); sums and maxima are fp32, over the unrounded weights.
+//
+// A masked weight is 0, and 0 * NaN is NaN: in tiles that some row of the CTA
+// masks, two warps take values that are not finite out of V before the
+// product (rows past the sequence's end become zero), and the rows that do see
+// such a key get its values added at the end, as the formula has them.
+#include <cuda_bf16.h>
+
+#include "gqa.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kTile = 128;               // queries and keys a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -1e30f;          // running maximum before the first key
+// The accumulators are rescaled only when a row's maximum has grown by more
+// than 2^8 since (weights up to 256 are exact in range for bf16 and fp32).
+constexpr float kLag = 8.f;
+// Tiles of keys that some row of a CTA masks: at most 3 that the causal edge
+// of 256 rows crosses, 3 that the window's edge crosses, the sequence's last.
+constexpr int kMaxMasked = 8;
+constexpr int kCleanThreads = 64;
+
+template <int D, int QT>
+struct Cfg {
+  static constexpr int kThreads = QT * 128 + 128;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
+  static constexpr int kBlockBytes = kTile * 128;
+  static constexpr int kStages = 4;                   // K and V tiles in flight, alternating
+  static constexpr int kSmem = QT * kTileBytes + kStages * kTileBytes + 1024;
+  static constexpr int kSCol(int t) { return t * kTile; }
+  static constexpr int kOCol(int t) { return QT * kTile + t * D; }
+  static constexpr int kCols = QT == 2 ? 512 : 256;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+
+// The tiles of keys [lo, hi) that `rows` queries from row `first` on see.
+struct Range {
+  int lo, hi;
+};
+
+struct Seq {
+  int64_t q0, k0;  // first rows of the sequence
+  int nq, nk;
+};
+
+template <int D, int QT>
+__global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a) {
+  using C = Cfg<D, QT>;
+  constexpr int kTmaWarp = 4 * QT, kMmaWarp = 4 * QT + 1, kCleanWarp = 4 * QT + 2;
+  constexpr int kRowsCta = QT * kTile;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int64_t sh[C::kThreads / 32 + 2];
+  __shared__ uint64_t q_full, full[C::kStages], empty[C::kStages], cleaned[C::kStages];
+  __shared__ uint64_t s_full[QT], p_full[QT], o_full[QT], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_s;
+  __shared__ uint32_t odd_rows[kMaxMasked][4];  // keys of each masked tile whose values are not all finite
+  __shared__ int odd_tile[kMaxMasked], n_odd;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* q_s = smem;
+  uint8_t* ring = smem + QT * C::kTileBytes;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* abort_flag = &abort_s;
+  if (tid == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+      mbar_init(cleaned + i, kCleanThreads);
+    }
+    for (int t = 0; t < QT; ++t) {
+      mbar_init(s_full + t, 1);
+      mbar_init(p_full + t, kTile);
+      mbar_init(o_full + t, 1);
+    }
+    fence_mbar_init();
+    abort_s = 0;
+    n_odd = 0;
+  }
+  if (tid < kMaxMasked * 4) odd_rows[tid >> 2][tid & 3] = 0u;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // this CTA's sequence and tiles: the later tiles of a sequence (more keys
+  // under the causal mask) first
+  const int head = static_cast<int>(blockIdx.x % a.n_heads);
+  const int kv_head = head / (a.n_heads / a.n_kv_heads);
+  auto seq_at = [&](int b) {
+    Seq s;
+    const int32_t q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+    const int32_t k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
+    if (!ok) record_error(a.status, kErrIndexRange);
+    s.q0 = q0;
+    s.k0 = k0;
+    s.nq = ok ? q1 - q0 : 0;
+    s.nk = ok ? k1 - k0 : 0;
+    return s;
+  };
+  int64_t index;
+  const int b = find_item<C::kThreads>(
+      a.B, blockIdx.x / a.n_heads,
+      [&](int s) { return static_cast<int64_t>((seq_at(s).nq + kRowsCta - 1) / kRowsCta); }, sh, &index, nullptr);
+  if (b < 0) return;
+  const Seq sq = seq_at(b);
+  const int row0 = ((sq.nq + kRowsCta - 1) / kRowsCta - 1 - static_cast<int>(index)) * kRowsCta;
+  const int shift = sq.nk - sq.nq;  // row i sits at position i + shift among the keys
+
+  // tiles of keys that rows [first, first + rows) see, and whether some of
+  // those rows masks a part of tile j
+  auto range_of = [&](int first, int rows) {
+    Range r;
+    const int64_t last = static_cast<int64_t>(first) + rows - 1 + shift;
+    int64_t hi = sq.nk, lo = 0;
+    if (a.causal && last + 1 < hi) hi = last + 1;
+    if (a.window > 0) lo = static_cast<int64_t>(first) + shift - a.window + 1;
+    if (lo < 0) lo = 0;
+    if (rows <= 0 || hi <= lo) {
+      r.lo = r.hi = 0;
+      return r;
+    }
+    r.lo = static_cast<int>(lo / kTile);
+    r.hi = static_cast<int>((hi + kTile - 1) / kTile);
+    return r;
+  };
+  auto masked = [&](int j, int first, int rows) {
+    const int64_t c0 = static_cast<int64_t>(j) * kTile, c1 = c0 + kTile;  // keys of the tile
+    return c1 > sq.nk || (a.causal && c1 - 1 > static_cast<int64_t>(first) + shift) ||
+           (a.window > 0 && c0 <= static_cast<int64_t>(first) + rows - 1 + shift - a.window);
+  };
+  auto rows_of = [&](int t) { return max(0, min(kTile, sq.nq - row0 - t * kTile)); };
+  const int rows_cta = min(kRowsCta, sq.nq - row0);
+  Range rt[QT];
+  int j_lo = 0x7fffffff, j_hi = 0;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    rt[t] = range_of(row0 + t * kTile, rows_of(t));
+    if (rt[t].lo < rt[t].hi) {
+      j_lo = min(j_lo, rt[t].lo);
+      j_hi = max(j_hi, rt[t].hi);
+    }
+  }
+  const int n_it = j_hi > 0 ? j_hi - j_lo : 0;  // iteration it works on tile j_hi - 1 - it
+  auto active = [&](int t, int it) {
+    const int j = j_hi - 1 - it;
+    return j >= rt[t].lo && j < rt[t].hi;
+  };
+
+  if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == kTmaWarp) {
+    // ---------------- loads ----------------
+    if (lane == 0 && n_it > 0) {
+      mbar_arrive_expect_tx(&q_full, QT * C::kTileBytes);
+      for (int t = 0; t < QT; ++t)
+        for (int k = 0; k < C::kBlocks; ++k)
+          tma_load_3d(q_s + t * C::kTileBytes + k * C::kBlockBytes, &tm_q, k * 64, head,
+                      static_cast<int32_t>(sq.q0 + row0 + t * kTile), &q_full);
+      int issued = 0;
+      for (int s = 0; s < 2 * n_it; ++s) {
+        const int slot = s % C::kStages;
+        if (s >= C::kStages && !wait_or_abort(empty + slot, ((s / C::kStages) - 1) & 1, abort_flag, a.status)) break;
+        mbar_arrive_expect_tx(full + slot, C::kTileBytes);
+        const int row = static_cast<int>(sq.k0) + (j_hi - 1 - (s >> 1)) * kTile;
+        for (int k = 0; k < C::kBlocks; ++k)
+          tma_load_3d(ring + slot * C::kTileBytes + k * C::kBlockBytes, (s & 1) ? &tm_v : &tm_k, k * 64, kv_head, row,
+                      full + slot);
+        ++issued;
+      }
+      // every copy lands before the CTA ends (also after an abort)
+      mbar_wait(&q_full, 0, a.status);
+      for (int s = issued > C::kStages ? issued - C::kStages : 0; s < issued; ++s)
+        mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, a.status);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ---------------- products ----------------
+    if (lane == 0 && n_it > 0) {
+      constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 1, 1, 0, 0);  // bf16, K-major A and B
+      constexpr uint32_t idesc_o = instr_desc(kTile, D, 1, 1, 0, 1);      // A from TMEM, B (= V) MN-major
+      const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
+      const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
+      bool ok = wait_or_abort(&q_full, 0, abort_flag, a.status);
+      uint32_t n_p[QT] = {};            // weights taken so far, by tile
+      uint32_t clean_phase = 0;         // bit s: phase of cleaned[s]
+      for (int it = -1; it < n_it && ok; ++it) {
+        bool v_ready = false;
+        const int v_seq = 2 * it + 1, k_seq = 2 * it + 2;
+        const int v_slot = v_seq % C::kStages, k_slot = k_seq % C::kStages;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          if (it >= 0 && active(t, it)) {
+            ok = wait_or_abort(p_full + t, n_p[t]++ & 1u, abort_flag, a.status);
+            if (!ok) break;
+            if (!v_ready) {
+              ok = wait_or_abort(full + v_slot, (v_seq / C::kStages) & 1, abort_flag, a.status);
+              if (ok && masked(j_hi - 1 - it, row0, rows_cta)) {
+                ok = wait_or_abort(cleaned + v_slot, (clean_phase >> v_slot) & 1u, abort_flag, a.status);
+                clean_phase ^= 1u << v_slot;
+              }
+              if (!ok) break;
+              v_ready = true;
+            }
+            tc_fence_after();
+            const uint32_t vb = rb + v_slot * C::kTileBytes;
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+              mma_f16_ts(tmem + C::kOCol(t), tmem + C::kSCol(t) + s * 8,
+                         smem_desc(vb + s * 2048, C::kBlockBytes, 1024, kSwizzle128B), idesc_o,
+                         (n_p[t] > 1 || s > 0) ? 1u : 0u);
+            if (!active(t, it + 1)) tc_commit(o_full + t);
+          }
+          if (it + 1 < n_it && active(t, it + 1)) {
+            ok = wait_or_abort(full + k_slot, (k_seq / C::kStages) & 1, abort_flag, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kb = rb + k_slot * C::kTileBytes, qt = qb + t * C::kTileBytes;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              mma_f16(tmem + C::kSCol(t),
+                      smem_desc(qt + (s >> 2) * C::kBlockBytes + (s & 3) * 32, 16, 1024, kSwizzle128B),
+                      smem_desc(kb + (s >> 2) * C::kBlockBytes + (s & 3) * 32, 16, 1024, kSwizzle128B), idesc_s,
+                      s > 0 ? 1u : 0u);
+            if (!skip_s) tc_commit(s_full + t);
+          }
+        }
+        if (!ok) break;
+        if (it >= 0) tc_commit(empty + v_slot);
+        if (it + 1 < n_it) tc_commit(empty + k_slot);
+      }
+      // whatever was issued finishes before TMEM and shared memory are released
+      tc_commit(&drain);
+      mbar_wait(&drain, 0, a.status);
+    }
+    __syncwarp();
+  } else if (warp >= kCleanWarp) {
+    // ---------------- values that are not finite, taken out of masked tiles ----------------
+    const int ct = tid - kCleanWarp * 32;
+    int n_masked = 0;
+    for (int it = 0; it < n_it; ++it) {
+      const int j = j_hi - 1 - it;
+      if (!masked(j, row0, rows_cta)) continue;
+      const int seq = 2 * it + 1, slot = seq % C::kStages;
+      if (!wait_or_abort(full + slot, (seq / C::kStages) & 1, abort_flag, a.status)) break;
+      uint4* tile = reinterpret_cast<uint4*>(ring + slot * C::kTileBytes);
+      const int past = sq.nk - j * kTile;  // first row past the sequence
+      for (int i = ct; i < C::kTileBytes / 16; i += kCleanThreads) {
+        const int r = (i >> 3) & (kTile - 1);  // the swizzle moves chunks within their row only
+        if (r >= past) {
+          tile[i] = make_uint4(0u, 0u, 0u, 0u);
+          continue;
+        }
+        const uint4 u = tile[i];
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (not_finite(w[k])) {
+            w[k] &= 0xFFFF0000u;
+            odd = true;
+          }
+          if (not_finite(w[k] >> 16)) {
+            w[k] &= 0xFFFFu;
+            odd = true;
+          }
+        }
+        if (odd) {
+          tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (n_masked < kMaxMasked) {
+            atomicOr(&odd_rows[n_masked][r >> 5], 1u << (r & 31));
+            odd_tile[n_masked] = j;
+            n_odd = 1;
+          }
+        }
+      }
+      ++n_masked;
+      fence_proxy_async_smem();
+      mbar_arrive(cleaned + slot);
+    }
+  } else {
+    // ---------------- softmax: one thread a query row ----------------
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const int first = row0 + t * kTile, rows = rows_of(t);
+    const int i = first + r;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_base + C::kSCol(t), o_tmem = tmem + lane_base + C::kOCol(t);
+    const float scale2 = a.sm_scale * kLog2e;
+    float m2 = kNone, l = 0.f;
+    bool ok = true;
+    const int n_tiles = rt[t].hi - rt[t].lo;
+    for (int n = 0; n < n_tiles; ++n) {
+      const int j = rt[t].hi - 1 - n;
+      ok = wait_or_abort(s_full + t, n & 1, abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
+      tmem_wait_ld();
+      if (masked(j, first, rows)) {
+        int64_t hi = sq.nk - 1, lo = 0;
+        if (a.causal && static_cast<int64_t>(i) + shift < hi) hi = static_cast<int64_t>(i) + shift;
+        if (a.window > 0) lo = static_cast<int64_t>(i) + shift - a.window + 1;
+        hi -= static_cast<int64_t>(j) * kTile;
+        lo -= static_cast<int64_t>(j) * kTile;
+        const int c_hi = static_cast<int>(hi < -1 ? -1 : hi > kTile ? kTile : hi);
+        const int c_lo = static_cast<int>(lo < 0 ? 0 : lo > kTile ? kTile : lo);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k > c_hi || 32 * c + k < c_lo) s[c][k] = 0xFF800000u;  // -inf
+      }
+      float top[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int k = 1; k < 32; ++k) top[c] = fmaxf(top[c], __uint_as_float(s[c][k]));
+      }
+      const float top2 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
+      if (__any_sync(0xffffffffu, top2 > m2 + kLag)) {
+        const float m1 = fmaxf(m2, top2), f = ex2(m2 - m1);
+        m2 = m1;
+        l *= f;
+        if (n > 0) {  // the products of the tiles before have finished: S was issued after them
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_tmem + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(o_tmem + 32 * c, o);
+          }
+        }
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float x = ex2(fmaf(__uint_as_float(s[c][2 * k]), scale2, -m2));
+          const float y = ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), scale2, -m2));
+          sum[c] += x + y;
+          const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+          p[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        tmem_st16(s_tmem + 16 * c, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full + t);
+    }
+    if (ok && n_tiles > 0) {
+      ok = wait_or_abort(o_full + t, 0, abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok && rows > 0) {
+      // the masked tiles were cleaned before their products, so n_odd is final
+      const int64_t row = (sq.q0 + i) * a.n_heads + head;
+      if (a.sink) {
+        const float s2 = __ldg(a.sink + head) * kLog2e, m1 = fmaxf(m2, s2), f = ex2(m2 - m1);
+        l = l * f + ex2(s2 - m1);
+        const float inv = l == 0.f ? 0.f : f / l;
+        if (a.lse && r < rows) a.lse[row] = l == 0.f ? -INFINITY : (m1 + log2f(l)) * kLn2;
+        l = inv;
+      } else {
+        if (a.lse && r < rows) a.lse[row] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
+        l = l == 0.f ? 0.f : 1.f / l;
+      }
+      const bool odd = *const_cast<volatile int*>(&n_odd) != 0;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n_tiles > 0) {
+          tmem_ld32(o_tmem + 32 * c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * l;
+        if (odd && r < rows) {
+          for (int e = 0; e < kMaxMasked * kTile; ++e) {
+            const uint32_t word = odd_rows[e >> 7][(e >> 5) & 3];
+            if (!((word >> (e & 31)) & 1u)) continue;
+            const int64_t key = static_cast<int64_t>(odd_tile[e >> 7]) * kTile + (e & (kTile - 1));
+            const int64_t pos = static_cast<int64_t>(i) + shift;
+            if ((a.causal && key > pos) || (a.window > 0 && key <= pos - a.window)) continue;
+            const uint16_t* v = a.v + (sq.k0 + key) * a.v_stride + kv_head * a.v_stride_h + 32 * c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t h = v[k];
+              if (not_finite(h)) x[k] += __uint_as_float(h << 16);
+            }
+          }
+        }
+        if (r < rows) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]);
+              w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// Rows of `heads` heads as a 3-D tensor, read in boxes of 64 channels of 128
+// rows of one head (128-byte swizzle); rows past the end read as zero.
+bool encode_rows(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 encode, const uint16_t* base, int dim, int heads,
+                 int64_t rows, int64_t stride, int64_t stride_h) {
+  cuuint64_t size[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, 1, kTile};
+  cuuint32_t ones[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), size, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int QT>
+cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
+  using C = Cfg<D, QT>;
+  CUtensorMap tm_q, tm_k, tm_v;
+  const int64_t n_k = a.n_k > 0 ? a.n_k : 1;  // (no keys: the maps are not read)
+  if (!encode || !encode_rows(&tm_q, encode, a.q, D, a.n_heads, a.n_q, a.q_stride, a.q_stride_h) ||
+      !encode_rows(&tm_k, encode, a.n_k > 0 ? a.k : a.q, D, a.n_kv_heads, n_k, a.k_stride, a.k_stride_h) ||
+      !encode_rows(&tm_v, encode, a.n_k > 0 ? a.v : a.q, D, a.n_kv_heads, n_k, a.v_stride, a.v_stride_h))
+    return cudaErrorInvalidValue;
+  cudaError_t e =
+      cudaFuncSetAttribute(prompt_attn_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  // n rows are at most n / R + 1 tiles of R rows, and at most n
+  const int64_t most = a.n_q / (QT * kTile) + a.B;
+  const int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl(prompt_attn_kernel<D, QT>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream,
+                    tm_q, tm_k, tm_v, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
+  if (a.B <= 0 || a.n_q <= 0) return cudaSuccess;
+  return a.head_dim == 128 ? launch_dim<128, 1>(a, encode, stream) : launch_dim<64, 1>(a, encode, stream);
+}
+
+}  // namespace csa

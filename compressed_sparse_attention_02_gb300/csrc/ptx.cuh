@@ -144,6 +144,24 @@ __device__ __forceinline__ bool mbar_try_wait_cluster_sleep(uint64_t* bar, uint3
   return ok != 0;
 }
 
+// A bounded wait that also ends when another thread of the CTA has raised
+// the abort flag; a wait that runs out records kErrTimeout and raises it.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                              unsigned* status) {
+  constexpr uint32_t kSleepNs = 20000;  // the thread wakes when the phase completes
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns(), limit = wait_limit_ns(status);
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit) {
+      record_error(status, kErrTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
 // Arrives (release, cluster scope) on an mbarrier of a CTA of the cluster,
 // given as a cluster address (dsmem_addr).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
@@ -514,6 +532,17 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same product with A in TMEM: row r of A at lane r, two consecutive K
+// values (16-bit, the first in the low half) a 32-bit column from a_tmem on.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 

@@ -1,0 +1,144 @@
+// Rotary positions of query and key rows ("CSA2 详解" §12.1 "Partial RoPE" is
+// the same rotation on a latent's last channels): pair j of a row at position
+// p turns by the angle p * f_j, (x, y) -> m (x cos - y sin, x sin + y cos);
+// the inverse turns back (and is the rotation's gradient, its transpose).
+//
+// Bound by memory: every channel is read and written once.  A CTA computes
+// the sines and cosines of its tokens once into shared memory (all heads of a
+// token share them), then each thread rotates items of 16 channels, two
+// 16-byte loads and stores an item, up to four items in flight.
+#include <cuda_bf16.h>
+
+#include "gqa.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxTokens = 16;   // tokens a CTA
+constexpr int kMaxRopeDim = 512;
+
+struct RopeGrid {
+  int tokens;       // tokens a CTA
+  int heads;        // heads a CTA
+  int items;        // items a row: head_dim / 16, or rope_dim / 16 in place
+  uint32_t inv_items, inv_heads;  // ceil(2^32 / items), ceil(2^32 / heads)
+};
+
+__device__ __forceinline__ uint32_t div_by(uint32_t x, uint32_t inv, int n) {
+  return n == 1 ? x : __umulhi(x, inv);
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeRowsArgs a, const RopeGrid g) {
+  extern __shared__ float2 sc_s[];  // [tokens][rope_dim / 2] (sin, cos)
+  __shared__ int32_t pos_s[kRopeMaxTokens];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * g.tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(g.tokens), a.n_rows - t0));
+  const int h0 = static_cast<int>(blockIdx.y) * g.heads;
+  const int nh = min(g.heads, a.n_heads - h0);
+  const int pairs = a.rope.rope_dim >> 1;
+  if (tid < nt) pos_s[tid] = __ldg(a.pos + t0 + tid);
+  __syncthreads();
+  for (int i = tid; i < nt * pairs; i += kRopeThreads) {
+    const int t = i / pairs, j = i - t * pairs;
+    float s, c;
+    rope_sincos_exact(pos_s[t], __ldg(a.rope.turns + j), &s, &c);
+    sc_s[i] = make_float2((a.inverse ? -s : s) * a.rope.mscale, c * a.rope.mscale);
+  }
+  __syncthreads();
+  const int per_token = g.heads * g.items;  // (a last group of fewer heads leaves its items out)
+  const int n = nt * per_token;
+  const int rotated = a.rope.rope_dim >> 4;
+  constexpr int kFlight = 4;
+  for (int i0 = tid; i0 < n; i0 += kFlight * kRopeThreads) {
+    uint4 u[kFlight], v[kFlight];
+    uint16_t *lo[kFlight], *hi[kFlight];
+    int at[kFlight];  // the item's (sin, cos) in sc_s; -1: copied; -2: nothing
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int i = i0 + k * kRopeThreads;
+      at[k] = -2;
+      if (i >= n) continue;
+      const int row = static_cast<int>(div_by(i, g.inv_items, g.items));
+      const int it = i - row * g.items;
+      const int t = static_cast<int>(div_by(row, g.inv_heads, g.heads));
+      const int h = row - t * g.heads;
+      if (h >= nh || pos_s[t] < 0) continue;
+      int cl, ch;
+      item_chunks(a.rope, it, &cl, &ch);
+      const uint16_t* src = a.in + (t0 + t) * a.in_stride + (h0 + h) * a.in_stride_h;
+      uint16_t* dst = a.out + (t0 + t) * a.out_stride + (h0 + h) * a.out_stride_h;
+      u[k] = *reinterpret_cast<const uint4*>(src + cl);
+      v[k] = *reinterpret_cast<const uint4*>(src + ch);
+      lo[k] = dst + cl;
+      hi[k] = dst + ch;
+      at[k] = it < rotated ? t * pairs + 8 * it : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      if (at[k] == -2) continue;
+      if (at[k] >= 0) {
+        float x[8], y[8];
+        float2 sc[8];
+        unpack_bf16(u[k], x);
+        unpack_bf16(v[k], y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sc[j] = sc_s[at[k] + j];
+        rotate_item(a.rope.half != 0, sc, x, y);
+        u[k] = pack_bf16(x);
+        v[k] = pack_bf16(y);
+      }
+      *reinterpret_cast<uint4*>(lo[k]) = u[k];
+      *reinterpret_cast<uint4*>(hi[k]) = v[k];
+    }
+  }
+}
+
+uint32_t inverse_of(int n) { return static_cast<uint32_t>(((1ull << 32) + n - 1) / n); }
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeRowsArgs& a, cudaStream_t stream) {
+  if (a.n_rows <= 0 || a.n_heads <= 0) return cudaSuccess;
+  RopeGrid g;
+  const bool in_place = a.in == a.out;
+  g.items = (in_place ? a.rope.rope_dim : a.head_dim) >> 4;
+  // A CTA of 256 threads takes about 2048 items (8 a thread, four in flight):
+  // several tokens of few heads, or one token whose heads are split while the
+  // grid would not fill the GPU.
+  const int64_t row_items = static_cast<int64_t>(a.n_heads) * g.items;
+  int64_t tokens = 2048 / row_items;
+  tokens = tokens < 1 ? 1 : tokens > kRopeMaxTokens ? kRopeMaxTokens : tokens;
+  while (tokens > 1 && (a.n_rows + tokens - 1) / tokens < 600) tokens >>= 1;
+  g.tokens = static_cast<int>(tokens);
+  g.heads = a.n_heads;
+  // one token a CTA: at most 8192 items (also the range of the reciprocals)
+  while (g.tokens == 1 && g.heads > 1 &&
+         (static_cast<int64_t>(g.heads) * g.items > 8192 ||
+          (g.heads * g.items > kRopeThreads && a.n_rows * ((a.n_heads + g.heads - 1) / g.heads) < 600)))
+    g.heads = (g.heads + 1) / 2;
+  g.inv_items = inverse_of(g.items);
+  g.inv_heads = inverse_of(g.heads);
+  const int64_t gx = (a.n_rows + g.tokens - 1) / g.tokens;
+  if (gx > 0x7fffffff) return cudaErrorInvalidValue;
+  const size_t smem = static_cast<size_t>(g.tokens) * (a.rope.rope_dim / 2) * sizeof(float2);
+  static_assert(kRopeMaxTokens * (kMaxRopeDim / 2) * sizeof(float2) <= 48 * 1024, "the default shared-memory limit");
+  return launch_pdl(rope_kernel, dim3(static_cast<unsigned>(gx), (a.n_heads + g.heads - 1) / g.heads),
+                    dim3(kRopeThreads), smem, stream, a, g);
+}
+
+}  // namespace csa

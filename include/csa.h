@@ -661,6 +661,166 @@ csa_status csa_hca_layer_decode(const csa_params *p, int32_t B,
                                 void *stream);
 
 /*
+ * ---- Grouped-query attention layers ------------------------------------------
+ * Hybrid models place ordinary attention layers beside the compressed ones:
+ * query heads that share key / value heads in groups ([结构对比] "MHA、GQA",
+ * the layers that CSA and HCA are compared with).  The calls below serve such
+ * a layer: rotate queries and keys, attend over packed prompts, append keys
+ * and values to a paged 8-bit cache, and attend to it one token at a time.
+ * They take no csa_params.  Conventions are those at the top, with these
+ * additions: rows are [rows][heads][head_dim] bf16 with strides in elements
+ * for rows and heads (multiples of 8, at least head_dim; the channels are
+ * contiguous), so views of a fused projection pass as they are; row pointers
+ * are 16-byte aligned, int32 and fp32 arrays 4-byte aligned; query head h
+ * reads key / value head h / (n_heads / n_kv_heads); n_heads at most 1024.
+ */
+
+/*
+ * csa_rope_params — rotary positions.  Pair j of the rope_dim channels from
+ * `offset` on turns by pos * f_j, f_j = theta^(-2j/rope_dim) unscaled:
+ *   (x, y) -> mscale * (x cos - y sin, x sin + y cos).
+ * Pairs: CSA_ROPE_INTERLEAVED channels (2j, 2j+1), CSA_ROPE_HALF channels
+ * (j, j + rope_dim/2).  Scaling for positions beyond the trained length:
+ *   CSA_ROPE_LINEAR   f_j / factor;
+ *   CSA_ROPE_BY_PARTS f_j (1 - g_j) + f_j / factor * g_j with
+ *     g_j = clamp((j - low) / max(high - low, 0.001), 0, 1), c(beta) =
+ *     rope_dim * ln(orig_len / (2 pi beta)) / (2 ln theta), low =
+ *     max(floor(c(beta_fast)), 0), high = min(ceil(c(beta_slow)),
+ *     rope_dim - 1): pairs that turn often keep their frequency, slow ones
+ *     are interpolated.
+ * rope_dim (16..512) and offset are multiples of 16; theta >= 1, factor >= 1.
+ */
+enum { CSA_ROPE_INTERLEAVED = 0, CSA_ROPE_HALF = 1 };
+enum { CSA_ROPE_UNSCALED = 0, CSA_ROPE_LINEAR = 1, CSA_ROPE_BY_PARTS = 2 };
+typedef struct {
+  int32_t rope_dim, offset, layout, scaling;
+  float theta, factor;
+  int32_t orig_len;
+  float beta_fast, beta_slow, mscale;
+} csa_rope_params;
+
+/* Fills *r: 128 channels from 0, half pairs, unscaled, theta 1e4, mscale 1. */
+void csa_default_rope(csa_rope_params *r);
+
+/* Fills the HOST array turns[rope_dim/2] with each pair's turns a position
+ * times 2^64; the calls below take its copy in device memory.  (A position's
+ * angle is then an exact integer product modulo one turn, whatever the
+ * position.) */
+csa_status csa_rope_table(const csa_rope_params *r, uint64_t *turns);
+
+/*
+ * csa_rope — rotates n_rows rows of n_heads heads by their positions pos
+ * [n_rows] and rounds to bf16 once; channels outside the rotated part are
+ * copied.  inverse = 1 turns by the opposite angle (times mscale all the
+ * same): the rotation's gradient.  Rows with a negative position are left as
+ * they were in `out`.  head_dim: a multiple of 16 up to 512.  out may be in
+ * (same strides); otherwise the two must not overlap.
+ */
+csa_status csa_rope(const csa_rope_params *r, const uint64_t *turns,
+                    int64_t n_rows, int32_t n_heads, int32_t head_dim,
+                    const int32_t *pos, const uint16_t *in, int64_t in_stride,
+                    int64_t in_stride_h, uint16_t *out, int64_t out_stride,
+                    int64_t out_stride_h, int32_t inverse, void *stream);
+
+/*
+ * csa_paged_cache — a pool of pages of page_size tokens (16, 32, 64 or 128)
+ * of E4M3 codes with one fp32 scale per page and head; a row stands for
+ * scale * code.  Sequence b's token t lies in page table[b][t / page_size],
+ * row t % page_size.  A host struct of device pointers, read during the call.
+ *   k, v             [n_pages][n_kv_heads][page_size][head_dim] codes
+ *   k_scale, v_scale [n_pages][n_kv_heads], positive (csa_kv_append writes
+ *                    powers of two; csa_paged_attn reads any)
+ *   table            [sequences][table_stride] page numbers; table_stride *
+ *                    page_size at most 2^30
+ * head_dim: 64 or 128.
+ */
+typedef struct {
+  int32_t n_kv_heads, head_dim, page_size;
+  int64_t n_pages;
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t *table;
+  int64_t table_stride;
+} csa_paged_cache;
+
+/*
+ * csa_kv_append — rows cu_rows[b] .. cu_rows[b+1]-1 of k and v become tokens
+ * pos0[b], pos0[b]+1, ... of sequence b (cu_rows NULL: row b, one token each;
+ * n_rows is then B).  Keys are rotated by their token's position first (r
+ * NULL: as they are), in fp32 without a rounding in between.
+ * A page's scale is 2^e with the smallest e >= -126 for which no finite value
+ * exceeds 448 * 2^e, over the page's rows: tokens before pos0[b] in its page
+ * count with the scale that is there, and where the new rows need a larger
+ * one their codes are re-rounded to it.  A page whose first token is new
+ * starts afresh.  A code is the E4M3 value nearest to x / scale (ties to
+ * even; the quotient in binary32); NaN stays NaN, infinities saturate.
+ * Rows of k and v past cu_rows[B] are not read, and tokens other than those
+ * above are not written.  Sequences with pos0[b] < 0 or no rows store
+ * nothing.  A token past the table or in a page outside the pool, and a
+ * cu_rows entry that falls or passes n_rows, record CSA_ERR_INDEX_RANGE and
+ * store nothing.  Pages that several sequences of one call append to hold
+ * unspecified tokens afterwards (nothing outside them is touched).
+ */
+csa_status csa_kv_append(const csa_paged_cache *c, const csa_rope_params *r,
+                         const uint64_t *turns, int32_t B, int64_t n_rows,
+                         const int32_t *cu_rows, const int32_t *pos0,
+                         const uint16_t *k, int64_t k_stride,
+                         int64_t k_stride_h, const uint16_t *v,
+                         int64_t v_stride, int64_t v_stride_h, void *stream);
+
+/*
+ * csa_paged_attn — one query token a sequence over its cached tokens
+ * 0 .. lens[b]-1 (the query's own included), the last `window` of them if
+ * window > 0:
+ *   l_t = sm_scale * q . key_t   (sm_scale > 0),
+ *   out[b,h] = sum_t e^{l_t} value_t / (sum_t e^{l_t} + e^{sink[h]})
+ * (sink NULL: no such term), lse[b,h] (optional) = the log of the sum.  A
+ * sequence of length 0 gives 0 and lse = sink, or -inf without one.
+ * q: [B][n_heads][head_dim] with strides.  out: [B][n_heads][head_dim], lse
+ * [B][n_heads], contiguous.  sink: [n_heads] fp32, finite or -inf.
+ * A length past the table is clamped, and tokens in a page outside the pool
+ * are left out; both record CSA_ERR_INDEX_RANGE.
+ * Workspace: csa_paged_attn_workspace_size bytes (a constant of the device
+ * and head_dim), of the call's own while it runs: calls that can overlap on
+ * the GPU, replayed graphs among them, need one each.
+ * Equal calls give equal bits.
+ */
+size_t csa_paged_attn_workspace_size(const csa_paged_cache *c, int32_t B,
+                                     int32_t n_heads);
+csa_status csa_paged_attn(const csa_paged_cache *c, int32_t B, int32_t n_heads,
+                          const int32_t *lens, const uint16_t *q,
+                          int64_t q_stride, int64_t q_stride_h, float sm_scale,
+                          int32_t window, const float *sink, uint16_t *out,
+                          float *lse, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * csa_prompt_attn — attention of packed sequences: sequence b's queries are
+ * rows cu_q[b] .. cu_q[b+1]-1 of q, its keys and values rows cu_k[b] ..
+ * cu_k[b+1]-1 of k and v.  Its last query stands at its last key: with
+ * s = (keys - queries), query i sees keys j <= i + s (causal = 1; all keys
+ * with causal = 0), and with window > 0 (causal only) j > i + s - window.
+ * The sums, sink and lse are csa_paged_attn's; a query that sees nothing
+ * gives 0 and lse = sink, or -inf.  Keys and values that a query does not
+ * see have no effect on it, whatever they hold.
+ * n_q, n_k: rows of q and of k / v; rows behind the last sequence are left as
+ * they are in out.  out: [n_q][n_heads][head_dim], lse [n_q][n_heads],
+ * contiguous.  head_dim: 64 or 128.  A sequence with a cu_q or cu_k entry
+ * that falls or passes its rows records CSA_ERR_INDEX_RANGE and is left out.
+ * No workspace.  Weights are rounded to bf16 for the product with the values.
+ */
+csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads,
+                           int32_t head_dim, int64_t n_q, int64_t n_k,
+                           const int32_t *cu_q, const int32_t *cu_k,
+                           const uint16_t *q, int64_t q_stride,
+                           int64_t q_stride_h, const uint16_t *k,
+                           int64_t k_stride, int64_t k_stride_h,
+                           const uint16_t *v, int64_t v_stride,
+                           int64_t v_stride_h, float sm_scale, int32_t causal,
+                           int32_t window, const float *sink, uint16_t *out,
+                           float *lse, void *stream);
+
+/*
  * Optional stage tracing, for profiling.  With events != NULL (n_events == 5
  * cudaEvent_t handles passed as void*), every csa_layer_decode(_append,
  * _with_keys) and csa_layer_prefill(_with_keys) call records events[0] on
@@ -701,7 +861,8 @@ csa_status csa_check_status(void *stream);
  *     TOPK     a top-k cluster's rank 0 never sends its first crossing (rows
  *              of more than 4096 keys);
  *     ATTN     the sparse attention's MMA thread never announces the first
- *              tile's scores (every form: single CTA, cluster, split-KV).
+ *              tile's scores (every form: single CTA, cluster, split-KV),
+ *              nor does csa_prompt_attn's.
  *   A non-zero faults needs a non-zero wait_limit_us.
  * Synchronises the device first.  Process-wide per device: set it only while
  * no other call runs.  Errors: CSA_ERR_INVALID_ARG for unknown bits or faults
