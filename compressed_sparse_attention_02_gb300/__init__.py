@@ -123,8 +123,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream (0.1 us
+# instead of 2.9 us a call), where this torch has the call for it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -353,28 +360,44 @@ for _f in ("csa_rope_table", "csa_rope", "csa_kv_append", "csa_paged_attn", "csa
     getattr(_lib, _f).restype = ctypes.c_int
 
 
-def _need(ok: bool, where: str, what: str):
-    if not ok:
-        raise CsaError(1, "%s (%s)" % (where, what))
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
-def _arg(where, name, t, dtypes, shape, contiguous=True):
-    """Checks one tensor; shape entries of None are free.  Returns the tensor."""
-    _need(torch.is_tensor(t), where, "%s: no tensor" % name)
-    _need(t.dtype in dtypes, where, "%s: %s" % (name, t.dtype))
-    _need(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), where,
-          "%s: shape %s, expected %s" % (name, tuple(t.shape), tuple("any" if n is None else n for n in shape)))
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device(), where, "%s: on %s" % (name, t.device))
-    _need(t.is_contiguous() if contiguous else t.shape[-1] <= 1 or t.stride(-1) == 1, where, "%s: strides" % name)
-    return t
+def _bad(where, name, t=None, expected=""):
+    """Refuses an argument (the checks that lead here are written out at each call: they are most of a call's time
+    on the host)."""
+    if torch.is_tensor(t):
+        name = "%s: %s %s, strides %s, on %s" % (name, t.dtype, tuple(t.shape), tuple(t.stride()), t.device)
+    raise CsaError(1, "%s (%s%s)" % (where, name, "; expected " + expected if expected else ""))
 
 
-def _strides(t):
-    """Row and head strides of a [rows][heads][channels] tensor; of a dimension of size one, whose stride has no
-    meaning, a valid one."""
-    rows, heads, dim = t.shape
-    h = t.stride(1) if heads > 1 else dim
-    return (t.stride(0) if rows > 1 else max(h * heads, dim)), h
+def _flat(where, name, t, dtype, shape, dev):
+    """A contiguous tensor of this type and shape on the current device: its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _bad(where, name, t, "contiguous %s %s on the current device" % (dtype, tuple(shape)))
+    return t.data_ptr()
+
+
+def _rows(where, name, t, shape, dev):
+    """[rows][heads][channels] bf16 with contiguous channels on the current device: address, row and head stride (of
+    a dimension of size one, whose stride has no meaning, a valid one)."""
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+        _bad(where, name, t, "bfloat16 %s on the current device" % (tuple(shape),))
+    rows, heads, dim = shape
+    row, head, one = t.stride()
+    if one != 1 and dim > 1:
+        _bad(where, name, t, "contiguous channels")
+    if heads <= 1:
+        head = dim
+    if rows <= 1:
+        row = heads * head
+    return t.data_ptr(), row, head
+
+
+def _shape3(where, name, t):
+    if not torch.is_tensor(t) or t.dim() != 3 or not t.is_cuda:
+        _bad(where, name, t, "[rows][heads][channels] in device memory")
+    return t.shape
 
 
 def rope_params(**fields) -> CsaRopeParams:
@@ -382,7 +405,8 @@ def rope_params(**fields) -> CsaRopeParams:
     r = CsaRopeParams()
     _lib.csa_default_rope(ctypes.byref(r))
     for k, v in fields.items():
-        _need(k in dict(CsaRopeParams._fields_), "rope_params", "no field %s" % k)
+        if k not in dict(CsaRopeParams._fields_):
+            _bad("rope_params", "no field %s" % k)
         setattr(r, k, v)
     return r
 
@@ -397,29 +421,33 @@ def rope_table(r: CsaRopeParams, device=None) -> torch.Tensor:
 def csa_rope(r, turns, pos, x, out=None, inverse=False, stream=None):
     """Rotates x [rows][heads][channels] by pos [rows] (int32) into out, a new tensor where it is None; returns it."""
     w = "csa_rope"
-    bf16 = (torch.bfloat16,)
-    _arg(w, "x", x, bf16, (None, None, None), contiguous=False)
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    _arg(w, "out", out, bf16, tuple(x.shape), contiguous=False)
-    _arg(w, "pos", pos, (torch.int32,), (x.shape[0],))
-    _arg(w, "turns", turns, (torch.int64,), (r.rope_dim // 2,))
-    _check(_lib.csa_rope(ctypes.byref(r), _ptr(turns), *x.shape, _ptr(pos), _ptr(x), *_strides(x), _ptr(out),
-                         *_strides(out), int(inverse), _stream(stream)), w)
+    shape = _shape3(w, "x", x)
+    dev = torch.cuda.current_device()
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
+    n, heads, dim = shape
+    _check(_lib.csa_rope(ctypes.byref(r), _flat(w, "turns", turns, _I64, (r.rope_dim // 2,), dev), n, heads, dim,
+                         _flat(w, "pos", pos, _I32, (n,), dev), *_rows(w, "x", x, shape, dev),
+                         *_rows(w, "out", out, shape, dev), 1 if inverse else 0, _stream(stream)), w)
     return out
 
 
 def paged_cache(k, v, k_scale, v_scale, table) -> CsaPagedCache:
     """A ``csa_paged_cache`` over device tensors: k, v [pages][kv heads][page size][channels] E4M3 (or uint8 codes),
     k_scale, v_scale [pages][kv heads] fp32, table [sequences][pages] int32.  It keeps the tensors."""
-    w, f8 = "paged_cache", (torch.float8_e4m3fn, torch.uint8)
-    n, heads, page, dim = _arg(w, "k", k, f8, (None,) * 4).shape
-    _arg(w, "v", v, f8, (n, heads, page, dim))
-    _arg(w, "k_scale", k_scale, (torch.float32,), (n, heads))
-    _arg(w, "v_scale", v_scale, (torch.float32,), (n, heads))
-    _arg(w, "table", table, (torch.int32,), (None, None))
-    c = CsaPagedCache(heads, dim, page, n, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(table),
-                      table.shape[1])
-    c.tensors = (k, v, k_scale, v_scale, table)
+    w = "paged_cache"
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 4 or t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_cuda:
+            _bad(w, name, t, "E4M3 or uint8 [pages][kv heads][page size][channels] in device memory")
+    dev = torch.cuda.current_device()
+    if table.dim() != 2:
+        _bad(w, "table", table, "[sequences][pages]")
+    n, heads, page, dim = k.shape
+    c = CsaPagedCache(heads, dim, page, n, _flat(w, "k", k, k.dtype, k.shape, dev),
+                      _flat(w, "v", v, v.dtype, k.shape, dev), _flat(w, "k_scale", k_scale, _F32, (n, heads), dev),
+                      _flat(w, "v_scale", v_scale, _F32, (n, heads), dev),
+                      _flat(w, "table", table, _I32, table.shape, dev), table.shape[1])
+    c.tensors, c.n_seqs, c.device = (k, v, k_scale, v_scale, table), table.shape[0], dev
     return c
 
 
@@ -427,18 +455,18 @@ def csa_kv_append(cache, r, turns, cu_rows, pos0, k, v, stream=None):
     """Appends rows of k and v [rows][kv heads][channels] to the cache from positions pos0 [B] on; sequence b's rows
     are cu_rows[b] .. cu_rows[b+1]-1 (cu_rows [B+1], or None: one row each).  r and turns None: keys as they are."""
     w = "csa_kv_append"
-    bf16, i32 = (torch.bfloat16,), (torch.int32,)
-    B = _arg(w, "pos0", pos0, i32, (None,)).shape[0]
-    _need(B <= cache.tensors[4].shape[0], w, "pos0: more sequences than the table has")
-    _arg(w, "k", k, bf16, (None if cu_rows is not None else B, cache.n_kv_heads, cache.head_dim), contiguous=False)
-    _arg(w, "v", v, bf16, tuple(k.shape), contiguous=False)
-    if cu_rows is not None:
-        _arg(w, "cu_rows", cu_rows, i32, (B + 1,))
-    if r is not None:
-        _arg(w, "turns", turns, (torch.int64,), (r.rope_dim // 2,))
+    B, shape = pos0.numel(), _shape3(w, "k", k)
+    dev = torch.cuda.current_device()
+    n, heads, dim = shape
+    if heads != cache.n_kv_heads or dim != cache.head_dim or (cu_rows is None and n != B):
+        _bad(w, "k", k, "[%s][%d][%d]" % (B if cu_rows is None else "rows", cache.n_kv_heads, cache.head_dim))
+    if B > cache.n_seqs or cache.device != dev:
+        _bad(w, "pos0", pos0, "at most %d sequences, the cache on the current device" % cache.n_seqs)
     _check(_lib.csa_kv_append(ctypes.byref(cache), None if r is None else ctypes.byref(r),
-                              None if r is None else _ptr(turns), B, k.shape[0], _ptr(cu_rows), _ptr(pos0), _ptr(k),
-                              *_strides(k), _ptr(v), *_strides(v), _stream(stream)), w)
+                              None if r is None else _flat(w, "turns", turns, _I64, (r.rope_dim // 2,), dev), B, n,
+                              None if cu_rows is None else _flat(w, "cu_rows", cu_rows, _I32, (B + 1,), dev),
+                              _flat(w, "pos0", pos0, _I32, (B,), dev), *_rows(w, "k", k, shape, dev),
+                              *_rows(w, "v", v, shape, dev), _stream(stream)), w)
 
 
 def paged_attn_workspace(cache, B: int, n_heads: int) -> torch.Tensor:
@@ -452,40 +480,44 @@ def paged_attn_workspace(cache, B: int, n_heads: int) -> torch.Tensor:
 def csa_paged_attn(cache, lens, q, sm_scale, window, sink, out, lse, ws, stream=None):
     """q [B][heads][channels] over the cached tokens 0 .. lens[b]-1 into out [B][heads][channels] (and lse
     [B][heads] fp32, or None)."""
-    w, f32 = "csa_paged_attn", (torch.float32,)
-    B, heads, dim = _arg(w, "q", q, (torch.bfloat16,), (None, None, cache.head_dim), contiguous=False).shape
-    _need(B <= cache.tensors[4].shape[0], w, "q: more sequences than the table has")
-    _arg(w, "lens", lens, (torch.int32,), (B,))
-    _arg(w, "out", out, (torch.bfloat16,), (B, heads, dim))
-    if sink is not None:
-        _arg(w, "sink", sink, f32, (heads,))
-    if lse is not None:
-        _arg(w, "lse", lse, f32, (B, heads))
-    if ws is not None:
-        _arg(w, "ws", ws, (torch.uint8,), (None,))
-    _check(_lib.csa_paged_attn(ctypes.byref(cache), B, heads, _ptr(lens), _ptr(q), *_strides(q), sm_scale, window,
-                               _ptr(sink), _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(),
+    w = "csa_paged_attn"
+    shape = _shape3(w, "q", q)
+    dev = torch.cuda.current_device()
+    B, heads, dim = shape
+    if dim != cache.head_dim or B > cache.n_seqs or cache.device != dev:
+        _bad(w, "q", q, "at most %d sequences, heads of %d, the cache on the current device" %
+             (cache.n_seqs, cache.head_dim))
+    size = 0 if ws is None else ws.numel()
+    _check(_lib.csa_paged_attn(ctypes.byref(cache), B, heads, _flat(w, "lens", lens, _I32, (B,), dev),
+                               *_rows(w, "q", q, shape, dev), sm_scale, window,
+                               None if sink is None else _flat(w, "sink", sink, _F32, (heads,), dev),
+                               _flat(w, "out", out, _BF16, shape, dev),
+                               None if lse is None else _flat(w, "lse", lse, _F32, (B, heads), dev),
+                               None if ws is None else _flat(w, "ws", ws, torch.uint8, (size,), dev), size,
                                _stream(stream)), w)
 
 
 def csa_prompt_attn(cu_q, cu_k, q, k, v, sm_scale, causal, window, sink, out, lse=None, stream=None):
     """Packed sequences: q [rows][heads][channels] by cu_q [B+1], k and v [rows][kv heads][channels] by cu_k [B+1],
     into out (like q, contiguous) and lse [rows][heads] fp32 or None."""
-    w, bf16, i32, f32 = "csa_prompt_attn", (torch.bfloat16,), (torch.int32,), (torch.float32,)
-    n_q, heads, dim = _arg(w, "q", q, bf16, (None, None, None), contiguous=False).shape
-    n_k, kv_heads, _ = _arg(w, "k", k, bf16, (None, None, dim), contiguous=False).shape
-    _arg(w, "v", v, bf16, (n_k, kv_heads, dim), contiguous=False)
-    n = _arg(w, "cu_q", cu_q, i32, (None,)).shape[0]
-    _need(n >= 1, w, "cu_q: empty")
-    _arg(w, "cu_k", cu_k, i32, (n,))
-    _arg(w, "out", out, bf16, (n_q, heads, dim))
-    if sink is not None:
-        _arg(w, "sink", sink, f32, (heads,))
-    if lse is not None:
-        _arg(w, "lse", lse, f32, (n_q, heads))
-    _check(_lib.csa_prompt_attn(n - 1, heads, kv_heads, dim, n_q, n_k, _ptr(cu_q), _ptr(cu_k), _ptr(q), *_strides(q),
-                                _ptr(k), *_strides(k), _ptr(v), *_strides(v), sm_scale, int(bool(causal)), window,
-                                _ptr(sink), _ptr(out), _ptr(lse), _stream(stream)), w)
+    w = "csa_prompt_attn"
+    shape, kv_shape = _shape3(w, "q", q), _shape3(w, "k", k)
+    dev = torch.cuda.current_device()
+    n, heads, dim = shape
+    if kv_shape[2] != dim:
+        _bad(w, "k", k, "heads of %d" % dim)
+    B = cu_q.numel() - 1
+    if B < 0:
+        _bad(w, "cu_q", cu_q, "sequences + 1 offsets")
+    _check(_lib.csa_prompt_attn(B, heads, kv_shape[1], dim, n, kv_shape[0],
+                                _flat(w, "cu_q", cu_q, _I32, (B + 1,), dev),
+                                _flat(w, "cu_k", cu_k, _I32, (B + 1,), dev), *_rows(w, "q", q, shape, dev),
+                                *_rows(w, "k", k, kv_shape, dev), *_rows(w, "v", v, kv_shape, dev), sm_scale,
+                                1 if causal else 0, window,
+                                None if sink is None else _flat(w, "sink", sink, _F32, (heads,), dev),
+                                _flat(w, "out", out, _BF16, shape, dev),
+                                None if lse is None else _flat(w, "lse", lse, _F32, (n, heads), dev),
+                                _stream(stream)), w)
 
 
 CSA_TEST_FAULT_INDEXER, CSA_TEST_FAULT_TOPK, CSA_TEST_FAULT_ATTN = 1, 2, 4

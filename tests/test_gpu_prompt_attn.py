@@ -116,6 +116,32 @@ def test_long_rows_sampled(csa):
         ref.check_attention(out[rows.to(DEV), h], lse[rows.to(DEV), h], *w, STEP, "long")
 
 
+@pytest.mark.parametrize("window", [520, 1024, 1500])
+def test_windows_of_several_tiles(csa, window):
+    """Rows whose keys begin and end in masked tiles with whole tiles between them, values that are not finite at
+    both ends (a row has infinities only where its window holds them)."""
+    T = 2200
+    for D in (64, 128):
+        x = make([(T, T), (300, T)], 2, 1, D, seed=window)
+        clean = run(csa, x, window=window)[0]
+        y = {k: v.clone() for k, v in x.items()}
+        want_ = clean.clone()
+        for first, shift, n in ((0, 0, T), (T, T - 300, 300)):
+            for key in (700, 1100, 1101, 2100):
+                y["v"][(0 if first == 0 else T) + key, 0, 9] = float("inf")
+                pos = torch.arange(n) + shift
+                want_[first + ((pos >= key) & (pos < key + window)).nonzero()[:, 0].to(DEV), :, 9] = float("inf")
+        out = run(csa, y, window=window)[0]
+        assert torch.equal(out, want_)
+        rows = torch.tensor([0, window - 1, window, 1300, T - 1])
+        for h in range(2):
+            pos = torch.arange(T)
+            seen = (pos <= rows[:, None]) & (pos > rows[:, None] - window)
+            w = ref.attend(x["q"][rows.to(DEV), h].cpu(), x["k"][:T, 0].cpu(), x["v"][:T, 0].cpu(), D ** -0.5, seen)
+            ref.check_attention(clean[rows.to(DEV), h], None, *w, STEP, "window")
+    assert csa.csa_check_status() == 0
+
+
 @pytest.mark.parametrize("window", [0, 50])
 def test_values_that_are_not_finite(csa, window):
     """NaN and infinities in keys and values: rows that do not see them are as without them, bit for bit; rows that
