@@ -47,7 +47,7 @@ struct Cfg {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
   static constexpr int kBlockBytes = kTile * 128;
-  static constexpr int kStages = 4;                   // K and V tiles in flight, alternating
+  static constexpr int kStages = 4;                   // K and V tiles in flight, alternating; a power of two
   static constexpr int kSmem = QT * kTileBytes + kStages * kTileBytes + 1024;
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
@@ -246,68 +246,92 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ---------------- products ----------------
-      if (lane == 0 && n_it > 0) {
-        constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 1, 1, 0, 0);  // bf16, K-major A and B
-        constexpr uint32_t idesc_o = instr_desc(kTile, D, 1, 1, 0, 1);      // A from TMEM, B (= V) MN-major
-        const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
-        const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
-        bool ok = wait_or_abort(&q_full, 0, abort_flag, a.status);
-        uint32_t n_p[QT] = {};            // weights taken so far, by tile
-        uint32_t n_cleaned = 0;           // masked tiles so far
-        for (int it = -1; it < n_it && ok; ++it) {
-          bool v_ready = false;
-          const int v_seq = 2 * it + 1, k_seq = 2 * it + 2;
-          const int v_slot = v_seq % C::kStages, k_slot = k_seq % C::kStages;
+      // The whole warp walks the loop and one elected lane issues: with the
+      // loop's values warp-uniform (the shuffles say so to the compiler) an
+      // issue costs a few cycles; from a branch on lane 0 each product took
+      // about 115, more than it takes to compute.
+      constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 1, 1, 0, 0);  // bf16, K-major A and B
+      constexpr uint32_t idesc_o = instr_desc(kTile, D, 1, 1, 0, 1);      // A from TMEM, B (= V) MN-major
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const int u_it = uniform(n_it), u_hi = uniform(j_hi);
+      int u_lo[QT], u_end[QT];          // iterations of tile t: [u_lo, u_end)
 #pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            if (it >= 0 && active(t, it)) {
-              ok = wait_or_abort(p_full + t, n_p[t]++ & 1u, abort_flag, a.status);
-              if (!ok) break;
-              if (!v_ready) {
-                ok = wait_or_abort(full + v_slot, (v_seq / C::kStages) & 1, abort_flag, a.status);
-                if (ok && masked(j_hi - 1 - it, row0, rows_cta)) {
-                  ok = wait_or_abort(&cleaned, n_cleaned++ & 1u, abort_flag, a.status);
-                }
-                if (!ok) break;
-                v_ready = true;
-              }
-              tc_fence_after();
-              const uint32_t vb = rb + v_slot * C::kTileBytes;
+      for (int t = 0; t < QT; ++t) {
+        u_lo[t] = uniform(rt[t].lo < rt[t].hi ? j_hi - rt[t].hi : 0);
+        u_end[t] = uniform(rt[t].lo < rt[t].hi ? j_hi - rt[t].lo : 0);
+      }
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
+      const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.status)) != 0;
+      };
+      bool ok = u_it == 0 || wait(&q_full, 0);
+      uint32_t n_p[QT] = {};            // weights taken so far, by tile
+      uint32_t n_cleaned = 0;           // masked tiles so far
+      for (int it = -1; it < u_it && ok; ++it) {
+        bool v_ready = false;
+        const int v_seq = 2 * it + 1, k_seq = 2 * it + 2;
+        const int v_slot = v_seq & (C::kStages - 1), k_slot = k_seq & (C::kStages - 1);
+        const uint64_t v_desc = smem_desc(rb + v_slot * C::kTileBytes, C::kBlockBytes, 1024, kSwizzle128B);
+        const uint64_t k_desc = smem_desc(rb + k_slot * C::kTileBytes, 16, 1024, kSwizzle128B);
 #pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                mma_f16_ts(tmem + C::kOCol(t), tmem + C::kSCol(t) + s * 8,
-                           smem_desc(vb + s * 2048, C::kBlockBytes, 1024, kSwizzle128B), idesc_o,
-                           (n_p[t] > 1 || s > 0) ? 1u : 0u);
-              if (!active(t, it + 1)) tc_commit(o_full + t);
+        for (int t = 0; t < QT; ++t) {
+          if (ok && it >= u_lo[t] && it < u_end[t]) {
+            ok = wait(p_full + t, n_p[t] & 1u);
+            if (ok && !v_ready) {
+              ok = wait(full + v_slot, (v_seq / C::kStages) & 1);
+              if (ok && masked(u_hi - 1 - it, row0, rows_cta)) ok = wait(&cleaned, n_cleaned++ & 1u);
+              v_ready = true;
             }
-            if (it + 1 < n_it && active(t, it + 1)) {
-              ok = wait_or_abort(full + k_slot, (k_seq / C::kStages) & 1, abort_flag, a.status);
-              if (!ok) break;
+            if (ok) {
               tc_fence_after();
-              const uint32_t kb = rb + k_slot * C::kTileBytes, qt = qb + t * C::kTileBytes;
+              if (elect_one()) {
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s)
-                mma_f16(tmem + C::kSCol(t),
-                        smem_desc(qt + (s >> 2) * C::kBlockBytes + (s & 3) * 32, 16, 1024, kSwizzle128B),
-                        smem_desc(kb + (s >> 2) * C::kBlockBytes + (s & 3) * 32, 16, 1024, kSwizzle128B), idesc_s,
-                        s > 0 ? 1u : 0u);
-              if (!skip_s) tc_commit(s_full + t);
+                for (int s = 0; s < kTile / 16; ++s)
+                  mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (s * 2048 >> 4), idesc_o,
+                             (n_p[t] > 0 || s > 0) ? 1u : 0u);
+                if (it + 1 == u_end[t]) tc_commit(o_full + t);
+              }
+              __syncwarp();
+              ++n_p[t];
             }
           }
-          if (!ok) break;
-          if (it >= 0) tc_commit(empty + v_slot);
-          if (it + 1 < n_it) {
-            tc_commit(empty + k_slot);
-            // hand a masked tile of values to the cleaning warps as soon as it
-            // is there; one tile at a time: the product waits for `cleaned`
-            if (masked(j_hi - 2 - it, row0, rows_cta)) {
-              const int next = v_seq + 2;
-              ok = wait_or_abort(full + next % C::kStages, (next / C::kStages) & 1, abort_flag, a.status);
-              if (ok) mbar_arrive(&dirty);
+          if (ok && it + 1 >= u_lo[t] && it + 1 < u_end[t]) {
+            ok = wait(full + k_slot, (k_seq / C::kStages) & 1);
+            if (ok) {
+              tc_fence_after();
+              const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
+              if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                  constexpr int kStep = 32 >> 4;  // 16 channels along a 128-byte line, in the descriptors' units
+                  const int off = (s >> 2) * (C::kBlockBytes >> 4) + (s & 3) * kStep;
+                  mma_f16(tm + C::kSCol(t), q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
+                }
+                if (!skip_s) tc_commit(s_full + t);
+              }
+              __syncwarp();
             }
           }
         }
-        // whatever was issued finishes before TMEM and shared memory are released
+        if (!ok) break;
+        if (elect_one()) {
+          if (it >= 0) tc_commit(empty + v_slot);
+          if (it + 1 < u_it) tc_commit(empty + k_slot);
+        }
+        __syncwarp();
+        // hand a masked tile of values to the cleaning warps as soon as it is
+        // there; one tile at a time: the product waits for `cleaned`
+        if (it + 1 < u_it && masked(u_hi - 2 - it, row0, rows_cta)) {
+          const int next = v_seq + 2;
+          ok = wait(full + (next & (C::kStages - 1)), (next / C::kStages) & 1);
+          if (ok && elect_one()) mbar_arrive(&dirty);
+          __syncwarp();
+        }
+      }
+      // whatever was issued finishes before TMEM and shared memory are released
+      if (elect_one()) {
         tc_commit(&drain);
         mbar_wait(&drain, 0, a.status);
       }

@@ -364,6 +364,17 @@ __device__ __forceinline__ void relu_fma4(uint64_t& a01, uint64_t& a23, uint32_t
       : "memory");
 }
 
+// True in one lane of a converged warp, the same one each time.  Unlike a test
+// of the lane number, the compiler knows the branch as one thread's of a
+// uniform warp and keeps tcgen05 operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---- proxy fences -----------------------------------------------------------
 
 // Makes generic-proxy shared-memory writes visible to the async proxy (TMA,
