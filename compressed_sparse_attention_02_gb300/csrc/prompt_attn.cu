@@ -53,8 +53,8 @@ struct Cfg {
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
   static constexpr int kCols = QT == 2 ? 512 : 256;
   // QT == 2: 384 threads are launched with 168 registers each, 64512 in all;
-  // 256 x 216 + 128 x 64 = 63488 of them are used.
-  static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 64;
+  // as are 256 x 208 + 128 x 88.
+  static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
   static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * kLaunchRegs, "registers of the block");
 };
 
@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
   const int row0 = ((sq.nq + kRowsCta - 1) / kRowsCta - 1 - static_cast<int>(index)) * kRowsCta;
   const int shift = sq.nk - sq.nq;  // row i sits at position i + shift among the keys
 
-  // tiles of keys that rows [first, first + rows) see, and whether some of
-  // those rows masks a part of tile j
+  // tiles of keys that rows [first, first + rows) see
   auto range_of = [&](int first, int rows) {
     Range r;
     const int64_t last = static_cast<int64_t>(first) + rows - 1 + shift;
@@ -187,10 +186,19 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
     r.hi = static_cast<int>((hi + kTile - 1) / kTile);
     return r;
   };
-  auto masked = [&](int j, int first, int rows) {
-    const int64_t c0 = static_cast<int64_t>(j) * kTile, c1 = c0 + kTile;  // keys of the tile
-    return c1 > sq.nk || (a.causal && c1 - 1 > static_cast<int64_t>(first) + shift) ||
-           (a.window > 0 && c0 <= static_cast<int64_t>(first) + rows - 1 + shift - a.window);
+  // some of those rows masks a part of tile j: j >= from or j <= upto
+  struct Masked {
+    int from, upto;
+    __device__ __forceinline__ bool at(int j) const { return j >= from || j <= upto; }
+  };
+  auto masked_of = [&](int first, int rows) {
+    Masked m;
+    m.from = sq.nk / kTile;  // the sequence ends inside the tile (or before it)
+    const int64_t x = static_cast<int64_t>(first) + shift;  // the first row's last key
+    if (a.causal) m.from = min(m.from, x < 0 ? 0 : static_cast<int>((x + 1) / kTile));
+    const int64_t y = x + rows - 1 - a.window;  // the last key outside the last row's window
+    m.upto = a.window > 0 && y >= 0 ? static_cast<int>(y / kTile) : -1;
+    return m;
   };
   auto rows_of = [&](int t) { return max(0, min(kTile, sq.nq - row0 - t * kTile)); };
   const int rows_cta = min(kRowsCta, sq.nq - row0);
@@ -204,11 +212,8 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
       j_hi = max(j_hi, rt[t].hi);
     }
   }
+  const Masked masked = masked_of(row0, rows_cta);
   const int n_it = j_hi > 0 ? j_hi - j_lo : 0;  // iteration it works on tile j_hi - 1 - it
-  auto active = [&](int t, int it) {
-    const int j = j_hi - 1 - it;
-    return j >= rt[t].lo && j < rt[t].hi;
-  };
 
   if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
   tc_fence_before();
@@ -261,72 +266,68 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
         u_end[t] = uniform(rt[t].lo < rt[t].hi ? j_hi - rt[t].lo : 0);
       }
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int m_from = uniform(j_hi - masked.from), m_upto = uniform(j_hi - 1 - masked.upto);
+      auto masked_it = [&](int it) { return it < m_from || it >= m_upto; };
       const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
       const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.status)) != 0;
       };
-      bool ok = u_it == 0 || wait(&q_full, 0);
-      uint32_t n_p[QT] = {};            // weights taken so far, by tile
-      uint32_t n_cleaned = 0;           // masked tiles so far
-      for (int it = -1; it < u_it && ok; ++it) {
-        bool v_ready = false;
+      auto s_of = [&](int t, uint64_t k_desc) {  // S_t = Q_t K^T (one lane)
+        const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          constexpr int kStep = 32 >> 4;  // 16 channels along a 128-byte line, in the descriptors' units
+          const int off = (s >> 2) * (C::kBlockBytes >> 4) + (s & 3) * kStep;
+          mma_f16(tm + C::kSCol(t), q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
+        }
+        if (!skip_s) tc_commit(s_full + t);
+      };
+      bool ok = u_it == 0 || (wait(&q_full, 0) && wait(full, 0));
+      if (ok && u_it > 0) {  // the first tile of keys
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+            if (u_lo[t] == 0 && u_end[t] > 0) s_of(t, smem_desc(rb, 16, 1024, kSwizzle128B));
+          tc_commit(empty);
+        }
+        __syncwarp();
+      }
+      uint32_t n_cleaned = 0;
+      for (int it = 0; it < u_it && ok; ++it) {
         const int v_seq = 2 * it + 1, k_seq = 2 * it + 2;
         const int v_slot = v_seq & (C::kStages - 1), k_slot = k_seq & (C::kStages - 1);
         const uint64_t v_desc = smem_desc(rb + v_slot * C::kTileBytes, C::kBlockBytes, 1024, kSwizzle128B);
         const uint64_t k_desc = smem_desc(rb + k_slot * C::kTileBytes, 16, 1024, kSwizzle128B);
+        const bool more = it + 1 < u_it;
+        // this tile's values and the next tile's keys are usually there long
+        // before the weights are
+        ok = wait(full + v_slot, (v_seq / C::kStages) & 1);
+        if (ok && masked_it(it)) {  // one masked tile at a time is with the cleaning warps
+          if (elect_one()) mbar_arrive(&dirty);
+          __syncwarp();
+          ok = wait(&cleaned, n_cleaned++ & 1u);
+        }
+        if (ok && more) ok = wait(full + k_slot, (k_seq / C::kStages) & 1);
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-          if (ok && it >= u_lo[t] && it < u_end[t]) {
-            ok = wait(p_full + t, n_p[t] & 1u);
-            if (ok && !v_ready) {
-              ok = wait(full + v_slot, (v_seq / C::kStages) & 1);
-              if (ok && masked(u_hi - 1 - it, row0, rows_cta)) ok = wait(&cleaned, n_cleaned++ & 1u);
-              v_ready = true;
-            }
-            if (ok) {
-              tc_fence_after();
-              if (elect_one()) {
+          const bool pv = it >= u_lo[t] && it < u_end[t], next = more && it + 1 >= u_lo[t] && it + 1 < u_end[t];
+          if (ok && pv) ok = wait(p_full + t, (it - u_lo[t]) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (pv) {
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                  mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (s * 2048 >> 4), idesc_o,
-                             (n_p[t] > 0 || s > 0) ? 1u : 0u);
-                if (it + 1 == u_end[t]) tc_commit(o_full + t);
-              }
-              __syncwarp();
-              ++n_p[t];
+              for (int s = 0; s < kTile / 16; ++s)
+                mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (s * 2048 >> 4), idesc_o,
+                           (it > u_lo[t] || s > 0) ? 1u : 0u);
+              if (it + 1 == u_end[t]) tc_commit(o_full + t);
             }
+            if (t == QT - 1) tc_commit(empty + v_slot);
+            if (next) s_of(t, k_desc);
+            if (t == QT - 1 && more) tc_commit(empty + k_slot);
           }
-          if (ok && it + 1 >= u_lo[t] && it + 1 < u_end[t]) {
-            ok = wait(full + k_slot, (k_seq / C::kStages) & 1);
-            if (ok) {
-              tc_fence_after();
-              const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
-              if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                  constexpr int kStep = 32 >> 4;  // 16 channels along a 128-byte line, in the descriptors' units
-                  const int off = (s >> 2) * (C::kBlockBytes >> 4) + (s & 3) * kStep;
-                  mma_f16(tm + C::kSCol(t), q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
-                }
-                if (!skip_s) tc_commit(s_full + t);
-              }
-              __syncwarp();
-            }
-          }
-        }
-        if (!ok) break;
-        if (elect_one()) {
-          if (it >= 0) tc_commit(empty + v_slot);
-          if (it + 1 < u_it) tc_commit(empty + k_slot);
-        }
-        __syncwarp();
-        // hand a masked tile of values to the cleaning warps as soon as it is
-        // there; one tile at a time: the product waits for `cleaned`
-        if (it + 1 < u_it && masked(u_hi - 2 - it, row0, rows_cta)) {
-          const int next = v_seq + 2;
-          ok = wait(full + (next & (C::kStages - 1)), (next / C::kStages) & 1);
-          if (ok && elect_one()) mbar_arrive(&dirty);
           __syncwarp();
         }
       }
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
       int n_masked = 0;
       for (int it = 0; it < n_it; ++it) {
         const int j = j_hi - 1 - it;
-        if (!masked(j, row0, rows_cta)) continue;
+        if (!masked.at(j)) continue;
         const int seq = 2 * it + 1, slot = seq % C::kStages;
         // the MMA thread has seen the tile's copy complete and holds its slot
         // until `cleaned`, so the second wait returns at once (and makes the
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
     const float scale2 = a.sm_scale * kLog2e;
     float m2 = kNone, l = 0.f;
     bool ok = true;
+    const Masked masked_t = masked_of(first, rows);
     const int n_tiles = rt[t].hi - rt[t].lo;
     for (int n = 0; n < n_tiles; ++n) {
       const int j = rt[t].hi - 1 - n;
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
       tmem_wait_ld();
-      if (masked(j, first, rows)) {
+      if (masked_t.at(j)) {
         int64_t hi = sq.nk - 1, lo = 0;
         if (a.causal && static_cast<int64_t>(i) + shift < hi) hi = static_cast<int64_t>(i) + shift;
         if (a.window > 0) lo = static_cast<int64_t>(i) + shift - a.window + 1;
