@@ -52,10 +52,16 @@ struct Cfg {
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
   static constexpr int kCols = QT == 2 ? 512 : 256;
-  // QT == 2: 384 threads are launched with 168 registers each, 64512 in all;
-  // as are 256 x 208 + 128 x 88.
-  static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-  static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * kLaunchRegs, "registers of the block");
+  // CTAs an SM: two of one tile each at width 64 (their 256 columns and 81 KB
+  // fit twice), so one's start and end run under the other's products.
+  static constexpr int kCtas = QT == 1 && D == 64 ? 2 : 1;
+  // Where 168 (or 128) registers a thread are launched, the softmax warps
+  // take some that the other four give up: 256 x 208 + 128 x 88 = 384 x 168,
+  // 128 x 200 + 128 x 56 = 256 x 128.
+  static constexpr bool kSplit = QT == 2 || kCtas == 2;
+  static constexpr int kLaunchRegs = QT == 2 ? 168 : 128;
+  static constexpr int kSoftmaxRegs = QT == 2 ? 208 : 200, kOtherRegs = QT == 2 ? 88 : 56;
+  static_assert(QT * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "registers of the block");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -92,6 +98,16 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 
 __device__ __forceinline__ bool not_finite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
+// Non-zero where a half of the word is a bf16 infinity or NaN (magnitude bits
+// of 0x7F80 and more carry into the half's top bit).
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+// The word with such halves zeroed.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+  if (not_finite(w)) w &= 0xFFFF0000u;
+  if (not_finite(w >> 16)) w &= 0xFFFFu;
+  return w;
+}
+
 // The tiles of keys [lo, hi) that `rows` queries from row `first` on see.
 struct Range {
   int lo, hi;
@@ -103,7 +119,7 @@ struct Seq {
 };
 
 template <int D, int QT>
-__global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a) {
   using C = Cfg<D, QT>;
@@ -142,8 +158,17 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
     n_odd = 0;
   }
   if (tid < kMaxMasked * 4) odd_rows[tid >> 2][tid & 3] = 0u;
-  pdl_launch_dependents();
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  // Tensor memory is taken after the kernel before has ended and before the
+  // one after may start: no CTA of either can then hold what this one, or
+  // what it waits for, still needs.
   pdl_wait();
+  if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
+  tc_fence_before();
 
   // this CTA's sequence and tiles: the later tiles of a sequence (more keys
   // under the causal mask) first
@@ -165,7 +190,14 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
   const int b = find_item<C::kThreads>(
       a.B, blockIdx.x / a.n_heads,
       [&](int s) { return static_cast<int64_t>((seq_at(s).nq + kRowsCta - 1) / kRowsCta); }, sh, &index, nullptr);
-  if (b < 0) return;
+  // (the search's barriers also order the allocation and the mbarriers' set-up)
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = tmem_slot;
+  if (b < 0) {
+    if (warp == kMmaWarp) tmem_dealloc(tmem, C::kCols);
+    return;
+  }
   const Seq sq = seq_at(b);
   const int row0 = ((sq.nq + kRowsCta - 1) / kRowsCta - 1 - static_cast<int>(index)) * kRowsCta;
   const int shift = sq.nk - sq.nq;  // row i sits at position i + shift among the keys
@@ -215,15 +247,8 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
   const Masked masked = masked_of(row0, rows_cta);
   const int n_it = j_hi > 0 ? j_hi - j_lo : 0;  // iteration it works on tile j_hi - 1 - it
 
-  if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-
-  // (two tiles: the softmax warps take registers that the other four give up)
   if (warp >= 4 * QT) {
-    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if constexpr (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == kTmaWarp) {
       // ---------------- loads ----------------
       if (lane == 0 && n_it > 0) {
@@ -352,29 +377,34 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
             !wait_or_abort(full + slot, (seq / C::kStages) & 1, abort_flag, a.status))
           break;
         uint4* tile = reinterpret_cast<uint4*>(ring + slot * C::kTileBytes);
-        const int past = sq.nk - j * kTile;  // first row past the sequence
-        for (int i = ct; i < C::kTileBytes / 16; i += kCleanThreads) {
-          const int r = (i >> 3) & (kTile - 1);  // the swizzle moves chunks within their row only
-          if (r >= past) {
-            tile[i] = make_uint4(0u, 0u, 0u, 0u);
-            continue;
+        // rows past the sequence become zero; of the others, eight 16-byte
+        // chunks at a time are looked at for an exponent of all ones (the
+        // swizzle moves chunks within their row only: chunk i is of row i/8 % 128)
+        const int past = min(sq.nk - j * kTile, kTile);
+        if (past < kTile)
+          for (int i = ct; i < (kTile - past) * 8 * C::kBlocks; i += kCleanThreads) {
+            const int block = i / ((kTile - past) * 8);
+            tile[block * kTile * 8 + past * 8 + i - block * (kTile - past) * 8] = make_uint4(0u, 0u, 0u, 0u);
           }
-          const uint4 u = tile[i];
-          uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          bool odd = false;
+#pragma unroll 1
+        for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += 8 * kCleanThreads) {
+          uint4 u[8];
+          uint32_t any = 0u;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (not_finite(w[k])) {
-              w[k] &= 0xFFFF0000u;
-              odd = true;
-            }
-            if (not_finite(w[k] >> 16)) {
-              w[k] &= 0xFFFFu;
-              odd = true;
-            }
-          }
-          if (odd) {
-            tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 8; ++k) u[k] = tile[i0 + k * kCleanThreads];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) any |= odd_halves(u[k].x) | odd_halves(u[k].y) | odd_halves(u[k].z) | odd_halves(u[k].w);
+          if (any == 0u) continue;
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kCleanThreads, r = (i >> 3) & (kTile - 1);
+            uint4 w = tile[i];
+            if (r >= past || !(odd_halves(w.x) | odd_halves(w.y) | odd_halves(w.z) | odd_halves(w.w))) continue;
+            w.x = finite_halves(w.x);
+            w.y = finite_halves(w.y);
+            w.z = finite_halves(w.z);
+            w.w = finite_halves(w.w);
+            tile[i] = w;
             if (n_masked < kMaxMasked) {
               atomicOr(&odd_rows[n_masked][r >> 5], 1u << (r & 31));
               odd_tile[n_masked] = j;
@@ -389,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
     }
   } else {
     // ---------------- softmax: one thread a query row ----------------
-    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    if constexpr (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const int first = row0 + t * kTile, rows = rows_of(t);
@@ -397,6 +427,10 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lane_base + C::kSCol(t), o_tmem = tmem + lane_base + C::kOCol(t);
     const float scale2 = a.sm_scale * kLog2e;
+    // the row's keys [first_key, last_key]
+    const int64_t at_key = static_cast<int64_t>(i) + shift;
+    const int last_key = static_cast<int>(a.causal && at_key < sq.nk - 1 ? (at_key < -1 ? -1 : at_key) : sq.nk - 1);
+    const int first_key = a.window > 0 && at_key - a.window >= 0 ? static_cast<int>(at_key - a.window + 1) : 0;
     float m2 = kNone, l = 0.f;
     bool ok = true;
     const Masked masked_t = masked_of(first, rows);
@@ -411,19 +445,22 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
       tmem_wait_ld();
-      if (masked_t.at(j)) {
-        int64_t hi = sq.nk - 1, lo = 0;
-        if (a.causal && static_cast<int64_t>(i) + shift < hi) hi = static_cast<int64_t>(i) + shift;
-        if (a.window > 0) lo = static_cast<int64_t>(i) + shift - a.window + 1;
-        hi -= static_cast<int64_t>(j) * kTile;
-        lo -= static_cast<int64_t>(j) * kTile;
-        const int c_hi = static_cast<int>(hi < -1 ? -1 : hi > kTile ? kTile : hi);
-        const int c_lo = static_cast<int>(lo < 0 ? 0 : lo > kTile ? kTile : lo);
+      // a masked tile: this row's last key, and its first, among the tile's columns
+      if (j >= masked_t.from) {
+        const int c_hi = min(last_key - j * kTile, kTile);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (32 * c + k > c_hi || 32 * c + k < c_lo) s[c][k] = 0xFF800000u;  // -inf
+            if (32 * c + k > c_hi) s[c][k] = 0xFF800000u;  // -inf
+      }
+      if (j <= masked_t.upto) {
+        const int c_lo = first_key - j * kTile;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k < c_lo) s[c][k] = 0xFF800000u;
       }
       float top[4];
 #pragma unroll
@@ -474,8 +511,8 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(p_full + t);
     }
-    if (ok && n_tiles > 0) {
-      ok = wait_or_abort(o_full + t, 0, abort_flag, a.status);
+    if (ok && n_it > 0) {  // (a tile that sees no keys: its queries have landed where its output is staged)
+      ok = wait_or_abort(n_tiles > 0 ? o_full + t : &q_full, 0, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
@@ -521,19 +558,30 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, 1)
             }
           }
         }
-        if (r < rows) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 32 * c);
+        uint8_t* line = q_s + t * C::kTileBytes + (c >> 1) * C::kBlockBytes + r * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]);
-              w[e] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&v);
           }
+          *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + k) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+      // the warp's 32 rows, staged where its queries were (every product with
+      // them has finished), stored with neighbouring lanes on one row
+      __syncwarp();
+      constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
+      const int w0 = (warp & 3) * 32;
+#pragma unroll 4
+      for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
+        const int rr = w0 + k * kRowsAtOnce + lane / kChunks, ch = lane % kChunks;
+        const uint4 v = *reinterpret_cast<const uint4*>(q_s + t * C::kTileBytes + (ch >> 3) * C::kBlockBytes + rr * 128 +
+                                                        (((ch & 7) ^ (rr & 7)) << 4));
+        if (rr < rows)
+          *reinterpret_cast<uint4*>(a.out + ((sq.q0 + first + rr) * a.n_heads + head) * D + ch * 8) = v;
       }
     }
     tc_fence_before();
@@ -570,7 +618,7 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
   cudaError_t e =
       cudaFuncSetAttribute(prompt_attn_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  if (QT == 2) {  // the split of registers assumes what the kernel is launched with
+  if (C::kSplit) {  // the split of registers assumes what the kernel is launched with
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, prompt_attn_kernel<D, QT>);
     if (e != cudaSuccess) return e;
@@ -591,13 +639,15 @@ cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTil
   // Two tiles a CTA overlap one's softmax with the other's products; one tile
   // a CTA spreads few queries over more SMs.  (32 heads of width 128: 16384
   // queries 1.95 ms with two tiles, 2.72 ms with one; 200 queries over 1100
-  // keys 31 us with two, 24 us with one.)
+  // keys 31 us with two, 24 us with one.)  At width 64 two CTAs of one tile
+  // share an SM instead (16 packed prompts, window 1024: 305 us, 350 us with
+  // two tiles a CTA).
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const bool one = (a.n_q / kTile + a.B) * a.n_heads <= sms;
   if (a.head_dim == 128) return one ? launch_dim<128, 1>(a, encode, stream) : launch_dim<128, 2>(a, encode, stream);
-  return one ? launch_dim<64, 1>(a, encode, stream) : launch_dim<64, 2>(a, encode, stream);
+  return launch_dim<64, 1>(a, encode, stream);
 }
 
 }  // namespace csa
