@@ -75,30 +75,32 @@ __device__ __forceinline__ void rotate_item(bool half, const float2 (&sc)[8], fl
 
 // Finds the sequence that work item w belongs to, where sequence b has
 // count(b) >= 0 items: returns b and the item's index in it, or -1 when w is
-// past the last; *total, if asked for, gets the sum of all counts (a search
-// for w < 0 gives the sum alone).  Every thread of the CTA calls it (THREADS
-// threads, a multiple of 32); sh holds THREADS / 32 + 2 values.
-template <int THREADS, typename Count>
-__device__ __forceinline__ int find_item(int B, int64_t w, Count count, int64_t* sh, int64_t* index, int64_t* total) {
+// past the last.  T holds the sum of all counts.  Every thread of the CTA
+// calls it (THREADS threads, a multiple of 32); sh holds THREADS / 32 + 2
+// values.
+template <int THREADS, typename T, typename Count>
+__device__ __forceinline__ int find_item(int B, T w, Count count, T* sh, T* index) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWarps = THREADS / 32;
   if (threadIdx.x == 0) sh[kWarps] = -1;
-  int64_t base = 0;
+  T base = 0;
   for (int b0 = 0; b0 < B; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    const int64_t n = b < B ? count(b) : 0;
-    int64_t x = n;
+    const T n = b < B ? count(b) : 0;
+    T x = n;
+    if (B - b0 > 1) {
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
+      for (int off = 1; off < 32; off <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
     }
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    int64_t before = base, all = 0;
+    T before = base, all = 0;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      const int64_t t = sh[k];
+      const T t = sh[k];
       if (k < warp) before += t;
       all += t;
     }
@@ -109,10 +111,8 @@ __device__ __forceinline__ int find_item(int B, int64_t w, Count count, int64_t*
     }
     base += all;
     __syncthreads();
-    if (!total && sh[kWarps] >= 0) break;
+    if (sh[kWarps] >= 0) break;
   }
-  if (B <= 0) __syncthreads();
-  if (total) *total = base;
   *index = sh[kWarps + 1];
   return static_cast<int>(sh[kWarps]);
 }

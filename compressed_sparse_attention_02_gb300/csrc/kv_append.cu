@@ -50,7 +50,7 @@ __device__ __forceinline__ int64_t pages_of(int64_t p, int64_t n, int shift) {
 template <int THREADS, int NI>
 __global__ void __launch_bounds__(THREADS) kv_append_kernel(const KvAppendArgs a) {
   constexpr int kWarps = THREADS / 32;
-  __shared__ int64_t sh[kWarps + 2];
+  __shared__ int sh[kWarps + 2];
   __shared__ float max_s[kWarps];
   pdl_launch_dependents();
   pdl_wait();
@@ -70,13 +70,13 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const KvAppendArgs a
     return hi - lo;
   };
   int b;
-  int64_t index = 0;
+  int index = 0;
   if (!a.cu_rows) {
     b = blockIdx.x;
   } else {
     b = find_item<THREADS>(
-        a.B, blockIdx.x, [&](int s) { return pages_of(__ldg(a.pos0 + s), rows_of(s), c.page_shift); }, sh, &index,
-        nullptr);
+        a.B, static_cast<int>(blockIdx.x),
+        [&](int s) { return static_cast<int>(pages_of(__ldg(a.pos0 + s), rows_of(s), c.page_shift)); }, sh, &index);
     if (b < 0) return;
   }
   const int64_t p0 = __ldg(a.pos0 + b);

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   if (at >= end) return;
   int64_t index;
   int b = find_item<kThreads>(
-      a.B, at, [&](int s) { return static_cast<int64_t>(span_of(a, s).units()) * pairs; }, sh, &index, nullptr);
+      a.B, at, [&](int s) { return static_cast<int64_t>(span_of(a, s).units()) * pairs; }, sh, &index);
   Span sp = span_of(a, b);
   int pair = static_cast<int>(index / sp.units());
   int u = static_cast<int>(index - static_cast<int64_t>(pair) * sp.units());

@@ -29,7 +29,8 @@
 namespace csa {
 namespace {
 
-constexpr int kTile = 128;               // queries and keys a tile
+constexpr int kTileShift = 7;
+constexpr int kTile = 1 << kTileShift;   // queries and keys a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;          // running maximum before the first key
@@ -47,14 +48,14 @@ struct Cfg {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
   static constexpr int kBlockBytes = kTile * 128;
-  static constexpr int kStages = 4;                   // K and V tiles in flight, alternating; a power of two
+  static constexpr int kStages = QT == 1 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
   static constexpr int kSmem = QT * kTileBytes + kStages * kTileBytes + 1024;
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
   static constexpr int kCols = QT == 2 ? 512 : 256;
   // CTAs an SM: two of one tile each at width 64 (their 256 columns and 81 KB
   // fit twice), so one's start and end run under the other's products.
-  static constexpr int kCtas = QT == 1 && D == 64 ? 2 : 1;
+  static constexpr int kCtas = QT == 1 ? 2 : 1;
   // Where 168 (or 128) registers a thread are launched, the softmax warps
   // take some that the other four give up: 256 x 208 + 128 x 88 = 384 x 168,
   // 128 x 200 + 128 x 56 = 256 x 128.
@@ -85,6 +86,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
 __device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
   constexpr int kTmaWarp = 4 * QT, kMmaWarp = 4 * QT + 1, kCleanWarp = 4 * QT + 2;
   constexpr int kRowsCta = QT * kTile;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t sh[C::kThreads / 32 + 2];
+  __shared__ int sh[C::kThreads / 32 + 2];
   __shared__ uint64_t q_full, full[C::kStages], empty[C::kStages];
   __shared__ uint64_t s_full[QT], p_full[QT], o_full[QT], dirty, cleaned, drain;
   __shared__ uint32_t tmem_slot;
@@ -186,10 +192,10 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
     s.nk = ok ? k1 - k0 : 0;
     return s;
   };
-  int64_t index;
+  int index;
   const int b = find_item<C::kThreads>(
-      a.B, blockIdx.x / a.n_heads,
-      [&](int s) { return static_cast<int64_t>((seq_at(s).nq + kRowsCta - 1) / kRowsCta); }, sh, &index, nullptr);
+      a.B, static_cast<int>(blockIdx.x / a.n_heads), [&](int s) { return (seq_at(s).nq + kRowsCta - 1) / kRowsCta; },
+      sh, &index);
   // (the search's barriers also order the allocation and the mbarriers' set-up)
   tc_fence_after();
   pdl_launch_dependents();
@@ -199,23 +205,18 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
     return;
   }
   const Seq sq = seq_at(b);
-  const int row0 = ((sq.nq + kRowsCta - 1) / kRowsCta - 1 - static_cast<int>(index)) * kRowsCta;
+  const int row0 = ((sq.nq + kRowsCta - 1) / kRowsCta - 1 - index) * kRowsCta;
   const int shift = sq.nk - sq.nq;  // row i sits at position i + shift among the keys
 
   // tiles of keys that rows [first, first + rows) see
   auto range_of = [&](int first, int rows) {
+    const int pos = first + shift;  // (lengths are below 2^30 each: no overflow)
+    const int hi = a.causal ? min(sq.nk, pos + rows) : sq.nk;
+    const int lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
     Range r;
-    const int64_t last = static_cast<int64_t>(first) + rows - 1 + shift;
-    int64_t hi = sq.nk, lo = 0;
-    if (a.causal && last + 1 < hi) hi = last + 1;
-    if (a.window > 0) lo = static_cast<int64_t>(first) + shift - a.window + 1;
-    if (lo < 0) lo = 0;
-    if (rows <= 0 || hi <= lo) {
-      r.lo = r.hi = 0;
-      return r;
-    }
-    r.lo = static_cast<int>(lo / kTile);
-    r.hi = static_cast<int>((hi + kTile - 1) / kTile);
+    const bool none = rows <= 0 || hi <= lo;
+    r.lo = none ? 0 : lo >> kTileShift;
+    r.hi = none ? 0 : (hi + kTile - 1) >> kTileShift;
     return r;
   };
   // some of those rows masks a part of tile j: j >= from or j <= upto
@@ -225,11 +226,11 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
   };
   auto masked_of = [&](int first, int rows) {
     Masked m;
-    m.from = sq.nk / kTile;  // the sequence ends inside the tile (or before it)
-    const int64_t x = static_cast<int64_t>(first) + shift;  // the first row's last key
-    if (a.causal) m.from = min(m.from, x < 0 ? 0 : static_cast<int>((x + 1) / kTile));
-    const int64_t y = x + rows - 1 - a.window;  // the last key outside the last row's window
-    m.upto = a.window > 0 && y >= 0 ? static_cast<int>(y / kTile) : -1;
+    m.from = sq.nk >> kTileShift;  // the sequence ends inside the tile (or before it)
+    const int pos = first + shift;  // the first row's last key
+    if (a.causal) m.from = min(m.from, pos < 0 ? 0 : (pos + 1) >> kTileShift);
+    const int out = pos + rows - 1;  // the last row's last key: keys up to out - window are outside its window
+    m.upto = a.window > 0 && out >= a.window ? (out - a.window) >> kTileShift : -1;
     return m;
   };
   auto rows_of = [&](int t) { return max(0, min(kTile, sq.nq - row0 - t * kTile)); };
@@ -428,9 +429,9 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
     const uint32_t s_tmem = tmem + lane_base + C::kSCol(t), o_tmem = tmem + lane_base + C::kOCol(t);
     const float scale2 = a.sm_scale * kLog2e;
     // the row's keys [first_key, last_key]
-    const int64_t at_key = static_cast<int64_t>(i) + shift;
-    const int last_key = static_cast<int>(a.causal && at_key < sq.nk - 1 ? (at_key < -1 ? -1 : at_key) : sq.nk - 1);
-    const int first_key = a.window > 0 && at_key - a.window >= 0 ? static_cast<int>(at_key - a.window + 1) : 0;
+    const int at_key = i + shift;
+    const int last_key = a.causal ? min(at_key, sq.nk - 1) : sq.nk - 1;
+    const int first_key = a.window > 0 && at_key >= a.window ? at_key - a.window + 1 : 0;
     float m2 = kNone, l = 0.f;
     bool ok = true;
     const Masked masked_t = masked_of(first, rows);
@@ -445,22 +446,16 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
       tmem_wait_ld();
-      // a masked tile: this row's last key, and its first, among the tile's columns
-      if (j >= masked_t.from) {
-        const int c_hi = min(last_key - j * kTile, kTile);
+      if (masked_t.at(j)) {  // this row's keys among the tile's columns, as a bit each
+        const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * c + k > c_hi) s[c][k] = 0xFF800000u;  // -inf
-      }
-      if (j <= masked_t.upto) {
-        const int c_lo = first_key - j * kTile;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          const int hi = max(0, min(32, c_hi - 32 * c)), lo = max(0, min(32, c_lo - 32 * c));
+          const uint32_t seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (32 * c + k < c_lo) s[c][k] = 0xFF800000u;
+            if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
+        }
       }
       float top[4];
 #pragma unroll
@@ -540,16 +535,17 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
+        // (a row without keys has l = 0 and sums of 0 * value, all finite)
         float x[32];
+        const uint64_t l2 = pair_of(__float_as_uint(l), __float_as_uint(l));
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * l;
+        for (int k = 0; k < 32; k += 2) split(mul2(pair_of(o[k], o[k + 1]), l2), &x[k], &x[k + 1]);
         if (odd && r < rows) {
           for (int e = 0; e < kMaxMasked * kTile; ++e) {
             const uint32_t word = odd_rows[e >> 7][(e >> 5) & 3];
             if (!((word >> (e & 31)) & 1u)) continue;
             const int64_t key = static_cast<int64_t>(odd_tile[e >> 7]) * kTile + (e & (kTile - 1));
-            const int64_t pos = static_cast<int64_t>(i) + shift;
-            if ((a.causal && key > pos) || (a.window > 0 && key <= pos - a.window)) continue;
+            if (key > last_key || key < first_key) continue;
             const uint16_t* v = a.v + (sq.k0 + key) * a.v_stride + kv_head * a.v_stride_h + 32 * c;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
@@ -636,16 +632,17 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
 
 cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
   if (a.B <= 0 || a.n_q <= 0) return cudaSuccess;
-  // Two tiles a CTA overlap one's softmax with the other's products; one tile
-  // a CTA spreads few queries over more SMs.  (32 heads of width 128: 16384
-  // queries 1.95 ms with two tiles, 2.72 ms with one; 200 queries over 1100
-  // keys 31 us with two, 24 us with one.)  At width 64 two CTAs of one tile
-  // share an SM instead (16 packed prompts, window 1024: 305 us, 350 us with
-  // two tiles a CTA).
+  // Width 128: two tiles a CTA share the keys' copies and overlap one's softmax
+  // with the other's products; where sequences are short, or tiles few, two
+  // CTAs of one tile on an SM overlap their starts and ends instead.  Measured
+  // with 32 heads: 16384 queries 1.42 ms with two tiles, 1.54 ms with one; 32
+  // prompts of 500 189 and 194 us; 64 of 128 126 and 83 us; one of 200 16.4
+  // and 15.3 us.  At width 64 one tile was never slower (16 packed prompts,
+  // window 1024: 350 us with two, 305 us with one).
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const bool one = (a.n_q / kTile + a.B) * a.n_heads <= sms;
+  const bool one = a.n_q <= static_cast<int64_t>(256) * a.B || (a.n_q / kTile + a.B) * a.n_heads <= sms;
   if (a.head_dim == 128) return one ? launch_dim<128, 1>(a, encode, stream) : launch_dim<128, 2>(a, encode, stream);
   return launch_dim<64, 1>(a, encode, stream);
 }
