@@ -15,12 +15,24 @@ namespace csa {
 // so the remainder, at most an eighth of a turn, keeps 24 bits of its own:
 // the angle is right to 2e-8 rad whatever p is (a quarter of what rounding
 // the whole fraction to binary32 would leave).
+// Both functions there are their Taylor polynomials, cut where the next term
+// is below 2e-9 and 2e-10 of an angle of pi/4.
 __device__ __forceinline__ void rope_sincos_exact(int64_t p, uint64_t turns, float* s, float* c) {
   const uint64_t frac = static_cast<uint64_t>(p) * turns;
-  const uint32_t quarter = static_cast<uint32_t>((frac + (1ull << 61)) >> 62);
-  const int64_t rest = static_cast<int64_t>(frac - (static_cast<uint64_t>(quarter) << 62));
-  float sr, cr;  // of half-turns in [-1/4, 1/4]
-  sincospif(static_cast<float>(static_cast<int32_t>(rest >> 32)) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31
+  const uint32_t top = static_cast<uint32_t>(frac >> 32);
+  const uint32_t quarter = (top + (1u << 29)) >> 30;
+  const int32_t rest = static_cast<int32_t>(top - (quarter << 30));  // in 2^-32 turns, at most an eighth of a turn
+  const float x = static_cast<float>(rest) * 1.4629180792671596e-09f;  // 2 pi * 2^-32
+  const float z = x * x;
+  float sr = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+  sr = fmaf(z, sr, 1.f / 120.f);
+  sr = fmaf(z, sr, -1.f / 6.f);
+  sr = fmaf(z * x, sr, x);
+  float cr = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+  cr = fmaf(z, cr, -1.f / 720.f);
+  cr = fmaf(z, cr, 1.f / 24.f);
+  cr = fmaf(z, cr, -0.5f);
+  cr = fmaf(z, cr, 1.f);
   const float a = (quarter & 1u) ? cr : sr, b = (quarter & 1u) ? sr : cr;
   *s = (quarter & 2u) ? -a : a;
   *c = ((quarter + 1u) & 2u) ? -b : b;

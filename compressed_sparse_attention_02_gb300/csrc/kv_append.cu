@@ -8,11 +8,15 @@
 // to x / s.  A scale that grows re-rounds the page's older codes to the new
 // one, which is exact but for codes that become subnormal (powers of two).
 //
-// One CTA per (page touched, head, K or V): it holds the page's new rows in
-// registers, 16 channels an item, rotates them, takes their maximum and
-// stores the codes, so the rows are read once and the codes written once.
-// Bound by memory for prompts and by latency (sequence search, page table,
-// row, scale: dependent loads) for single tokens.
+// Bound by memory for prompts (a row's bf16 read once, its codes written once)
+// and by latency for single tokens (sequence search, page table, scale: loads
+// that depend on each other).  Two forms:
+//  - pages: a CTA takes a page's new rows for a few heads of K or V, one head
+//    after the other with the next one's rows on their way: the angles of the
+//    page's rows are computed once, and a row's channels stay in registers
+//    from their rotation over the maximum to their codes;
+//  - rows: a warp takes the rows of one head of K or V in a page, a CTA eight
+//    of them, so a decoded token's heads all run at once.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <float.h>
@@ -47,142 +51,287 @@ __device__ __forceinline__ int64_t pages_of(int64_t p, int64_t n, int shift) {
   return n > 0 && p >= 0 ? ((p + n - 1) >> shift) - (p >> shift) + 1 : 0;
 }
 
-template <int THREADS, int NI>
-__global__ void __launch_bounds__(THREADS) kv_append_kernel(const KvAppendArgs a) {
-  constexpr int kWarps = THREADS / 32;
-  __shared__ int sh[kWarps + 2];
-  __shared__ float max_s[kWarps];
-  pdl_launch_dependents();
-  pdl_wait();
-  const PagedCache& c = a.cache;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int head = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
+// Rows of sequence b in this call; a bad entry of cu_rows gives none.
+__device__ __forceinline__ int64_t rows_of(const KvAppendArgs& a, int b) {
+  if (!a.cu_rows) return 1;
+  const int32_t lo = __ldg(a.cu_rows + b), hi = __ldg(a.cu_rows + b + 1);
+  if (lo < 0 || hi < lo || hi > a.n_rows) {
+    record_error(a.status, kErrIndexRange);
+    return 0;
+  }
+  return hi - lo;
+}
 
-  // the sequence and the page of this work item
-  auto rows_of = [&](int b) -> int64_t {
-    if (!a.cu_rows) return 1;
-    const int32_t lo = __ldg(a.cu_rows + b), hi = __ldg(a.cu_rows + b + 1);
-    if (lo < 0 || hi < lo || hi > a.n_rows) {
-      record_error(a.status, kErrIndexRange);
-      return 0;
-    }
-    return hi - lo;
-  };
-  int b;
-  int index = 0;
-  if (!a.cu_rows) {
-    b = blockIdx.x;
-  } else {
+// A page touched by the call: new rows [first, last) of it, from row src_row
+// of k / v on.
+struct PageRows {
+  int64_t page, pos0, src_row;  // pos0: position of the page's row 0
+  int first, last;
+};
+
+// The work item's page; false where there is nothing to store.  Every thread
+// of the CTA calls it.
+template <int THREADS>
+__device__ __forceinline__ bool find_page(const KvAppendArgs& a, int* sh, PageRows* p) {
+  const PagedCache& c = a.cache;
+  int b = blockIdx.x, index = 0;
+  if (a.cu_rows) {
     b = find_item<THREADS>(
         a.B, static_cast<int>(blockIdx.x),
-        [&](int s) { return static_cast<int>(pages_of(__ldg(a.pos0 + s), rows_of(s), c.page_shift)); }, sh, &index);
-    if (b < 0) return;
+        [&](int s) { return static_cast<int>(pages_of(__ldg(a.pos0 + s), rows_of(a, s), c.page_shift)); }, sh, &index);
+    if (b < 0) return false;
   }
   const int64_t p0 = __ldg(a.pos0 + b);
-  if (p0 < 0) return;
-  const int64_t row0 = a.cu_rows ? __ldg(a.cu_rows + b) : b;
-  const int64_t n = rows_of(b);
+  if (p0 < 0) return false;
   const int64_t pg = (p0 >> c.page_shift) + index;
-  int64_t page = -1;
-  if (pg < c.table_stride) page = __ldg(c.table + static_cast<int64_t>(b) * c.table_stride + pg);
-  if (page < 0 || page >= c.n_pages) {
-    if (tid == 0) record_error(a.status, kErrIndexRange);
-    return;
+  p->page = pg < c.table_stride ? __ldg(c.table + static_cast<int64_t>(b) * c.table_stride + pg) : -1;
+  if (p->page < 0 || p->page >= c.n_pages) {
+    if (threadIdx.x == 0) record_error(a.status, kErrIndexRange);
+    return false;
   }
-  const int64_t start = pg << c.page_shift;
-  const int first = static_cast<int>(p0 > start ? p0 - start : 0);  // rows there before
-  const int last = static_cast<int>(min(p0 + n - start, static_cast<int64_t>(c.page)));
-  const int64_t slab = page * c.n_kv_heads + head;
-  uint8_t* codes = (is_v ? c.v : c.k) + (slab << c.page_shift) * c.head_dim;
-  float* scale_at = (is_v ? c.v_scale : c.k_scale) + slab;
-  const float was = first > 0 ? *scale_at : 0.f;
-  const uint16_t* src = (is_v ? a.v : a.k) + (row0 + (start + first - p0)) * (is_v ? a.v_stride : a.k_stride) +
-                        head * (is_v ? a.v_stride_h : a.k_stride_h);
-  const int64_t src_stride = is_v ? a.v_stride : a.k_stride;
+  const int64_t n = rows_of(a, b);
+  p->pos0 = pg << c.page_shift;
+  p->first = static_cast<int>(p0 > p->pos0 ? p0 - p->pos0 : 0);
+  p->last = static_cast<int>(min(p0 + n - p->pos0, static_cast<int64_t>(c.page)));
+  p->src_row = (a.cu_rows ? __ldg(a.cu_rows + b) : b) + (p->pos0 + p->first - p0);
+  return true;
+}
+
+// The largest magnitude of an item and amax; NaN does not count, infinities
+// do (see finite_max).
+__device__ __forceinline__ float item_max(const float (&lo)[8], const float (&hi)[8], float amax) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(lo[j]), fabsf(hi[j])));
+  return amax;
+}
+__device__ __forceinline__ float finite_max(const float (&lo)[8], const float (&hi)[8], float amax) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(finite_abs(lo[j]), finite_abs(hi[j])));
+  return amax;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
+}
+
+// An item's 16 codes.
+__device__ __forceinline__ void store_item(uint8_t* row, int cl, int ch, const float (&lo)[8], const float (&hi)[8],
+                                           float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    w[j] = e4m3_pair(lo[4 * j] * inv, lo[4 * j + 1] * inv) | e4m3_pair(lo[4 * j + 2] * inv, lo[4 * j + 3] * inv) << 16;
+    w[2 + j] =
+        e4m3_pair(hi[4 * j] * inv, hi[4 * j + 1] * inv) | e4m3_pair(hi[4 * j + 2] * inv, hi[4 * j + 3] * inv) << 16;
+  }
+  *reinterpret_cast<uint2*>(row + cl) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(row + ch) = make_uint2(w[2], w[3]);
+}
+
+// A page's older codes, `bytes` of them, to a scale that grew (threads tid of n).
+__device__ __forceinline__ void round_again(uint8_t* codes, int bytes, float ratio, int tid, int n) {
+  uint32_t* old = reinterpret_cast<uint32_t*>(codes);
+  for (int i = tid; i < bytes >> 2; i += n) {
+    const uint32_t w = old[i];
+    const __half2 x(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3));
+    const __half2 y(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3));
+    const float2 fx = __half22float2(x), fy = __half22float2(y);
+    old[i] = e4m3_pair(fx.x * ratio, fx.y * ratio) | e4m3_pair(fy.x * ratio, fy.y * ratio) << 16;
+  }
+}
+
+__device__ __forceinline__ float scale_of(float amax, float was) {
+  return fmaxf(was, __uint_as_float(static_cast<uint32_t>(e4m3_scale_exp(amax) + 127) << 23));
+}
+
+// K or V of the call, of one page and head.
+struct Slab {
+  uint8_t* codes;
+  float* scale;
+  const uint16_t* src;  // row `first`
+  int64_t src_stride;
+};
+__device__ __forceinline__ Slab slab_of(const KvAppendArgs& a, const PageRows& p, int head, bool is_v) {
+  const PagedCache& c = a.cache;
+  const int64_t at = p.page * c.n_kv_heads + head;
+  Slab s;
+  s.codes = (is_v ? c.v : c.k) + (at << c.page_shift) * c.head_dim;
+  s.scale = (is_v ? c.v_scale : c.k_scale) + at;
+  s.src_stride = is_v ? a.v_stride : a.k_stride;
+  s.src = (is_v ? a.v : a.k) + p.src_row * s.src_stride + head * (is_v ? a.v_stride_h : a.k_stride_h);
+  return s;
+}
+
+#ifndef APP_MIN
+#define APP_MIN 512
+#endif
+template <int THREADS, int NI>
+__global__ void __launch_bounds__(THREADS, APP_MIN / THREADS) kv_append_pages_kernel(const KvAppendArgs a, const int heads) {
+  constexpr int kWarps = THREADS / 32;
+  extern __shared__ float2 sc_s[];  // K: [rows][rope_dim / 2] (sin, cos)
+  __shared__ int sh[kWarps + 2];
+  __shared__ float max_s[2][kWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool is_v = blockIdx.z != 0;
+  PageRows p;
+  if (!find_page<THREADS>(a, sh, &p)) return;
   RopeArgs rope = a.rope;
   if (is_v) rope.rope_dim = rope.offset = 0;
-
-  // new rows into registers, rotated; their largest magnitude
-  const int items = c.head_dim >> 4;  // a power of two
+  const int pairs = rope.rope_dim >> 1, rotated = rope.rope_dim >> 4;
+  const int items = a.cache.head_dim >> 4;  // a power of two
   const int items_shift = __ffs(items) - 1;
-  const int n_items = (last - first) << items_shift;
-  float lo[NI][8], hi[NI][8];
-  float amax = 0.f;
+  const int n_items = (p.last - p.first) << items_shift;
+  const int h1 = min(static_cast<int>(blockIdx.y + 1) * heads, a.cache.n_kv_heads);
+  uint4 u[NI], v[NI];  // the rows of the head to come
+  auto fetch = [&](int head) {
+    const Slab sl = slab_of(a, p, head, is_v);
 #pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int i = tid + k * THREADS;
-    if (i >= n_items) continue;
-    int cl, ch;
-    item_chunks(rope, i & (items - 1), &cl, &ch);
-    const uint16_t* row = src + (i >> items_shift) * src_stride;
-    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + cl)), lo[k]);
-    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + ch)), hi[k]);
+    for (int k = 0; k < NI; ++k) {
+      const int i = tid + k * THREADS;
+      u[k] = v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i >= n_items) continue;
+      int cl, ch;
+      item_chunks(rope, i & (items - 1), &cl, &ch);
+      const uint16_t* row = sl.src + (i >> items_shift) * sl.src_stride;
+      u[k] = __ldg(reinterpret_cast<const uint4*>(row + cl));
+      v[k] = __ldg(reinterpret_cast<const uint4*>(row + ch));
+    }
+  };
+  const int h0 = blockIdx.y * heads;
+  fetch(h0);
+  for (int i = tid; i < (p.last - p.first) * pairs; i += THREADS) {
+    const int r = i / pairs;
+    float s, c;
+    rope_sincos_exact(p.pos0 + p.first + r, __ldg(rope.turns + i - r * pairs), &s, &c);
+    sc_s[i] = make_float2(s * rope.mscale, c * rope.mscale);
   }
+  __syncthreads();
+  for (int head = h0; head < h1; ++head) {
+    const Slab sl = slab_of(a, p, head, is_v);
+    const float was = p.first > 0 ? *sl.scale : 0.f;
+    float lo[NI][8], hi[NI][8];
+    float amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int i = tid + k * THREADS;
-    if (i >= n_items) continue;
-    const int it = i & (items - 1);
+    for (int k = 0; k < NI; ++k) {
+      const int i = tid + k * THREADS, it = i & (items - 1);
+      unpack_bf16(u[k], lo[k]);
+      unpack_bf16(v[k], hi[k]);
+      if (it < rotated && i < n_items) {
+        float2 sc[8];
+        const float2* at = sc_s + (i >> items_shift) * pairs + 8 * it;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 f = *reinterpret_cast<const float4*>(at + 2 * j);
+          sc[2 * j] = make_float2(f.x, f.y);
+          sc[2 * j + 1] = make_float2(f.z, f.w);
+        }
+        rotate_item(rope.half != 0, sc, lo[k], hi[k]);
+      }
+      amax = item_max(lo[k], hi[k], amax);
+    }
+    if (head + 1 < h1) fetch(head + 1);
+    // (two arrays of maxima in turn: the next head's do not wait for this one's readers)
+    float* top = max_s[head & 1];
+    amax = warp_max(amax);
+    if (lane == 0) top[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) amax = fmaxf(amax, top[k]);
+    if (amax > FLT_MAX) {  // an infinity: the largest finite value decides (the whole CTA is here)
+      __syncthreads();
+      amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) amax = finite_max(lo[k], hi[k], amax);
+      amax = warp_max(amax);
+      if (lane == 0) top[warp] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) amax = fmaxf(amax, top[k]);
+    }
+    const float s = scale_of(amax, was), inv = __frcp_rn(s);  // exact for a power of two
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int i = tid + k * THREADS;
+      if (i >= n_items) continue;
+      int cl, ch;
+      item_chunks(rope, i & (items - 1), &cl, &ch);
+      store_item(sl.codes + (p.first + (i >> items_shift)) * a.cache.head_dim, cl, ch, lo[k], hi[k], inv);
+    }
+    if (p.first > 0 && s != was) round_again(sl.codes, p.first * a.cache.head_dim, __fdiv_rn(was, s), tid, THREADS);
+    if (tid == 0 && (p.first == 0 || s != was)) *sl.scale = s;
+  }
+}
+
+constexpr int kRowThreads = 256;
+__global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvAppendArgs a) {
+  __shared__ int sh[kRowThreads / 32 + 2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  PageRows p;
+  if (!find_page<kRowThreads>(a, sh, &p)) return;
+  const int which = blockIdx.y * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (which >= 2 * a.cache.n_kv_heads) return;
+  const bool is_v = (which & 1) != 0;
+  const Slab sl = slab_of(a, p, which >> 1, is_v);
+  const float was = p.first > 0 ? *sl.scale : 0.f;
+  RopeArgs rope = a.rope;
+  if (is_v) rope.rope_dim = rope.offset = 0;
+  const int items = a.cache.head_dim >> 4;  // 4 or 8: the warp takes 8 or 4 rows at a time
+  const int it = lane & (items - 1), at_once = 32 / items;
+  int cl, ch;
+  item_chunks(rope, it, &cl, &ch);
+  const int n = p.last - p.first;
+  float lo[8], hi[8];
+  auto load = [&](int r) {
+    const uint16_t* row = sl.src + r * sl.src_stride;
+    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + cl)), lo);
+    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + ch)), hi);
     if (it < (rope.rope_dim >> 4)) {
       float2 sc[8];
-      const int64_t pos = start + first + (i >> items_shift);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        rope_sincos_exact(pos, __ldg(rope.turns + 8 * it + j), &sc[j].x, &sc[j].y);
+        rope_sincos_exact(p.pos0 + p.first + r, __ldg(rope.turns + 8 * it + j), &sc[j].x, &sc[j].y);
         sc[j].x *= rope.mscale;
         sc[j].y *= rope.mscale;
       }
-      rotate_item(rope.half != 0, sc, lo[k], hi[k]);
+      rotate_item(rope.half != 0, sc, lo, hi);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(finite_abs(lo[k][j]), finite_abs(hi[k][j])));
+  };
+  float amax = 0.f;
+  for (int r = lane / items; r < n; r += at_once) {
+    load(r);
+    amax = finite_max(lo, hi, amax);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  if (lane == 0) max_s[warp] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) amax = fmaxf(amax, max_s[k]);
-  const float s = fmaxf(was, ldexpf(1.f, e4m3_scale_exp(amax)));
-  const float inv = __frcp_rn(s);  // exact for a power of two
-
-#pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int i = tid + k * THREADS;
-    if (i >= n_items) continue;
-    int cl, ch;
-    item_chunks(rope, i & (items - 1), &cl, &ch);
-    uint8_t* row = codes + static_cast<int64_t>(first + (i >> items_shift)) * c.head_dim;
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      w[j] = e4m3_pair(lo[k][4 * j] * inv, lo[k][4 * j + 1] * inv) |
-             e4m3_pair(lo[k][4 * j + 2] * inv, lo[k][4 * j + 3] * inv) << 16;
-      w[2 + j] = e4m3_pair(hi[k][4 * j] * inv, hi[k][4 * j + 1] * inv) |
-                 e4m3_pair(hi[k][4 * j + 2] * inv, hi[k][4 * j + 3] * inv) << 16;
-    }
-    *reinterpret_cast<uint2*>(row + cl) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(row + ch) = make_uint2(w[2], w[3]);
+  amax = warp_max(amax);
+  const float s = scale_of(amax, was), inv = __frcp_rn(s);
+  for (int r = lane / items; r < n; r += at_once) {
+    if (n > at_once) load(r);  // (else still in registers)
+    store_item(sl.codes + (p.first + r) * a.cache.head_dim, cl, ch, lo, hi, inv);
   }
-  // older rows of the page, re-rounded to a scale that grew
-  if (first > 0 && s != was) {
-    const float ratio = __fdiv_rn(was, s);
-    uint32_t* old = reinterpret_cast<uint32_t*>(codes);
-    for (int i = tid; i < (first * c.head_dim) >> 2; i += THREADS) {
-      const uint32_t w = old[i];
-      const __half2 x(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3));
-      const __half2 y(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3));
-      const float2 fx = __half22float2(x), fy = __half22float2(y);
-      old[i] = e4m3_pair(fx.x * ratio, fx.y * ratio) | e4m3_pair(fy.x * ratio, fy.y * ratio) << 16;
-    }
-  }
-  if (tid == 0 && (first == 0 || s != was)) *scale_at = s;
+  if (p.first > 0 && s != was) round_again(sl.codes, p.first * a.cache.head_dim, __fdiv_rn(was, s), lane, 32);
+  if (lane == 0 && (p.first == 0 || s != was)) *sl.scale = s;
 }
 
+#ifndef APP_CTAS
+#define APP_CTAS 2
+#endif
 template <int THREADS, int NI>
-cudaError_t launch_items(const KvAppendArgs& a, unsigned gx, cudaStream_t stream) {
-  return launch_pdl(kv_append_kernel<THREADS, NI>, dim3(gx, a.cache.n_kv_heads, 2), dim3(THREADS), 0, stream, a);
+cudaError_t launch_pages(const KvAppendArgs& a, unsigned items, int sms, cudaStream_t stream) {
+  // heads a CTA: as many as leave about APP_CTAS CTAs an SM
+  const int H = a.cache.n_kv_heads;
+  int groups = static_cast<int>((static_cast<int64_t>(sms) * APP_CTAS + 2 * items - 1) / (2 * items));
+  groups = groups < 1 ? 1 : groups > H ? H : groups;
+  const int heads = (H + groups - 1) / groups;
+  const size_t smem = static_cast<size_t>(a.cache.page) * (a.rope.rope_dim / 2) * sizeof(float2);
+  cudaError_t e = cudaFuncSetAttribute(kv_append_pages_kernel<THREADS, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv_append_pages_kernel<THREADS, NI>, dim3(items, (H + heads - 1) / heads, 2), dim3(THREADS), smem,
+                    stream, a, heads);
 }
 
 }  // namespace
@@ -195,13 +344,19 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
   const int64_t gx = a.cu_rows ? (most < a.n_rows ? most : a.n_rows) : a.B;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   const unsigned x = static_cast<unsigned>(gx);
+  // Few rows a sequence: a warp a head.
+  if (a.n_rows <= 2 * static_cast<int64_t>(a.B))
+    return launch_pdl(kv_append_rows_kernel, dim3(x, (2 * a.cache.n_kv_heads + 7) / 8), dim3(kRowThreads), 0, stream, a);
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // 16-channel items of a page: page * head_dim / 16, 64 .. 1024
   const int items = a.cache.page * a.cache.head_dim / 16;
-  if (items <= 64) return launch_items<64, 1>(a, x, stream);
-  if (items <= 128) return launch_items<128, 1>(a, x, stream);
-  if (items <= 256) return launch_items<128, 2>(a, x, stream);
-  if (items <= 512) return launch_items<128, 4>(a, x, stream);
-  return launch_items<256, 4>(a, x, stream);
+  if (items <= 64) return launch_pages<64, 1>(a, x, sms, stream);
+  if (items <= 128) return launch_pages<64, 2>(a, x, sms, stream);
+  if (items <= 256) return launch_pages<128, 2>(a, x, sms, stream);
+  if (items <= 512) return launch_pages<256, 2>(a, x, sms, stream);
+  return launch_pages<512, 2>(a, x, sms, stream);
 }
 
 }  // namespace csa

@@ -40,9 +40,15 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeRowsArgs a, const RopeGrid g) {
+#ifndef ROPE_CTAS
+#define ROPE_CTAS 4
+#define ROPE_FLIGHT 3
+#define ROPE_ITEMS 2400
+#endif
+constexpr int kFlight = ROPE_FLIGHT;  // items a thread has in flight
+
+__global__ void __launch_bounds__(kRopeThreads, ROPE_CTAS) rope_kernel(const RopeRowsArgs a, const RopeGrid g) {
   extern __shared__ float2 sc_s[];  // [tokens][rope_dim / 2] (sin, cos)
-  __shared__ int32_t pos_s[kRopeMaxTokens];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -51,59 +57,62 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeRowsArgs a
   const int h0 = static_cast<int>(blockIdx.y) * g.heads;
   const int nh = min(g.heads, a.n_heads - h0);
   const int pairs = a.rope.rope_dim >> 1;
-  if (tid < nt) pos_s[tid] = __ldg(a.pos + t0 + tid);
-  __syncthreads();
-  for (int i = tid; i < nt * pairs; i += kRopeThreads) {
-    const int t = i / pairs, j = i - t * pairs;
-    float s, c;
-    rope_sincos_exact(pos_s[t], __ldg(a.rope.turns + j), &s, &c);
-    sc_s[i] = make_float2((a.inverse ? -s : s) * a.rope.mscale, c * a.rope.mscale);
-  }
-  __syncthreads();
-  const int per_token = g.heads * g.items;  // (a last group of fewer heads leaves its items out)
-  const int n = nt * per_token;
+  const int n = nt * g.heads * g.items;  // (a last group of fewer heads leaves its items out)
   const int rotated = a.rope.rope_dim >> 4;
-  constexpr int kFlight = 4;
-  for (int i0 = tid; i0 < n; i0 += kFlight * kRopeThreads) {
+  const uint16_t* in = a.in + t0 * a.in_stride + h0 * a.in_stride_h;
+  uint16_t* out = a.out + t0 * a.out_stride + h0 * a.out_stride_h;
+  for (int i0 = tid; i0 - tid < n; i0 += kFlight * kRopeThreads) {
     uint4 u[kFlight], v[kFlight];
-    uint16_t *lo[kFlight], *hi[kFlight];
-    int at[kFlight];  // the item's (sin, cos) in sc_s; -1: copied; -2: nothing
+    int64_t dst[kFlight];
+    int at[kFlight];  // the item's (sin, cos) in sc_s and, above, its distance to the second chunk; -1: nothing
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
       const int i = i0 + k * kRopeThreads;
-      at[k] = -2;
+      at[k] = -1;
       if (i >= n) continue;
       const int row = static_cast<int>(div_by(i, g.inv_items, g.items));
       const int it = i - row * g.items;
       const int t = static_cast<int>(div_by(row, g.inv_heads, g.heads));
       const int h = row - t * g.heads;
-      if (h >= nh || pos_s[t] < 0) continue;
+      if (h >= nh || __ldg(a.pos + t0 + t) < 0) continue;
       int cl, ch;
       item_chunks(a.rope, it, &cl, &ch);
-      const uint16_t* src = a.in + (t0 + t) * a.in_stride + (h0 + h) * a.in_stride_h;
-      uint16_t* dst = a.out + (t0 + t) * a.out_stride + (h0 + h) * a.out_stride_h;
-      u[k] = *reinterpret_cast<const uint4*>(src + cl);
-      v[k] = *reinterpret_cast<const uint4*>(src + ch);
-      lo[k] = dst + cl;
-      hi[k] = dst + ch;
-      at[k] = it < rotated ? t * pairs + 8 * it : -1;
+      const uint16_t* src = in + t * a.in_stride + h * a.in_stride_h + cl;
+      u[k] = *reinterpret_cast<const uint4*>(src);
+      v[k] = *reinterpret_cast<const uint4*>(src + (ch - cl));
+      dst[k] = t * a.out_stride + h * a.out_stride_h + cl;
+      at[k] = (ch - cl) << 16 | (it < rotated ? t * pairs + 8 * it : 0xFFFF);
+    }
+    if (i0 == tid) {  // the tokens' sines and cosines, while the first loads are on their way
+      for (int i = tid; i < nt * pairs; i += kRopeThreads) {
+        const int t = i / pairs, j = i - t * pairs;
+        float s, c;
+        rope_sincos_exact(__ldg(a.pos + t0 + t), __ldg(a.rope.turns + j), &s, &c);
+        sc_s[i] = make_float2((a.inverse ? -s : s) * a.rope.mscale, c * a.rope.mscale);
+      }
+      __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      if (at[k] == -2) continue;
-      if (at[k] >= 0) {
+      if (at[k] < 0) continue;
+      const int sc_at = at[k] & 0xFFFF;
+      if (sc_at != 0xFFFF) {
         float x[8], y[8];
         float2 sc[8];
         unpack_bf16(u[k], x);
         unpack_bf16(v[k], y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sc[j] = sc_s[at[k] + j];
+        for (int j = 0; j < 4; ++j) {
+          const float4 f = *reinterpret_cast<const float4*>(sc_s + sc_at + 2 * j);
+          sc[2 * j] = make_float2(f.x, f.y);
+          sc[2 * j + 1] = make_float2(f.z, f.w);
+        }
         rotate_item(a.rope.half != 0, sc, x, y);
         u[k] = pack_bf16(x);
         v[k] = pack_bf16(y);
       }
-      *reinterpret_cast<uint4*>(lo[k]) = u[k];
-      *reinterpret_cast<uint4*>(hi[k]) = v[k];
+      *reinterpret_cast<uint4*>(out + dst[k]) = u[k];
+      *reinterpret_cast<uint4*>(out + dst[k] + (at[k] >> 16)) = v[k];
     }
   }
 }
@@ -117,11 +126,11 @@ cudaError_t launch_rope(const RopeRowsArgs& a, cudaStream_t stream) {
   RopeGrid g;
   const bool in_place = a.in == a.out;
   g.items = (in_place ? a.rope.rope_dim : a.head_dim) >> 4;
-  // A CTA of 256 threads takes about 2048 items (8 a thread, four in flight):
+  // A CTA of 256 threads takes about 2048 items (8 a thread, kFlight in flight):
   // several tokens of few heads, or one token whose heads are split while the
   // grid would not fill the GPU.
   const int64_t row_items = static_cast<int64_t>(a.n_heads) * g.items;
-  int64_t tokens = 2048 / row_items;
+  int64_t tokens = ROPE_ITEMS / row_items;
   tokens = tokens < 1 ? 1 : tokens > kRopeMaxTokens ? kRopeMaxTokens : tokens;
   while (tokens > 1 && (a.n_rows + tokens - 1) / tokens < 600) tokens >>= 1;
   g.tokens = static_cast<int>(tokens);
