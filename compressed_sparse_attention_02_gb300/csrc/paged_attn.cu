@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 2;
 constexpr int kUnitShift = 7;             // tokens a unit: 32 a warp
 constexpr int kUnit = 1 << kUnitShift;
 constexpr int kWarpTokens = kUnit / kWarps;
@@ -43,14 +42,21 @@ constexpr float kLag = 4.f;
 constexpr float kWeightExp = 11.f;
 constexpr float kNone = -1e30f;           // running maximum before the first token
 
+#ifndef C64
+#define C64 4
+#define S64 3
+#define C128 2
+#define S128 3
+#endif
 template <int D>
 struct Cfg {
-  static constexpr int kStages = 3;
+  static constexpr int kCtas = D == 64 ? C64 : C128;        // CTAs an SM
+  static constexpr int kStages = D == 64 ? S64 : S128;
   static constexpr int kTileBytes = kWarpTokens * D;        // K or V of one warp's 32 tokens
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmem = kWarps * kWarpBytes;
-  static constexpr int kRecord = kRows * (D + 2);           // floats of a partial result
+  static constexpr int kRecord = kRows * (D + 2);           // floats of a partial result: sums, maxima, weights' sums
   // A warp's accumulators in its ring at the end: one float of padding after
   // every 32, so that the 32 lanes' channels fall into different banks.
   static constexpr int kRowFloats = D + D / 32;
@@ -63,6 +69,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes, or zeros without reading.
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -82,11 +91,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-// Two E4M3 codes (low byte first) as f16, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
-  return h;
+// Four E4M3 codes (low byte first) as two pairs of f16, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -128,29 +137,42 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int b) {
   return s;
 }
 
-// Sum over the CTA of two values.
-__device__ __forceinline__ void block_sum2(int64_t& x, int64_t& y, int64_t* sh, int threads) {
+// What a CTA leaves for the merge of the pair that its share ends inside.
+struct __align__(16) Cut {
+  int32_t row, rows;  // first output row ([B][n_heads]) and rows; rows 0: the pair did not begin in this share, or ends here
+  int32_t slot;       // the CTA's record of it (later CTAs: record 0)
+  int32_t last;       // the CTA that ends it
+};
+
+// Sum over the CTA.
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, off);
-    y += __shfl_xor_sync(0xffffffffu, y, off);
-  }
-  if (lane == 0) {
-    sh[2 * warp] = x;
-    sh[2 * warp + 1] = y;
-  }
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  if (lane == 0) sh[warp] = x;
   __syncthreads();
-  x = y = 0;
-  for (int w = 0; w < threads / 32; ++w) {
-    x += sh[2 * w];
-    y += sh[2 * w + 1];
-  }
+  x = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) x += sh[w];
   __syncthreads();
+  return x;
+}
+
+// An output row from its sums (in units of 2^m) and the sink's logit, if any.
+__device__ __forceinline__ float finish_row(float m, float& l, const float* sink, int head, float* lse) {
+  float f = 1.f;
+  if (sink) {
+    const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
+    f = ex2(m - m1);
+    l = l * f + ex2(s2 - m1);
+    m = m1;
+  }
+  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  return l == 0.f ? 0.f : f / l;  // times the sums: the output
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
   using C = Cfg<D>;
   constexpr int kK = D / 16;       // 16-channel steps of q . k
   constexpr int kN = D / 8;        // 8-channel tiles of the output
@@ -170,15 +192,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   const int pairs = cache.n_kv_heads * blocks;
 
   // this CTA's share [at, end) of the line of units
-  int64_t total = 0, unused = 0;
+  int64_t total = 0;
   for (int s = tid; s < a.B; s += kThreads) total += span_of(a, s).units();
-  block_sum2(total, unused, sh, kThreads);
-  total *= pairs;
+  total = block_sum(total, sh) * pairs;
+  // empty sequences, in turn over the CTAs
+  for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
+    if (span_of(a, s).len > 0) continue;
+    const int64_t row = static_cast<int64_t>(s) * a.n_heads;
+    for (int i = tid; i < a.n_heads * D; i += kThreads) a.out[row * D + i] = 0;
+    if (a.lse)
+      for (int i = tid; i < a.n_heads; i += kThreads) a.lse[row + i] = a.sink ? __ldg(a.sink + i) : -INFINITY;
+  }
   const int64_t per = (total + gridDim.x - 1) / gridDim.x;
   const int64_t begin = blockIdx.x * per;
   int64_t at = begin;
   const int64_t end = min(total, begin + per);
-  if (at >= end) return;
+  Cut cut = {0, 0, 0, 0};
+  Cut* cuts = reinterpret_cast<Cut*>(a.part);
+  float* records = a.part + gridDim.x * (sizeof(Cut) / sizeof(float));
+  if (at >= end) {
+    if (tid == 0) cuts[blockIdx.x] = cut;
+    return;
+  }
   int64_t index;
   int b = find_item<kThreads>(
       a.B, at, [&](int s) { return static_cast<int64_t>(span_of(a, s).units()) * pairs; }, sh, &index);
@@ -224,21 +259,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
         const int64_t off_b = ((slab_b << cache.page_shift) + ((t0 + 16) & in_page)) * D - 16 * D;
         constexpr int kRowsAtOnce = 32 / kChunks;
         const int r0 = lane / kChunks, c = lane % kChunks;
+        if (t0 >= sp.lo && t0 + kWarpTokens <= sp.len && ok_a && ok_b) {  // (uniform) all rows are there
+          const uint8_t *ka = cache.k + off_a + r0 * D + c * 16, *kb = cache.k + off_b + r0 * D + c * 16;
+          const uint8_t *va = cache.v + off_a + r0 * D + c * 16, *vb = cache.v + off_b + r0 * D + c * 16;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int r = r0 + i * kRowsAtOnce;
-          const bool first = i < kChunks / 2;  // rows below 16
-          const int t = t0 + r;
-          const bool there = (first ? ok_a : ok_b) && t >= sp.lo && t < sp.len;
-          const int64_t off = (first ? off_a : off_b) + r * D + c * 16;
-          const uint32_t dst = chunk_at<D>(r, c);
-          cp_async_16_or_zero(ks + dst, there ? cache.k + off : cache.k, there);
-          cp_async_16_or_zero(vs + dst, there ? cache.v + off : cache.v, there);
-        }
-        if (lane < 4) {
-          const bool there = (lane & 1) ? ok_b : ok_a;
-          const float* from = ((lane & 2) ? cache.v_scale : cache.k_scale) + ((lane & 1) ? slab_b : slab_a);
-          cp_async_4_or_zero(smem_u32(&scale_s[warp][st][lane]), from, there);
+          for (int i = 0; i < kChunks; ++i) {
+            const uint32_t dst = chunk_at<D>(r0 + i * kRowsAtOnce, c);
+            const int off = i * kRowsAtOnce * D;
+            cp_async_16(ks + dst, (i < kChunks / 2 ? ka : kb) + off);
+            cp_async_16(vs + dst, (i < kChunks / 2 ? va : vb) + off);
+          }
+          if (lane < 4)
+            cp_async_4_or_zero(smem_u32(&scale_s[warp][st][lane]),
+                               ((lane & 2) ? cache.v_scale : cache.k_scale) + ((lane & 1) ? slab_b : slab_a), true);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kChunks; ++i) {
+            const int r = r0 + i * kRowsAtOnce, t = t0 + r;
+            const bool first = i < kChunks / 2;  // rows below 16
+            const bool there = (first ? ok_a : ok_b) && t >= sp.lo && t < sp.len;
+            const int64_t off = (first ? off_a : off_b) + r * D + c * 16;
+            const uint32_t dst = chunk_at<D>(r, c);
+            cp_async_16_or_zero(ks + dst, there ? cache.k + off : cache.k, there);
+            cp_async_16_or_zero(vs + dst, there ? cache.v + off : cache.v, there);
+          }
+          if (lane < 4) {
+            const bool there = (lane & 1) ? ok_b : ok_a;
+            const float* from = ((lane & 2) ? cache.v_scale : cache.k_scale) + ((lane & 1) ? slab_b : slab_a);
+            cp_async_4_or_zero(smem_u32(&scale_s[warp][st][lane]), from, there);
+          }
         }
         if (lane == 0) bad_s[warp][st] = (bads & 1u) | ((bads >> 31) << 1);
       }
@@ -311,7 +360,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
             w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
           }
 #pragma unroll
-          for (int s = 0; s < kK; ++s) mma_f16_16816(x[n], qf[s], e4m3x2_to_f16x2(w[s]), e4m3x2_to_f16x2(w[s] >> 16));
+          for (int s = 0; s < kK; ++s) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16(w[s], b0, b1);
+            mma_f16_16816(x[n], qf[s], b0, b1);
+          }
         }
         const float4 sc = *reinterpret_cast<const float4*>(scale_s[warp][st]);
         const int bad = bad_s[warp][st];
@@ -397,10 +450,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
           for (int w = 0; w < D / 32; ++w) {
             const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), a23 = __byte_perm(v[0][w], v[1][w], 0x7362);
             const uint32_t b01 = __byte_perm(v[2][w], v[3][w], 0x5140), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-            mma_f16_16816(o[4 * w], pf[s], e4m3x2_to_f16x2(a01), e4m3x2_to_f16x2(b01));
-            mma_f16_16816(o[4 * w + 1], pf[s], e4m3x2_to_f16x2(a01 >> 16), e4m3x2_to_f16x2(b01 >> 16));
-            mma_f16_16816(o[4 * w + 2], pf[s], e4m3x2_to_f16x2(a23), e4m3x2_to_f16x2(b23));
-            mma_f16_16816(o[4 * w + 3], pf[s], e4m3x2_to_f16x2(a23 >> 16), e4m3x2_to_f16x2(b23 >> 16));
+            uint32_t p0, p1, q0, q1;
+            e4m3x4_to_f16(a01, p0, p1);
+            e4m3x4_to_f16(b01, q0, q1);
+            mma_f16_16816(o[4 * w], pf[s], p0, q0);
+            mma_f16_16816(o[4 * w + 1], pf[s], p1, q1);
+            e4m3x4_to_f16(a23, p0, p1);
+            e4m3x4_to_f16(b23, q0, q1);
+            mma_f16_16816(o[4 * w + 2], pf[s], p0, q0);
+            mma_f16_16816(o[4 * w + 3], pf[s], p1, q1);
           }
         }
       }
@@ -432,7 +490,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     }
     __syncthreads();
     const bool whole = take == nt;
-    float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (at == begin ? 0 : 1)) * C::kRecord;
+    const int slot = at == begin ? 0 : 1;
+    float* part = records + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kRecord;
+    if (!whole && u == 0) {  // the pair begins here and goes on
+      cut.row = b * a.n_heads + head0;
+      cut.rows = rows;
+      cut.slot = slot;
+      cut.last = static_cast<int>((at + nt - 1) / per);
+    }
     for (int i = tid; i < rows * D; i += kThreads) {
       const int r = i / D, d = i % D;
       float mt = m_s[0][r];
@@ -446,16 +511,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
         n += reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[r * C::kRowFloats + d + (d >> 5)] * f;
       }
       if (whole) {
-        if (a.sink) {
-          const float s2 = __ldg(a.sink + head0 + r) * kLog2e, m1 = fmaxf(mt, s2);
-          lt = lt * ex2(mt - m1) + ex2(s2 - m1);
-          n *= ex2(mt - m1);
-          mt = m1;
-        }
         const int64_t row = static_cast<int64_t>(b) * a.n_heads + head0 + r;
-        const __nv_bfloat16 y = __float2bfloat16_rn(lt == 0.f ? 0.f : n / lt);
+        float lse;
+        const __nv_bfloat16 y = __float2bfloat16_rn(n * finish_row(mt, lt, a.sink, head0 + r, &lse));
         a.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&y);
-        if (a.lse && d == 0) a.lse[row] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+        if (a.lse && d == 0) a.lse[row] = lse;
       } else {
         part[r * D + d] = n;
         if (d == 0) {
@@ -474,87 +534,86 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
       } while (sp.units() == 0);
     }
   }
+  if (tid == 0) cuts[blockIdx.x] = cut;
 }
 
-// Finishes the pairs that the shares' borders divide (from their CTAs'
-// records, first to last), and the rows of empty sequences.
+// Finishes the pairs that the shares' borders divide, from their CTAs' records
+// first to last.  A CTA looks at one share's end; where a pair begins there and
+// goes on, warps take `split` stretches of the records of each of its rows
+// (8 / split rows at a time; grid.y parts of the rows).
 constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnArgs a, const int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnArgs a, const int ctas,
+                                                                    const int split) {
   using C = Cfg<D>;
   constexpr int kMergeWarps = kMergeThreads / 32;
-  __shared__ int64_t sh[2 * kMergeWarps];
+  constexpr int kPer = D / 32;  // channels a lane
   __shared__ float m_s[kMergeWarps], l_s[kMergeWarps];
   __shared__ float n_s[kMergeWarps][D];
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group = a.n_heads / a.cache.n_kv_heads;
-  const int blocks = (group + kRows - 1) / kRows;
-  const int pairs = a.cache.n_kv_heads * blocks;
-  const int b = blockIdx.x / pairs, pair = blockIdx.x - b * pairs;
-  const int hk = pair / blocks, row0 = (pair - hk * blocks) * kRows;
-  const int r = blockIdx.y;
-  if (r >= min(kRows, group - row0)) return;
-  const int head = hk * group + row0 + r;
-  const int64_t row = static_cast<int64_t>(b) * a.n_heads + head;
-  const float sink2 = a.sink ? __ldg(a.sink + head) * kLog2e : -INFINITY;
-
-  int64_t total = 0, before = 0;
-  for (int s = tid; s < a.B; s += kMergeThreads) {
-    const int n = span_of(a, s).units();
-    total += n;
-    before += s < b ? n : 0;
+  const Cut cut = reinterpret_cast<const Cut*>(a.part)[blockIdx.x];
+  if (cut.rows == 0) return;
+  const float* records = a.part + ctas * (sizeof(Cut) / sizeof(float));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x, n_rec = cut.last - c0 + 1;
+  auto record = [&](int k) {
+    return records + (static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? cut.slot : 0)) * C::kRecord;
+  };
+  const int part = warp % split, at_once = kMergeWarps / split;
+  for (int r0 = blockIdx.y * at_once; r0 < cut.rows; r0 += gridDim.y * at_once) {
+    const int r = r0 + warp / split;
+    const bool there = r < cut.rows;
+    float m = kNone, l = 0.f, n[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) n[j] = 0.f;
+    if (there) {
+      for (int k = part + lane * split; k < n_rec; k += 32 * split) m = fmaxf(m, record(k)[kRows * D + r]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+#pragma unroll 4
+      for (int k = part; k < n_rec; k += split) {
+        const float* p = record(k);
+        const float f = ex2(p[kRows * D + r] - m);
+        l += p[kRows * D + kRows + r] * f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) n[j] += p[r * D + lane + 32 * j] * f;
+      }
+    }
+    if (split > 1) {  // the stretches' sums, first to last
+      __syncthreads();
+      if (lane == 0) {
+        m_s[warp] = m;
+        l_s[warp] = l;
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) n_s[warp][lane + 32 * j] = n[j];
+      __syncthreads();
+      if (part != 0) continue;
+      const float m0 = m;
+      for (int w = 1; w < split; ++w) m = fmaxf(m, m_s[warp + w]);
+      const float f0 = ex2(m0 - m);
+      l *= f0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) n[j] *= f0;
+      for (int w = 1; w < split; ++w) {
+        const float f = ex2(m_s[warp + w] - m);
+        l += l_s[warp + w] * f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) n[j] += n_s[warp + w][lane + 32 * j] * f;
+      }
+    }
+    if (!there) continue;
+    const int64_t row = static_cast<int64_t>(cut.row) + r;
+    float lse;
+    const float f = finish_row(m, l, a.sink, static_cast<int>(row % a.n_heads), &lse);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const __nv_bfloat16 y = __float2bfloat16_rn(n[j] * f);
+      a.out[row * D + lane + 32 * j] = *reinterpret_cast<const uint16_t*>(&y);
+    }
+    if (a.lse && lane == 0) a.lse[row] = lse;
   }
-  block_sum2(total, before, sh, kMergeThreads);
-  const int nt = span_of(a, b).units();
-  if (nt == 0) {
-    if (tid < D) a.out[row * D + tid] = 0;
-    if (a.lse && tid == 0) a.lse[row] = a.sink ? __ldg(a.sink + head) : -INFINITY;
-    return;
-  }
-  const int64_t per = (total * pairs + ctas - 1) / ctas;
-  const int64_t first = before * pairs + static_cast<int64_t>(pair) * nt;
-  const int c0 = static_cast<int>(first / per), c1 = static_cast<int>((first + nt - 1) / per);
-  if (c0 == c1) return;
-  // a CTA's record 0 is that of its first segment, 1 that of a later one
-  auto record = [&](int c) { return a.part + (static_cast<int64_t>(c) * 2 + (c * per < first ? 1 : 0)) * C::kRecord; };
-  float m = kNone;
-  for (int c = c0 + tid; c <= c1; c += kMergeThreads) m = fmaxf(m, record(c)[kRows * D + r]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (lane == 0) m_s[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, m_s[w]);
-  m = fmaxf(m, sink2);
-  constexpr int kPer = D / 32;  // channels a lane
-  float n[kPer], l = 0.f;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) n[j] = 0.f;
-#pragma unroll 2
-  for (int c = c0 + warp; c <= c1; c += kMergeWarps) {
-    const float* p = record(c);
-    const float f = ex2(p[kRows * D + r] - m);
-    l += p[kRows * D + kRows + r] * f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) n[j] += p[r * D + lane + 32 * j] * f;
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) n_s[warp][lane + 32 * j] = n[j];
-  if (lane == 0) l_s[warp] = l;
-  __syncthreads();
-  if (tid >= D) return;
-  float nt_sum = 0.f, lt = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    nt_sum += n_s[w][tid];
-    lt += l_s[w];
-  }
-  if (a.sink) lt += ex2(sink2 - m);
-  const __nv_bfloat16 y = __float2bfloat16_rn(lt == 0.f ? 0.f : nt_sum / lt);
-  a.out[row * D + tid] = *reinterpret_cast<const uint16_t*>(&y);
-  if (a.lse && tid == 0) a.lse[row] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
 }
 
 template <int D>
@@ -562,20 +621,23 @@ cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
   using C = Cfg<D>;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int ctas = sms * kCtasPerSm;
+  const int ctas = sms * C::kCtas;
   e = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kThreads), C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  const int group = a.n_heads / a.cache.n_kv_heads;
+  const int group = a.n_heads / a.cache.n_kv_heads, rows = group < kRows ? group : kRows;
   const int64_t pairs = static_cast<int64_t>(a.B) * a.cache.n_kv_heads * ((group + kRows - 1) / kRows);
-  if (pairs > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(paged_merge_kernel<D>, dim3(static_cast<unsigned>(pairs), group < kRows ? group : kRows),
-                    dim3(kMergeThreads), 0, stream, a, ctas);
+  // Many pairs: few records each, a warp a row.  Few pairs: up to all CTAs'
+  // records of one, eight warps a row and a CTA for each row.
+  const bool many = pairs * 4 >= ctas;
+  return launch_pdl(paged_merge_kernel<D>, dim3(ctas - 1, many ? 1 : rows), dim3(kMergeThreads), 0, stream, a, ctas,
+                    many ? 1 : 8);
 }
 
 }  // namespace
 
 size_t paged_attn_bytes(int head_dim, int sms) {
-  return static_cast<size_t>(sms) * kCtasPerSm * 2 * kRows * (head_dim + 2) * sizeof(float);
+  const size_t ctas = static_cast<size_t>(sms) * (head_dim == 64 ? Cfg<64>::kCtas : Cfg<128>::kCtas);
+  return ctas * (sizeof(Cut) + 2 * kRows * (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
