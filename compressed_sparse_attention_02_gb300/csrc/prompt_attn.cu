@@ -42,27 +42,29 @@ constexpr float kLag = 8.f;
 constexpr int kMaxMasked = 8;
 constexpr int kCleanThreads = 64;
 
-template <int D, int QT>
+// QT tiles of queries a CTA, CTAS CTAs an SM.
+template <int D, int QT, int CTAS>
 struct Cfg {
   static constexpr int kThreads = QT * 128 + 128;
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
   static constexpr int kBlockBytes = kTile * 128;
-  static constexpr int kStages = QT == 1 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
+  static constexpr int kStages = CTAS == 2 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
   static constexpr int kSmem = QT * kTileBytes + kStages * kTileBytes + 1024;
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
   static constexpr int kCols = QT == 2 ? 512 : 256;
-  // CTAs an SM: two of one tile each at width 64 (their 256 columns and 81 KB
-  // fit twice), so one's start and end run under the other's products.
-  static constexpr int kCtas = QT == 1 ? 2 : 1;
   // Where 168 (or 128) registers a thread are launched, the softmax warps
   // take some that the other four give up: 256 x 208 + 128 x 88 = 384 x 168,
-  // 128 x 200 + 128 x 56 = 256 x 128.
-  static constexpr bool kSplit = QT == 2 || kCtas == 2;
+  // 128 x 208 + 128 x 48 = 256 x 128.
+  static constexpr bool kSplit = QT == 2 || CTAS == 2;
   static constexpr int kLaunchRegs = QT == 2 ? 168 : 128;
-  static constexpr int kSoftmaxRegs = QT == 2 ? 208 : 200, kOtherRegs = QT == 2 ? 88 : 56;
-  static_assert(QT * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "registers of the block");
+  static constexpr int kSoftmaxRegs = 208, kOtherRegs = QT == 2 ? 88 : 48;
+  static_assert(!kSplit || QT * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "registers of the block");
+  // One CTA of one tile an SM: the keys may be shared out over a cluster,
+  // whose fp32 sums meet in the rings.
+  static constexpr bool kCluster = QT == 1 && CTAS == 1;
+  static_assert(!kCluster || kStages * kTileBytes >= kTile * D * 4, "the sums fit the ring");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -119,16 +121,30 @@ struct Range {
   int lo, hi;
 };
 
+// From a row's reference (in log2) and sum of weights to the factor of its
+// weighted values and its lse, the sink's weight in.
+__device__ __forceinline__ float finish_row(float m, float l, const float* sink, int head, float* lse) {
+  float f = 1.f;
+  if (sink) {
+    const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
+    f = ex2(m - m1);
+    l = l * f + ex2(s2 - m1);
+    m = m1;
+  }
+  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  return l == 0.f ? 0.f : f / l;
+}
+
 struct Seq {
   int64_t q0, k0;  // first rows of the sequence
   int nq, nk;
 };
 
-template <int D, int QT>
-__global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
+template <int D, int QT, int CTAS>
+__global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a) {
-  using C = Cfg<D, QT>;
+                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a, const int cluster) {
+  using C = Cfg<D, QT, CTAS>;
   constexpr int kTmaWarp = 4 * QT, kMmaWarp = 4 * QT + 1, kCleanWarp = 4 * QT + 2;
   constexpr int kRowsCta = QT * kTile;
   extern __shared__ uint8_t smem_raw[];
@@ -139,6 +155,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
   __shared__ int abort_s;
   __shared__ uint32_t odd_rows[kMaxMasked][4];  // keys of each masked tile whose values are not all finite
   __shared__ int odd_tile[kMaxMasked], n_odd;
+  __shared__ float m_s[C::kCluster ? kTile : 1], l_s[C::kCluster ? kTile : 1];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_s = smem;
   uint8_t* ring = smem + QT * C::kTileBytes;
@@ -178,7 +195,10 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
 
   // this CTA's sequence and tiles: the later tiles of a sequence (more keys
   // under the causal mask) first
-  const int head = static_cast<int>(blockIdx.x % a.n_heads);
+  // (a cluster's CTAs: the same tile, each a part of its keys)
+  const int unit = C::kCluster ? static_cast<int>(blockIdx.x) / cluster : static_cast<int>(blockIdx.x);
+  const int rank = C::kCluster ? static_cast<int>(blockIdx.x) - unit * cluster : 0;
+  const int head = unit % a.n_heads;
   const int kv_head = head / (a.n_heads / a.n_kv_heads);
   auto seq_at = [&](int b) {
     Seq s;
@@ -194,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
   };
   int index;
   const int b = find_item<C::kThreads>(
-      a.B, static_cast<int>(blockIdx.x / a.n_heads), [&](int s) { return (seq_at(s).nq + kRowsCta - 1) / kRowsCta; },
+      a.B, unit / a.n_heads, [&](int s) { return (seq_at(s).nq + kRowsCta - 1) / kRowsCta; },
       sh, &index);
   // (the search's barriers also order the allocation and the mbarriers' set-up)
   tc_fence_after();
@@ -240,6 +260,12 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     rt[t] = range_of(row0 + t * kTile, rows_of(t));
+    if (C::kCluster && cluster > 1) {
+      const int per = (rt[t].hi - rt[t].lo + cluster - 1) / cluster, hi = rt[t].hi - rank * per;
+      rt[t].lo = max(rt[t].lo, hi - per);
+      rt[t].hi = hi;
+      if (hi <= rt[t].lo) rt[t].lo = rt[t].hi = 0;
+    }
     if (rt[t].lo < rt[t].hi) {
       j_lo = min(j_lo, rt[t].lo);
       j_hi = max(j_hi, rt[t].hi);
@@ -432,7 +458,8 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
     const int at_key = i + shift;
     const int last_key = a.causal ? min(at_key, sq.nk - 1) : sq.nk - 1;
     const int first_key = a.window > 0 && at_key >= a.window ? at_key - a.window + 1 : 0;
-    float m2 = kNone, l = 0.f;
+    float m = kNone, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
+    bool large = false;      // of the warp: some row's logits are large (see below)
     bool ok = true;
     const Masked masked_t = masked_of(first, rows);
     const int n_tiles = rt[t].hi - rt[t].lo;
@@ -464,11 +491,12 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
 #pragma unroll
         for (int k = 2; k < 32; k += 2) top[c] = max3(top[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
       }
-      const float top2 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
-      if (__any_sync(0xffffffffu, top2 > m2 + kLag)) {
-        const float m1 = fmaxf(m2, top2), f = ex2(m2 - m1);
-        m2 = m1;
+      const float top1 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      if (__any_sync(0xffffffffu, (top1 - m) * scale2 > kLag)) {
+        const float m1 = fmaxf(m, top1), f = ex2((m - m1) * scale2);
+        m = m1;
         l *= f;
+        large = __any_sync(0xffffffffu, m > kNone && fabsf(m * scale2) > 65536.f);
         if (n > 0) {  // the products of the tiles before have finished: S was issued after them
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -482,7 +510,17 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
         }
       }
       const uint64_t scale_2 = pair_of(__float_as_uint(scale2), __float_as_uint(scale2));
-      const uint64_t minus_m = pair_of(__float_as_uint(-m2), __float_as_uint(-m2));
+      // scale s - scale m in one rounding; where the logits are so large that
+      // the rounding of scale m shows, s - m first
+      float offset = -m * scale2;
+      if (large) {
+        offset = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - m);
+      }
+      const uint64_t minus_m = pair_of(__float_as_uint(offset), __float_as_uint(offset));
       uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -514,15 +552,15 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
     if (ok && rows > 0) {
       // the masked tiles were cleaned before their products, so n_odd is final
       const int64_t row = (sq.q0 + i) * a.n_heads + head;
-      if (a.sink) {
-        const float s2 = __ldg(a.sink + head) * kLog2e, m1 = fmaxf(m2, s2), f = ex2(m2 - m1);
-        l = l * f + ex2(s2 - m1);
-        const float inv = l == 0.f ? 0.f : f / l;
-        if (a.lse && r < rows) a.lse[row] = l == 0.f ? -INFINITY : (m1 + log2f(l)) * kLn2;
-        l = inv;
+      const bool shared = C::kCluster && cluster > 1;
+      if (shared) {  // the sums as they are
+        m_s[r] = m * scale2;
+        l_s[r] = l;
+        l = 1.f;
       } else {
-        if (a.lse && r < rows) a.lse[row] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
-        l = l == 0.f ? 0.f : 1.f / l;
+        float lse;
+        l = finish_row(m * scale2, l, a.sink, head, &lse);
+        if (a.lse && r < rows) a.lse[row] = lse;
       }
       const bool odd = *const_cast<volatile int*>(&n_odd) != 0;
 #pragma unroll
@@ -554,6 +592,13 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
             }
           }
         }
+        if (shared) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4*>(ring + r * D * 4 + (((8 * c + k) ^ (r & (D / 4 - 1))) << 4)) =
+                make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          continue;
+        }
         uint8_t* line = q_s + t * C::kTileBytes + (c >> 1) * C::kBlockBytes + r * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -572,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
       constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
       const int w0 = (warp & 3) * 32;
 #pragma unroll 4
-      for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
+      for (int k = 0; k < (shared ? 0 : 32 / kRowsAtOnce); ++k) {
         const int rr = w0 + k * kRowsAtOnce + lane / kChunks, ch = lane % kChunks;
         const uint4 v = *reinterpret_cast<const uint4*>(q_s + t * C::kTileBytes + (ch >> 3) * C::kBlockBytes + rr * 128 +
                                                         (((ch & 7) ^ (rr & 7)) << 4));
@@ -586,6 +631,41 @@ __global__ void __launch_bounds__(Cfg<D, QT>::kThreads, Cfg<D, QT>::kCtas)
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
+  }
+  if constexpr (C::kCluster) {
+    if (cluster > 1) {
+      // every CTA adds up its share of the rows over the cluster, a row (of
+      // 64 channels two) a warp at a time, 4 channels a lane
+      cluster_sync();
+      constexpr int kLanes = D / 4, kRowsAtOnce = 32 / kLanes;
+      const int share = kTile / cluster, rows = min(kTile, sq.nq - row0);
+#pragma unroll 2
+      for (int k = warp * kRowsAtOnce + lane / kLanes; k < share; k += C::kThreads / 32 * kRowsAtOnce) {
+        const int r = rank * share + k, ch = lane % kLanes;
+        if (r >= rows) continue;
+        float m = kNone, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < cluster; ++p) {  // (few: the maximum is taken along)
+          const float mp = dsmem_ld_f32(dsmem_addr(m_s + r, p)), lp = dsmem_ld_f32(dsmem_addr(l_s + r, p));
+          const float4 v = dsmem_ld_f32x4(dsmem_addr(ring + r * D * 4 + ((ch ^ (r & (D / 4 - 1))) << 4), p));
+          const float m1 = fmaxf(m, mp), f = ex2(m - m1), fp = ex2(mp - m1);
+          m = m1;
+          l = l * f + lp * fp;
+          o.x = o.x * f + v.x * fp;
+          o.y = o.y * f + v.y * fp;
+          o.z = o.z * f + v.z * fp;
+          o.w = o.w * f + v.w * fp;
+        }
+        const int64_t row = (sq.q0 + row0 + r) * a.n_heads + head;
+        float lse;
+        const float f = finish_row(m, l, a.sink, head, &lse);
+        if (a.lse && ch == 0) a.lse[row] = lse;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f, o.y * f), hi = __floats2bfloat162_rn(o.z * f, o.w * f);
+        *reinterpret_cast<uint2*>(a.out + row * D + 4 * ch) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+      cluster_sync();  // a CTA's shared memory outlives its readers
+    }
   }
 }
 
@@ -602,49 +682,62 @@ bool encode_rows(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 encode, const
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int QT>
-cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
-  using C = Cfg<D, QT>;
+template <int D, int QT, int CTAS>
+cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int cluster,
+                       cudaStream_t stream) {
+  using C = Cfg<D, QT, CTAS>;
+  const auto kernel = prompt_attn_kernel<D, QT, CTAS>;
   CUtensorMap tm_q, tm_k, tm_v;
   const int64_t n_k = a.n_k > 0 ? a.n_k : 1;  // (no keys: the maps are not read)
   if (!encode || !encode_rows(&tm_q, encode, a.q, D, a.n_heads, a.n_q, a.q_stride, a.q_stride_h) ||
       !encode_rows(&tm_k, encode, a.n_k > 0 ? a.k : a.q, D, a.n_kv_heads, n_k, a.k_stride, a.k_stride_h) ||
       !encode_rows(&tm_v, encode, a.n_k > 0 ? a.v : a.q, D, a.n_kv_heads, n_k, a.v_stride, a.v_stride_h))
     return cudaErrorInvalidValue;
-  cudaError_t e =
-      cudaFuncSetAttribute(prompt_attn_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   if (C::kSplit) {  // the split of registers assumes what the kernel is launched with
     cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, prompt_attn_kernel<D, QT>);
+    e = cudaFuncGetAttributes(&at, kernel);
     if (e != cudaSuccess) return e;
     if (at.numRegs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
   }
   // n rows are at most n / R + 1 tiles of R rows, and at most n
   const int64_t most = a.n_q / (QT * kTile) + a.B;
-  const int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads;
+  const int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads * cluster;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(prompt_attn_kernel<D, QT>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream,
-                    tm_q, tm_k, tm_v, a);
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream,
+                            static_cast<unsigned>(cluster), tm_q, tm_k, tm_v, a, cluster);
+}
+
+template <int D>
+cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t most = a.n_q / kTile + a.B, tiles = (most < a.n_q ? most : a.n_q) * a.n_heads;
+  if (tiles <= sms) {
+    // Few tiles, an SM each; a cluster shares out the keys of a tile while
+    // SMs are left and a CTA has two tiles of keys at least.
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster * 2 <= sms && a.n_k >= static_cast<int64_t>(a.B) * 4 * cluster * kTile)
+      cluster *= 2;
+    return launch_dim<D, 1, 1>(a, encode, cluster, stream);
+  }
+  // Two tiles a CTA share the keys' copies and overlap one's softmax with the
+  // other's products; where sequences are short two CTAs of one tile on an SM
+  // overlap their starts and ends instead.  Width 128, 32 heads: 16384 queries
+  // 1.42 ms with two tiles, 1.54 ms with one; 32 prompts of 500 189 and 194
+  // us; 64 of 128 126 and 79 us.  At width 64 one tile was never slower (16
+  // packed prompts, window 1024: 350 us with two, 305 us with one).
+  if (D == 64 || a.n_q <= static_cast<int64_t>(256) * a.B) return launch_dim<D, 1, 2>(a, encode, 1, stream);
+  return launch_dim<D, D == 64 ? 1 : 2, D == 64 ? 2 : 1>(a, encode, 1, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
   if (a.B <= 0 || a.n_q <= 0) return cudaSuccess;
-  // Width 128: two tiles a CTA share the keys' copies and overlap one's softmax
-  // with the other's products; where sequences are short, or tiles few, two
-  // CTAs of one tile on an SM overlap their starts and ends instead.  Measured
-  // with 32 heads: 16384 queries 1.42 ms with two tiles, 1.54 ms with one; 32
-  // prompts of 500 189 and 194 us; 64 of 128 126 and 83 us; one of 200 16.4
-  // and 15.3 us.  At width 64 one tile was never slower (16 packed prompts,
-  // window 1024: 350 us with two, 305 us with one).
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const bool one = a.n_q <= static_cast<int64_t>(256) * a.B || (a.n_q / kTile + a.B) * a.n_heads <= sms;
-  if (a.head_dim == 128) return one ? launch_dim<128, 1>(a, encode, stream) : launch_dim<128, 2>(a, encode, stream);
-  return launch_dim<64, 1>(a, encode, stream);
+  return a.head_dim == 128 ? launch_tiles<128>(a, encode, stream) : launch_tiles<64>(a, encode, stream);
 }
 
 }  // namespace csa

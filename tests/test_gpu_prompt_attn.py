@@ -85,6 +85,51 @@ def test_packed(csa, D, window, sink):
     assert csa.csa_check_status() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 1, 129, 300, 600])
+@pytest.mark.parametrize("lens", [
+    [(700, 700), (300, 900), (129, 40), (1, 300)],                        # more tiles than SMs, long sequences
+    [(130, 130), (0, 5), (33, 500), (3, 0), (200, 90), (1, 1), (100, 100), (1, 700)],  # ... short ones
+])
+def test_many_tiles(csa, D, window, lens):
+    """With 48 heads the tiles outnumber the SMs: two tiles a CTA, or two CTAs an SM."""
+    x = make(lens, 48, 2, D, seed=window, pad=9)
+    check(csa, x, "many tiles", heads=[0, 29, 47], window=window, sink=window % 2 == 0)
+    if window in (0, 300):  # a value that is not finite: seen or not as the formula has it
+        clean = run(csa, x, window=window)[0]
+        y = {k: v.clone() for k, v in x.items()}
+        key = lens[0][1] - 60
+        y["v"][key, 1, 7] = float("nan")
+        y["v"][sum(b for _, b in lens):] = float("nan")
+        out = run(csa, y, window=window)[0]
+        n = lens[0][0]
+        pos = torch.arange(n) + lens[0][1] - n
+        rows = ((pos >= key) & (pos < key + (window or 10 ** 6))).nonzero()[:, 0].to(DEV)
+        clean[rows, 24:, 7] = float("nan")
+        assert torch.equal(out.isnan(), clean.isnan())
+        assert torch.equal(out[~out.isnan()], clean[~clean.isnan()])
+    assert csa.csa_check_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sink", [(0, True), (0, False), (700, True)])
+@pytest.mark.parametrize("lens", [[(1, 2300)], [(130, 2300)], [(200, 1100)], [(128, 600)], [(64, 3100), (70, 2900)],
+                                  [(3, 4000), (2, 9)]])
+def test_few_queries_over_many_keys(csa, D, window, sink, lens):
+    """Few tiles: a cluster of two, four or eight CTAs shares out a tile's keys."""
+    x = make(lens, 3, 1, D, seed=len(lens) + window)
+    check(csa, x, "cluster", window=window, sink=sink)
+    clean = run(csa, x, window=window)[0]
+    y = {k: v.clone() for k, v in x.items()}
+    key = lens[0][1] - lens[0][0] // 2 - 1
+    y["v"][key, 0, 3] = float("inf")
+    out = run(csa, y, window=window)[0]
+    pos = torch.arange(lens[0][0]) + lens[0][1] - lens[0][0]
+    clean[((pos >= key) & (pos < key + (window or 10 ** 6))).nonzero()[:, 0].to(DEV), :, 3] = float("inf")
+    assert torch.equal(out, clean)
+    assert csa.csa_check_status() == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (6, 1), (8, 2), (28, 4)])
 def test_groups(csa, Hq, Hkv):
     x = make([(140, 140), (60, 300)], Hq, Hkv, 128, seed=Hq)
@@ -100,7 +145,8 @@ def test_not_causal(csa):
 def test_many_short_sequences(csa):
     g = torch.Generator().manual_seed(1)
     lens = [(int(n), int(n)) for n in torch.randint(0, 9, (900,), generator=g)]
-    check(csa, make(lens, 1, 1, 64, seed=4), "short")
+    for D in (64, 128):
+        check(csa, make(lens, 1, 1, D, seed=4), "short")
     assert csa.csa_check_status() == 0
 
 
@@ -190,6 +236,22 @@ def test_large_logits_and_equal_rows(csa):
     check(csa, x, "equal")
 
 
+def test_logits_beyond_what_fp32_resolves(csa):
+    """Logits of 2^50 and more: the weights are those of the row's largest key alone, whose values the row returns."""
+    T = 300
+    x = make([(T, T)], 2, 1, 64, seed=12)
+    x["q"][:, 0] *= 2.0 ** 50
+    out, lse = run(csa, x)
+    q, k, v = (x[n].double().cpu() for n in "qkv")
+    logits = (q[:, 0] @ k[:, 0].T).masked_fill_(torch.ones(T, T).triu(1).bool(), float("-inf"))
+    best, second = logits.topk(2, dim=1).values[1:].T
+    assert ((best - second) > 2.0 ** 30).all()  # (a tie would be shared)
+    assert torch.equal(out[:, 0].cpu(), x["v"][:, 0].cpu()[logits.argmax(1)])
+    assert ((lse[:, 0].cpu().double() - logits.max(1).values / 8).abs() <= 2.0 ** -16 * logits.max(1).values.abs()).all()
+    w = want(x, heads=[1])
+    ref.check_attention(out[:, 1:], lse[:, 1:], *w, STEP, "the other head")
+
+
 def test_layouts_streams_and_graphs(csa):
     """A fused projection's views, heads outermost, another stream, a replayed graph: the same bits."""
     T, Hq, Hkv, D = 333, 8, 2, 128
@@ -232,16 +294,18 @@ def test_bad_offsets(csa):
 
 def test_a_wait_that_runs_out(csa):
     """The products never announce the first scores: the call ends, reports the timeout, and the next one is right."""
-    x = make([(500, 500)], 4, 2, 128, seed=10)
-    good = run(csa, x)[0]
-    csa.csa_test_set_wait_fault(200, csa.CSA_TEST_FAULT_ATTN)
-    try:
-        run(csa, x)
-        assert csa.csa_check_status() == 4
-    finally:
-        csa.csa_test_set_wait_fault(0, 0)
-    assert torch.equal(run(csa, x)[0], good)
-    assert csa.csa_check_status() == 0
+    for D, Hq, lens in ((128, 4, [(500, 500)]), (128, 48, [(700, 700)]), (64, 48, [(700, 700)]), (64, 2, [(20, 3000)]),
+                        (128, 48, [(100, 100)] * 8)):
+        x = make(lens, Hq, 2, D, seed=10)
+        good = run(csa, x)[0]
+        csa.csa_test_set_wait_fault(200, csa.CSA_TEST_FAULT_ATTN)
+        try:
+            run(csa, x)
+            assert csa.csa_check_status() == 4
+        finally:
+            csa.csa_test_set_wait_fault(0, 0)
+        assert torch.equal(run(csa, x)[0], good)
+        assert csa.csa_check_status() == 0
 
 
 def test_refusals(csa):
