@@ -50,7 +50,8 @@ struct Cfg {
   static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
   static constexpr int kBlockBytes = kTile * 128;
   static constexpr int kStages = CTAS == 2 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
-  static constexpr int kSmem = QT * kTileBytes + kStages * kTileBytes + 1024;
+  static constexpr int kQBufs = CTAS == 2 && D == 64 ? 2 : 1;     // of the queries: the next tile's, where there is room
+  static constexpr int kSmem = (kQBufs * QT + kStages) * kTileBytes + 1024;
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
   static constexpr int kCols = QT == 2 ? 512 : 256;
@@ -116,9 +117,14 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
   return w;
 }
 
-// The tiles of keys [lo, hi) that `rows` queries from row `first` on see.
+// Tiles of keys [lo, hi).
 struct Range {
   int lo, hi;
+};
+// Tiles of keys that some row masks a part of: those from `from` on, and those up to `upto`.
+struct Masked {
+  int from, upto;
+  __device__ __forceinline__ bool at(int j) const { return j >= from || j <= upto; }
 };
 
 // From a row's reference (in log2) and sum of weights to the factor of its
@@ -136,34 +142,148 @@ __device__ __forceinline__ float finish_row(float m, float l, const float* sink,
 }
 
 struct Seq {
-  int64_t q0, k0;  // first rows of the sequence
+  int q0, k0;  // first rows of the sequence
   int nq, nk;
+};
+
+// A CTA's tiles of one head: queries row0 .. of a sequence.
+struct Work {
+  Seq sq;
+  int row0, head, shift;  // row i sits at position i + shift among the keys
+
+  __device__ __forceinline__ int rows(int t) const { return max(0, min(kTile, sq.nq - row0 - t * kTile)); }
+  // the tiles of keys that rows [first, first + n) see (lengths are below 2^30 each: no overflow)
+  __device__ __forceinline__ Range range(const PromptAttnArgs& a, int first, int n) const {
+    const int pos = first + shift;
+    const int hi = a.causal ? min(sq.nk, pos + n) : sq.nk;
+    const int lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+    const bool none = n <= 0 || hi <= lo;
+    Range r;
+    r.lo = none ? 0 : lo >> kTileShift;
+    r.hi = none ? 0 : (hi + kTile - 1) >> kTileShift;
+    return r;
+  }
+  __device__ __forceinline__ Masked masked(const PromptAttnArgs& a, int first, int n) const {
+    Masked m;
+    m.from = sq.nk >> kTileShift;   // the sequence ends inside the tile (or before it)
+    const int pos = first + shift;  // the first row's last key
+    if (a.causal) m.from = min(m.from, pos < 0 ? 0 : (pos + 1) >> kTileShift);
+    const int last = pos + n - 1;  // the last row's last key: keys up to last - window are outside its window
+    m.upto = a.window > 0 && last >= a.window ? (last - a.window) >> kTileShift : -1;
+    return m;
+  }
+};
+
+// The ranges of a CTA's tiles and their union, walked downwards: iteration it
+// works on tile j_hi - 1 - it of the keys.  (With a window neighbouring
+// tiles' ranges meet, so every iteration has a tile that works.)
+template <int QT>
+struct Walk {
+  Range rt[QT];
+  int j_hi, n_it;
+
+  __device__ __forceinline__ Walk(const PromptAttnArgs& a, const Work& w, int rank, int cluster) {
+    int j_lo = 0x7fffffff;
+    j_hi = 0;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      rt[t] = w.range(a, w.row0 + t * kTile, w.rows(t));
+      if (cluster > 1) {  // this CTA's part of the keys
+        const int per = (rt[t].hi - rt[t].lo + cluster - 1) / cluster, hi = rt[t].hi - rank * per;
+        rt[t].lo = max(rt[t].lo, hi - per);
+        rt[t].hi = hi;
+        if (hi <= rt[t].lo) rt[t].lo = rt[t].hi = 0;
+      }
+      if (rt[t].lo < rt[t].hi) {
+        j_lo = min(j_lo, rt[t].lo);
+        j_hi = max(j_hi, rt[t].hi);
+      }
+    }
+    n_it = j_hi > 0 ? j_hi - j_lo : 0;
+  }
+  // iterations [begin, end) of tile t
+  __device__ __forceinline__ int begin(int t) const { return rt[t].lo < rt[t].hi ? j_hi - rt[t].hi : 0; }
+  __device__ __forceinline__ int end(int t) const { return rt[t].lo < rt[t].hi ? j_hi - rt[t].lo : 0; }
+};
+
+// Walks a CTA's share of the work: items (tiles of ROWS queries of a sequence,
+// the later ones first: under the causal mask they see more keys) times
+// heads.  CTA c of G takes c, 2G - 1 - c, 2G + c, ...: forward and backward in
+// turn, so that no CTA gets the longer one of every G.  Each warp walks by
+// itself; the places grow, so it never looks back.
+template <int ROWS>
+struct Walker {
+  int b0 = 0, base = 0, round = 0;  // sequences before b0 hold `base` items
+
+  __device__ __forceinline__ bool next(const PromptAttnArgs& a, int cta, int ctas, Work* w) {
+    const int place = round * ctas + ((round & 1) ? ctas - 1 - cta : cta);
+    ++round;
+    return at(a, place, w);
+  }
+  __device__ __forceinline__ bool at(const PromptAttnArgs& a, int place, Work* w) {
+    const int item = place / a.n_heads, lane = threadIdx.x & 31;
+    w->head = place - item * a.n_heads;
+    for (; b0 < a.B; b0 += 32) {
+      Seq s = {0, 0, 0, 0};
+      if (b0 + lane < a.B) {
+        const int32_t q0 = __ldg(a.cu_q + b0 + lane), q1 = __ldg(a.cu_q + b0 + lane + 1);
+        const int32_t k0 = __ldg(a.cu_k + b0 + lane), k1 = __ldg(a.cu_k + b0 + lane + 1);
+        if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k)
+          s = {q0, k0, q1 - q0, k1 - k0};
+        else
+          record_error(a.status, kErrIndexRange);
+      }
+      const int n = (s.nq + ROWS - 1) / ROWS;
+      int x = n;
+      if (a.B - b0 > 1) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, off);
+          if (lane >= off) x += y;
+        }
+      }
+      const int all = __shfl_sync(0xffffffffu, x, a.B - b0 > 1 ? 31 : 0);
+      if (item < base + all) {
+        const int from = __ffs(__ballot_sync(0xffffffffu, base + x > item)) - 1;
+        w->sq.q0 = __shfl_sync(0xffffffffu, s.q0, from);
+        w->sq.k0 = __shfl_sync(0xffffffffu, s.k0, from);
+        w->sq.nq = __shfl_sync(0xffffffffu, s.nq, from);
+        w->sq.nk = __shfl_sync(0xffffffffu, s.nk, from);
+        w->row0 = (base + __shfl_sync(0xffffffffu, x, from) - 1 - item) * ROWS;
+        w->shift = w->sq.nk - w->sq.nq;
+        return true;
+      }
+      base += all;
+    }
+    return false;
+  }
 };
 
 template <int D, int QT, int CTAS>
 __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a, const int cluster) {
+                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a, const int cluster_size) {
   using C = Cfg<D, QT, CTAS>;
   constexpr int kTmaWarp = 4 * QT, kMmaWarp = 4 * QT + 1, kCleanWarp = 4 * QT + 2;
-  constexpr int kRowsCta = QT * kTile;
+  constexpr int kRowsCta = QT * kTile, kQBufs = C::kQBufs;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int sh[C::kThreads / 32 + 2];
-  __shared__ uint64_t q_full, full[C::kStages], empty[C::kStages];
+  __shared__ uint64_t q_full[kQBufs][QT], q_empty[kQBufs][QT], full[C::kStages], empty[C::kStages];
   __shared__ uint64_t s_full[QT], p_full[QT], o_full[QT], dirty, cleaned, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
-  __shared__ uint32_t odd_rows[kMaxMasked][4];  // keys of each masked tile whose values are not all finite
-  __shared__ int odd_tile[kMaxMasked], n_odd;
+  // keys of each masked tile whose values are not all finite, as each of the
+  // two cleaning warps found them, of a work item and the next: those of item
+  // number n are valid if odd_item[n & 1] is n + 1
+  __shared__ uint32_t odd_rows[2][2][kMaxMasked][4];
+  __shared__ int odd_tile[2][kMaxMasked], odd_item[2][2];
   __shared__ float m_s[C::kCluster ? kTile : 1], l_s[C::kCluster ? kTile : 1];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* q_s = smem;
-  uint8_t* ring = smem + QT * C::kTileBytes;
+  uint8_t* q_bufs = smem;
+  uint8_t* ring = smem + kQBufs * QT * C::kTileBytes;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* abort_flag = &abort_s;
   if (tid == 0) {
-    mbar_init(&q_full, 1);
     mbar_init(&drain, 1);
     mbar_init(&dirty, 1);
     mbar_init(&cleaned, kCleanThreads);
@@ -172,15 +292,18 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       mbar_init(empty + i, 1);
     }
     for (int t = 0; t < QT; ++t) {
+      for (int q = 0; q < kQBufs; ++q) {
+        mbar_init(&q_full[q][t], 1);
+        mbar_init(&q_empty[q][t], kTile);
+      }
       mbar_init(s_full + t, 1);
       mbar_init(p_full + t, kTile);
       mbar_init(o_full + t, 1);
     }
     fence_mbar_init();
     abort_s = 0;
-    n_odd = 0;
+    odd_item[0][0] = odd_item[0][1] = odd_item[1][0] = odd_item[1][1] = 0;
   }
-  if (tid < kMaxMasked * 4) odd_rows[tid >> 2][tid & 3] = 0u;
   if (warp == kTmaWarp && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
@@ -192,113 +315,68 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   pdl_wait();
   if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
   tc_fence_before();
-
-  // this CTA's sequence and tiles: the later tiles of a sequence (more keys
-  // under the causal mask) first
-  // (a cluster's CTAs: the same tile, each a part of its keys)
-  const int unit = C::kCluster ? static_cast<int>(blockIdx.x) / cluster : static_cast<int>(blockIdx.x);
-  const int rank = C::kCluster ? static_cast<int>(blockIdx.x) - unit * cluster : 0;
-  const int head = unit % a.n_heads;
-  const int kv_head = head / (a.n_heads / a.n_kv_heads);
-  auto seq_at = [&](int b) {
-    Seq s;
-    const int32_t q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
-    const int32_t k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
-    if (!ok) record_error(a.status, kErrIndexRange);
-    s.q0 = q0;
-    s.k0 = k0;
-    s.nq = ok ? q1 - q0 : 0;
-    s.nk = ok ? k1 - k0 : 0;
-    return s;
-  };
-  int index;
-  const int b = find_item<C::kThreads>(
-      a.B, unit / a.n_heads, [&](int s) { return (seq_at(s).nq + kRowsCta - 1) / kRowsCta; },
-      sh, &index);
-  // (the search's barriers also order the allocation and the mbarriers' set-up)
+  __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = tmem_slot;
-  if (b < 0) {
-    if (warp == kMmaWarp) tmem_dealloc(tmem, C::kCols);
-    return;
-  }
-  const Seq sq = seq_at(b);
-  const int row0 = ((sq.nq + kRowsCta - 1) / kRowsCta - 1 - index) * kRowsCta;
-  const int shift = sq.nk - sq.nq;  // row i sits at position i + shift among the keys
 
-  // tiles of keys that rows [first, first + rows) see
-  auto range_of = [&](int first, int rows) {
-    const int pos = first + shift;  // (lengths are below 2^30 each: no overflow)
-    const int hi = a.causal ? min(sq.nk, pos + rows) : sq.nk;
-    const int lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-    Range r;
-    const bool none = rows <= 0 || hi <= lo;
-    r.lo = none ? 0 : lo >> kTileShift;
-    r.hi = none ? 0 : (hi + kTile - 1) >> kTileShift;
-    return r;
+  // A cluster's CTAs work on one item, each on a part of its keys; other CTAs
+  // walk through their share of the items.
+  const int cluster = C::kCluster ? cluster_size : 1;
+  const int cta = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) - cta * cluster;
+  const int ctas = C::kCluster ? 0x40000000 : static_cast<int>(gridDim.x);
+  auto more = [&](Walker<kRowsCta>& walker, Work* w) {
+    if (C::kCluster) return walker.round++ == 0 && walker.at(a, cta, w);
+    return walker.next(a, cta, ctas, w);
   };
-  // some of those rows masks a part of tile j: j >= from or j <= upto
-  struct Masked {
-    int from, upto;
-    __device__ __forceinline__ bool at(int j) const { return j >= from || j <= upto; }
-  };
-  auto masked_of = [&](int first, int rows) {
-    Masked m;
-    m.from = sq.nk >> kTileShift;  // the sequence ends inside the tile (or before it)
-    const int pos = first + shift;  // the first row's last key
-    if (a.causal) m.from = min(m.from, pos < 0 ? 0 : (pos + 1) >> kTileShift);
-    const int out = pos + rows - 1;  // the last row's last key: keys up to out - window are outside its window
-    m.upto = a.window > 0 && out >= a.window ? (out - a.window) >> kTileShift : -1;
-    return m;
-  };
-  auto rows_of = [&](int t) { return max(0, min(kTile, sq.nq - row0 - t * kTile)); };
-  const int rows_cta = min(kRowsCta, sq.nq - row0);
-  Range rt[QT];
-  int j_lo = 0x7fffffff, j_hi = 0;
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    rt[t] = range_of(row0 + t * kTile, rows_of(t));
-    if (C::kCluster && cluster > 1) {
-      const int per = (rt[t].hi - rt[t].lo + cluster - 1) / cluster, hi = rt[t].hi - rank * per;
-      rt[t].lo = max(rt[t].lo, hi - per);
-      rt[t].hi = hi;
-      if (hi <= rt[t].lo) rt[t].lo = rt[t].hi = 0;
-    }
-    if (rt[t].lo < rt[t].hi) {
-      j_lo = min(j_lo, rt[t].lo);
-      j_hi = max(j_hi, rt[t].hi);
-    }
-  }
-  const Masked masked = masked_of(row0, rows_cta);
-  const int n_it = j_hi > 0 ? j_hi - j_lo : 0;  // iteration it works on tile j_hi - 1 - it
+  Walker<kRowsCta> walker;
+  Work w;
 
   if (warp >= 4 * QT) {
     if constexpr (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == kTmaWarp) {
       // ---------------- loads ----------------
-      if (lane == 0 && n_it > 0) {
-        mbar_arrive_expect_tx(&q_full, QT * C::kTileBytes);
-        for (int t = 0; t < QT; ++t)
-          for (int k = 0; k < C::kBlocks; ++k)
-            tma_load_3d(q_s + t * C::kTileBytes + k * C::kBlockBytes, &tm_q, k * 64, head,
-                        static_cast<int32_t>(sq.q0 + row0 + t * kTile), &q_full);
-        int issued = 0;
-        for (int s = 0; s < 2 * n_it; ++s) {
-          const int slot = s % C::kStages;
-          if (s >= C::kStages && !wait_or_abort(empty + slot, ((s / C::kStages) - 1) & 1, abort_flag, a.status)) break;
-          mbar_arrive_expect_tx(full + slot, C::kTileBytes);
-          const int row = static_cast<int>(sq.k0) + (j_hi - 1 - (s >> 1)) * kTile;
-          for (int k = 0; k < C::kBlocks; ++k)
-            tma_load_3d(ring + slot * C::kTileBytes + k * C::kBlockBytes, (s & 1) ? &tm_v : &tm_k, k * 64, kv_head, row,
-                        full + slot);
-          ++issued;
+      int seq = 0, n_q[QT] = {};  // ring slots and query tiles filled so far
+      bool ok = true;
+      for (int item = 0; ok && more(walker, &w); ++item) {
+        const Walk<QT> walk(a, w, rank, cluster);
+        if (lane == 0) {
+          const int kv_head = w.head / (a.n_heads / a.n_kv_heads);
+          auto load = [&](int s) {
+            const int slot = seq & (C::kStages - 1);
+            if (seq >= C::kStages) ok = wait_or_abort(empty + slot, ((seq / C::kStages) - 1) & 1, abort_flag, a.status);
+            if (!ok) return;
+            mbar_arrive_expect_tx(full + slot, C::kTileBytes);
+            const int row = w.sq.k0 + (walk.j_hi - 1 - (s >> 1)) * kTile;
+            for (int k = 0; k < C::kBlocks; ++k)
+              tma_load_3d(ring + slot * C::kTileBytes + k * C::kBlockBytes, (s & 1) ? &tm_v : &tm_k, k * 64, kv_head,
+                          row, full + slot);
+            ++seq;
+          };
+          // the first keys and values before the queries, whose place may
+          // still hold the item before's output
+          int s = 0;
+          for (; ok && s < min(2, 2 * walk.n_it); ++s) load(s);
+          const int buf = item % kQBufs, use = item / kQBufs;
+          for (int t = 0; ok && t < QT; ++t) {
+            if (use > 0) ok = wait_or_abort(&q_empty[buf][t], (use - 1) & 1, abort_flag, a.status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[buf][t], C::kTileBytes);
+            for (int k = 0; k < C::kBlocks; ++k)
+              tma_load_3d(q_bufs + (buf * QT + t) * C::kTileBytes + k * C::kBlockBytes, &tm_q, k * 64, w.head,
+                          w.sq.q0 + w.row0 + t * kTile, &q_full[buf][t]);
+            ++n_q[t];
+          }
+          for (; ok && s < 2 * walk.n_it; ++s) load(s);
         }
-        // every copy lands before the CTA ends (also after an abort)
-        mbar_wait(&q_full, 0, a.status);
-        for (int s = issued > C::kStages ? issued - C::kStages : 0; s < issued; ++s)
-          mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, a.status);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0) {  // every copy lands before the CTA ends (also after an abort)
+        for (int t = 0; t < QT; ++t)
+          for (int k = max(0, n_q[t] - kQBufs); k < n_q[t]; ++k)
+            mbar_wait(&q_full[k % kQBufs][t], (k / kQBufs) & 1, a.status);
+        for (int k = max(0, seq - C::kStages); k < seq; ++k)
+          mbar_wait(full + (k & (C::kStages - 1)), (k / C::kStages) & 1, a.status);
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -310,78 +388,93 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 1, 1, 0, 0);  // bf16, K-major A and B
       constexpr uint32_t idesc_o = instr_desc(kTile, D, 1, 1, 0, 1);      // A from TMEM, B (= V) MN-major
       auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-      const int u_it = uniform(n_it), u_hi = uniform(j_hi);
-      int u_lo[QT], u_end[QT];          // iterations of tile t: [u_lo, u_end)
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        u_lo[t] = uniform(rt[t].lo < rt[t].hi ? j_hi - rt[t].hi : 0);
-        u_end[t] = uniform(rt[t].lo < rt[t].hi ? j_hi - rt[t].lo : 0);
-      }
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const int m_from = uniform(j_hi - masked.from), m_upto = uniform(j_hi - 1 - masked.upto);
-      auto masked_it = [&](int it) { return it < m_from || it >= m_upto; };
-      const uint32_t qb = smem_u32(q_s), rb = smem_u32(ring);
+      const uint32_t rb = smem_u32(ring);
       const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.status)) != 0;
       };
-      auto s_of = [&](int t, uint64_t k_desc) {  // S_t = Q_t K^T (one lane)
-        const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          constexpr int kStep = 32 >> 4;  // 16 channels along a 128-byte line, in the descriptors' units
-          const int off = (s >> 2) * (C::kBlockBytes >> 4) + (s & 3) * kStep;
-          mma_f16(tm + C::kSCol(t), q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
-        }
-        if (!skip_s) tc_commit(s_full + t);
+      auto wait_slot = [&](int seq) {
+        return wait(full + (seq & (C::kStages - 1)), (seq / C::kStages) & 1);
       };
-      bool ok = u_it == 0 || (wait(&q_full, 0) && wait(full, 0));
-      if (ok && u_it > 0) {  // the first tile of keys
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int t = 0; t < QT; ++t)
-            if (u_lo[t] == 0 && u_end[t] > 0) s_of(t, smem_desc(rb, 16, 1024, kSwizzle128B));
-          tc_commit(empty);
-        }
-        __syncwarp();
-      }
+      bool ok = true;
+      int seq0 = 0;               // ring slots of the items before
+      uint32_t n_p[QT] = {};      // weights taken so far, by tile
       uint32_t n_cleaned = 0;
-      for (int it = 0; it < u_it && ok; ++it) {
-        const int v_seq = 2 * it + 1, k_seq = 2 * it + 2;
-        const int v_slot = v_seq & (C::kStages - 1), k_slot = k_seq & (C::kStages - 1);
-        const uint64_t v_desc = smem_desc(rb + v_slot * C::kTileBytes, C::kBlockBytes, 1024, kSwizzle128B);
-        const uint64_t k_desc = smem_desc(rb + k_slot * C::kTileBytes, 16, 1024, kSwizzle128B);
-        const bool more = it + 1 < u_it;
-        // this tile's values and the next tile's keys are usually there long
-        // before the weights are
-        ok = wait(full + v_slot, (v_seq / C::kStages) & 1);
-        if (ok && masked_it(it)) {  // one masked tile at a time is with the cleaning warps
-          if (elect_one()) mbar_arrive(&dirty);
-          __syncwarp();
-          ok = wait(&cleaned, n_cleaned++ & 1u);
-        }
-        if (ok && more) ok = wait(full + k_slot, (k_seq / C::kStages) & 1);
+      for (int item = 0; ok && more(walker, &w); ++item) {
+        const Walk<QT> walk(a, w, rank, cluster);
+        const Masked masked = w.masked(a, w.row0, min(kRowsCta, w.sq.nq - w.row0));
+        const int n_it = uniform(walk.n_it);
+        int begin[QT], end[QT];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-          const bool pv = it >= u_lo[t] && it < u_end[t], next = more && it + 1 >= u_lo[t] && it + 1 < u_end[t];
-          if (ok && pv) ok = wait(p_full + t, (it - u_lo[t]) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            if (pv) {
-#pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (s * 2048 >> 4), idesc_o,
-                           (it > u_lo[t] || s > 0) ? 1u : 0u);
-              if (it + 1 == u_end[t]) tc_commit(o_full + t);
-            }
-            if (t == QT - 1) tc_commit(empty + v_slot);
-            if (next) s_of(t, k_desc);
-            if (t == QT - 1 && more) tc_commit(empty + k_slot);
-          }
-          __syncwarp();
+          begin[t] = uniform(walk.begin(t));
+          end[t] = uniform(walk.end(t));
         }
+        const int m_from = uniform(walk.j_hi - masked.from), m_upto = uniform(walk.j_hi - 1 - masked.upto);
+        const int buf = item % kQBufs;
+        const uint32_t qb = smem_u32(q_bufs + buf * QT * C::kTileBytes), q_par = (item / kQBufs) & 1;
+        auto s_of = [&](int t, uint64_t k_desc) {  // S_t = Q_t K^T (one lane)
+          const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            constexpr int kStep = 32 >> 4;  // 16 channels along a 128-byte line, in the descriptors' units
+            const int off = (s >> 2) * (C::kBlockBytes >> 4) + (s & 3) * kStep;
+            mma_f16(tm + C::kSCol(t), q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
+          }
+          if (!skip_s) tc_commit(s_full + t);
+        };
+        // the first tile of keys (the queries are waited for even without one:
+        // a phase that is not waited for could be taken for a later one)
+        if (n_it > 0) ok = wait_slot(seq0);
+        const uint64_t k_first = smem_desc(rb + (seq0 & (C::kStages - 1)) * C::kTileBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          if (ok) ok = wait(&q_full[buf][t], q_par);
+          if (ok && begin[t] == 0 && end[t] > 0) {
+            tc_fence_after();
+            if (elect_one()) s_of(t, k_first);
+            __syncwarp();
+          }
+        }
+        if (ok && n_it > 0 && elect_one()) tc_commit(empty + (seq0 & (C::kStages - 1)));
+        __syncwarp();
+        for (int it = 0; it < n_it && ok; ++it) {
+          const int v_seq = seq0 + 2 * it + 1, v_slot = v_seq & (C::kStages - 1), k_slot = (v_seq + 1) & (C::kStages - 1);
+          const uint64_t v_desc = smem_desc(rb + v_slot * C::kTileBytes, C::kBlockBytes, 1024, kSwizzle128B);
+          const uint64_t k_desc = smem_desc(rb + k_slot * C::kTileBytes, 16, 1024, kSwizzle128B);
+          const bool again = it + 1 < n_it;
+          // this tile's values and the next tile's keys are usually there long
+          // before the weights are
+          ok = wait_slot(v_seq);
+          if (ok && (it < m_from || it >= m_upto)) {  // one masked tile at a time is with the cleaning warps
+            if (elect_one()) mbar_arrive(&dirty);
+            __syncwarp();
+            ok = wait(&cleaned, n_cleaned++ & 1u);
+          }
+          if (ok && again) ok = wait_slot(v_seq + 1);
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            const bool pv = it >= begin[t] && it < end[t], next = again && it + 1 >= begin[t] && it + 1 < end[t];
+            if (ok && pv) ok = wait(p_full + t, n_p[t]++ & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              if (pv) {
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                  mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (s * 2048 >> 4), idesc_o,
+                             (it > begin[t] || s > 0) ? 1u : 0u);
+                if (it + 1 == end[t]) tc_commit(o_full + t);
+              }
+              if (t == QT - 1) tc_commit(empty + v_slot);
+              if (next) s_of(t, k_desc);
+              if (t == QT - 1 && again) tc_commit(empty + k_slot);
+            }
+            __syncwarp();
+          }
+        }
+        seq0 += 2 * n_it;
       }
       // whatever was issued finishes before TMEM and shared memory are released
       if (elect_one()) {
@@ -392,56 +485,73 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     } else {
       // ---------------- values that are not finite, taken out of masked tiles ----------------
       const int ct = tid - kCleanWarp * 32;
-      int n_masked = 0;
-      for (int it = 0; it < n_it; ++it) {
-        const int j = j_hi - 1 - it;
-        if (!masked.at(j)) continue;
-        const int seq = 2 * it + 1, slot = seq % C::kStages;
-        // the MMA thread has seen the tile's copy complete and holds its slot
-        // until `cleaned`, so the second wait returns at once (and makes the
-        // copied bytes visible here)
-        if (!wait_or_abort(&dirty, n_masked & 1, abort_flag, a.status) ||
-            !wait_or_abort(full + slot, (seq / C::kStages) & 1, abort_flag, a.status))
-          break;
-        uint4* tile = reinterpret_cast<uint4*>(ring + slot * C::kTileBytes);
-        // rows past the sequence become zero; of the others, eight 16-byte
-        // chunks at a time are looked at for an exponent of all ones (the
-        // swizzle moves chunks within their row only: chunk i is of row i/8 % 128)
-        const int past = min(sq.nk - j * kTile, kTile);
-        if (past < kTile)
-          for (int i = ct; i < (kTile - past) * 8 * C::kBlocks; i += kCleanThreads) {
-            const int block = i / ((kTile - past) * 8);
-            tile[block * kTile * 8 + past * 8 + i - block * (kTile - past) * 8] = make_uint4(0u, 0u, 0u, 0u);
+      int seq0 = 0;
+      uint32_t n_cleaned = 0;
+      bool ok = true;
+      for (int item = 0; ok && more(walker, &w); ++item) {
+        const Walk<QT> walk(a, w, rank, cluster);
+        const Masked masked = w.masked(a, w.row0, min(kRowsCta, w.sq.nq - w.row0));
+        const int o = item & 1, half = warp - kCleanWarp;
+        static_assert(kMaxMasked * 4 == 32, "a word a lane");
+        int n_masked = 0;
+        for (int it = 0; it < walk.n_it; ++it) {
+          const int j = walk.j_hi - 1 - it;
+          if (!masked.at(j)) continue;
+          const int seq = seq0 + 2 * it + 1, slot = seq & (C::kStages - 1);
+          // the product warp has seen the tile's copy complete and holds its slot
+          // until `cleaned`, so the second wait returns at once (and makes the
+          // copied bytes visible here)
+          ok = wait_or_abort(&dirty, n_cleaned & 1, abort_flag, a.status) &&
+               wait_or_abort(full + slot, (seq / C::kStages) & 1, abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          if (!ok) break;
+          if (n_masked == 0) {  // (the item before the last, whose places these were, is done with)
+            odd_rows[o][half][lane >> 2][lane & 3] = 0u;
+            __syncwarp();
           }
+          uint4* tile = reinterpret_cast<uint4*>(ring + slot * C::kTileBytes);
+          // rows past the sequence become zero; of the others, eight 16-byte
+          // chunks at a time are looked at for an exponent of all ones (the
+          // swizzle moves chunks within their row only: chunk i is of row i/8 % 128)
+          const int past = min(w.sq.nk - j * kTile, kTile);
+          if (past < kTile)
+            for (int i = ct; i < (kTile - past) * 8 * C::kBlocks; i += kCleanThreads) {
+              const int block = i / ((kTile - past) * 8);
+              tile[block * kTile * 8 + past * 8 + i - block * (kTile - past) * 8] = make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll 1
-        for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += 8 * kCleanThreads) {
-          uint4 u[8];
-          uint32_t any = 0u;
+          for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += 8 * kCleanThreads) {
+            uint4 u[8];
+            uint32_t any = 0u;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) u[k] = tile[i0 + k * kCleanThreads];
+            for (int k = 0; k < 8; ++k) u[k] = tile[i0 + k * kCleanThreads];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) any |= odd_halves(u[k].x) | odd_halves(u[k].y) | odd_halves(u[k].z) | odd_halves(u[k].w);
-          if (any == 0u) continue;
+            for (int k = 0; k < 8; ++k)
+              any |= odd_halves(u[k].x) | odd_halves(u[k].y) | odd_halves(u[k].z) | odd_halves(u[k].w);
+            if (any == 0u) continue;
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
-            const int i = i0 + k * kCleanThreads, r = (i >> 3) & (kTile - 1);
-            uint4 w = tile[i];
-            if (r >= past || !(odd_halves(w.x) | odd_halves(w.y) | odd_halves(w.z) | odd_halves(w.w))) continue;
-            w.x = finite_halves(w.x);
-            w.y = finite_halves(w.y);
-            w.z = finite_halves(w.z);
-            w.w = finite_halves(w.w);
-            tile[i] = w;
-            if (n_masked < kMaxMasked) {
-              atomicOr(&odd_rows[n_masked][r >> 5], 1u << (r & 31));
-              odd_tile[n_masked] = j;
-              n_odd = 1;
+            for (int k = 0; k < 8; ++k) {
+              const int i = i0 + k * kCleanThreads, r = (i >> 3) & (kTile - 1);
+              uint4 v = tile[i];
+              if (r >= past || !(odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w))) continue;
+              v.x = finite_halves(v.x);
+              v.y = finite_halves(v.y);
+              v.z = finite_halves(v.z);
+              v.w = finite_halves(v.w);
+              tile[i] = v;
+              if (n_masked < kMaxMasked) {
+                atomicOr(&odd_rows[o][half][n_masked][r >> 5], 1u << (r & 31));
+                odd_tile[o][n_masked] = j;
+                odd_item[o][half] = item + 1;
+              }
             }
           }
+          ++n_masked;
+          ++n_cleaned;
+          fence_proxy_async_smem();
+          mbar_arrive(&cleaned);
         }
-        ++n_masked;
-        fence_proxy_async_smem();
-        mbar_arrive(&cleaned);
+        seq0 += 2 * walk.n_it;
       }
     }
   } else {
@@ -449,183 +559,204 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     if constexpr (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const int first = row0 + t * kTile, rows = rows_of(t);
-    const int i = first + r;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lane_base + C::kSCol(t), o_tmem = tmem + lane_base + C::kOCol(t);
     const float scale2 = a.sm_scale * kLog2e;
-    // the row's keys [first_key, last_key]
-    const int at_key = i + shift;
-    const int last_key = a.causal ? min(at_key, sq.nk - 1) : sq.nk - 1;
-    const int first_key = a.window > 0 && at_key >= a.window ? at_key - a.window + 1 : 0;
-    float m = kNone, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
-    bool large = false;      // of the warp: some row's logits are large (see below)
+    uint32_t n_s = 0, n_o = 0;  // tiles of scores and sums taken so far
     bool ok = true;
-    const Masked masked_t = masked_of(first, rows);
-    const int n_tiles = rt[t].hi - rt[t].lo;
-    for (int n = 0; n < n_tiles; ++n) {
-      const int j = rt[t].hi - 1 - n;
-      ok = wait_or_abort(s_full + t, n & 1, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
-      tmem_wait_ld();
-      if (masked_t.at(j)) {  // this row's keys among the tile's columns, as a bit each
-        const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int hi = max(0, min(32, c_hi - 32 * c)), lo = max(0, min(32, c_lo - 32 * c));
-          const uint32_t seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
-        }
+    for (int item = 0; ok && more(walker, &w); ++item) {
+      int n_tiles, j_top, last_key, first_key;
+      bool loaded;
+      Masked masked_t;
+      {
+        const Walk<QT> walk(a, w, rank, cluster);
+        const Range mine = QT == 1 || t == 0 ? walk.rt[0] : walk.rt[QT - 1];
+        n_tiles = mine.hi - mine.lo;
+        j_top = mine.hi - 1;
+        masked_t = w.masked(a, w.row0 + t * kTile, w.rows(t));
+        // the row's keys [first_key, last_key]
+        const int at_key = w.row0 + t * kTile + r + w.shift;
+        last_key = a.causal ? min(at_key, w.sq.nk - 1) : w.sq.nk - 1;
+        first_key = a.window > 0 && at_key >= a.window ? at_key - a.window + 1 : 0;
+        loaded = n_tiles > 0;
       }
-      float top[4];
+      float m = kNone, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
+      bool large = false;        // of the warp: some row's logits are large (see below)
+      for (int n = 0; n < n_tiles; ++n) {
+        const int j = j_top - n;
+        ok = wait_or_abort(s_full + t, n_s++ & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
+        tmem_wait_ld();
+        if (masked_t.at(j)) {  // this row's keys among the tile's columns, as a bit each
+          const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
 #pragma unroll
-        for (int k = 2; k < 32; k += 2) top[c] = max3(top[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
-      }
-      const float top1 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      if (__any_sync(0xffffffffu, (top1 - m) * scale2 > kLag)) {
-        const float m1 = fmaxf(m, top1), f = ex2((m - m1) * scale2);
-        m = m1;
-        l *= f;
-        large = __any_sync(0xffffffffu, m > kNone && fabsf(m * scale2) > 65536.f);
-        if (n > 0) {  // the products of the tiles before have finished: S was issued after them
+          for (int c = 0; c < 4; ++c) {
+            const int hi = max(0, min(32, c_hi - 32 * c)), lo = max(0, min(32, c_lo - 32 * c));
+            const uint32_t seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_tmem + 32 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(o_tmem + 32 * c, o);
+            for (int k = 0; k < 32; ++k)
+              if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
           }
         }
-      }
-      const uint64_t scale_2 = pair_of(__float_as_uint(scale2), __float_as_uint(scale2));
-      // scale s - scale m in one rounding; where the logits are so large that
-      // the rounding of scale m shows, s - m first
-      float offset = -m * scale2;
-      if (large) {
-        offset = 0.f;
+        float top[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - m);
-      }
-      const uint64_t minus_m = pair_of(__float_as_uint(offset), __float_as_uint(offset));
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x, y;
-          split(fma2(pair_of(s[c][2 * k], s[c][2 * k + 1]), scale_2, minus_m), &x, &y);
-          x = ex2(x);
-          y = ex2(y);
-          sum[k & 1] = add2(sum[k & 1], pair_of(__float_as_uint(x), __float_as_uint(y)));
-          const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-          p[k] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int k = 2; k < 32; k += 2) top[c] = max3(top[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
         }
-        tmem_st16(s_tmem + 16 * c, p);
-      }
-      float sx, sy;
-      split(add2(sum[0], sum[1]), &sx, &sy);
-      l += sx + sy;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full + t);
-    }
-    if (ok && n_it > 0) {  // (a tile that sees no keys: its queries have landed where its output is staged)
-      ok = wait_or_abort(n_tiles > 0 ? o_full + t : &q_full, 0, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (ok && rows > 0) {
-      // the masked tiles were cleaned before their products, so n_odd is final
-      const int64_t row = (sq.q0 + i) * a.n_heads + head;
-      const bool shared = C::kCluster && cluster > 1;
-      if (shared) {  // the sums as they are
-        m_s[r] = m * scale2;
-        l_s[r] = l;
-        l = 1.f;
-      } else {
-        float lse;
-        l = finish_row(m * scale2, l, a.sink, head, &lse);
-        if (a.lse && r < rows) a.lse[row] = lse;
-      }
-      const bool odd = *const_cast<volatile int*>(&n_odd) != 0;
+        const float top1 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (__any_sync(0xffffffffu, (top1 - m) * scale2 > kLag)) {
+          const float m1 = fmaxf(m, top1), f = ex2((m - m1) * scale2);
+          m = m1;
+          l *= f;
+          large = __any_sync(0xffffffffu, m > kNone && fabsf(m * scale2) > 65536.f);
+          if (n > 0) {  // the products of the tiles before have finished: S was issued after them
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (n_tiles > 0) {
-          tmem_ld32(o_tmem + 32 * c, o);
-          tmem_wait_ld();
-        } else {
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_tmem + 32 * c, o);
+              tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        // (a row without keys has l = 0 and sums of 0 * value, all finite)
-        float x[32];
-        const uint64_t l2 = pair_of(__float_as_uint(l), __float_as_uint(l));
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) split(mul2(pair_of(o[k], o[k + 1]), l2), &x[k], &x[k + 1]);
-        if (odd && r < rows) {
-          for (int e = 0; e < kMaxMasked * kTile; ++e) {
-            const uint32_t word = odd_rows[e >> 7][(e >> 5) & 3];
-            if (!((word >> (e & 31)) & 1u)) continue;
-            const int64_t key = static_cast<int64_t>(odd_tile[e >> 7]) * kTile + (e & (kTile - 1));
-            if (key > last_key || key < first_key) continue;
-            const uint16_t* v = a.v + (sq.k0 + key) * a.v_stride + kv_head * a.v_stride_h + 32 * c;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const uint32_t h = v[k];
-              if (not_finite(h)) x[k] += __uint_as_float(h << 16);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(o_tmem + 32 * c, o);
             }
           }
         }
-        if (shared) {
+        const uint64_t scale_2 = pair_of(__float_as_uint(scale2), __float_as_uint(scale2));
+        // scale s - scale m in one rounding; where the logits are so large that
+        // the rounding of scale m shows, s - m first
+        float offset = -m * scale2;
+        if (large) {
+          offset = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float4*>(ring + r * D * 4 + (((8 * c + k) ^ (r & (D / 4 - 1))) << 4)) =
-                make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-          continue;
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - m);
         }
-        uint8_t* line = q_s + t * C::kTileBytes + (c >> 1) * C::kBlockBytes + r * 128;
+        const uint64_t minus_m = pair_of(__float_as_uint(offset), __float_as_uint(offset));
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int k = 0; k < 16; ++k) {
+            float x, y;
+            split(fma2(pair_of(s[c][2 * k], s[c][2 * k + 1]), scale_2, minus_m), &x, &y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[k & 1] = add2(sum[k & 1], pair_of(__float_as_uint(x), __float_as_uint(y)));
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+            p[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + k) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          tmem_st16(s_tmem + 16 * c, p);
+        }
+        float sx, sy;
+        split(add2(sum[0], sum[1]), &sx, &sy);
+        l += sx + sy;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full + t);
+      }
+      uint8_t* q_s = q_bufs + ((item % kQBufs) * QT + t) * C::kTileBytes;
+      if (ok) {  // (a tile that sees no keys: its queries have landed where its output is staged)
+        ok = loaded ? wait_or_abort(o_full + t, n_o++ & 1, abort_flag, a.status)
+                    : wait_or_abort(&q_full[item % kQBufs][t], (item / kQBufs) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      const int rows = w.rows(t);
+      if (rows > 0) {
+        // (masked tiles were cleaned before their products, so odd_item is final)
+        const int64_t row = static_cast<int64_t>(w.sq.q0 + w.row0 + t * kTile + r) * a.n_heads + w.head;
+        const bool shared = C::kCluster && cluster > 1;
+        if (shared) {  // the sums as they are
+          m_s[r] = m * scale2;
+          l_s[r] = l;
+          l = 1.f;
+        } else {
+          float lse;
+          l = finish_row(m * scale2, l, a.sink, w.head, &lse);
+          if (a.lse && r < rows) a.lse[row] = lse;
+        }
+        const int o2 = item & 1;
+        const bool odd0 = *const_cast<volatile int*>(&odd_item[o2][0]) == item + 1;
+        const bool odd1 = *const_cast<volatile int*>(&odd_item[o2][1]) == item + 1;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n_tiles > 0) {
+            tmem_ld32(o_tmem + 32 * c, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          // (a row without keys has l = 0 and sums of 0 * value, all finite)
+          float x[32];
+          const uint64_t l2 = pair_of(__float_as_uint(l), __float_as_uint(l));
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) split(mul2(pair_of(o[k], o[k + 1]), l2), &x[k], &x[k + 1]);
+          if ((odd0 || odd1) && r < rows) {
+            const uint16_t* values =
+                a.v + w.sq.k0 * a.v_stride + w.head / (a.n_heads / a.n_kv_heads) * a.v_stride_h + 32 * c;
+            for (int e = 0; e < kMaxMasked * kTile; ++e) {
+              const uint32_t word = (odd0 ? odd_rows[o2][0][e >> 7][(e >> 5) & 3] : 0u) |
+                                    (odd1 ? odd_rows[o2][1][e >> 7][(e >> 5) & 3] : 0u);
+              if (!((word >> (e & 31)) & 1u)) continue;
+              const int key = odd_tile[o2][e >> 7] * kTile + (e & (kTile - 1));
+              if (key > last_key || key < first_key) continue;
+              const uint16_t* v = values + key * a.v_stride;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const uint32_t h = v[k];
+                if (not_finite(h)) x[k] += __uint_as_float(h << 16);
+              }
+            }
+          }
+          if (shared) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(ring + r * D * 4 + (((8 * c + k) ^ (r & (D / 4 - 1))) << 4)) =
+                  make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            continue;
+          }
+          uint8_t* line = q_s + (c >> 1) * C::kBlockBytes + r * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]);
+              v[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + k) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        // the warp's 32 rows, staged where its queries were (every product with
+        // them has finished), stored with neighbouring lanes on one row
+        __syncwarp();
+        constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
+        const int w0 = (warp & 3) * 32;
+        uint16_t* out = a.out + (static_cast<int64_t>(w.sq.q0 + w.row0 + t * kTile) * a.n_heads + w.head) * D;
+#pragma unroll 4
+        for (int k = 0; k < (shared ? 0 : 32 / kRowsAtOnce); ++k) {
+          const int rr = w0 + k * kRowsAtOnce + lane / kChunks, ch = lane % kChunks;
+          const uint4 v = *reinterpret_cast<const uint4*>(q_s + (ch >> 3) * C::kBlockBytes + rr * 128 +
+                                                          (((ch & 7) ^ (rr & 7)) << 4));
+          if (rr < rows) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(rr) * a.n_heads * D + ch * 8) = v;
         }
       }
-      // the warp's 32 rows, staged where its queries were (every product with
-      // them has finished), stored with neighbouring lanes on one row
-      __syncwarp();
-      constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
-      const int w0 = (warp & 3) * 32;
-#pragma unroll 4
-      for (int k = 0; k < (shared ? 0 : 32 / kRowsAtOnce); ++k) {
-        const int rr = w0 + k * kRowsAtOnce + lane / kChunks, ch = lane % kChunks;
-        const uint4 v = *reinterpret_cast<const uint4*>(q_s + t * C::kTileBytes + (ch >> 3) * C::kBlockBytes + rr * 128 +
-                                                        (((ch & 7) ^ (rr & 7)) << 4));
-        if (rr < rows)
-          *reinterpret_cast<uint4*>(a.out + ((sq.q0 + first + rr) * a.n_heads + head) * D + ch * 8) = v;
-      }
+      tc_fence_before();
+      fence_proxy_async_smem();  // the next queries are copied over what was staged
+      mbar_arrive(&q_empty[item % kQBufs][t]);
     }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -637,8 +768,10 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       // every CTA adds up its share of the rows over the cluster, a row (of
       // 64 channels two) a warp at a time, 4 channels a lane
       cluster_sync();
+      Walker<kRowsCta> again;
+      const bool there = again.at(a, cta, &w);  // (the whole cluster alike)
       constexpr int kLanes = D / 4, kRowsAtOnce = 32 / kLanes;
-      const int share = kTile / cluster, rows = min(kTile, sq.nq - row0);
+      const int share = kTile / cluster, rows = there ? w.rows(0) : 0;
 #pragma unroll 2
       for (int k = warp * kRowsAtOnce + lane / kLanes; k < share; k += C::kThreads / 32 * kRowsAtOnce) {
         const int r = rank * share + k, ch = lane % kLanes;
@@ -656,9 +789,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           o.z = o.z * f + v.z * fp;
           o.w = o.w * f + v.w * fp;
         }
-        const int64_t row = (sq.q0 + row0 + r) * a.n_heads + head;
+        const int64_t row = static_cast<int64_t>(w.sq.q0 + w.row0 + r) * a.n_heads + w.head;
         float lse;
-        const float f = finish_row(m, l, a.sink, head, &lse);
+        const float f = finish_row(m, l, a.sink, w.head, &lse);
         if (a.lse && ch == 0) a.lse[row] = lse;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f, o.y * f), hi = __floats2bfloat162_rn(o.z * f, o.w * f);
         *reinterpret_cast<uint2*>(a.out + row * D + 4 * ch) =
@@ -683,8 +816,8 @@ bool encode_rows(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 encode, const
 }
 
 template <int D, int QT, int CTAS>
-cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int cluster,
-                       cudaStream_t stream) {
+cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int sms,
+                       int cluster, cudaStream_t stream) {
   using C = Cfg<D, QT, CTAS>;
   const auto kernel = prompt_attn_kernel<D, QT, CTAS>;
   CUtensorMap tm_q, tm_k, tm_v;
@@ -703,8 +836,12 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
   }
   // n rows are at most n / R + 1 tiles of R rows, and at most n
   const int64_t most = a.n_q / (QT * kTile) + a.B;
-  const int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads * cluster;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads;
+  if (grid > 0x3fffffff) return cudaErrorInvalidValue;
+  if (C::kCluster)
+    grid *= cluster;  // an item a cluster
+  else if (grid > static_cast<int64_t>(sms) * CTAS)
+    grid = static_cast<int64_t>(sms) * CTAS;  // resident CTAs, that walk through the items
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream,
                             static_cast<unsigned>(cluster), tm_q, tm_k, tm_v, a, cluster);
 }
@@ -721,7 +858,7 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
     int cluster = 1;
     while (cluster < 8 && tiles * cluster * 2 <= sms && a.n_k >= static_cast<int64_t>(a.B) * 4 * cluster * kTile)
       cluster *= 2;
-    return launch_dim<D, 1, 1>(a, encode, cluster, stream);
+    return launch_dim<D, 1, 1>(a, encode, sms, cluster, stream);
   }
   // Two tiles a CTA share the keys' copies and overlap one's softmax with the
   // other's products; where sequences are short two CTAs of one tile on an SM
@@ -729,8 +866,8 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
   // 1.42 ms with two tiles, 1.54 ms with one; 32 prompts of 500 189 and 194
   // us; 64 of 128 126 and 79 us.  At width 64 one tile was never slower (16
   // packed prompts, window 1024: 350 us with two, 305 us with one).
-  if (D == 64 || a.n_q <= static_cast<int64_t>(256) * a.B) return launch_dim<D, 1, 2>(a, encode, 1, stream);
-  return launch_dim<D, D == 64 ? 1 : 2, D == 64 ? 2 : 1>(a, encode, 1, stream);
+  if (D == 64 || a.n_q <= static_cast<int64_t>(256) * a.B) return launch_dim<D, 1, 2>(a, encode, sms, 1, stream);
+  return launch_dim<D, D == 64 ? 1 : 2, D == 64 ? 2 : 1>(a, encode, sms, 1, stream);
 }
 
 }  // namespace
