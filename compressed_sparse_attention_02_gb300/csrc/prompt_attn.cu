@@ -52,15 +52,19 @@ struct Cfg {
   static constexpr int kStages = CTAS == 2 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
   static constexpr int kQBufs = CTAS == 2 && D == 64 ? 2 : 1;     // of the queries: the next tile's, where there is room
   static constexpr int kSmem = (kQBufs * QT + kStages) * kTileBytes + 1024;
+  // Parts that a tile of keys is worked on in: with one tile of queries the
+  // scores of one half are computed while the other's softmax runs.
+  static constexpr int kParts = QT == 1 ? 2 : 1;
+  static constexpr int kPart = kTile / kParts;
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return QT * kTile + t * D; }
   static constexpr int kCols = QT == 2 ? 512 : 256;
   // Where 168 (or 128) registers a thread are launched, the softmax warps
   // take some that the other four give up: 256 x 208 + 128 x 88 = 384 x 168,
-  // 128 x 208 + 128 x 48 = 256 x 128.
+  // 128 x 168 + 128 x 88 = 256 x 128.
   static constexpr bool kSplit = QT == 2 || CTAS == 2;
   static constexpr int kLaunchRegs = QT == 2 ? 168 : 128;
-  static constexpr int kSoftmaxRegs = 208, kOtherRegs = QT == 2 ? 88 : 48;
+  static constexpr int kSoftmaxRegs = QT == 2 ? 208 : 168, kOtherRegs = 88;
   static_assert(!kSplit || QT * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "registers of the block");
   // One CTA of one tile an SM: the keys may be shared out over a cluster,
   // whose fp32 sums meet in the rings.
@@ -268,7 +272,8 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   constexpr int kRowsCta = QT * kTile, kQBufs = C::kQBufs;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t q_full[kQBufs][QT], q_empty[kQBufs][QT], full[C::kStages], empty[C::kStages];
-  __shared__ uint64_t s_full[QT], p_full[QT], o_full[QT], dirty, cleaned, drain;
+  __shared__ uint64_t s_full[QT][C::kParts], p_full[QT][C::kParts], pv_done[QT][C::kParts];
+  __shared__ uint64_t o_full[QT], dirty, cleaned, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   // keys of each masked tile whose values are not all finite, as each of the
@@ -296,8 +301,11 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         mbar_init(&q_full[q][t], 1);
         mbar_init(&q_empty[q][t], kTile);
       }
-      mbar_init(s_full + t, 1);
-      mbar_init(p_full + t, kTile);
+      for (int h = 0; h < C::kParts; ++h) {
+        mbar_init(&s_full[t][h], 1);
+        mbar_init(&p_full[t][h], kTile);
+        mbar_init(&pv_done[t][h], 1);
+      }
       mbar_init(o_full + t, 1);
     }
     fence_mbar_init();
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       // loop's values warp-uniform (the shuffles say so to the compiler) an
       // issue costs a few cycles; from a branch on lane 0 each product took
       // about 115, more than it takes to compute.
-      constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 1, 1, 0, 0);  // bf16, K-major A and B
+      constexpr uint32_t idesc_s = instr_desc(kTile, C::kPart, 1, 1, 0, 0);  // bf16, K-major A and B
       constexpr uint32_t idesc_o = instr_desc(kTile, D, 1, 1, 0, 1);      // A from TMEM, B (= V) MN-major
       auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -414,15 +422,17 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         const int m_from = uniform(walk.j_hi - masked.from), m_upto = uniform(walk.j_hi - 1 - masked.upto);
         const int buf = item % kQBufs;
         const uint32_t qb = smem_u32(q_bufs + buf * QT * C::kTileBytes), q_par = (item / kQBufs) & 1;
-        auto s_of = [&](int t, uint64_t k_desc) {  // S_t = Q_t K^T (one lane)
+        // scores of part h of a tile of keys, S_t = Q_t K^T (one lane)
+        auto s_of = [&](int t, int h, uint64_t k_desc) {
           const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
+          k_desc += h * (C::kPart * 128 >> 4);
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             constexpr int kStep = 32 >> 4;  // 16 channels along a 128-byte line, in the descriptors' units
             const int off = (s >> 2) * (C::kBlockBytes >> 4) + (s & 3) * kStep;
-            mma_f16(tm + C::kSCol(t), q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
+            mma_f16(tm + C::kSCol(t) + h * C::kPart, q_desc + off, k_desc + off, idesc_s, s > 0 ? 1u : 0u);
           }
-          if (!skip_s) tc_commit(s_full + t);
+          if (!skip_s) tc_commit(&s_full[t][h]);
         };
         // the first tile of keys (the queries are waited for even without one:
         // a phase that is not waited for could be taken for a later one)
@@ -433,7 +443,10 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           if (ok) ok = wait(&q_full[buf][t], q_par);
           if (ok && begin[t] == 0 && end[t] > 0) {
             tc_fence_after();
-            if (elect_one()) s_of(t, k_first);
+            if (elect_one()) {
+#pragma unroll
+              for (int h = 0; h < C::kParts; ++h) s_of(t, h, k_first);
+            }
             __syncwarp();
           }
         }
@@ -456,22 +469,29 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
 #pragma unroll
           for (int t = 0; t < QT; ++t) {
             const bool pv = it >= begin[t] && it < end[t], next = again && it + 1 >= begin[t] && it + 1 < end[t];
-            if (ok && pv) ok = wait(p_full + t, n_p[t]++ & 1u);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              if (pv) {
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                  mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (s * 2048 >> 4), idesc_o,
-                             (it > begin[t] || s > 0) ? 1u : 0u);
-                if (it + 1 == end[t]) tc_commit(o_full + t);
+            for (int h = 0; h < C::kParts; ++h) {
+              const bool last = t == QT - 1 && h == C::kParts - 1;
+              if (ok && pv) ok = wait(&p_full[t][h], n_p[t] & 1u);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                if (pv) {
+#pragma unroll
+                  for (int s = 0; s < C::kPart / 16; ++s)
+                    mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + h * C::kPart + s * 8,
+                               v_desc + ((h * C::kPart + 16 * s) * 128 >> 4), idesc_o,
+                               (it > begin[t] || h > 0 || s > 0) ? 1u : 0u);
+                  if (C::kParts > 1) tc_commit(&pv_done[t][h]);
+                  if (it + 1 == end[t] && h == C::kParts - 1) tc_commit(o_full + t);
+                }
+                if (last) tc_commit(empty + v_slot);
+                if (next) s_of(t, h, k_desc);
+                if (last && again) tc_commit(empty + k_slot);
               }
-              if (t == QT - 1) tc_commit(empty + v_slot);
-              if (next) s_of(t, k_desc);
-              if (t == QT - 1 && again) tc_commit(empty + k_slot);
+              __syncwarp();
             }
-            __syncwarp();
+            if (pv) ++n_p[t];
           }
         }
         seq0 += 2 * n_it;
@@ -582,20 +602,21 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       }
       float m = kNone, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
       bool large = false;        // of the warp: some row's logits are large (see below)
-      for (int n = 0; n < n_tiles; ++n) {
-        const int j = j_top - n;
-        ok = wait_or_abort(s_full + t, n_s++ & 1, abort_flag, a.status);
+      for (int part = 0; part < n_tiles * C::kParts; ++part) {
+        const int n = part / C::kParts, h = part % C::kParts, j = j_top - n;
+        ok = wait_or_abort(&s_full[t][h], (n_s + n) & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];
+        constexpr int kC = C::kPart / 32;
+        uint32_t s[kC][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
+        for (int c = 0; c < kC; ++c) tmem_ld32(s_tmem + h * C::kPart + 32 * c, s[c]);
         tmem_wait_ld();
         if (masked_t.at(j)) {  // this row's keys among the tile's columns, as a bit each
-          const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
+          const int c0 = j * kTile + h * C::kPart, c_hi = last_key + 1 - c0, c_lo = first_key - c0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kC; ++c) {
             const int hi = max(0, min(32, c_hi - 32 * c)), lo = max(0, min(32, c_lo - 32 * c));
             const uint32_t seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
 #pragma unroll
@@ -603,20 +624,30 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
               if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
           }
         }
-        float top[4];
+        float top[kC];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kC; ++c) {
           top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
           for (int k = 2; k < 32; k += 2) top[c] = max3(top[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
         }
-        const float top1 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        float top1 = top[0];
+#pragma unroll
+        for (int c = 1; c < kC; ++c) top1 = fmaxf(top1, top[c]);
         if (__any_sync(0xffffffffu, (top1 - m) * scale2 > kLag)) {
           const float m1 = fmaxf(m, top1), f = ex2((m - m1) * scale2);
           m = m1;
           l *= f;
           large = __any_sync(0xffffffffu, m > kNone && fabsf(m * scale2) > 65536.f);
-          if (n > 0) {  // the products of the tiles before have finished: S was issued after them
+          if (part > 0) {
+            // the products of the parts before have finished: these scores were
+            // issued after them, but for the last one's where parts alternate
+            if (C::kParts > 1) {
+              ok = wait_or_abort(&pv_done[t][h ^ 1], (n_s + n - (h ^ 1)) & 1, abort_flag, a.status);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+            }
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -635,14 +666,14 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         if (large) {
           offset = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < kC; ++c)
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - m);
         }
         const uint64_t minus_m = pair_of(__float_as_uint(offset), __float_as_uint(offset));
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kC; ++c) {
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -654,15 +685,16 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
             const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
             p[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          tmem_st16(s_tmem + 16 * c, p);
+          tmem_st16(s_tmem + h * C::kPart + 16 * c, p);
         }
         float sx, sy;
         split(add2(sum[0], sum[1]), &sx, &sy);
         l += sx + sy;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full + t);
+        mbar_arrive(&p_full[t][h]);
       }
+      n_s += n_tiles;
       uint8_t* q_s = q_bufs + ((item % kQBufs) * QT + t) * C::kTileBytes;
       if (ok) {  // (a tile that sees no keys: its queries have landed where its output is staged)
         ok = loaded ? wait_or_abort(o_full + t, n_o++ & 1, abort_flag, a.status)
