@@ -128,10 +128,10 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, device=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -428,7 +428,7 @@ def csa_rope(r, turns, pos, x, out=None, inverse=False, stream=None):
     n, heads, dim = shape
     _check(_lib.csa_rope(ctypes.byref(r), _flat(w, "turns", turns, _I64, (r.rope_dim // 2,), dev), n, heads, dim,
                          _flat(w, "pos", pos, _I32, (n,), dev), *_rows(w, "x", x, shape, dev),
-                         *_rows(w, "out", out, shape, dev), 1 if inverse else 0, _stream(stream)), w)
+                         *_rows(w, "out", out, shape, dev), 1 if inverse else 0, _stream(stream, dev)), w)
     return out
 
 
@@ -466,7 +466,7 @@ def csa_kv_append(cache, r, turns, cu_rows, pos0, k, v, stream=None):
                               None if r is None else _flat(w, "turns", turns, _I64, (r.rope_dim // 2,), dev), B, n,
                               None if cu_rows is None else _flat(w, "cu_rows", cu_rows, _I32, (B + 1,), dev),
                               _flat(w, "pos0", pos0, _I32, (B,), dev), *_rows(w, "k", k, shape, dev),
-                              *_rows(w, "v", v, shape, dev), _stream(stream)), w)
+                              *_rows(w, "v", v, shape, dev), _stream(stream, dev)), w)
 
 
 def paged_attn_workspace(cache, B: int, n_heads: int) -> torch.Tensor:
@@ -494,7 +494,7 @@ def csa_paged_attn(cache, lens, q, sm_scale, window, sink, out, lse, ws, stream=
                                _flat(w, "out", out, _BF16, shape, dev),
                                None if lse is None else _flat(w, "lse", lse, _F32, (B, heads), dev),
                                None if ws is None else _flat(w, "ws", ws, torch.uint8, (size,), dev), size,
-                               _stream(stream)), w)
+                               _stream(stream, dev)), w)
 
 
 def csa_prompt_attn(cu_q, cu_k, q, k, v, sm_scale, causal, window, sink, out, lse=None, stream=None):
@@ -517,7 +517,7 @@ def csa_prompt_attn(cu_q, cu_k, q, k, v, sm_scale, causal, window, sink, out, ls
                                 None if sink is None else _flat(w, "sink", sink, _F32, (heads,), dev),
                                 _flat(w, "out", out, _BF16, shape, dev),
                                 None if lse is None else _flat(w, "lse", lse, _F32, (n, heads), dev),
-                                _stream(stream)), w)
+                                _stream(stream, dev)), w)
 
 
 CSA_TEST_FAULT_INDEXER, CSA_TEST_FAULT_TOPK, CSA_TEST_FAULT_ATTN = 1, 2, 4

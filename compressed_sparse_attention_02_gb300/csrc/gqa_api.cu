@@ -90,17 +90,47 @@ bool heads_ok(int32_t n_heads, int32_t n_kv_heads) {
   return n_heads >= 1 && n_heads <= kMaxHeads && n_kv_heads >= 1 && n_heads % n_kv_heads == 0;
 }
 
+}  // namespace
+
+namespace csa {
+
+constexpr int kMaxDevices = 64;  // one bit a device
+
 int current_sms() {
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
+  if (dev >= 0 && dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev >= 0 && dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
-}  // namespace
+cudaError_t kernel_limits(const void* kernel, int smem, int min_regs, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < kMaxDevices ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  if (min_regs > 0) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < min_regs) return cudaErrorInvalidConfiguration;
+  }
+  done->fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
+
+}  // namespace csa
 
 extern "C" {
 
@@ -206,7 +236,7 @@ csa_status csa_kv_append(const csa_paged_cache* c, const csa_rope_params* r, con
 
 size_t csa_paged_attn_workspace_size(const csa_paged_cache* c, int32_t B, int32_t n_heads) {
   if (check_cache(c, false) != CSA_OK || B < 0 || !heads_ok(n_heads, c->n_kv_heads)) return 0;
-  const int sms = current_sms();
+  const int sms = csa::current_sms();
   return sms > 0 ? csa::paged_attn_bytes(c->head_dim, sms) : 0;
 }
 
@@ -225,7 +255,7 @@ csa_status csa_paged_attn(const csa_paged_cache* c, int32_t B, int32_t n_heads, 
     return CSA_ERR_INVALID_ARG;
   csa::PagedAttnArgs a = {};
   a.status = csa::device_status();
-  const int sms = current_sms();
+  const int sms = csa::current_sms();
   if (!a.status || sms <= 0) return CSA_ERR_CUDA;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < csa::paged_attn_bytes(c->head_dim, sms))
     return CSA_ERR_WORKSPACE;

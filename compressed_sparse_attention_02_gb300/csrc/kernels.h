@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace csa {
 
 // Counts successful kernel launches (reported by csa_launch_count).
@@ -370,6 +372,12 @@ struct PromptAttnArgs {
 };
 cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream);
 
+// Once per device and kernel: the shared memory a kernel may use and, where
+// min_regs is given, that it is launched with that many registers a thread.
+// `done` is the kernel's own mask of devices it was done for.
+cudaError_t kernel_limits(const void* kernel, int smem, int min_regs, std::atomic<uint64_t>* done);
+// SMs of the current device (0 without one), looked up once per device.
+int current_sms();
 // The device status word of the current device and the tensor-map encoder
 // (null when the CUDA runtime does not give them).
 unsigned* device_status();

@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvApp
   if (lane == 0 && (p.first == 0 || s != was)) *sl.scale = s;
 }
 
+constexpr int kMaxAngles = 128 * 64 * static_cast<int>(sizeof(float2));  // of 128 rows of width 128
 template <int THREADS, int NI>
 cudaError_t launch_pages(const KvAppendArgs& a, unsigned items, int sms, cudaStream_t stream) {
   // Heads a CTA: as many as leave about two CTAs an SM (5 prompts of 16000
@@ -322,8 +323,9 @@ cudaError_t launch_pages(const KvAppendArgs& a, unsigned items, int sms, cudaStr
   groups = groups < 1 ? 1 : groups > H ? H : groups;
   const int heads = (H + groups - 1) / groups;
   const size_t smem = static_cast<size_t>(a.cache.page) * (a.rope.rope_dim / 2) * sizeof(float2);
-  cudaError_t e = cudaFuncSetAttribute(kv_append_pages_kernel<THREADS, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = kernel_limits(reinterpret_cast<const void*>(kv_append_pages_kernel<THREADS, NI>), kMaxAngles, 0,
+                                      &done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_append_pages_kernel<THREADS, NI>, dim3(items, (H + heads - 1) / heads, 2), dim3(THREADS), smem,
                     stream, a, heads);
@@ -343,9 +345,8 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
   // CTA for each page and head took 7.7).
   if (a.n_rows <= 2 * static_cast<int64_t>(a.B))
     return launch_pdl(kv_append_rows_kernel, dim3(x, (2 * a.cache.n_kv_heads + 7) / 8), dim3(kRowThreads), 0, stream, a);
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = current_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   // 16-channel items of a page: page * head_dim / 16, 64 .. 1024
   const int items = a.cache.page * a.cache.head_dim / 16;
   if (items <= 64) return launch_pages<64, 1>(a, x, sms, stream);

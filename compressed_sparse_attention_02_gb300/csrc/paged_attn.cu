@@ -617,7 +617,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 template <int D>
 cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
   using C = Cfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = kernel_limits(reinterpret_cast<const void*>(paged_attn_kernel<D>), C::kSmem, 0, &done);
   if (e != cudaSuccess) return e;
   const int ctas = sms * C::kCtas;
   e = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kThreads), C::kSmem, stream, a);

@@ -858,14 +858,11 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
       !encode_rows(&tm_k, encode, a.n_k > 0 ? a.k : a.q, D, a.n_kv_heads, n_k, a.k_stride, a.k_stride_h) ||
       !encode_rows(&tm_v, encode, a.n_k > 0 ? a.v : a.q, D, a.n_kv_heads, n_k, a.v_stride, a.v_stride_h))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> done{0};
+  // (the split of registers assumes what the kernel is launched with)
+  const cudaError_t e = kernel_limits(reinterpret_cast<const void*>(kernel), C::kSmem, C::kSplit ? C::kLaunchRegs : 0,
+                                      &done);
   if (e != cudaSuccess) return e;
-  if (C::kSplit) {  // the split of registers assumes what the kernel is launched with
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, kernel);
-    if (e != cudaSuccess) return e;
-    if (at.numRegs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  }
   // n rows are at most n / R + 1 tiles of R rows, and at most n
   const int64_t most = a.n_q / (QT * kTile) + a.B;
   int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads;
@@ -880,9 +877,8 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
 
 template <int D>
 cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = current_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   const int64_t most = a.n_q / kTile + a.B, tiles = (most < a.n_q ? most : a.n_q) * a.n_heads;
   if (tiles <= sms) {
     // Few tiles, an SM each; a cluster shares out the keys of a tile while
