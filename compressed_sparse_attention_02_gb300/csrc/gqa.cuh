@@ -53,6 +53,21 @@ __device__ __forceinline__ void item_chunks(const RopeArgs& r, int i, int* lo, i
   }
 }
 
+// A row's (sin, cos) in shared memory, [rope_dim / 2]: the four 16-byte pieces
+// of an item's 8 pairs lie apart, each kind of all items together, so that
+// neighbouring threads (items) read neighbouring pieces.
+__device__ __forceinline__ int angle_slot(int pair, int items) {
+  return ((((pair >> 1) & 3) * items + (pair >> 3)) << 1) | (pair & 1);
+}
+__device__ __forceinline__ void load_angles(const float2* row, int item, int items, float2 (&sc)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 f = *reinterpret_cast<const float4*>(row + ((j * items + item) << 1));
+    sc[2 * j] = make_float2(f.x, f.y);
+    sc[2 * j + 1] = make_float2(f.z, f.w);
+  }
+}
+
 __device__ __forceinline__ void unpack_bf16(const uint4& u, float (&x)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll

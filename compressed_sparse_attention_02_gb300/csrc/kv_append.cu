@@ -166,7 +166,7 @@ __device__ __forceinline__ Slab slab_of(const KvAppendArgs& a, const PageRows& p
 template <int THREADS, int NI>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel(const KvAppendArgs a, const int heads) {
   constexpr int kWarps = THREADS / 32;
-  extern __shared__ float2 sc_s[];  // K: [rows][rope_dim / 2] (sin, cos)
+  extern __shared__ float2 sc_s[];  // K: the rows' (sin, cos), rope_dim / 2 each
   __shared__ int sh[kWarps + 2];
   __shared__ float max_s[2][kWarps];
   pdl_launch_dependents();
@@ -200,10 +200,10 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel
   const int h0 = blockIdx.y * heads;
   fetch(h0);
   for (int i = tid; i < (p.last - p.first) * pairs; i += THREADS) {
-    const int r = i / pairs;
+    const int r = i / pairs, j = i - r * pairs;
     float s, c;
-    rope_sincos_exact(p.pos0 + p.first + r, __ldg(rope.turns + i - r * pairs), &s, &c);
-    sc_s[i] = make_float2(s * rope.mscale, c * rope.mscale);
+    rope_sincos_exact(p.pos0 + p.first + r, __ldg(rope.turns + j), &s, &c);
+    sc_s[r * pairs + angle_slot(j, rotated)] = make_float2(s * rope.mscale, c * rope.mscale);
   }
   __syncthreads();
   for (int head = h0; head < h1; ++head) {
@@ -218,13 +218,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel
       unpack_bf16(v[k], hi[k]);
       if (it < rotated && i < n_items) {
         float2 sc[8];
-        const float2* at = sc_s + (i >> items_shift) * pairs + 8 * it;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 f = *reinterpret_cast<const float4*>(at + 2 * j);
-          sc[2 * j] = make_float2(f.x, f.y);
-          sc[2 * j + 1] = make_float2(f.z, f.w);
-        }
+        load_angles(sc_s + (i >> items_shift) * pairs, it, rotated, sc);
         rotate_item(rope.half != 0, sc, lo[k], hi[k]);
       }
       amax = item_max(lo[k], hi[k], amax);

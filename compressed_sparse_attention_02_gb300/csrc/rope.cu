@@ -47,7 +47,7 @@ constexpr int kFlight = 3;
 constexpr int kRopeCtas = 4;
 
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeRowsArgs a, const RopeGrid g) {
-  extern __shared__ float2 sc_s[];  // [tokens][rope_dim / 2] (sin, cos)
+  extern __shared__ float2 sc_s[];  // the tokens' (sin, cos), rope_dim / 2 each
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
   for (int i0 = tid; i0 - tid < n; i0 += kFlight * kRopeThreads) {
     uint4 u[kFlight], v[kFlight];
     int64_t dst[kFlight];
-    int at[kFlight];  // the item's (sin, cos) in sc_s and, above, its distance to the second chunk; -1: nothing
+    int at[kFlight];  // token (above bit 5) and rotated item, and above both its second chunk's distance; -1: nothing
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
       const int i = i0 + k * kRopeThreads;
@@ -80,14 +80,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
       u[k] = *reinterpret_cast<const uint4*>(src);
       v[k] = *reinterpret_cast<const uint4*>(src + (ch - cl));
       dst[k] = t * a.out_stride + h * a.out_stride_h + cl;
-      at[k] = (ch - cl) << 16 | (it < rotated ? t * pairs + 8 * it : 0xFFFF);
+      at[k] = (ch - cl) << 16 | (it < rotated ? t << 5 | it : 0xFFFF);
     }
     if (i0 == tid) {  // the tokens' sines and cosines, while the first loads are on their way
       for (int i = tid; i < nt * pairs; i += kRopeThreads) {
         const int t = i / pairs, j = i - t * pairs;
         float s, c;
         rope_sincos_exact(__ldg(a.pos + t0 + t), __ldg(a.rope.turns + j), &s, &c);
-        sc_s[i] = make_float2((a.inverse ? -s : s) * a.rope.mscale, c * a.rope.mscale);
+        sc_s[t * pairs + angle_slot(j, rotated)] = make_float2((a.inverse ? -s : s) * a.rope.mscale, c * a.rope.mscale);
       }
       __syncthreads();
     }
@@ -100,12 +100,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
         float2 sc[8];
         unpack_bf16(u[k], x);
         unpack_bf16(v[k], y);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 f = *reinterpret_cast<const float4*>(sc_s + sc_at + 2 * j);
-          sc[2 * j] = make_float2(f.x, f.y);
-          sc[2 * j + 1] = make_float2(f.z, f.w);
-        }
+        load_angles(sc_s + (sc_at >> 5) * pairs, sc_at & 31, rotated, sc);
         rotate_item(a.rope.half != 0, sc, x, y);
         u[k] = pack_bf16(x);
         v[k] = pack_bf16(y);
