@@ -100,6 +100,57 @@ __device__ __forceinline__ void rotate_item(bool half, const float2 (&sc)[8], fl
   }
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 values as one register pair: Blackwell's packed multiply-add and
+// add take half the issue slots of the scalar ones.
+__device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(x), "r"(y));
+  return p;
+}
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  return pair_of(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
+}
+// From a row's reference (in log2) and sum of weights to the factor of its
+// weighted values and its lse, the sink's weight in.
+__device__ __forceinline__ float finish_row(float m, float l, const float* sink, int head, float* lse) {
+  float f = 1.f;
+  if (sink) {
+    const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
+    f = ex2(m - m1);
+    l = l * f + ex2(s2 - m1);
+    m = m1;
+  }
+  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  return l == 0.f ? 0.f : f / l;
+}
+
 // Finds the sequence that work item w belongs to, where sequence b has
 // count(b) >= 0 items: returns b and the item's index in it, or -1 when w is
 // past the last.  T holds the sum of all counts.  Every thread of the CTA

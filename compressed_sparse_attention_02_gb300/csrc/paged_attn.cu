@@ -33,8 +33,6 @@ constexpr int kUnitShift = 7;             // tokens a unit: 32 a warp
 constexpr int kUnit = 1 << kUnitShift;
 constexpr int kWarpTokens = kUnit / kWarps;
 constexpr int kRows = 16;                 // query heads a CTA
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 // A maximum may lag behind by this much (in log2) before the accumulators are
 // rescaled: weights are then at most 2^4 times 1, and as f16 they carry 2^11
 // more, so weights down to 2^-25 of the largest keep f16's full precision.
@@ -60,12 +58,6 @@ struct Cfg {
   static constexpr int kRowFloats = D + D / 32;
   static_assert(kWarpBytes >= kRows * kRowFloats * 4, "a warp's accumulators fit its ring");
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -154,19 +146,6 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
   for (int w = 0; w < kWarps; ++w) x += sh[w];
   __syncthreads();
   return x;
-}
-
-// An output row from its sums (in units of 2^m) and the sink's logit, if any.
-__device__ __forceinline__ float finish_row(float m, float& l, const float* sink, int head, float* lse) {
-  float f = 1.f;
-  if (sink) {
-    const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
-    f = ex2(m - m1);
-    l = l * f + ex2(s2 - m1);
-    m = m1;
-  }
-  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  return l == 0.f ? 0.f : f / l;  // times the sums: the output
 }
 
 template <int D>
@@ -333,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
     float o[kN][4];
 #pragma unroll
     for (int j = 0; j < kN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[2] = {kNone, kNone}, mv[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+    float m[2] = {kNone, kNone}, mv[2] = {kNone, kNone};
+    uint64_t l2[2] = {0ull, 0ull};  // sums of weights, as pairs of partial sums
 
     for (int it = 0; it < take; ++it) {
       cp_async_wait_pending(C::kStages - 2);
@@ -367,13 +347,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
         const float4 sc = *reinterpret_cast<const float4*>(scale_s[warp][st]);
         const int bad = bad_s[warp][st];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float k = n < 2 ? sc.x : sc.y;
-          x[n][0] *= fac[0] * k;
-          x[n][1] *= fac[0] * k;
-          x[n][2] *= fac[1] * k;
-          x[n][3] *= fac[1] * k;
-        }
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float k = fac[h] * (n < 2 ? sc.x : sc.y);
+            split(mul2(pair_of(x[n][2 * h], x[n][2 * h + 1]), pair_of(k, k)), &x[n][2 * h], &x[n][2 * h + 1]);
+          }
         if (t0 < sp.lo || t0 + kWarpTokens > sp.len || bad) {
 #pragma unroll
           for (int n = 0; n < 4; ++n)
@@ -404,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
               topv[h] = fmaxf(topv[h], __shfl_xor_sync(0xffffffffu, topv[h], off));
             }
             const float m1 = fmaxf(m[h], top[h]), mv1 = fmaxf(mv[h], topv[h]);
-            l[h] *= ex2(m[h] - m1);
+            const float fl = ex2(m[h] - m1);
+            l2[h] = mul2(l2[h], pair_of(fl, fl));
             const float f = ex2(mv[h] - mv1);
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
@@ -421,11 +401,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float w = ex2(lv[s] + (m[h] - mv[h]) + kWeightExp);
-            const float p0 = ex2(x[2 * s][2 * h] - m[h]), p1 = ex2(x[2 * s][2 * h + 1] - m[h]);
-            const float p2 = ex2(x[2 * s + 1][2 * h] - m[h]), p3 = ex2(x[2 * s + 1][2 * h + 1] - m[h]);
-            l[h] += (p0 + p1) + (p2 + p3);
-            pf[s][h] = pack_f16(p0 * w, p1 * w);
-            pf[s][2 + h] = pack_f16(p2 * w, p3 * w);
+            const uint64_t ww = pair_of(w, w), mm = pair_of(-m[h], -m[h]);
+            float p0, p1, p2, p3;
+            split(add2(pair_of(x[2 * s][2 * h], x[2 * s][2 * h + 1]), mm), &p0, &p1);
+            split(add2(pair_of(x[2 * s + 1][2 * h], x[2 * s + 1][2 * h + 1]), mm), &p2, &p3);
+            const uint64_t p01 = pair_of(ex2(p0), ex2(p1)), p23 = pair_of(ex2(p2), ex2(p3));
+            l2[h] = add2(l2[h], add2(p01, p23));
+            split(mul2(p01, ww), &p0, &p1);
+            split(mul2(p23, ww), &p2, &p3);
+            pf[s][h] = pack_f16(p0, p1);
+            pf[s][2 + h] = pack_f16(p2, p3);
           }
         // out += weights . V: tokens 2cq, 2cq+1, 2cq+8, 2cq+9 of each 16, the
         // bytes of two tokens paired by channel; lane group g holds channels
@@ -471,8 +456,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = g + 8 * h;
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      float l, other;
+      split(l2[h], &l, &other);
+      l += other;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
       const float f = ex2(mv[h] - m[h] - kWeightExp);
       // accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j
 #pragma unroll
@@ -483,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
       }
       if (cq == 0) {
         m_s[warp][r] = m[h];
-        l_s[warp][r] = l[h];
+        l_s[warp][r] = l;
       }
     }
     __syncthreads();

@@ -31,8 +31,6 @@ namespace {
 
 constexpr int kTileShift = 7;
 constexpr int kTile = 1 << kTileShift;   // queries and keys a tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;          // running maximum before the first key
 // The accumulators are rescaled only when a row's maximum has grown by more
 // than 2^8 since (weights up to 256 are exact in range for bf16 and fp32).
@@ -72,37 +70,6 @@ struct Cfg {
   static_assert(!kCluster || kStages * kTileBytes >= kTile * D * 4, "the sums fit the ring");
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two fp32 values as one register pair: Blackwell's packed multiply-add and
-// add take half the issue slots of the scalar ones.
-__device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) {
-  uint64_t p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(x), "r"(y));
-  return p;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
-}
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -130,20 +97,6 @@ struct Masked {
   int from, upto;
   __device__ __forceinline__ bool at(int j) const { return j >= from || j <= upto; }
 };
-
-// From a row's reference (in log2) and sum of weights to the factor of its
-// weighted values and its lse, the sink's weight in.
-__device__ __forceinline__ float finish_row(float m, float l, const float* sink, int head, float* lse) {
-  float f = 1.f;
-  if (sink) {
-    const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
-    f = ex2(m - m1);
-    l = l * f + ex2(s2 - m1);
-    m = m1;
-  }
-  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  return l == 0.f ? 0.f : f / l;
-}
 
 struct Seq {
   int q0, k0;  // first rows of the sequence
@@ -659,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
             }
           }
         }
-        const uint64_t scale_2 = pair_of(__float_as_uint(scale2), __float_as_uint(scale2));
+        const uint64_t scale_2 = pair_of(scale2, scale2);
         // scale s - scale m in one rounding; where the logits are so large that
         // the rounding of scale m shows, s - m first
         float offset = -m * scale2;
@@ -670,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - m);
         }
-        const uint64_t minus_m = pair_of(__float_as_uint(offset), __float_as_uint(offset));
+        const uint64_t minus_m = pair_of(offset, offset);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
@@ -681,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
             split(fma2(pair_of(s[c][2 * k], s[c][2 * k + 1]), scale_2, minus_m), &x, &y);
             x = ex2(x);
             y = ex2(y);
-            sum[k & 1] = add2(sum[k & 1], pair_of(__float_as_uint(x), __float_as_uint(y)));
+            sum[k & 1] = add2(sum[k & 1], pair_of(x, y));
             const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
             p[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
@@ -732,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           }
           // (a row without keys has l = 0 and sums of 0 * value, all finite)
           float x[32];
-          const uint64_t l2 = pair_of(__float_as_uint(l), __float_as_uint(l));
+          const uint64_t l2 = pair_of(l, l);
 #pragma unroll
           for (int k = 0; k < 32; k += 2) split(mul2(pair_of(o[k], o[k + 1]), l2), &x[k], &x[k + 1]);
           if ((odd0 || odd1) && r < rows) {
