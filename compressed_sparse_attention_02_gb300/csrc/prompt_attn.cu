@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         const int o2 = item & 1;
         const bool odd0 = *const_cast<volatile int*>(&odd_item[o2][0]) == item + 1;
         const bool odd1 = *const_cast<volatile int*>(&odd_item[o2][1]) == item + 1;
-#pragma unroll
+#pragma unroll 1  // (code that runs once waits for its instructions)
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           if (n_tiles > 0) {
@@ -750,37 +750,53 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   }
   if constexpr (C::kCluster) {
     if (cluster > 1) {
-      // every CTA adds up its share of the rows over the cluster, a row (of
-      // 64 channels two) a warp at a time, 4 channels a lane
-      cluster_sync();
+      // Every CTA adds up its share of the rows over the cluster, 16 / cluster
+      // rows a warp: the references and sums of all its rows and CTAs at once,
+      // one a lane, then a row (of 64 channels two) at a time, 4 channels a lane.
       Walker<kRowsCta> again;
       const bool there = again.at(a, cta, &w);  // (the whole cluster alike)
+      cluster_sync();
       constexpr int kLanes = D / 4, kRowsAtOnce = 32 / kLanes;
-      const int share = kTile / cluster, rows = there ? w.rows(0) : 0;
-#pragma unroll 2
-      for (int k = warp * kRowsAtOnce + lane / kLanes; k < share; k += C::kThreads / 32 * kRowsAtOnce) {
-        const int r = rank * share + k, ch = lane % kLanes;
-        if (r >= rows) continue;
-        float m = kNone, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < cluster; ++p) {  // (few: the maximum is taken along)
-          const float mp = dsmem_ld_f32(dsmem_addr(m_s + r, p)), lp = dsmem_ld_f32(dsmem_addr(l_s + r, p));
-          const float4 v = dsmem_ld_f32x4(dsmem_addr(ring + r * D * 4 + ((ch ^ (r & (D / 4 - 1))) << 4), p));
-          const float m1 = fmaxf(m, mp), f = ex2(m - m1), fp = ex2(mp - m1);
-          m = m1;
-          l = l * f + lp * fp;
-          o.x = o.x * f + v.x * fp;
-          o.y = o.y * f + v.y * fp;
-          o.z = o.z * f + v.z * fp;
-          o.w = o.w * f + v.w * fp;
-        }
-        const int64_t row = static_cast<int64_t>(w.sq.q0 + w.row0 + r) * a.n_heads + w.head;
+      const int per_warp = 16 / cluster, rows = there ? w.rows(0) : 0;
+      const int first = rank * (kTile / cluster) + warp * per_warp;
+      static_assert(C::kThreads == 256, "eight warps");
+      float g;
+      {
+        const int p = lane % cluster, r = first + (lane & 15) / cluster;
+        const float m = dsmem_ld_f32(dsmem_addr(m_s + r, p)), l = dsmem_ld_f32(dsmem_addr(l_s + r, p));
+        float top = m;
+        for (int off = 1; off < cluster; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float f = ex2(m - top);
+        float sum = l * f;
+        for (int off = 1; off < cluster; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         float lse;
-        const float f = finish_row(m, l, a.sink, w.head, &lse);
-        if (a.lse && ch == 0) a.lse[row] = lse;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f, o.y * f), hi = __floats2bfloat162_rn(o.z * f, o.w * f);
-        *reinterpret_cast<uint2*>(a.out + row * D + 4 * ch) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        g = f * finish_row(top, sum, a.sink, w.head, &lse);
+        if (a.lse && lane < 16 && p == 0 && r < rows)
+          a.lse[static_cast<int64_t>(w.sq.q0 + w.row0 + r) * a.n_heads + w.head] = lse;
+      }
+#pragma unroll 2
+      for (int i0 = 0; i0 < per_warp; i0 += kRowsAtOnce) {
+        const int i = i0 + lane / kLanes, ch = lane % kLanes, r = first + i;
+        float4 v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < cluster) v[p] = dsmem_ld_f32x4(dsmem_addr(ring + r * D * 4 + ((ch ^ (r & (D / 4 - 1))) << 4), p));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < cluster) {
+            const float f = __shfl_sync(0xffffffffu, g, i * cluster + p);
+            o.x = fmaf(v[p].x, f, o.x);
+            o.y = fmaf(v[p].y, f, o.y);
+            o.z = fmaf(v[p].z, f, o.z);
+            o.w = fmaf(v[p].w, f, o.w);
+          }
+        if (r < rows) {
+          const int64_t row = static_cast<int64_t>(w.sq.q0 + w.row0 + r) * a.n_heads + w.head;
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+          *reinterpret_cast<uint2*>(a.out + row * D + 4 * ch) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
       }
       cluster_sync();  // a CTA's shared memory outlives its readers
     }
