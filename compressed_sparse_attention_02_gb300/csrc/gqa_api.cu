@@ -17,6 +17,9 @@ bool words_opt(const void* p) { return aligned(p, 4); }
 
 constexpr int kMaxHeads = 1024;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
+// Rows of a prompt call: a CTA that walks all keys for one tile of queries then
+// takes about a second, inside the limit of its other warps' waits.
+constexpr int64_t kMaxPromptRows = int64_t(1) << 27;
 constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements (a tensor map's strides stay below 2^40 bytes)
 
 // Element strides of rows and heads of a [rows][heads][dim] tensor.
@@ -282,11 +285,13 @@ csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32
                            float sm_scale, int32_t causal, int32_t window, const float* sink, uint16_t* out,
                            float* lse, void* stream) {
   if (head_dim != 64 && head_dim != 128) return CSA_ERR_UNSUPPORTED;
-  if (B < 0 || !heads_ok(n_heads, n_kv_heads) || n_q < 0 || n_q > kMaxRows || n_k < 0 || n_k > kMaxRows ||
+  if (B < 0 || !heads_ok(n_heads, n_kv_heads) || n_q < 0 || n_q > kMaxPromptRows || n_k < 0 ||
+      n_k > kMaxPromptRows || B > kMaxPromptRows ||
       (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) || !isfinite(sm_scale) ||
       !(sm_scale > 0.f))
     return CSA_ERR_INVALID_ARG;
   if (B == 0 || n_q == 0) return CSA_OK;
+  if ((n_q / 128 + B) * n_heads >= (int64_t(1) << 30)) return CSA_ERR_UNSUPPORTED;  // tiles of 128 queries, all heads
   if (!words_ok(cu_q) || !words_ok(cu_k) || !rows_ok(q) || !words_opt(sink) || !rows_ok(out) || !words_opt(lse) ||
       (n_k > 0 && (!rows_ok(k) || !rows_ok(v))))
     return CSA_ERR_INVALID_ARG;

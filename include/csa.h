@@ -775,7 +775,7 @@ csa_status csa_kv_append(const csa_paged_cache *c, const csa_rope_params *r,
  *   l_t = sm_scale * q . key_t   (sm_scale > 0),
  *   out[b,h] = sum_t e^{l_t} value_t / (sum_t e^{l_t} + e^{sink[h]})
  * (sink NULL: no such term), lse[b,h] (optional) = the log of the sum.  A
- * sequence of length 0 gives 0 and lse = sink, or -inf without one.
+ * sequence of length 0 (or less) gives 0 and lse = sink, or -inf without one.
  * q: [B][n_heads][head_dim] with strides.  out: [B][n_heads][head_dim], lse
  * [B][n_heads], contiguous.  sink: [n_heads] fp32, finite or -inf.
  * A length past the table is clamped, and tokens in a page outside the pool
@@ -803,8 +803,9 @@ csa_status csa_paged_attn(const csa_paged_cache *c, int32_t B, int32_t n_heads,
  * The sums, sink and lse are csa_paged_attn's; a query that sees nothing
  * gives 0 and lse = sink, or -inf.  Keys and values that a query does not
  * see have no effect on it, whatever they hold.
- * n_q, n_k: rows of q and of k / v; rows behind the last sequence are left as
- * they are in out.  out: [n_q][n_heads][head_dim], lse [n_q][n_heads],
+ * n_q, n_k: rows of q and of k / v, at most 2^27 (and (n_q / 128 + B) *
+ * n_heads below 2^30); rows behind the last sequence are left as they are in
+ * out.  out: [n_q][n_heads][head_dim], lse [n_q][n_heads],
  * contiguous.  head_dim: 64 or 128.  A sequence with a cu_q or cu_k entry
  * that falls or passes its rows records CSA_ERR_INDEX_RANGE and is left out.
  * No workspace.  Weights are rounded to bf16 for the product with the values.

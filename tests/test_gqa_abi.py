@@ -105,13 +105,14 @@ def test_prompt_attention_refusals(csa):
         return csa._lib.csa_prompt_attn(B, heads, kv, dim, nq, nk, cu_q, cu_k, q, qs, qh, k, ks, kh, v, vs, vh, sm,
                                         causal, window, sink, out, lse, None)
     for kw in (dict(B=-1), dict(heads=3), dict(heads=0), dict(kv=0), dict(heads=2048), dict(nq=-1), dict(nk=-1),
-               dict(nq=1 << 31), dict(cu_q=None), dict(cu_k=ODD), dict(q=None), dict(k=None), dict(v=FAKE + 8),
+               dict(nq=(1 << 27) + 1), dict(nk=(1 << 27) + 1), dict(cu_q=None), dict(cu_k=ODD), dict(q=None), dict(k=None), dict(v=FAKE + 8),
                dict(qs=64), dict(kh=100), dict(vs=257), dict(sm=0.0), dict(sm=math.nan), dict(causal=2),
                dict(window=-1), dict(window=5, causal=0), dict(sink=ODD), dict(out=FAKE + 2), dict(out=None),
                dict(lse=ODD), dict(ks=1 << 39)):
         assert call(**kw) == 1, kw
     for d in (32, 96, 256):
         assert call(dim=d) == 2
+    assert call(heads=1024, kv=1, nq=1 << 27) == 2
     assert call(nq=0, q=None, out=None) == 0 and call(B=0) == 0
 
 
