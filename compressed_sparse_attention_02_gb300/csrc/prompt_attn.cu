@@ -139,7 +139,7 @@ struct Walk {
   Range rt[QT];
   int j_hi, n_it;
 
-  __device__ __forceinline__ Walk(const PromptAttnArgs& a, const Work& w, int rank, int cluster) {
+  __device__ __forceinline__ void set(const PromptAttnArgs& a, const Work& w, int rank, int cluster) {
     int j_lo = 0x7fffffff;
     j_hi = 0;
 #pragma unroll
@@ -166,8 +166,8 @@ struct Walk {
 // Walks a CTA's share of the work: items (tiles of ROWS queries of a sequence,
 // the later ones first: under the causal mask they see more keys) times
 // heads.  CTA c of G takes c, 2G - 1 - c, 2G + c, ...: forward and backward in
-// turn, so that no CTA gets the longer one of every G.  Each warp walks by
-// itself; the places grow, so it never looks back.
+// turn, so that no CTA gets the longer one of every G.  The places grow, so
+// it never looks back.
 template <int ROWS>
 struct Walker {
   int b0 = 0, base = 0, round = 0;  // sequences before b0 hold `base` items
@@ -216,6 +216,16 @@ struct Walker {
   }
 };
 
+// A work item as the loading warp finds it and hands it to the others (the
+// search costs each item about 1000 cycles, which no other warp waits for).
+template <int QT>
+struct Order {
+  Work w;
+  Walk<QT> walk;
+  Masked masked;  // over all of the CTA's rows
+  int there;      // 0: no more
+};
+
 template <int D, int QT, int CTAS>
 __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -226,7 +236,8 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t q_full[kQBufs][QT], q_empty[kQBufs][QT], full[C::kStages], empty[C::kStages];
   __shared__ uint64_t s_full[QT][C::kParts], p_full[QT][C::kParts], pv_done[QT][C::kParts];
-  __shared__ uint64_t o_full[QT], dirty, cleaned, drain;
+  __shared__ uint64_t o_full[QT], dirty, cleaned, drain, order_full[2], order_empty[2];
+  __shared__ Order<QT> orders[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   // keys of each masked tile whose values are not all finite, as each of the
@@ -245,6 +256,10 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     mbar_init(&drain, 1);
     mbar_init(&dirty, 1);
     mbar_init(&cleaned, kCleanThreads);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(order_full + i, 1);
+      mbar_init(order_empty + i, C::kThreads / 32 - 1);
+    }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -285,13 +300,15 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   // walk through their share of the items.
   const int cluster = C::kCluster ? cluster_size : 1;
   const int cta = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) - cta * cluster;
-  const int ctas = C::kCluster ? 0x40000000 : static_cast<int>(gridDim.x);
-  auto more = [&](Walker<kRowsCta>& walker, Work* w) {
-    if (C::kCluster) return walker.round++ == 0 && walker.at(a, cta, w);
-    return walker.next(a, cta, ctas, w);
+  // the next item, of every warp but the loading one; false at the end and after an abort
+  auto take = [&](int item, Order<QT>* o) {
+    const bool ok = wait_or_abort(order_full + (item & 1), (item >> 1) & 1, abort_flag, a.status);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    *o = orders[item & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(order_empty + (item & 1));
+    return o->there != 0;
   };
-  Walker<kRowsCta> walker;
-  Work w;
 
   if (warp >= 4 * QT) {
     if constexpr (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -299,9 +316,28 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       // ---------------- loads ----------------
       int seq = 0, n_q[QT] = {};  // ring slots and query tiles filled so far
       bool ok = true;
-      for (int item = 0; ok && more(walker, &w); ++item) {
-        const Walk<QT> walk(a, w, rank, cluster);
+      Walker<kRowsCta> walker;
+      for (int item = 0, there = 1; ok && there; ++item) {
+        Order<QT> o;
+        const Work& w = o.w;
+        const Walk<QT>& walk = o.walk;
+        if (C::kCluster)
+          there = item == 0 && walker.at(a, cta, &o.w);
+        else
+          there = walker.next(a, cta, static_cast<int>(gridDim.x), &o.w);
+        o.there = there;
+        if (there) {
+          o.walk.set(a, w, rank, cluster);
+          o.masked = w.masked(a, w.row0, min(kRowsCta, w.sq.nq - w.row0));
+        }
         if (lane == 0) {
+          if (item >= 2) ok = wait_or_abort(order_empty + (item & 1), ((item >> 1) - 1) & 1, abort_flag, a.status);
+          if (ok) {
+            orders[item & 1] = o;
+            mbar_arrive(order_full + (item & 1));
+          }
+        }
+        if (lane == 0 && there && ok) {
           const int kv_head = w.head / (a.n_heads / a.n_kv_heads);
           auto load = [&](int s) {
             const int slot = seq & (C::kStages - 1);
@@ -362,9 +398,10 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       int seq0 = 0;               // ring slots of the items before
       uint32_t n_p[QT] = {};      // weights taken so far, by tile
       uint32_t n_cleaned = 0;
-      for (int item = 0; ok && more(walker, &w); ++item) {
-        const Walk<QT> walk(a, w, rank, cluster);
-        const Masked masked = w.masked(a, w.row0, min(kRowsCta, w.sq.nq - w.row0));
+      Order<QT> order;
+      for (int item = 0; ok && take(item, &order); ++item) {
+        const Walk<QT>& walk = order.walk;
+        const Masked& masked = order.masked;
         const int n_it = uniform(walk.n_it);
         int begin[QT], end[QT];
 #pragma unroll
@@ -461,9 +498,11 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       int seq0 = 0;
       uint32_t n_cleaned = 0;
       bool ok = true;
-      for (int item = 0; ok && more(walker, &w); ++item) {
-        const Walk<QT> walk(a, w, rank, cluster);
-        const Masked masked = w.masked(a, w.row0, min(kRowsCta, w.sq.nq - w.row0));
+      Order<QT> order;
+      for (int item = 0; ok && take(item, &order); ++item) {
+        const Work& w = order.w;
+        const Walk<QT>& walk = order.walk;
+        const Masked& masked = order.masked;
         const int o = item & 1, half = warp - kCleanWarp;
         static_assert(kMaxMasked * 4 == 32, "a word a lane");
         int n_masked = 0;
@@ -537,13 +576,16 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     const float scale2 = a.sm_scale * kLog2e;
     uint32_t n_s = 0, n_o = 0;  // tiles of scores and sums taken so far
     bool ok = true;
-    for (int item = 0; ok && more(walker, &w); ++item) {
+    for (int item = 0; ok; ++item) {
+      Work w;
       int n_tiles, j_top, last_key, first_key;
       bool loaded;
       Masked masked_t;
       {
-        const Walk<QT> walk(a, w, rank, cluster);
-        const Range mine = QT == 1 || t == 0 ? walk.rt[0] : walk.rt[QT - 1];
+        Order<QT> order;
+        if (!take(item, &order)) break;
+        w = order.w;
+        const Range mine = QT == 1 || t == 0 ? order.walk.rt[0] : order.walk.rt[QT - 1];
         n_tiles = mine.hi - mine.lo;
         j_top = mine.hi - 1;
         masked_t = w.masked(a, w.row0 + t * kTile, w.rows(t));
@@ -753,8 +795,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       // Every CTA adds up its share of the rows over the cluster, 16 / cluster
       // rows a warp: the references and sums of all its rows and CTAs at once,
       // one a lane, then a row (of 64 channels two) at a time, 4 channels a lane.
-      Walker<kRowsCta> again;
-      const bool there = again.at(a, cta, &w);  // (the whole cluster alike)
+      const bool there = *abort_flag == 0 && orders[0].there != 0;
+      Work w = {};  // (one item, the whole cluster's)
+      if (there) w = orders[0].w;
       cluster_sync();
       constexpr int kLanes = D / 4, kRowsAtOnce = 32 / kLanes;
       const int per_warp = 16 / cluster, rows = there ? w.rows(0) : 0;
