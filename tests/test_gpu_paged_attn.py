@@ -197,8 +197,8 @@ def test_strided_queries_streams_graphs_and_repeats(csa):
         out2, lse2 = run(csa, x)
     side.synchronize()
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
-    # two captured calls with a workspace each, replayed on two streams at once
-    graphs = []
+    # two captured calls with a workspace each (kept as long as its graph), replayed on two streams at once
+    graphs, kept = [], []
     for _ in range(2):
         ws = csa.paged_attn_workspace(cache, 3, 16)
         o, l = torch.zeros_like(out), torch.zeros_like(lse)
@@ -206,6 +206,7 @@ def test_strided_queries_streams_graphs_and_repeats(csa):
         with torch.cuda.graph(gr):
             csa.csa_paged_attn(cache, x["lens"], x["q"], 128 ** -0.5, 0, None, o, l, ws)
         graphs.append((gr, o, l))
+        kept.append(ws)
     streams = [torch.cuda.Stream() for _ in graphs]
     torch.cuda.synchronize()
     for _ in range(5):
