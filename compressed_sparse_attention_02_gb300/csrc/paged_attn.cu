@@ -11,15 +11,19 @@
 // f16 exactly; queries become f16 after scaling each row by a power of two to
 // [2^14, 2^15), exact but for values 2^-28 below the row's largest.
 //
-// The tokens of all (sequence, head) pairs form one line of 128-token units
-// that is cut into equal shares, one per resident CTA, whatever the lengths
+// The tokens of all (sequence, head) pairs form one line of 32-token units
+// that is cut into equal shares, one per resident warp, whatever the lengths
 // are; a pair that a cut divides is finished by the merge kernel from fp32
-// partial results in a fixed order.  A warp takes 32 tokens of each unit with
-// its own asynchronous copies, running maximum and accumulators, so warps
-// never wait for one another inside a share.
+// partial results in a fixed order.  A warp has its own ring of asynchronous
+// copies, running maximum and accumulators: it waits for no other, and its
+// copies run on into the next pair while it finishes one (with a share a CTA, whose
+// warps joined their sums at each pair's end: 256 sequences of up to 600
+// tokens 91 us, 50 so; 64 of up to 32768, 393 and 381 us, 6.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
+
+#include <type_traits>
 
 #include "gqa.cuh"
 #include "ptx.cuh"
@@ -29,10 +33,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnitShift = 7;             // tokens a unit: 32 a warp
+constexpr int kUnitShift = 5;             // tokens a unit
 constexpr int kUnit = 1 << kUnitShift;
-constexpr int kWarpTokens = kUnit / kWarps;
-constexpr int kRows = 16;                 // query heads a CTA
+constexpr int kRows = 16;                 // query heads a warp
 // A maximum may lag behind by this much (in log2) before the accumulators are
 // rescaled: weights are then at most 2^4 times 1, and as f16 they carry 2^11
 // more, so weights down to 2^-25 of the largest keep f16's full precision.
@@ -42,21 +45,16 @@ constexpr float kNone = -1e30f;           // running maximum before the first to
 
 template <int D>
 struct Cfg {
-  // CTAs an SM and tiles in flight a warp.  64 sequences of up to 32768 tokens,
-  // 8 heads of width 128: 393 us with 2 CTAs of 3 tiles, 452 with 3 of 2, 508
-  // with 2 of 2.  96 sequences under a window of 4096 at width 64, where a
-  // token's arithmetic weighs twice as much: 83 us with 4 CTAs of 3.
-  static constexpr int kCtas = D == 64 ? 4 : 2;
+  // CTAs an SM and tiles in flight a warp.  At width 64 with 8 heads: 64
+  // sequences of up to 8192 tokens 66 us with 3 CTAs and no spills, 85 with 4;
+  // 96 under a window of 4096 77 and 80; a fourth tile changes nothing.
+  static constexpr int kCtas = D == 64 ? 3 : 2;
   static constexpr int kStages = 3;
-  static constexpr int kTileBytes = kWarpTokens * D;        // K or V of one warp's 32 tokens
+  static constexpr int kTileBytes = kUnit * D;              // K or V of a unit
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmem = kWarps * kWarpBytes;
   static constexpr int kRecord = kRows * (D + 2);           // floats of a partial result: sums, maxima, weights' sums
-  // A warp's accumulators in its ring at the end: one float of padding after
-  // every 32, so that the 32 lanes' channels fall into different banks.
-  static constexpr int kRowFloats = D + D / 32;
-  static_assert(kWarpBytes >= kRows * kRowFloats * 4, "a warp's accumulators fit its ring");
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
@@ -127,12 +125,35 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int b) {
   return s;
 }
 
-// What a CTA leaves for the merge of the pair that its share ends inside.
-struct __align__(16) Cut {
-  int32_t row, rows;  // first output row ([B][n_heads]) and rows; rows 0: the pair did not begin in this share, or ends here
-  int32_t slot;       // the CTA's record of it (later CTAs: record 0)
-  int32_t last;       // the CTA that ends it
+// A place on the line: unit u of a pair (16-row block of a KV head's queries) of sequence b.
+struct Place {
+  Span sp;
+  int b, pair, u;
+  __device__ __forceinline__ int token() const { return (sp.unit0() + u) << kUnitShift; }
+  __device__ __forceinline__ void advance(const PagedAttnArgs& a, int pairs) {
+    if (++u < sp.units()) return;
+    u = 0;
+    if (++pair < pairs) return;
+    pair = 0;
+    do {
+      ++b;
+      sp.len = sp.lo = 0;
+      if (b < a.B) sp = span_of(a, b);
+    } while (b < a.B && sp.units() == 0);
+  }
 };
+
+// What the merge has to know of a pair that begins in one share and ends in a later one.
+struct __align__(16) Cut {
+  int32_t row;    // first output row ([B][n_heads])
+  int32_t rows;   // rows, doubled, + the first share's record of it (later shares: record 0); 0: no such pair
+  int32_t first;  // the share in which it begins
+  int32_t last;   // and ends
+};
+// They stand by share, and a share has at most one; by pair where there are few pairs, so that the merge
+// needs no search (16 sequences of up to 4000 tokens, 8 heads: 24.9 us, 26.8 with a CTA a share; 32 sequences
+// of 100 tokens: 14.5 us, 9.8 with a CTA a share).
+__host__ __device__ __forceinline__ bool few_pairs(int64_t pairs, int64_t shares) { return pairs * 8 < shares; }
 
 // Sum over the CTA.
 __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
@@ -155,10 +176,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
   constexpr int kN = D / 8;        // 8-channel tiles of the output
   constexpr int kChunks = D / 16;  // 16-byte chunks a row
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sh[2 * kWarps];
-  __shared__ float scale_s[kWarps][C::kStages][4];  // k, k, v, v scales of the tile's two halves
+  __shared__ int64_t sh[kWarps], found_at[kWarps];
+  __shared__ int found_b[kWarps];
+  __shared__ float scale_s[kWarps][C::kStages][4];  // k, k, v, v scales of the unit's two halves
   __shared__ int bad_s[kWarps][C::kStages];         // halves whose page is outside the cache
-  __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -168,10 +189,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
   const int blocks = (group + kRows - 1) / kRows;   // 16-row blocks a KV head
   const int pairs = cache.n_kv_heads * blocks;
 
-  // this CTA's share [at, end) of the line of units
+  // The warps' shares of the line; neighbouring shares are of different CTAs,
+  // so that a short line is spread over the SMs.
   int64_t total = 0;
   for (int s = tid; s < a.B; s += kThreads) total += span_of(a, s).units();
   total = block_sum(total, sh) * pairs;
+  const int64_t shares = static_cast<int64_t>(gridDim.x) * kWarps;
+  const bool by_pair = few_pairs(static_cast<int64_t>(a.B) * pairs, shares);
+  Cut* cuts = reinterpret_cast<Cut*>(a.part);
+  float* records = a.part + shares * (sizeof(Cut) / sizeof(float));
   // empty sequences, in turn over the CTAs
   for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
     if (span_of(a, s).len > 0) continue;
@@ -179,48 +205,80 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
     for (int i = tid; i < a.n_heads * D; i += kThreads) a.out[row * D + i] = 0;
     if (a.lse)
       for (int i = tid; i < a.n_heads; i += kThreads) a.lse[row + i] = a.sink ? __ldg(a.sink + i) : -INFINITY;
+    if (by_pair)
+      for (int i = tid; i < pairs; i += kThreads) cuts[s * pairs + i].rows = 0;
   }
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t begin = blockIdx.x * per;
-  int64_t at = begin;
-  const int64_t end = min(total, begin + per);
+  const int64_t per = max((total + shares - 1) / shares, static_cast<int64_t>(1));
+  const int64_t share = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const int64_t begin = share * per;
+  int left = static_cast<int>(max(min(total - begin, per), static_cast<int64_t>(0)));  // units to go
+
+  // where the four shares begin: one pass over the sequences' prefix sums
+  if (tid < kWarps) found_b[tid] = -1;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    const int64_t n = b < a.B ? static_cast<int64_t>(span_of(a, b).units()) * pairs : 0;
+    int64_t x = n;
+    if (a.B - b0 > 1) {
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    int64_t before = base + x - n;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const int64_t t = sh[k];
+      if (k < warp) before += t;
+      base += t;
+    }
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const int64_t target = (static_cast<int64_t>(k) * gridDim.x + blockIdx.x) * per;
+      if (target >= before && target < before + n) {  // one thread at most
+        found_b[k] = b;
+        found_at[k] = target - before;
+      }
+    }
+    __syncthreads();
+  }
   Cut cut = {0, 0, 0, 0};
-  Cut* cuts = reinterpret_cast<Cut*>(a.part);
-  float* records = a.part + gridDim.x * (sizeof(Cut) / sizeof(float));
-  if (at >= end) {
-    if (tid == 0) cuts[blockIdx.x] = cut;
+  if (left == 0 || found_b[warp] < 0) {
+    if (lane == 0 && !by_pair) cuts[share] = cut;
     return;
   }
-  int64_t index;
-  int b = find_item<kThreads>(
-      a.B, at, [&](int s) { return static_cast<int64_t>(span_of(a, s).units()) * pairs; }, sh, &index);
-  Span sp = span_of(a, b);
-  int pair = static_cast<int>(index / sp.units());
-  int u = static_cast<int>(index - static_cast<int64_t>(pair) * sp.units());
 
+  Place p, c;  // of the next copy and of the next unit worked on
+  p.b = found_b[warp];
+  p.sp = span_of(a, p.b);
+  p.pair = static_cast<int>(found_at[warp] / p.sp.units());
+  p.u = static_cast<int>(found_at[warp] - static_cast<int64_t>(p.pair) * p.sp.units());
+  c = p;
+  int to_copy = left, p_stage = 0, c_stage = 0;
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-  while (at < end) {
-    const int nt = sp.units();
-    const int take = static_cast<int>(min(static_cast<int64_t>(nt - u), end - at));
-    const int hk = pair / blocks, row0 = (pair - hk * blocks) * kRows;
-    const int rows = min(kRows, group - row0);
-    const int head0 = hk * group + row0;
-    const int32_t* table = cache.table + static_cast<int64_t>(b) * cache.table_stride;
-
-    // copies of iteration it's 32 tokens into its stage; page ids are read an
-    // iteration ahead (next_page: of the 16 tokens of the lane's half)
-    auto tokens_at = [&](int it) { return ((sp.unit0() + u + it) << kUnitShift) + warp * kWarpTokens; };
-    auto page_at = [&](int it) -> int32_t {
-      const int t = tokens_at(it) + (lane & 16);
-      return it < take && t < sp.len && t + 16 > sp.lo ? __ldg(table + (t >> cache.page_shift)) : -1;
-    };
-    int32_t next_page = page_at(0);
-    auto issue = [&](int it) {
+  // page numbers are read a unit ahead (of the 16 tokens of the lane's half)
+  auto page_of = [&](const Place& x) -> int32_t {
+    const int t = x.token() + (lane & 16);
+    return t < x.sp.len && t + 16 > x.sp.lo
+               ? __ldg(cache.table + static_cast<int64_t>(x.b) * cache.table_stride + (t >> cache.page_shift))
+               : -1;
+  };
+  int32_t next_page = page_of(p);
+  auto issue = [&]() {
+    if (to_copy > 0) {
       const int32_t mine = next_page;
-      next_page = page_at(it + 1);
-      const int t0 = tokens_at(it);
-      const int st = it % C::kStages;
-      if (it < take && t0 < sp.len && t0 + kWarpTokens > sp.lo) {
+      const Span sp = p.sp;
+      const int t0 = p.token(), hk = blocks == 1 ? p.pair : p.pair / blocks, st = p_stage;
+      if (--to_copy > 0) {
+        p.advance(a, pairs);
+        next_page = page_of(p);
+      }
+      p_stage = p_stage + 1 == C::kStages ? 0 : p_stage + 1;
+      {
         const uint32_t ks = ring + st * C::kStageBytes, vs = ks + C::kTileBytes;
         const bool ok = mine >= 0 && mine < cache.n_pages;
         const int th = t0 + (lane & 16);
@@ -236,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
         const int64_t off_b = ((slab_b << cache.page_shift) + ((t0 + 16) & in_page)) * D - 16 * D;
         constexpr int kRowsAtOnce = 32 / kChunks;
         const int r0 = lane / kChunks, c = lane % kChunks;
-        if (t0 >= sp.lo && t0 + kWarpTokens <= sp.len && ok_a && ok_b) {  // (uniform) all rows are there
+        if (t0 >= sp.lo && t0 + kUnit <= sp.len && ok_a && ok_b) {  // (uniform) all rows are there
           const uint8_t *ka = cache.k + off_a + r0 * D + c * 16, *kb = cache.k + off_b + r0 * D + c * 16;
           const uint8_t *va = cache.v + off_a + r0 * D + c * 16, *vb = cache.v + off_b + r0 * D + c * 16;
 #pragma unroll
@@ -268,10 +326,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
         }
         if (lane == 0) bad_s[warp][st] = (bads & 1u) | ((bads >> 31) << 1);
       }
-      cp_async_commit();
-    };
+    }
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+  for (int s = 0; s < C::kStages - 1; ++s) issue();
+
+  bool first = true;
+  while (left > 0) {
+    const Span sp = c.sp;
+    const int nt = sp.units(), take = min(nt - c.u, left);
+    const int hk = blocks == 1 ? c.pair : c.pair / blocks, row0 = (c.pair - hk * blocks) * kRows;
+    const int rows = min(kRows, group - row0);
+    const int head0 = hk * group + row0;
 
     // the query rows g and g + 8 as fragments: lane cq holds channels
     // cq * D/4 .. of each, in the order in which it reads the keys' bytes
@@ -282,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
       const int r = g + 8 * half;
       float x[D / 4];
       if (r < rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_stride + (head0 + r) * a.q_stride_h + cq * (D / 4));
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + c.b * a.q_stride + (head0 + r) * a.q_stride_h + cq * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           float y[8];
@@ -318,9 +385,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
     for (int it = 0; it < take; ++it) {
       cp_async_wait_pending(C::kStages - 2);
       __syncwarp();
-      const int t0 = tokens_at(it);
-      const int st = it % C::kStages;
-      if (t0 < sp.len && t0 + kWarpTokens > sp.lo) {
+      const int t0 = (sp.unit0() + c.u + it) << kUnitShift, st = c_stage;
+      c_stage = c_stage + 1 == C::kStages ? 0 : c_stage + 1;
+      {
         const uint32_t ks = ring + st * C::kStageBytes, vs = ks + C::kTileBytes;
         // logits of 32 tokens: 4 tiles of 8
         float x[4][4];
@@ -353,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
             const float k = fac[h] * (n < 2 ? sc.x : sc.y);
             split(mul2(pair_of(x[n][2 * h], x[n][2 * h + 1]), pair_of(k, k)), &x[n][2 * h], &x[n][2 * h + 1]);
           }
-        if (t0 < sp.lo || t0 + kWarpTokens > sp.len || bad) {
+        if (t0 < sp.lo || t0 + kUnit > sp.len || bad) {
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -446,13 +513,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
         }
       }
       __syncwarp();
-      issue(it + C::kStages - 1);
+      issue();
     }
-    cp_async_wait_pending(0);
-    __syncwarp();
-
-    // the warps' results, in units of 2^m, into their rings; then one sum
-    float* mine = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);  // [16][kRowFloats]
+    // The pair's rows, or this share's part of them in units of 2^m.
+    // Accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j.
+    const bool whole = take == nt;
+    const int slot = first ? 0 : 1;
+    float* part = records + (share * 2 + slot) * C::kRecord;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = g + 8 * h;
@@ -461,143 +528,141 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
       l += other;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const float f = ex2(mv[h] - m[h] - kWeightExp);
-      // accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const int d = 2 * cq * kN + j;
-        mine[r * C::kRowFloats + d + (d >> 5)] = o[j][2 * h] * f;
-        mine[r * C::kRowFloats + d + kN + ((d + kN) >> 5)] = o[j][2 * h + 1] * f;
-      }
-      if (cq == 0) {
-        m_s[warp][r] = m[h];
-        l_s[warp][r] = l;
-      }
-    }
-    __syncthreads();
-    const bool whole = take == nt;
-    const int slot = at == begin ? 0 : 1;
-    float* part = records + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kRecord;
-    if (!whole && u == 0) {  // the pair begins here and goes on
-      cut.row = b * a.n_heads + head0;
-      cut.rows = rows;
-      cut.slot = slot;
-      cut.last = static_cast<int>((at + nt - 1) / per);
-    }
-    for (int i = tid; i < rows * D; i += kThreads) {
-      const int r = i / D, d = i % D;
-      float mt = m_s[0][r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) mt = fmaxf(mt, m_s[w][r]);
-      float lt = 0.f, n = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(m_s[w][r] - mt);
-        lt += l_s[w][r] * f;
-        n += reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[r * C::kRowFloats + d + (d >> 5)] * f;
-      }
+      float f = ex2(mv[h] - m[h] - kWeightExp);
+      if (r >= rows) continue;
       if (whole) {
-        const int64_t row = static_cast<int64_t>(b) * a.n_heads + head0 + r;
+        const int64_t row = static_cast<int64_t>(c.b) * a.n_heads + head0 + r;
         float lse;
-        const __nv_bfloat16 y = __float2bfloat16_rn(n * finish_row(mt, lt, a.sink, head0 + r, &lse));
-        a.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&y);
-        if (a.lse && d == 0) a.lse[row] = lse;
+        f *= finish_row(m[h], l, a.sink, head0 + r, &lse);
+        if (a.lse && cq == 0) a.lse[row] = lse;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + (2 * cq + e) * kN);
+#pragma unroll
+          for (int k = 0; k < kN / 8; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * k + 2 * i][2 * h + e] * f, o[8 * k + 2 * i + 1][2 * h + e] * f);
+              w[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
       } else {
-        part[r * D + d] = n;
-        if (d == 0) {
-          part[kRows * D + r] = mt;
-          part[kRows * D + kRows + r] = lt;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float4* dst = reinterpret_cast<float4*>(part + r * D + (2 * cq + e) * kN);
+#pragma unroll
+          for (int k = 0; k < kN / 4; ++k)
+            dst[k] = make_float4(o[4 * k][2 * h + e] * f, o[4 * k + 1][2 * h + e] * f, o[4 * k + 2][2 * h + e] * f,
+                                 o[4 * k + 3][2 * h + e] * f);
+        }
+        if (cq == 0) {
+          part[kRows * D + r] = m[h];
+          part[kRows * D + kRows + r] = l;
         }
       }
     }
-    __syncthreads();
-    at += take;
-    u = 0;
-    if (++pair == pairs && at < end) {
-      pair = 0;
-      do {
-        sp = span_of(a, ++b);
-      } while (sp.units() == 0);
+    left -= take;
+    if (c.u == 0) {  // the pair begins here
+      if (!whole) {   // and goes on, so this is the whole of a share of `per` units
+        cut.row = c.b * a.n_heads + head0;
+        cut.rows = 2 * rows + slot;
+        cut.first = static_cast<int>(share);
+        cut.last = static_cast<int>((begin + (per - left) - take + nt - 1) / per);
+      }
+      if (by_pair && lane == 0) cuts[c.b * pairs + c.pair] = cut;
+    }
+    first = false;
+    if (left > 0) {
+      c.u += take - 1;
+      c.advance(a, pairs);
     }
   }
-  if (tid == 0) cuts[blockIdx.x] = cut;
+  cp_async_wait_pending(0);
+  if (lane == 0 && !by_pair) cuts[share] = cut;
 }
 
-// Finishes the pairs that the shares' borders divide, from their CTAs' records
-// first to last.  A CTA looks at one share's end; where a pair begins there and
-// goes on, warps take `split` stretches of the records of each of its rows
-// (8 / split rows at a time; grid.y parts of the rows).
+// Finishes the pairs that the shares' borders divide, from their shares' records
+// first to last.  With SPLIT 1 a CTA looks at one share's end, and a warp takes
+// a row.  Else CTA (x, y) takes row y of pair x, each of its warps a stretch of
+// the records.
 constexpr int kMergeThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnArgs a, const int ctas,
-                                                                    const int split) {
+constexpr int kMergeWarps = kMergeThreads / 32;
+
+template <int D, int SPLIT>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnArgs a, const int shares) {
   using C = Cfg<D>;
-  constexpr int kMergeWarps = kMergeThreads / 32;
-  constexpr int kPer = D / 32;  // channels a lane
+  constexpr int kPer = D / 32;  // channels a lane, neighbours
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+  static_assert(SPLIT == 1 || SPLIT == kMergeWarps, "a row's stretches are a CTA's warps");
   __shared__ float m_s[kMergeWarps], l_s[kMergeWarps];
-  __shared__ float n_s[kMergeWarps][D];
+  __shared__ __align__(16) float n_s[kMergeWarps][D];
   pdl_launch_dependents();
   pdl_wait();
   const Cut cut = reinterpret_cast<const Cut*>(a.part)[blockIdx.x];
-  if (cut.rows == 0) return;
-  const float* records = a.part + ctas * (sizeof(Cut) / sizeof(float));
+  const float* records = a.part + shares * (sizeof(Cut) / sizeof(float));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c0 = blockIdx.x, n_rec = cut.last - c0 + 1;
+  const int n_rec = cut.last - cut.first + 1, rows = cut.rows >> 1;
   auto record = [&](int k) {
-    return records + (static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? cut.slot : 0)) * C::kRecord;
+    return records + (static_cast<int64_t>(cut.first + k) * 2 + (k == 0 ? cut.rows & 1 : 0)) * C::kRecord;
   };
-  const int part = warp % split, at_once = kMergeWarps / split;
-  for (int r0 = blockIdx.y * at_once; r0 < cut.rows; r0 += gridDim.y * at_once) {
-    const int r = r0 + warp / split;
-    const bool there = r < cut.rows;
+  for (int r = SPLIT == 1 ? warp : blockIdx.y; r < rows; r += SPLIT == 1 ? kMergeWarps : gridDim.y) {
+    const int part = SPLIT == 1 ? 0 : warp;
     float m = kNone, l = 0.f, n[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) n[j] = 0.f;
-    if (there) {
-      for (int k = part + lane * split; k < n_rec; k += 32 * split) m = fmaxf(m, record(k)[kRows * D + r]);
+    for (int k = part + lane * SPLIT; k < n_rec; k += 32 * SPLIT) m = fmaxf(m, record(k)[kRows * D + r]);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
 #pragma unroll 4
-      for (int k = part; k < n_rec; k += split) {
-        const float* p = record(k);
-        const float f = ex2(p[kRows * D + r] - m);
-        l += p[kRows * D + kRows + r] * f;
+    for (int k = part; k < n_rec; k += SPLIT) {
+      const float* p = record(k);
+      const float f = ex2(p[kRows * D + r] - m);
+      l += p[kRows * D + kRows + r] * f;
+      const Vec v = *reinterpret_cast<const Vec*>(p + r * D + lane * kPer);
+      const float* y = reinterpret_cast<const float*>(&v);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) n[j] += p[r * D + lane + 32 * j] * f;
-      }
+      for (int j = 0; j < kPer; ++j) n[j] += y[j] * f;
     }
-    if (split > 1) {  // the stretches' sums, first to last
+    if (SPLIT > 1) {  // the stretches' sums, first to last
       __syncthreads();
       if (lane == 0) {
         m_s[warp] = m;
         l_s[warp] = l;
       }
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) n_s[warp][lane + 32 * j] = n[j];
+      for (int j = 0; j < kPer; ++j) n_s[warp][lane * kPer + j] = n[j];
       __syncthreads();
       if (part != 0) continue;
       const float m0 = m;
-      for (int w = 1; w < split; ++w) m = fmaxf(m, m_s[warp + w]);
+      for (int w = 1; w < SPLIT; ++w) m = fmaxf(m, m_s[w]);
       const float f0 = ex2(m0 - m);
       l *= f0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) n[j] *= f0;
-      for (int w = 1; w < split; ++w) {
-        const float f = ex2(m_s[warp + w] - m);
-        l += l_s[warp + w] * f;
+      for (int w = 1; w < SPLIT; ++w) {
+        const float f = ex2(m_s[w] - m);
+        l += l_s[w] * f;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) n[j] += n_s[warp + w][lane + 32 * j] * f;
+        for (int j = 0; j < kPer; ++j) n[j] += n_s[w][lane * kPer + j] * f;
       }
     }
-    if (!there) continue;
     const int64_t row = static_cast<int64_t>(cut.row) + r;
     float lse;
     const float f = finish_row(m, l, a.sink, static_cast<int>(row % a.n_heads), &lse);
+    uint32_t y[kPer / 2];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const __nv_bfloat16 y = __float2bfloat16_rn(n[j] * f);
-      a.out[row * D + lane + 32 * j] = *reinterpret_cast<const uint16_t*>(&y);
+    for (int j = 0; j < kPer / 2; ++j) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(n[2 * j] * f, n[2 * j + 1] * f);
+      y[j] = *reinterpret_cast<const uint32_t*>(&two);
     }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + lane * kPer);
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    else
+      *dst = y[0];
     if (a.lse && lane == 0) a.lse[row] = lse;
   }
 }
@@ -613,18 +678,20 @@ cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int group = a.n_heads / a.cache.n_kv_heads, rows = group < kRows ? group : kRows;
   const int64_t pairs = static_cast<int64_t>(a.B) * a.cache.n_kv_heads * ((group + kRows - 1) / kRows);
-  // Many pairs: few records each, a warp a row.  Few pairs: up to all CTAs'
+  // Many pairs: few records each, a warp a row.  Few pairs: up to all shares'
   // records of one, eight warps a row and a CTA for each row.
-  const bool many = pairs * 4 >= ctas;
-  return launch_pdl(paged_merge_kernel<D>, dim3(ctas - 1, many ? 1 : rows), dim3(kMergeThreads), 0, stream, a, ctas,
-                    many ? 1 : 8);
+  const int shares = ctas * kWarps;
+  if (!few_pairs(pairs, shares))
+    return launch_pdl(paged_merge_kernel<D, 1>, dim3(shares - 1), dim3(kMergeThreads), 0, stream, a, shares);
+  return launch_pdl(paged_merge_kernel<D, kMergeWarps>, dim3(static_cast<unsigned>(pairs), rows), dim3(kMergeThreads), 0,
+                    stream, a, shares);
 }
 
 }  // namespace
 
 size_t paged_attn_bytes(int head_dim, int sms) {
   const size_t ctas = static_cast<size_t>(sms) * (head_dim == 64 ? Cfg<64>::kCtas : Cfg<128>::kCtas);
-  return ctas * (sizeof(Cut) + 2 * kRows * (head_dim + 2) * sizeof(float));
+  return ctas * kWarps * (sizeof(Cut) + 2 * kRows * (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
