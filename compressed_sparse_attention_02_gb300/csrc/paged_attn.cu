@@ -155,20 +155,6 @@ struct __align__(16) Cut {
 // of 100 tokens: 14.5 us, 9.8 with a CTA a share).
 __host__ __device__ __forceinline__ bool few_pairs(int64_t pairs, int64_t shares) { return pairs * 8 < shares; }
 
-// Sum over the CTA.
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  if (lane == 0) sh[warp] = x;
-  __syncthreads();
-  x = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) x += sh[w];
-  __syncthreads();
-  return x;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
   using C = Cfg<D>;
@@ -191,13 +177,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 
   // The warps' shares of the line; neighbouring shares are of different CTAs,
   // so that a short line is spread over the SMs.
-  int64_t total = 0;
-  for (int s = tid; s < a.B; s += kThreads) total += span_of(a, s).units();
-  total = block_sum(total, sh) * pairs;
   const int64_t shares = static_cast<int64_t>(gridDim.x) * kWarps;
   const bool by_pair = few_pairs(static_cast<int64_t>(a.B) * pairs, shares);
   Cut* cuts = reinterpret_cast<Cut*>(a.part);
   float* records = a.part + shares * (sizeof(Cut) / sizeof(float));
+  if (tid < kWarps) found_b[tid] = -1;
+  // where the four shares begin, from the sequences' prefix sums; more than a block of sequences takes a pass
+  // for the total first
+  int64_t per = 1, total = 0;
+  for (int pass = a.B > kThreads ? 0 : 1; pass < 2; ++pass) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      const int64_t n = b < a.B ? static_cast<int64_t>(span_of(a, b).units()) * pairs : 0;
+      int64_t x = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      if (lane == 31) sh[warp] = x;
+      __syncthreads();
+      int64_t before = base + x - n;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const int64_t t = sh[k];
+        if (k < warp) before += t;
+        base += t;
+      }
+      if (a.B <= kThreads) total = base;
+      if (pass == 1) {
+        per = max((total + shares - 1) / shares, static_cast<int64_t>(1));
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const int64_t target = (static_cast<int64_t>(k) * gridDim.x + blockIdx.x) * per;
+          if (target >= before && target < before + n) {  // one thread at most
+            found_b[k] = b;
+            found_at[k] = target - before;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    total = base;
+  }
+  const int64_t share = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const int64_t begin = share * per;
+  int left = static_cast<int>(max(min(total - begin, per), static_cast<int64_t>(0)));  // units to go
   // empty sequences, in turn over the CTAs
   for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
     if (span_of(a, s).len > 0) continue;
@@ -207,44 +233,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
       for (int i = tid; i < a.n_heads; i += kThreads) a.lse[row + i] = a.sink ? __ldg(a.sink + i) : -INFINITY;
     if (by_pair)
       for (int i = tid; i < pairs; i += kThreads) cuts[s * pairs + i].rows = 0;
-  }
-  const int64_t per = max((total + shares - 1) / shares, static_cast<int64_t>(1));
-  const int64_t share = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  const int64_t begin = share * per;
-  int left = static_cast<int>(max(min(total - begin, per), static_cast<int64_t>(0)));  // units to go
-
-  // where the four shares begin: one pass over the sequences' prefix sums
-  if (tid < kWarps) found_b[tid] = -1;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int64_t n = b < a.B ? static_cast<int64_t>(span_of(a, b).units()) * pairs : 0;
-    int64_t x = n;
-    if (a.B - b0 > 1) {
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-      }
-    }
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    int64_t before = base + x - n;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const int64_t t = sh[k];
-      if (k < warp) before += t;
-      base += t;
-    }
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const int64_t target = (static_cast<int64_t>(k) * gridDim.x + blockIdx.x) * per;
-      if (target >= before && target < before + n) {  // one thread at most
-        found_b[k] = b;
-        found_at[k] = target - before;
-      }
-    }
-    __syncthreads();
   }
   Cut cut = {0, 0, 0, 0};
   if (left == 0 || found_b[warp] < 0) {
@@ -349,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
       const int r = g + 8 * half;
       float x[D / 4];
       if (r < rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + c.b * a.q_stride + (head0 + r) * a.q_stride_h + cq * (D / 4));
+        const uint16_t* row = a.q + c.b * a.q_stride + (head0 + r) * a.q_stride_h;
+        const uint4* src = reinterpret_cast<const uint4*>(row + cq * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           float y[8];
@@ -543,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * k + 2 * i][2 * h + e] * f, o[8 * k + 2 * i + 1][2 * h + e] * f);
+              const int j = 8 * k + 2 * i;
+              const __nv_bfloat162 y = __floats2bfloat162_rn(o[j][2 * h + e] * f, o[j + 1][2 * h + e] * f);
               w[i] = *reinterpret_cast<const uint32_t*>(&y);
             }
             dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -683,8 +673,8 @@ cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
   const int shares = ctas * kWarps;
   if (!few_pairs(pairs, shares))
     return launch_pdl(paged_merge_kernel<D, 1>, dim3(shares - 1), dim3(kMergeThreads), 0, stream, a, shares);
-  return launch_pdl(paged_merge_kernel<D, kMergeWarps>, dim3(static_cast<unsigned>(pairs), rows), dim3(kMergeThreads), 0,
-                    stream, a, shares);
+  const dim3 grid(static_cast<unsigned>(pairs), rows);
+  return launch_pdl(paged_merge_kernel<D, kMergeWarps>, grid, dim3(kMergeThreads), 0, stream, a, shares);
 }
 
 }  // namespace
