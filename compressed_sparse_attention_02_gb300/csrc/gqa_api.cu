@@ -17,6 +17,7 @@ bool words_opt(const void* p) { return aligned(p, 4); }
 
 constexpr int kMaxHeads = 1024;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int32_t kMaxSeqs = 1 << 20;  // (a warp's walk through them then takes some 30 ms)
 // Rows of a prompt call: a CTA that walks all keys for one tile of queries then
 // takes about a second, inside the limit of its other warps' waits.
 constexpr int64_t kMaxPromptRows = int64_t(1) << 27;
@@ -212,7 +213,7 @@ csa_status csa_kv_append(const csa_paged_cache* c, const csa_rope_params* r, con
   csa_status s = check_cache(c, true);
   if (s != CSA_OK) return s;
   if (r && (s = check_rope(r, c->head_dim)) != CSA_OK) return s;
-  if (B < 0 || n_rows < 0 || n_rows > kMaxRows) return CSA_ERR_INVALID_ARG;
+  if (B < 0 || B > kMaxSeqs || n_rows < 0 || n_rows > kMaxRows) return CSA_ERR_INVALID_ARG;
   if (!cu_rows && n_rows != B) return CSA_ERR_INVALID_ARG;
   if (B == 0 || n_rows == 0) return CSA_OK;
   if ((r && (!turns || !aligned(turns, 8))) || !words_opt(cu_rows) || !words_ok(pos0) || !rows_ok(k) || !rows_ok(v))
@@ -249,7 +250,7 @@ csa_status csa_paged_attn(const csa_paged_cache* c, int32_t B, int32_t n_heads, 
                           void* stream) {
   const csa_status s = check_cache(c, true);
   if (s != CSA_OK) return s;
-  if (B < 0 || B > (1 << 20) || !heads_ok(n_heads, c->n_kv_heads) || window < 0 || !isfinite(sm_scale) ||
+  if (B < 0 || B > kMaxSeqs || !heads_ok(n_heads, c->n_kv_heads) || window < 0 || !isfinite(sm_scale) ||
       !(sm_scale > 0.f))
     return CSA_ERR_INVALID_ARG;
   if (B == 0) return CSA_OK;
@@ -286,7 +287,7 @@ csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32
                            float* lse, void* stream) {
   if (head_dim != 64 && head_dim != 128) return CSA_ERR_UNSUPPORTED;
   if (B < 0 || !heads_ok(n_heads, n_kv_heads) || n_q < 0 || n_q > kMaxPromptRows || n_k < 0 ||
-      n_k > kMaxPromptRows || B > kMaxPromptRows ||
+      n_k > kMaxPromptRows || B > kMaxSeqs ||
       (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) || !isfinite(sm_scale) ||
       !(sm_scale > 0.f))
     return CSA_ERR_INVALID_ARG;

@@ -672,7 +672,8 @@ csa_status csa_hca_layer_decode(const csa_params *p, int32_t B,
  * for rows and heads (multiples of 8, at least head_dim; the channels are
  * contiguous), so views of a fused projection pass as they are; row pointers
  * are 16-byte aligned, int32 and fp32 arrays 4-byte aligned; query head h
- * reads key / value head h / (n_heads / n_kv_heads); n_heads at most 1024.
+ * reads key / value head h / (n_heads / n_kv_heads); n_heads at most 1024;
+ * B (sequences) at most 2^20.
  */
 
 /*

@@ -127,3 +127,13 @@ def test_tensors_of_another_kind_are_refused(csa):
         with pytest.raises(csa.CsaError) as e:
             f()
         assert e.value.status == 1
+
+
+def test_more_sequences_than_a_call_takes(csa):
+    many, one, c = (1 << 20) + 1, ctypes.c_void_p(None), cache(csa)
+    assert csa._lib.csa_kv_append(ctypes.byref(c), None, None, many, many, None, FAKE, FAKE, 256, 128, FAKE, 256, 128,
+                                  one) == 1
+    assert csa._lib.csa_paged_attn(ctypes.byref(c), many, 4, FAKE, FAKE, 512, 128, 0.1, 0, None, FAKE, None, FAKE,
+                                   1 << 40, one) == 1
+    assert csa._lib.csa_prompt_attn(many, 4, 2, 128, 8, 8, FAKE, FAKE, FAKE, 512, 128, FAKE, 256, 128, FAKE, 256, 128,
+                                    0.1, 1, 0, None, FAKE, None, one) == 1
