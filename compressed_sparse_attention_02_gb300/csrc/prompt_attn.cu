@@ -7,12 +7,18 @@
 //
 // Bound by the tensor cores from a few hundred keys on (4 D operations a
 // query, key and head against 4 D bytes a key and head read once a tile of
-// 128 queries).  One CTA per QT tiles of 128 queries of one head: one warp
-// loads Q and a ring of 128-key K and V tiles by TMA, one thread issues the
-// tcgen05 products S = Q K^T and O += P V (S and O in tensor memory, P
-// written over S as bf16 and read from there), four warps a tile do the
-// softmax with one thread a row, so no value crosses threads.  Keys are
-// walked from the diagonal down: the masked tiles come first.
+// 128 queries); short of that, and at width 64, by the chain from a tile's
+// scores over their softmax to the next products.  Resident CTAs walk through
+// the items, each QT tiles of 128 queries of one head: one warp finds an item
+// and loads Q and a ring of 128-key K and V tiles by TMA, the next item's
+// under this one's end, one warp issues the tcgen05 products S = Q K^T and
+// O += P V (S and O in tensor memory, P written over S as bf16 and read from
+// there), four warps a tile do the softmax with one thread a row, so no value
+// crosses threads.  Keys are walked from the diagonal down: the masked tiles
+// come first.  With one tile a CTA its keys are worked on in halves, one's
+// scores under the other's softmax.  16384 queries of 32 heads of width 128:
+// 1.41 ms, 1560 TFLOP/s, 83% of the matrix product's rate; 16 prompts of 237 to
+// 2500 under a window of 1024 at width 64: 206 us, 550 TFLOP/s.
 //
 // P is rounded to bf16 (the products take one type for both operands, and V
 // is bf16); sums and maxima are fp32, over the unrounded weights.
@@ -901,12 +907,19 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
     return launch_dim<D, 1, 1>(a, encode, sms, cluster, stream);
   }
   // Two tiles a CTA share the keys' copies and overlap one's softmax with the
-  // other's products; where sequences are short two CTAs of one tile on an SM
-  // overlap their starts and ends instead.  Width 128, 32 heads: 16384 queries
-  // 1.42 ms with two tiles, 1.54 ms with one; 32 prompts of 500 189 and 194
-  // us; 64 of 128 126 and 79 us.  At width 64 one tile was never slower (16
-  // packed prompts, window 1024: 350 us with two, 305 us with one).
-  if (D == 64 || a.n_q <= static_cast<int64_t>(256) * a.B) return launch_dim<D, 1, 2>(a, encode, sms, 1, stream);
+  // other's products; where a tile sees few keys, or a sequence has one tile,
+  // two CTAs of one tile on an SM overlap their starts and ends instead.
+  // Width 128, 32 heads, us with one and with two tiles a CTA: 64 prompts of
+  // 300 189 and 238, 24 of 640 144 and 171, of 768 186 and 187, 16 of 1000 199
+  // and 196, one of 16384 1673 and 1406; 16 of 4000 under a window of 512 791
+  // and 825, of 1024 1091 and 1067; 64 times 200 queries over 4200 keys 984
+  // and 787, 32 times 100 over 200 44 and 65.  At width 64 one tile was never
+  // slower (16 packed prompts, window 1024: 206 and 281; 8 of 2048 185 and 232).
+  constexpr int64_t kFewKeys = 640;
+  const int64_t in_windows = static_cast<int64_t>(a.window) * a.B;
+  const int64_t keys = a.window > 0 && in_windows < a.n_k ? in_windows : a.n_k;
+  if (D == 64 || a.n_q <= static_cast<int64_t>(kTile) * a.B || keys <= kFewKeys * a.B)
+    return launch_dim<D, 1, 2>(a, encode, sms, 1, stream);
   return launch_dim<D, D == 64 ? 1 : 2, D == 64 ? 2 : 1>(a, encode, sms, 1, stream);
 }
 

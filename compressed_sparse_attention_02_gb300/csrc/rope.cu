@@ -41,8 +41,9 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16384 tokens of 72 heads of width 128 take 102 us (5.9 TB/s) with 3 items a
-// thread in flight and 4 CTAs an SM; 2 items 106, 4 items with 3 CTAs 108.
+// 16384 tokens of 72 heads of width 128 take 90.4 us (6.7 TB/s, 99% of the copy
+// rate) with 3 items a thread in flight and 4 CTAs an SM; 2 items 92.1, 4 items
+// with 3 CTAs 93.2.
 constexpr int kFlight = 3;
 constexpr int kRopeCtas = 4;
 
@@ -120,7 +121,7 @@ cudaError_t launch_rope(const RopeRowsArgs& a, cudaStream_t stream) {
   RopeGrid g;
   const bool in_place = a.in == a.out;
   g.items = (in_place ? a.rope.rope_dim : a.head_dim) >> 4;
-  // A CTA of 256 threads takes about 2400 items (1200: 113 us, 4700: 104):
+  // A CTA of 256 threads takes about 2400 items (1200: 92.7 us, 4700: 94.8):
   // several tokens of few heads, or one token whose heads are split while the
   // grid would not fill the GPU.
   const int64_t row_items = static_cast<int64_t>(a.n_heads) * g.items;

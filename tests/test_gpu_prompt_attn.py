@@ -92,10 +92,20 @@ def test_packed(csa, D, window, sink):
     [(130, 130), (0, 5), (33, 500), (3, 0), (200, 90), (1, 1), (100, 100), (1, 700)],  # ... short ones
 ])
 def test_many_tiles(csa, D, window, lens):
-    """With 48 heads the tiles outnumber the SMs: two tiles a CTA, or two CTAs an SM."""
+    """With 48 heads the tiles outnumber the SMs: two CTAs of one tile an SM."""
+    many_tiles(csa, D, window, lens)
+
+
+@pytest.mark.parametrize("window", [0, 641, 700, 769, 1100])
+def test_many_tiles_that_see_many_keys(csa, window):
+    """... and two tiles a CTA where they see more than 640 keys."""
+    many_tiles(csa, 128, window, [(1500, 1500), (300, 1300), (129, 40), (257, 900)])
+
+
+def many_tiles(csa, D, window, lens):
     x = make(lens, 48, 2, D, seed=window, pad=9)
     check(csa, x, "many tiles", heads=[0, 29, 47], window=window, sink=window % 2 == 0)
-    if window in (0, 300):  # a value that is not finite: seen or not as the formula has it
+    if window in (0, 300, 700):  # a value that is not finite: seen or not as the formula has it
         clean = run(csa, x, window=window)[0]
         y = {k: v.clone() for k, v in x.items()}
         key = lens[0][1] - 60
