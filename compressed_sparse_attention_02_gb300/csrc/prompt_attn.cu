@@ -17,15 +17,15 @@
 // crosses threads.  Keys are walked from the diagonal down: the masked tiles
 // come first.  With one tile a CTA its keys are worked on in halves, one's
 // scores under the other's softmax.  16384 queries of 32 heads of width 128:
-// 1.41 ms, 1560 TFLOP/s, 83% of the matrix product's rate; 16 prompts of 237 to
+// 1.39 ms, 1580 TFLOP/s, 83% of the matrix product's rate; 16 prompts of 237 to
 // 2500 under a window of 1024 at width 64: 206 us, 550 TFLOP/s.
 //
 // P is rounded to bf16 (the products take one type for both operands, and V
 // is bf16); sums and maxima are fp32, over the unrounded weights.
 //
 // A masked weight is 0, and 0 * NaN is NaN: in tiles that some row of the CTA
-// masks, two warps take values that are not finite out of V before the
-// product (rows past the sequence's end become zero), and the rows that do see
+// masks, two warps take values that are not finite out of V as soon as it has
+// landed (rows past the sequence's end become zero), and the rows that do see
 // such a key get its values added at the end, as the formula has them.
 #include <cuda_bf16.h>
 
@@ -87,6 +87,11 @@ __device__ __forceinline__ bool not_finite(uint32_t h) { return (h & 0x7F80u) ==
 // Non-zero where a half of the word is a bf16 infinity or NaN (magnitude bits
 // of 0x7F80 and more carry into the half's top bit).
 __device__ __forceinline__ uint32_t odd_halves(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+// acc + 0 * w, of bf16 pairs: NaN from the first such half on, else still zero.
+__device__ __forceinline__ uint32_t probe(uint32_t w, uint32_t acc) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+  return acc;
+}
 // The word with such halves zeroed.
 __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
   if (not_finite(w)) w &= 0xFFFF0000u;
@@ -242,15 +247,17 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t q_full[kQBufs][QT], q_empty[kQBufs][QT], full[C::kStages], empty[C::kStages];
   __shared__ uint64_t s_full[QT][C::kParts], p_full[QT][C::kParts], pv_done[QT][C::kParts];
-  __shared__ uint64_t o_full[QT], dirty, cleaned, drain, order_full[2], order_empty[2];
+  __shared__ uint64_t o_full[QT], dirty[C::kStages / 2], cleaned[C::kStages / 2];  // (by the values' ring slots)
+  __shared__ uint64_t drain, order_full[2], order_empty[2];
   __shared__ Order<QT> orders[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   // keys of each masked tile whose values are not all finite, as each of the
-  // two cleaning warps found them, of a work item and the next: those of item
-  // number n are valid if odd_item[n & 1] is n + 1
-  __shared__ uint32_t odd_rows[2][2][kMaxMasked][4];
-  __shared__ int odd_tile[2][kMaxMasked], odd_item[2][2];
+  // two cleaning warps found them, of three work items (who cleans item n + 2
+  // knows that every warp has begun item n): those of item number n are valid
+  // if odd_item[n % 3] is n + 1
+  __shared__ uint32_t odd_rows[3][2][kMaxMasked][4];
+  __shared__ int odd_tile[3][kMaxMasked], odd_item[3][2];
   __shared__ float m_s[C::kCluster ? kTile : 1], l_s[C::kCluster ? kTile : 1];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_bufs = smem;
@@ -260,8 +267,10 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   volatile int* abort_flag = &abort_s;
   if (tid == 0) {
     mbar_init(&drain, 1);
-    mbar_init(&dirty, 1);
-    mbar_init(&cleaned, kCleanThreads);
+    for (int i = 0; i < C::kStages / 2; ++i) {
+      mbar_init(dirty + i, 1);
+      mbar_init(cleaned + i, kCleanThreads);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(order_full + i, 1);
       mbar_init(order_empty + i, C::kThreads / 32 - 1);
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     }
     fence_mbar_init();
     abort_s = 0;
-    odd_item[0][0] = odd_item[0][1] = odd_item[1][0] = odd_item[1][1] = 0;
+    for (int i = 0; i < 3; ++i) odd_item[i][0] = odd_item[i][1] = 0;
   }
   if (warp == kTmaWarp && lane == 0) {
     prefetch_tensormap(&tm_q);
@@ -350,10 +359,11 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
             if (seq >= C::kStages) ok = wait_or_abort(empty + slot, ((seq / C::kStages) - 1) & 1, abort_flag, a.status);
             if (!ok) return;
             mbar_arrive_expect_tx(full + slot, C::kTileBytes);
-            const int row = w.sq.k0 + (walk.j_hi - 1 - (s >> 1)) * kTile;
+            const int j = walk.j_hi - 1 - (s >> 1), row = w.sq.k0 + j * kTile;
             for (int k = 0; k < C::kBlocks; ++k)
               tma_load_3d(ring + slot * C::kTileBytes + k * C::kBlockBytes, (s & 1) ? &tm_v : &tm_k, k * 64, kv_head,
                           row, full + slot);
+            if ((s & 1) && o.masked.at(j)) mbar_arrive(dirty + (slot >> 1));
             ++seq;
           };
           // the first keys and values before the queries, whose place may
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       bool ok = true;
       int seq0 = 0;               // ring slots of the items before
       uint32_t n_p[QT] = {};      // weights taken so far, by tile
-      uint32_t n_cleaned = 0;
+      uint32_t parity_c = 0;      // of `cleaned`, a bit a slot
       Order<QT> order;
       for (int item = 0; ok && take(item, &order); ++item) {
         const Walk<QT>& walk = order.walk;
@@ -456,10 +466,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           // this tile's values and the next tile's keys are usually there long
           // before the weights are
           ok = wait_slot(v_seq);
-          if (ok && (it < m_from || it >= m_upto)) {  // one masked tile at a time is with the cleaning warps
-            if (elect_one()) mbar_arrive(&dirty);
-            __syncwarp();
-            ok = wait(&cleaned, n_cleaned++ & 1u);
+          if (ok && (it < m_from || it >= m_upto)) {
+            ok = wait(cleaned + (v_slot >> 1), (parity_c >> (v_slot >> 1)) & 1u);
+            parity_c ^= 1u << (v_slot >> 1);
           }
           if (ok && again) ok = wait_slot(v_seq + 1);
 #pragma unroll
@@ -502,28 +511,29 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       // ---------------- values that are not finite, taken out of masked tiles ----------------
       const int ct = tid - kCleanWarp * 32;
       int seq0 = 0;
-      uint32_t n_cleaned = 0;
+      uint32_t parity_d = 0;  // of `dirty`, a bit a slot
       bool ok = true;
       Order<QT> order;
       for (int item = 0; ok && take(item, &order); ++item) {
         const Work& w = order.w;
         const Walk<QT>& walk = order.walk;
         const Masked& masked = order.masked;
-        const int o = item & 1, half = warp - kCleanWarp;
+        const int o = item % 3, half = warp - kCleanWarp;
         static_assert(kMaxMasked * 4 == 32, "a word a lane");
         int n_masked = 0;
         for (int it = 0; it < walk.n_it; ++it) {
           const int j = walk.j_hi - 1 - it;
           if (!masked.at(j)) continue;
           const int seq = seq0 + 2 * it + 1, slot = seq & (C::kStages - 1);
-          // the product warp has seen the tile's copy complete and holds its slot
-          // until `cleaned`, so the second wait returns at once (and makes the
-          // copied bytes visible here)
-          ok = wait_or_abort(&dirty, n_cleaned & 1, abort_flag, a.status) &&
+          // the tile's copy has been issued, so its slot's phase before is over
+          // (without that the second wait could take it for this one), and
+          // the product warp holds the slot until `cleaned`
+          ok = wait_or_abort(dirty + (slot >> 1), (parity_d >> (slot >> 1)) & 1u, abort_flag, a.status) &&
                wait_or_abort(full + slot, (seq / C::kStages) & 1, abort_flag, a.status);
+          parity_d ^= 1u << (slot >> 1);
           ok = __all_sync(0xffffffffu, ok) != 0;
           if (!ok) break;
-          if (n_masked == 0) {  // (the item before the last, whose places these were, is done with)
+          if (n_masked == 0) {  // (the item three before, whose places these were, is done with)
             odd_rows[o][half][lane >> 2][lane & 3] = 0u;
             __syncwarp();
           }
@@ -540,13 +550,17 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
 #pragma unroll 1
           for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += 8 * kCleanThreads) {
             uint4 u[8];
-            uint32_t any = 0u;
+            uint32_t any[4] = {};
 #pragma unroll
             for (int k = 0; k < 8; ++k) u[k] = tile[i0 + k * kCleanThreads];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              any |= odd_halves(u[k].x) | odd_halves(u[k].y) | odd_halves(u[k].z) | odd_halves(u[k].w);
-            if (any == 0u) continue;
+            for (int k = 0; k < 8; ++k) {
+              any[0] = probe(u[k].x, any[0]);
+              any[1] = probe(u[k].y, any[1]);
+              any[2] = probe(u[k].z, any[2]);
+              any[3] = probe(u[k].w, any[3]);
+            }
+            if (odd_halves(any[0] | any[1] | any[2] | any[3]) == 0u) continue;
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
               const int i = i0 + k * kCleanThreads, r = (i >> 3) & (kTile - 1);
@@ -565,9 +579,8 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
             }
           }
           ++n_masked;
-          ++n_cleaned;
           fence_proxy_async_smem();
-          mbar_arrive(&cleaned);
+          mbar_arrive(cleaned + (slot >> 1));
         }
         seq0 += 2 * walk.n_it;
       }
@@ -718,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           l = finish_row(m * scale2, l, a.sink, w.head, &lse);
           if (a.lse && r < rows) a.lse[row] = lse;
         }
-        const int o2 = item & 1;
+        const int o2 = item % 3;
         const bool odd0 = *const_cast<volatile int*>(&odd_item[o2][0]) == item + 1;
         const bool odd1 = *const_cast<volatile int*>(&odd_item[o2][1]) == item + 1;
 #pragma unroll 1  // (code that runs once waits for its instructions)
@@ -910,8 +923,8 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
   // other's products; where a tile sees few keys, or a sequence has one tile,
   // two CTAs of one tile on an SM overlap their starts and ends instead.
   // Width 128, 32 heads, us with one and with two tiles a CTA: 64 prompts of
-  // 300 189 and 238, 24 of 640 144 and 171, of 768 186 and 187, 16 of 1000 199
-  // and 196, one of 16384 1673 and 1406; 16 of 4000 under a window of 512 791
+  // 300 189 and 238, 24 of 640 144 and 171, of 768 186 and 176, 16 of 1000 199
+  // and 183, one of 16384 1673 and 1391; 16 of 4000 under a window of 512 791
   // and 825, of 1024 1091 and 1067; 64 times 200 queries over 4200 keys 984
   // and 787, 32 times 100 over 200 44 and 65.  At width 64 one tile was never
   // slower (16 packed prompts, window 1024: 206 and 281; 8 of 2048 185 and 232).
