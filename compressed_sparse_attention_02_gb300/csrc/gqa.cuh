@@ -109,6 +109,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // Two fp32 values as one register pair: Blackwell's packed multiply-add and
 // add take half the issue slots of the scalar ones.
 __device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) {

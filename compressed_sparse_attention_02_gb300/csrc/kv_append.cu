@@ -11,10 +11,11 @@
 // Bound by memory for prompts (a row's bf16 read once, its codes written once)
 // and by latency for single tokens (sequence search, page table, scale: loads
 // that depend on each other).  Two forms:
-//  - pages: a CTA takes a page's new rows for a few heads of K or V, one head
-//    after the other with the next one's rows on their way: the angles of the
-//    page's rows are computed once, and a row's channels stay in registers
-//    from their rotation over the maximum to their codes;
+//  - pages: a CTA takes a page's new rows for some heads of K, V or both, one
+//    head after the other with the next one's rows on their way: the angles of
+//    the page's rows are computed once, and a row's channels stay in registers
+//    from their rotation over the maximum to their codes (16000 rows of 8 heads
+//    of 128: 25.7 us, 3.8 TB/s, bound by issue: rotation and conversion);
 //  - rows: a warp takes the rows of one head of K or V in a page, a CTA eight
 //    of them, so a decoded token's heads all run at once.
 #include <cuda_fp16.h>
@@ -101,7 +102,7 @@ __device__ __forceinline__ bool find_page(const KvAppendArgs& a, int* sh, PageRo
 // do (see finite_max).
 __device__ __forceinline__ float item_max(const float (&lo)[8], const float (&hi)[8], float amax) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(lo[j]), fabsf(hi[j])));
+  for (int j = 0; j < 8; ++j) amax = max3(amax, fabsf(lo[j]), fabsf(hi[j]));
   return amax;
 }
 __device__ __forceinline__ float finite_max(const float (&lo)[8], const float (&hi)[8], float amax) {
@@ -118,13 +119,14 @@ __device__ __forceinline__ float warp_max(float x) {
 // An item's 16 codes.
 __device__ __forceinline__ void store_item(uint8_t* row, int cl, int ch, const float (&lo)[8], const float (&hi)[8],
                                            float inv) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    w[j] = e4m3_pair(lo[4 * j] * inv, lo[4 * j + 1] * inv) | e4m3_pair(lo[4 * j + 2] * inv, lo[4 * j + 3] * inv) << 16;
-    w[2 + j] =
-        e4m3_pair(hi[4 * j] * inv, hi[4 * j + 1] * inv) | e4m3_pair(hi[4 * j + 2] * inv, hi[4 * j + 3] * inv) << 16;
-  }
+  const uint64_t inv2 = pair_of(inv, inv);
+  auto four = [&](const float* x) {
+    float y[4];
+    split(mul2(pair_of(x[0], x[1]), inv2), &y[0], &y[1]);
+    split(mul2(pair_of(x[2], x[3]), inv2), &y[2], &y[3]);
+    return e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
+  };
+  const uint32_t w[4] = {four(lo), four(lo + 4), four(hi), four(hi + 4)};
   *reinterpret_cast<uint2*>(row + cl) = make_uint2(w[0], w[1]);
   *reinterpret_cast<uint2*>(row + ch) = make_uint2(w[2], w[3]);
 }
@@ -163,8 +165,12 @@ __device__ __forceinline__ Slab slab_of(const KvAppendArgs& a, const PageRows& p
   return s;
 }
 
+// CTAs an SM (what their registers leave room for).
 template <int THREADS, int NI>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel(const KvAppendArgs a, const int heads) {
+constexpr int kPagesCtas = (NI == 1 ? 768 : 512) / THREADS;
+template <int THREADS, int NI>
+__global__ void __launch_bounds__(THREADS, kPagesCtas<THREADS, NI>)
+    kv_append_pages_kernel(const KvAppendArgs a, const int heads) {
   constexpr int kWarps = THREADS / 32;
   extern __shared__ float2 sc_s[];  // K: the rows' (sin, cos), rope_dim / 2 each
   __shared__ int sh[kWarps + 2];
@@ -172,42 +178,54 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool is_v = blockIdx.z != 0;
   PageRows p;
   if (!find_page<THREADS>(a, sh, &p)) return;
-  RopeArgs rope = a.rope;
-  if (is_v) rope.rope_dim = rope.offset = 0;
+  const RopeArgs& rope = a.rope;
   const int pairs = rope.rope_dim >> 1, rotated = rope.rope_dim >> 4;
   const int items = a.cache.head_dim >> 4;  // a power of two
   const int items_shift = __ffs(items) - 1;
   const int n_items = (p.last - p.first) << items_shift;
-  const int h1 = min(static_cast<int>(blockIdx.y + 1) * heads, a.cache.n_kv_heads);
+  // K of the CTA's heads, then V of them, or (two CTAs in z) one of the two.
+  // src: where the thread's items of the head to come begin (their second
+  // chunks lie gap channels behind); dst: in a head's slab
+  const int h0 = blockIdx.y * heads, nh = min(heads, a.cache.n_kv_heads - h0);
+  const bool only_v = blockIdx.z != 0;
+  const int k_steps = only_v ? 0 : nh, steps = gridDim.z == 1 ? 2 * nh : nh;
+  Slab sl = slab_of(a, p, h0, only_v);
+  const uint16_t* src[NI];
+  int dst[NI], gap[NI];
+  int64_t src_next = only_v ? a.v_stride_h : a.k_stride_h;
+#pragma unroll
+  for (int k = 0; k < NI; ++k) {
+    const int i = tid + k * THREADS;
+    int cl, ch;
+    item_chunks(rope, i & (items - 1), &cl, &ch);
+    src[k] = sl.src + (i >> items_shift) * sl.src_stride + cl;
+    dst[k] = (p.first + (i >> items_shift)) * a.cache.head_dim + cl;
+    gap[k] = ch - cl;
+  }
   uint4 u[NI], v[NI];  // the rows of the head to come
-  auto fetch = [&](int head) {
-    const Slab sl = slab_of(a, p, head, is_v);
+  auto fetch = [&]() {
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
-      const int i = tid + k * THREADS;
       u[k] = v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i >= n_items) continue;
-      int cl, ch;
-      item_chunks(rope, i & (items - 1), &cl, &ch);
-      const uint16_t* row = sl.src + (i >> items_shift) * sl.src_stride;
-      u[k] = __ldg(reinterpret_cast<const uint4*>(row + cl));
-      v[k] = __ldg(reinterpret_cast<const uint4*>(row + ch));
+      if (tid + k * THREADS >= n_items) continue;
+      u[k] = __ldg(reinterpret_cast<const uint4*>(src[k]));
+      v[k] = __ldg(reinterpret_cast<const uint4*>(src[k] + gap[k]));
+      src[k] += src_next;
     }
   };
-  const int h0 = blockIdx.y * heads;
-  fetch(h0);
-  for (int i = tid; i < (p.last - p.first) * pairs; i += THREADS) {
+  fetch();
+  for (int i = tid; k_steps > 0 && i < (p.last - p.first) * pairs; i += THREADS) {
     const int r = i / pairs, j = i - r * pairs;
     float s, c;
     rope_sincos_exact(p.pos0 + p.first + r, __ldg(rope.turns + j), &s, &c);
     sc_s[r * pairs + angle_slot(j, rotated)] = make_float2(s * rope.mscale, c * rope.mscale);
   }
   __syncthreads();
-  for (int head = h0; head < h1; ++head) {
-    const Slab sl = slab_of(a, p, head, is_v);
+  for (int step = 0; step < steps; ++step) {
+    if (step == nh) sl = slab_of(a, p, h0, true);
+    const int turned = step < k_steps ? rotated : 0;
     const float was = p.first > 0 ? *sl.scale : 0.f;
     float lo[NI][8], hi[NI][8];
     float amax = 0.f;
@@ -216,16 +234,25 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel
       const int i = tid + k * THREADS, it = i & (items - 1);
       unpack_bf16(u[k], lo[k]);
       unpack_bf16(v[k], hi[k]);
-      if (it < rotated && i < n_items) {
+      if (it < turned && i < n_items) {
         float2 sc[8];
         load_angles(sc_s + (i >> items_shift) * pairs, it, rotated, sc);
         rotate_item(rope.half != 0, sc, lo[k], hi[k]);
       }
       amax = item_max(lo[k], hi[k], amax);
     }
-    if (head + 1 < h1) fetch(head + 1);
+    if (step + 1 == nh) {
+      const Slab sv = slab_of(a, p, h0, true);
+      src_next = a.v_stride_h;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const int i = tid + k * THREADS;
+        src[k] = sv.src + (i >> items_shift) * sv.src_stride + (dst[k] & (a.cache.head_dim - 1));
+      }
+    }
+    if (step + 1 < steps) fetch();
     // (two arrays of maxima in turn: the next head's do not wait for this one's readers)
-    float* top = max_s[head & 1];
+    float* top = max_s[step & 1];
     amax = warp_max(amax);
     if (lane == 0) top[warp] = amax;
     __syncthreads();
@@ -245,14 +272,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) kv_append_pages_kernel
     const float s = scale_of(amax, was), inv = __frcp_rn(s);  // exact for a power of two
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
-      const int i = tid + k * THREADS;
-      if (i >= n_items) continue;
-      int cl, ch;
-      item_chunks(rope, i & (items - 1), &cl, &ch);
-      store_item(sl.codes + (p.first + (i >> items_shift)) * a.cache.head_dim, cl, ch, lo[k], hi[k], inv);
+      if (tid + k * THREADS < n_items) store_item(sl.codes, dst[k], dst[k] + gap[k], lo[k], hi[k], inv);
     }
     if (p.first > 0 && s != was) round_again(sl.codes, p.first * a.cache.head_dim, __fdiv_rn(was, s), tid, THREADS);
     if (tid == 0 && (p.first == 0 || s != was)) *sl.scale = s;
+    sl.codes += a.cache.page * a.cache.head_dim;
+    ++sl.scale;
   }
 }
 
@@ -310,18 +335,25 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvApp
 constexpr int kMaxAngles = 128 * 64 * static_cast<int>(sizeof(float2));  // of 128 rows of width 128
 template <int THREADS, int NI>
 cudaError_t launch_pages(const KvAppendArgs& a, unsigned items, int sms, cudaStream_t stream) {
-  // Heads a CTA: as many as leave about two CTAs an SM (5 prompts of 16000
-  // rows in all, 8 heads of 128: 28.8 us; four CTAs an SM 33.1, seven 35.9).
+  // A CTA a page, K and V of all heads; while the GPU has room for more CTAs, K
+  // and V apart, then the heads in groups (each group computes the angles
+  // anew).  us, one CTA a page and K and V apart: 5 prompts of 16000 rows in
+  // all, 8 heads of 128, pages of 64 25.7 and 27.6; one of 16384, pages of 128
+  // 27.1 and 35.0; 32 of up to 500 22.8 and 19.5; 64 times 4 rows 12.8, 6.4 with
+  // two groups apart.
   const int H = a.cache.n_kv_heads;
-  int groups = static_cast<int>((static_cast<int64_t>(sms) * 2 + 2 * items - 1) / (2 * items));
-  groups = groups < 1 ? 1 : groups > H ? H : groups;
+  const int64_t slots = static_cast<int64_t>(sms) * kPagesCtas<THREADS, NI>;
+  const int64_t pages = (a.n_rows >> a.cache.page_shift) + a.B;  // about
+  const int z = 2 * slots >= 3 * pages ? 2 : 1;
+  const int64_t fit = slots / (z * pages);
+  const int groups = fit < 1 ? 1 : fit > H ? H : static_cast<int>(fit);
   const int heads = (H + groups - 1) / groups;
   const size_t smem = static_cast<size_t>(a.cache.page) * (a.rope.rope_dim / 2) * sizeof(float2);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = kernel_limits(reinterpret_cast<const void*>(kv_append_pages_kernel<THREADS, NI>), kMaxAngles, 0,
                                       &done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_append_pages_kernel<THREADS, NI>, dim3(items, (H + heads - 1) / heads, 2), dim3(THREADS), smem,
+  return launch_pdl(kv_append_pages_kernel<THREADS, NI>, dim3(items, (H + heads - 1) / heads, z), dim3(THREADS), smem,
                     stream, a, heads);
 }
 
@@ -338,7 +370,8 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
   // Few rows a sequence: a warp a head (128 tokens of 8 heads of 64 4.2 us, 5.8
   // in the other form; one token 3.3 and 2.9).
   if (a.n_rows <= 2 * static_cast<int64_t>(a.B))
-    return launch_pdl(kv_append_rows_kernel, dim3(x, (2 * a.cache.n_kv_heads + 7) / 8), dim3(kRowThreads), 0, stream, a);
+    return launch_pdl(kv_append_rows_kernel, dim3(x, (2 * a.cache.n_kv_heads + 7) / 8), dim3(kRowThreads), 0, stream,
+                      a);
   const int sms = current_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   // 16-channel items of a page: page * head_dim / 16, 64 .. 1024

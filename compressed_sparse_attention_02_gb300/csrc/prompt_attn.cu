@@ -76,12 +76,6 @@ struct Cfg {
   static_assert(!kCluster || kStages * kTileBytes >= kTile * D * 4, "the sums fit the ring");
 };
 
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
 __device__ __forceinline__ bool not_finite(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 // Non-zero where a half of the word is a bf16 infinity or NaN (magnitude bits
