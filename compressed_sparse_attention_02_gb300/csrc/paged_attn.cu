@@ -576,17 +576,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 
 // Finishes the pairs that the shares' borders divide, from their shares' records
 // first to last.  With SPLIT 1 a CTA looks at one share's end, and a warp takes
-// a row.  Else CTA (x, y) takes row y of pair x, each of its warps a stretch of
-// the records.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeWarps = kMergeThreads / 32;
+// a row.  Else CTA (x, y) takes row y of pair x, each of its SPLIT warps a
+// stretch of the records.
+constexpr int merge_warps(int split) { return split == 1 ? 8 : split; }
 
 template <int D, int SPLIT>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnArgs a, const int shares) {
+__global__ void __launch_bounds__(32 * merge_warps(SPLIT))
+    paged_merge_kernel(const PagedAttnArgs a, const int shares) {
   using C = Cfg<D>;
+  constexpr int kMergeWarps = merge_warps(SPLIT);
   constexpr int kPer = D / 32;  // channels a lane, neighbours
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
-  static_assert(SPLIT == 1 || SPLIT == kMergeWarps, "a row's stretches are a CTA's warps");
   __shared__ float m_s[kMergeWarps], l_s[kMergeWarps];
   __shared__ __align__(16) float n_s[kMergeWarps][D];
   pdl_launch_dependents();
@@ -668,13 +668,16 @@ cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int group = a.n_heads / a.cache.n_kv_heads, rows = group < kRows ? group : kRows;
   const int64_t pairs = static_cast<int64_t>(a.B) * a.cache.n_kv_heads * ((group + kRows - 1) / kRows);
-  // Many pairs: few records each, a warp a row.  Few pairs: up to all shares'
-  // records of one, eight warps a row and a CTA for each row.
+  // Many pairs: few records each, a warp a row.  Few pairs: a CTA a row, of 16
+  // warps from 32 records a pair on (4 sequences of 32768 tokens, 4 heads: 22.2
+  // us, 28.1 with 8; 16 of up to 4000, 10 records: 24.7 and 22.8).
   const int shares = ctas * kWarps;
-  if (!few_pairs(pairs, shares))
-    return launch_pdl(paged_merge_kernel<D, 1>, dim3(shares - 1), dim3(kMergeThreads), 0, stream, a, shares);
   const dim3 grid(static_cast<unsigned>(pairs), rows);
-  return launch_pdl(paged_merge_kernel<D, kMergeWarps>, grid, dim3(kMergeThreads), 0, stream, a, shares);
+  if (!few_pairs(pairs, shares))
+    return launch_pdl(paged_merge_kernel<D, 1>, dim3(shares - 1), dim3(32 * merge_warps(1)), 0, stream, a, shares);
+  if (pairs * 32 > shares)
+    return launch_pdl(paged_merge_kernel<D, 8>, grid, dim3(32 * merge_warps(8)), 0, stream, a, shares);
+  return launch_pdl(paged_merge_kernel<D, 16>, grid, dim3(32 * merge_warps(16)), 0, stream, a, shares);
 }
 
 }  // namespace

@@ -130,6 +130,20 @@ def test_many_sequences_of_mixed_lengths(csa):
     assert csa.csa_check_status() == 0
 
 
+@pytest.mark.parametrize("seqs,Hq,Hkv", [(1, 2, 1), (6, 16, 8), (12, 10, 10), (24, 8, 8)])
+def test_number_of_pairs(csa, seqs, Hq, Hkv):
+    """One pair of a sequence and a KV head to some hundred, empty sequences among them: a pair's parts are joined in
+    other ways where the pairs are few."""
+    g = torch.Generator().manual_seed(seqs)
+    lens = torch.randint(1, 900, (seqs,), generator=g).tolist()
+    lens[0] = 5000
+    if seqs > 2:
+        lens[2] = 0
+    for D in (64, 128):
+        check(csa, make(lens, Hq, Hkv, D, 64, seed=seqs), "pairs", sink=D == 64)
+    assert csa.csa_check_status() == 0
+
+
 def test_scales_of_any_size(csa):
     """Pages whose scales differ by 2^40, pages of zeros with the smallest scale, a value scale of zero."""
     x = make([500, 130, 64], 8, 2, 128, 16, seed=8)
