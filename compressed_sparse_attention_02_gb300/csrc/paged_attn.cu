@@ -18,7 +18,7 @@
 // copies, running maximum and accumulators: it waits for no other, and its
 // copies run on into the next pair while it finishes one (with a share a CTA, whose
 // warps joined their sums at each pair's end: 256 sequences of up to 600
-// tokens 91 us, 50 so; 64 of up to 32768, 393 and 381 us, 6.6 TB/s).
+// tokens 91 us, 47 so; 64 of up to 32768, 393 and 378 us, 6.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -43,7 +43,8 @@ constexpr float kLag = 4.f;
 constexpr float kWeightExp = 11.f;
 constexpr float kNone = -1e30f;           // running maximum before the first token
 
-template <int D>
+// H: halves of the 16 rows that hold query heads (1: groups of up to 8).
+template <int D, int H>
 struct Cfg {
   // CTAs an SM and tiles in flight a warp.  At width 64 with 8 heads: 64
   // sequences of up to 8192 tokens 66 us with 3 CTAs and no spills, 85 with 4;
@@ -54,8 +55,10 @@ struct Cfg {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmem = kWarps * kWarpBytes;
-  static constexpr int kRecord = kRows * (D + 2);           // floats of a partial result: sums, maxima, weights' sums
 };
+
+template <int D>
+constexpr int kRecord = kRows * (D + 2);  // floats of a partial result: sums, maxima, weights' sums
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -86,12 +89,17 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint3
       : "r"(four));
 }
 
+// c += a b; a of the halves that hold heads (the other half's rows are zero,
+// and so stay its sums).
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
+  mma_f16_16816(c, {a[0], 0u, a[1], 0u}, b0, b1);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
@@ -155,9 +163,9 @@ struct __align__(16) Cut {
 // of 100 tokens: 14.5 us, 9.8 with a CTA a share).
 __host__ __device__ __forceinline__ bool few_pairs(int64_t pairs, int64_t shares) { return pairs * 8 < shares; }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
-  using C = Cfg<D>;
+template <int D, int H>
+__global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
+  using C = Cfg<D, H>;
   constexpr int kK = D / 16;       // 16-channel steps of q . k
   constexpr int kN = D / 8;        // 8-channel tiles of the output
   constexpr int kChunks = D / 16;  // 16-byte chunks a row
@@ -330,10 +338,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 
     // the query rows g and g + 8 as fragments: lane cq holds channels
     // cq * D/4 .. of each, in the order in which it reads the keys' bytes
-    uint32_t qf[kK][4];
-    float fac[2];
+    uint32_t qf[kK][2 * H];
+    float fac[H];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < H; ++half) {
       const int r = g + 8 * half;
       float x[D / 4];
       if (r < rows) {
@@ -361,15 +369,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 #pragma unroll
       for (int s = 0; s < kK; ++s) {
         qf[s][half] = pack_f16(x[4 * s] * up, x[4 * s + 1] * up);
-        qf[s][2 + half] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
+        qf[s][H + half] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
       }
     }
 
     float o[kN][4];
 #pragma unroll
     for (int j = 0; j < kN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[2] = {kNone, kNone}, mv[2] = {kNone, kNone};
-    uint64_t l2[2] = {0ull, 0ull};  // sums of weights, as pairs of partial sums
+    float m[H], mv[H];
+    uint64_t l2[H];  // sums of weights, as pairs of partial sums
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      m[h] = mv[h] = kNone;
+      l2[h] = 0ull;
+    }
 
     for (int it = 0; it < take; ++it) {
       cp_async_wait_pending(C::kStages - 2);
@@ -405,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < H; ++h) {
             const float k = fac[h] * (n < 2 ? sc.x : sc.y);
             split(mul2(pair_of(x[n][2 * h], x[n][2 * h + 1]), pair_of(k, k)), &x[n][2 * h], &x[n][2 * h + 1]);
           }
@@ -415,15 +428,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int t = t0 + 8 * n + 2 * cq + e;
-              if (t < sp.lo || t >= sp.len || ((bad >> (n >> 1)) & 1)) x[n][e] = x[n][2 + e] = -INFINITY;
+              if (t < sp.lo || t >= sp.len || ((bad >> (n >> 1)) & 1))
+#pragma unroll
+                for (int h = 0; h < H; ++h) x[n][2 * h + e] = -INFINITY;
             }
         }
         // maxima of the logits, and of logit + log2(v_scale), the weights' exponents
         const float lv[2] = {__log2f(sc.z), __log2f(sc.w)};
-        float top[2], topv[2];
+        float top[H], topv[H];
         bool grown = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
           const float a0 = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
           const float a1 = fmaxf(fmaxf(x[2][2 * h], x[2][2 * h + 1]), fmaxf(x[3][2 * h], x[3][2 * h + 1]));
           top[h] = fmaxf(a0, a1);
@@ -432,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
         }
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < H; ++h) {
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
               top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
@@ -451,11 +466,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
             mv[h] = mv1;
           }
         }
-        uint32_t pf[2][4];
+        uint32_t pf[2][2 * H];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < H; ++h) {
             const float w = ex2(lv[s] + (m[h] - mv[h]) + kWeightExp);
             const uint64_t ww = pair_of(w, w), mm = pair_of(-m[h], -m[h]);
             float p0, p1, p2, p3;
@@ -466,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
             split(mul2(p01, ww), &p0, &p1);
             split(mul2(p23, ww), &p2, &p3);
             pf[s][h] = pack_f16(p0, p1);
-            pf[s][2 + h] = pack_f16(p2, p3);
+            pf[s][H + h] = pack_f16(p2, p3);
           }
         // out += weights . V: tokens 2cq, 2cq+1, 2cq+8, 2cq+9 of each 16, the
         // bytes of two tokens paired by channel; lane group g holds channels
@@ -508,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas) paged_attn_kernel(con
     // Accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j.
     const bool whole = take == nt;
     const int slot = first ? 0 : 1;
-    float* part = records + (share * 2 + slot) * C::kRecord;
+    float* part = records + (share * 2 + slot) * kRecord<D>;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
       const int r = g + 8 * h;
       float l, other;
       split(l2[h], &l, &other);
@@ -583,7 +598,6 @@ constexpr int merge_warps(int split) { return split == 1 ? 8 : split; }
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
     paged_merge_kernel(const PagedAttnArgs a, const int shares) {
-  using C = Cfg<D>;
   constexpr int kMergeWarps = merge_warps(SPLIT);
   constexpr int kPer = D / 32;  // channels a lane, neighbours
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
@@ -596,7 +610,7 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_rec = cut.last - cut.first + 1, rows = cut.rows >> 1;
   auto record = [&](int k) {
-    return records + (static_cast<int64_t>(cut.first + k) * 2 + (k == 0 ? cut.rows & 1 : 0)) * C::kRecord;
+    return records + (static_cast<int64_t>(cut.first + k) * 2 + (k == 0 ? cut.rows & 1 : 0)) * kRecord<D>;
   };
   for (int r = SPLIT == 1 ? warp : blockIdx.y; r < rows; r += SPLIT == 1 ? kMergeWarps : gridDim.y) {
     const int part = SPLIT == 1 ? 0 : warp;
@@ -657,14 +671,14 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
   }
 }
 
-template <int D>
+template <int D, int H>
 cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
-  using C = Cfg<D>;
+  using C = Cfg<D, H>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = kernel_limits(reinterpret_cast<const void*>(paged_attn_kernel<D>), C::kSmem, 0, &done);
+  cudaError_t e = kernel_limits(reinterpret_cast<const void*>(paged_attn_kernel<D, H>), C::kSmem, 0, &done);
   if (e != cudaSuccess) return e;
   const int ctas = sms * C::kCtas;
-  e = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kThreads), C::kSmem, stream, a);
+  e = launch_pdl(paged_attn_kernel<D, H>, dim3(ctas), dim3(kThreads), C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   const int group = a.n_heads / a.cache.n_kv_heads, rows = group < kRows ? group : kRows;
   const int64_t pairs = static_cast<int64_t>(a.B) * a.cache.n_kv_heads * ((group + kRows - 1) / kRows);
@@ -683,13 +697,20 @@ cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_attn_bytes(int head_dim, int sms) {
-  const size_t ctas = static_cast<size_t>(sms) * (head_dim == 64 ? Cfg<64>::kCtas : Cfg<128>::kCtas);
+  static_assert(Cfg<128, 1>::kCtas == Cfg<128, 2>::kCtas, "one size for both");
+  const size_t ctas = static_cast<size_t>(sms) * (head_dim == 64 ? Cfg<64, 2>::kCtas : Cfg<128, 2>::kCtas);
   return ctas * kWarps * (sizeof(Cut) + 2 * kRows * (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
   if (a.B <= 0) return cudaSuccess;
-  return a.cache.head_dim == 128 ? launch_dim<128>(a, sms, stream) : launch_dim<64>(a, sms, stream);
+  if (a.cache.head_dim == 64) return launch_dim<64, 2>(a, sms, stream);
+  // Groups of up to 8 leave the other half's softmax out (256 sequences of up
+  // to 600 tokens, groups of 4: 46.9 us, 50.1 with it; 64 of up to 32768, groups
+  // of 8: 378 and 381).  At width 64 that was no faster (96 sequences under a
+  // window: 83 and 77 us).
+  const bool low = a.n_heads / a.cache.n_kv_heads <= 8;
+  return low ? launch_dim<128, 1>(a, sms, stream) : launch_dim<128, 2>(a, sms, stream);
 }
 
 }  // namespace csa
