@@ -18,7 +18,7 @@
 // come first.  With one tile a CTA its keys are worked on in halves, one's
 // scores under the other's softmax.  16384 queries of 32 heads of width 128:
 // 1.39 ms, 1580 TFLOP/s, 83% of the matrix product's rate; 16 prompts of 237 to
-// 2500 under a window of 1024 at width 64: 206 us, 550 TFLOP/s.
+// 2500 under a window of 1024 at width 64: 204 us, 555 TFLOP/s.
 //
 // P is rounded to bf16 (the products take one type for both operands, and V
 // is bf16); sums and maxima are fp32, over the unrounded weights.
@@ -54,8 +54,14 @@ struct Cfg {
   static constexpr int kBlocks = D / 64;              // 128-byte wide blocks of a tile
   static constexpr int kBlockBytes = kTile * 128;
   static constexpr int kStages = CTAS == 2 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
-  static constexpr int kQBufs = CTAS == 2 && D == 64 ? 2 : 1;     // of the queries: the next tile's, where there is room
-  static constexpr int kSmem = (kQBufs * QT + kStages) * kTileBytes + 1024;
+  // The output is staged 32 channels at a time in a place of its own, so that
+  // the next queries are copied and multiplied under it; two tiles of them, of
+  // which one's softmax runs under the other's end anyway, stage it whole where
+  // their queries were (32 prompts of 500 131 us, 143 so; 16 of 1000 with two
+  // tiles a CTA 183 us, 210 otherwise).
+  static constexpr bool kOwnStage = QT == 1;
+  static constexpr int kOutBytes = kOwnStage ? kTile * 64 : 0;
+  static constexpr int kSmem = (QT + kStages) * kTileBytes + kOutBytes + 1024;
   // Parts that a tile of keys is worked on in: with one tile of queries the
   // scores of one half are computed while the other's softmax runs.
   static constexpr int kParts = QT == 1 ? 2 : 1;
@@ -237,9 +243,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
                        const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a, const int cluster_size) {
   using C = Cfg<D, QT, CTAS>;
   constexpr int kTmaWarp = 4 * QT, kMmaWarp = 4 * QT + 1, kCleanWarp = 4 * QT + 2;
-  constexpr int kRowsCta = QT * kTile, kQBufs = C::kQBufs;
+  constexpr int kRowsCta = QT * kTile;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t q_full[kQBufs][QT], q_empty[kQBufs][QT], full[C::kStages], empty[C::kStages];
+  __shared__ uint64_t q_full[QT], q_empty[QT], full[C::kStages], empty[C::kStages];
   __shared__ uint64_t s_full[QT][C::kParts], p_full[QT][C::kParts], pv_done[QT][C::kParts];
   __shared__ uint64_t o_full[QT], dirty[C::kStages / 2], cleaned[C::kStages / 2];  // (by the values' ring slots)
   __shared__ uint64_t drain, order_full[2], order_empty[2];
@@ -254,8 +260,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
   __shared__ int odd_tile[3][kMaxMasked], odd_item[3][2];
   __shared__ float m_s[C::kCluster ? kTile : 1], l_s[C::kCluster ? kTile : 1];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* q_bufs = smem;
-  uint8_t* ring = smem + kQBufs * QT * C::kTileBytes;
+  uint8_t* q_s = smem;
+  uint8_t* ring = smem + QT * C::kTileBytes;
+  uint8_t* out_s = ring + C::kStages * C::kTileBytes;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* abort_flag = &abort_s;
@@ -274,10 +281,8 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       mbar_init(empty + i, 1);
     }
     for (int t = 0; t < QT; ++t) {
-      for (int q = 0; q < kQBufs; ++q) {
-        mbar_init(&q_full[q][t], 1);
-        mbar_init(&q_empty[q][t], kTile);
-      }
+      mbar_init(q_full + t, 1);
+      mbar_init(q_empty + t, kTile);
       for (int h = 0; h < C::kParts; ++h) {
         mbar_init(&s_full[t][h], 1);
         mbar_init(&p_full[t][h], kTile);
@@ -360,18 +365,17 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
             if ((s & 1) && o.masked.at(j)) mbar_arrive(dirty + (slot >> 1));
             ++seq;
           };
-          // the first keys and values before the queries, whose place may
-          // still hold the item before's output
+          // the first keys before the queries, which wait for the item before's
+          // last scores, and the values, which wait for its last product
           int s = 0;
-          for (; ok && s < min(2, 2 * walk.n_it); ++s) load(s);
-          const int buf = item % kQBufs, use = item / kQBufs;
+          for (; ok && s < min(1, walk.n_it); ++s) load(s);
           for (int t = 0; ok && t < QT; ++t) {
-            if (use > 0) ok = wait_or_abort(&q_empty[buf][t], (use - 1) & 1, abort_flag, a.status);
+            if (item > 0) ok = wait_or_abort(q_empty + t, (item - 1) & 1, abort_flag, a.status);
             if (!ok) break;
-            mbar_arrive_expect_tx(&q_full[buf][t], C::kTileBytes);
+            mbar_arrive_expect_tx(q_full + t, C::kTileBytes);
             for (int k = 0; k < C::kBlocks; ++k)
-              tma_load_3d(q_bufs + (buf * QT + t) * C::kTileBytes + k * C::kBlockBytes, &tm_q, k * 64, w.head,
-                          w.sq.q0 + w.row0 + t * kTile, &q_full[buf][t]);
+              tma_load_3d(q_s + t * C::kTileBytes + k * C::kBlockBytes, &tm_q, k * 64, w.head,
+                          w.sq.q0 + w.row0 + t * kTile, q_full + t);
             ++n_q[t];
           }
           for (; ok && s < 2 * walk.n_it; ++s) load(s);
@@ -380,8 +384,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       }
       if (lane == 0) {  // every copy lands before the CTA ends (also after an abort)
         for (int t = 0; t < QT; ++t)
-          for (int k = max(0, n_q[t] - kQBufs); k < n_q[t]; ++k)
-            mbar_wait(&q_full[k % kQBufs][t], (k / kQBufs) & 1, a.status);
+          if (n_q[t] > 0) mbar_wait(q_full + t, (n_q[t] - 1) & 1, a.status);
         for (int k = max(0, seq - C::kStages); k < seq; ++k)
           mbar_wait(full + (k & (C::kStages - 1)), (k / C::kStages) & 1, a.status);
       }
@@ -420,11 +423,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           end[t] = uniform(walk.end(t));
         }
         const int m_from = uniform(walk.j_hi - masked.from), m_upto = uniform(walk.j_hi - 1 - masked.upto);
-        const int buf = item % kQBufs;
-        const uint32_t qb = smem_u32(q_bufs + buf * QT * C::kTileBytes), q_par = (item / kQBufs) & 1;
         // scores of part h of a tile of keys, S_t = Q_t K^T (one lane)
         auto s_of = [&](int t, int h, uint64_t k_desc) {
-          const uint64_t q_desc = smem_desc(qb + t * C::kTileBytes, 16, 1024, kSwizzle128B);
+          const uint64_t q_desc = smem_desc(smem_u32(q_s) + t * C::kTileBytes, 16, 1024, kSwizzle128B);
           k_desc += h * (C::kPart * 128 >> 4);
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         const uint64_t k_first = smem_desc(rb + (seq0 & (C::kStages - 1)) * C::kTileBytes, 16, 1024, kSwizzle128B);
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-          if (ok) ok = wait(&q_full[buf][t], q_par);
+          if (ok) ok = wait(q_full + t, item & 1);
           if (ok && begin[t] == 0 && end[t] > 0) {
             tc_fence_after();
             if (elect_one()) {
@@ -616,6 +617,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        if (C::kOwnStage && part + 1 == n_tiles * C::kParts) mbar_arrive(q_empty + t);  // the queries' last scores
         constexpr int kC = C::kPart / 32;
         uint32_t s[kC][32];
 #pragma unroll
@@ -703,12 +705,12 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         mbar_arrive(&p_full[t][h]);
       }
       n_s += n_tiles;
-      uint8_t* q_s = q_bufs + ((item % kQBufs) * QT + t) * C::kTileBytes;
-      if (ok) {  // (a tile that sees no keys: its queries have landed where its output is staged)
+      if (ok) {  // (a tile that sees no keys: not before its queries have landed, so that no phase is passed by)
         ok = loaded ? wait_or_abort(o_full + t, n_o++ & 1, abort_flag, a.status)
-                    : wait_or_abort(&q_full[item % kQBufs][t], (item / kQBufs) & 1, abort_flag, a.status);
+                    : wait_or_abort(q_full + t, item & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
+        if (!loaded) mbar_arrive(q_empty + t);
       }
       if (!ok) break;
       const int rows = w.rows(t);
@@ -728,6 +730,11 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         const int o2 = item % 3;
         const bool odd0 = *const_cast<volatile int*>(&odd_item[o2][0]) == item + 1;
         const bool odd1 = *const_cast<volatile int*>(&odd_item[o2][1]) == item + 1;
+        // the warp's 32 rows are staged, then stored with neighbouring lanes on
+        // one row
+        uint16_t* out = a.out + (static_cast<int64_t>(w.sq.q0 + w.row0 + t * kTile) * a.n_heads + w.head) * D;
+        const int w0 = (warp & 3) * 32;
+        uint8_t* stage = C::kOwnStage ? out_s + w0 * 64 : q_s + t * C::kTileBytes + w0 * 128;
 #pragma unroll 1  // (code that runs once waits for its instructions)
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -767,7 +774,6 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
                   make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
             continue;
           }
-          uint8_t* line = q_s + (c >> 1) * C::kBlockBytes + r * 128;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t v[4];
@@ -776,26 +782,41 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
               const __nv_bfloat162 y = __floats2bfloat162_rn(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]);
               v[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + k) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            uint8_t* to = C::kOwnStage ? stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)
+                                       : stage + (c >> 1) * C::kBlockBytes + lane * 128 +
+                                             ((((c & 1) * 4 + k) ^ (lane & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          if (C::kOwnStage) {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rr = 8 * k + lane / 4, ch = lane % 4;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+              if (w0 + rr < rows)
+                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(w0 + rr) * a.n_heads * D + 32 * c + 8 * ch) = v;
+            }
+            __syncwarp();
           }
         }
-        // the warp's 32 rows, staged where its queries were (every product with
-        // them has finished), stored with neighbouring lanes on one row
-        __syncwarp();
-        constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
-        const int w0 = (warp & 3) * 32;
-        uint16_t* out = a.out + (static_cast<int64_t>(w.sq.q0 + w.row0 + t * kTile) * a.n_heads + w.head) * D;
+        if (!C::kOwnStage) {
+          __syncwarp();
+          constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
 #pragma unroll 4
-        for (int k = 0; k < (shared ? 0 : 32 / kRowsAtOnce); ++k) {
-          const int rr = w0 + k * kRowsAtOnce + lane / kChunks, ch = lane % kChunks;
-          const uint4 v = *reinterpret_cast<const uint4*>(q_s + (ch >> 3) * C::kBlockBytes + rr * 128 +
-                                                          (((ch & 7) ^ (rr & 7)) << 4));
-          if (rr < rows) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(rr) * a.n_heads * D + ch * 8) = v;
+          for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
+            const int rr = k * kRowsAtOnce + lane / kChunks, ch = lane % kChunks;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + (ch >> 3) * C::kBlockBytes + rr * 128 +
+                                                            (((ch & 7) ^ (rr & 7)) << 4));
+            if (w0 + rr < rows)
+              *reinterpret_cast<uint4*>(out + static_cast<int64_t>(w0 + rr) * a.n_heads * D + 8 * ch) = v;
+          }
         }
       }
+      if (!C::kOwnStage && loaded) {
+        fence_proxy_async_smem();  // the next queries are copied over what was staged
+        mbar_arrive(q_empty + t);
+      }
       tc_fence_before();
-      fence_proxy_async_smem();  // the next queries are copied over what was staged
-      mbar_arrive(&q_empty[item % kQBufs][t]);
     }
   }
   __syncthreads();
@@ -917,11 +938,12 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
   // other's products; where a tile sees few keys, or a sequence has one tile,
   // two CTAs of one tile on an SM overlap their starts and ends instead.
   // Width 128, 32 heads, us with one and with two tiles a CTA: 64 prompts of
-  // 300 189 and 238, 24 of 640 144 and 171, of 768 186 and 176, 16 of 1000 199
-  // and 183, one of 16384 1673 and 1391; 16 of 4000 under a window of 512 791
-  // and 825, of 1024 1091 and 1067; 64 times 200 queries over 4200 keys 984
-  // and 787, 32 times 100 over 200 44 and 65.  At width 64 one tile was never
-  // slower (16 packed prompts, window 1024: 206 and 281; 8 of 2048 185 and 232).
+  // 300 167 and 227, 24 of 640 133 and 164, of 768 173 and 177, 16 of 1000 185
+  // and 185, 8 of 2000 293 and 280, one of 16384 1641 and 1387; 16 of 4000 under
+  // a window of 512 704 and 761, of 1024 1004 and 990; 64 times 200 queries over
+  // 1200 keys 322 and 295, 64 times 120 over 1120 165 and 238.  At width 64 one
+  // tile was never slower (16 packed prompts, window 1024: 206 and 281; 8 of
+  // 2048 185 and 232).
   constexpr int64_t kFewKeys = 640;
   const int64_t in_windows = static_cast<int64_t>(a.window) * a.B;
   const int64_t keys = a.window > 0 && in_windows < a.n_k ? in_windows : a.n_k;
