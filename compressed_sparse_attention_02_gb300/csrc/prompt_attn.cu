@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
                     : wait_or_abort(q_full + t, item & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        if (!loaded) mbar_arrive(q_empty + t);
+        if (C::kOwnStage && !loaded) mbar_arrive(q_empty + t);
       }
       if (!ok) break;
       const int rows = w.rows(t);
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           }
         }
       }
-      if (!C::kOwnStage && loaded) {
+      if (!C::kOwnStage) {
         fence_proxy_async_smem();  // the next queries are copied over what was staged
         mbar_arrive(q_empty + t);
       }

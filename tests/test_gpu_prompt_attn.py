@@ -160,6 +160,18 @@ def test_many_short_sequences(csa):
     assert csa.csa_check_status() == 0
 
 
+def test_many_tiles_without_keys(csa):
+    """Most tiles see no key (more queries than keys, or none): their softmax has nothing to wait for but the queries."""
+    for D, lens in ((64, [(700, 0), (900, 1), (300, 0), (500, 130)] * 2), (128, [(700, 0), (900, 1), (300, 0)] * 3),
+                    (128, [(700, 0), (2000, 9000), (900, 1), (1300, 300)])):
+        x = make(lens, 48, 2, D, seed=D)
+        check(csa, x, "no keys", heads=[0, 31], sink=D == 64)
+        first = run(csa, x)[0]
+        for _ in range(5):
+            assert torch.equal(first, run(csa, x)[0])
+    assert csa.csa_check_status() == 0
+
+
 def test_long_rows_sampled(csa):
     """4100 keys: the last rows of the oracle only, over every tile's border."""
     x = make([(4100, 4100)], 2, 1, 128, seed=5)
