@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     }
     for (int t = 0; t < QT; ++t) {
       mbar_init(q_full + t, 1);
-      mbar_init(q_empty + t, kTile);
+      mbar_init(q_empty + t, kTile + 1);
       for (int h = 0; h < C::kParts; ++h) {
         mbar_init(&s_full[t][h], 1);
         mbar_init(&p_full[t][h], kTile);
@@ -442,11 +442,14 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
           if (ok) ok = wait(q_full + t, item & 1);
-          if (ok && begin[t] == 0 && end[t] > 0) {
+          if (ok) {
             tc_fence_after();
             if (elect_one()) {
+              mbar_arrive(q_empty + t);  // (a tile without keys would be freed without this warp)
+              if (begin[t] == 0 && end[t] > 0) {
 #pragma unroll
-              for (int h = 0; h < C::kParts; ++h) s_of(t, h, k_first);
+                for (int h = 0; h < C::kParts; ++h) s_of(t, h, k_first);
+              }
             }
             __syncwarp();
           }
