@@ -472,7 +472,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
 #pragma unroll
           for (int t = 0; t < QT; ++t) {
             const bool pv = it >= begin[t] && it < end[t], next = again && it + 1 >= begin[t] && it + 1 < end[t];
-#pragma unroll
+            // (unrolled, the long products of width 128 spill where two CTAs share
+            // an SM's registers: 32 prompts of 500 130 us, 119 so)
+#pragma unroll(C::kStages == 2 ? 1 : C::kParts)
             for (int h = 0; h < C::kParts; ++h) {
               const bool last = t == QT - 1 && h == C::kParts - 1;
               if (ok && pv) ok = wait(&p_full[t][h], n_p[t] & 1u);
@@ -941,13 +943,13 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
   // other's products; where a tile sees few keys, or a sequence has one tile,
   // two CTAs of one tile on an SM overlap their starts and ends instead.
   // Width 128, 32 heads, us with one and with two tiles a CTA: 64 prompts of
-  // 300 167 and 227, 24 of 640 133 and 164, of 768 173 and 177, 16 of 1000 185
-  // and 185, 8 of 2000 293 and 280, one of 16384 1641 and 1387; 16 of 4000 under
-  // a window of 512 704 and 761, of 1024 1004 and 990; 64 times 200 queries over
-  // 1200 keys 322 and 295, 64 times 120 over 1120 165 and 238.  At width 64 one
-  // tile was never slower (16 packed prompts, window 1024: 206 and 281; 8 of
-  // 2048 185 and 232).
-  constexpr int64_t kFewKeys = 640;
+  // 300 152 and 227, 24 of 640 125 and 163, 16 of 1000 177 and 184, of 1200 245
+  // and 247, 8 of 2000 292 and 280, one of 16384 1.72 and 1.42 ms; 16 of 4000
+  // under a window of 512 684 and 775, of 1024 1003 and 999; 64 times 200
+  // queries over 1200 keys 326 and 297, 64 times 120 over 1120 167 and 239.  At
+  // width 64 one tile was never slower (16 packed prompts, window 1024: 206 and
+  // 281; 8 of 2048 185 and 232).
+  constexpr int64_t kFewKeys = 1024;
   const int64_t in_windows = static_cast<int64_t>(a.window) * a.B;
   const int64_t keys = a.window > 0 && in_windows < a.n_k ? in_windows : a.n_k;
   if (D == 64 || a.n_q <= static_cast<int64_t>(kTile) * a.B || keys <= kFewKeys * a.B)

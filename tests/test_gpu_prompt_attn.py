@@ -96,16 +96,16 @@ def test_many_tiles(csa, D, window, lens):
     many_tiles(csa, D, window, lens)
 
 
-@pytest.mark.parametrize("window", [0, 641, 700, 769, 1100])
+@pytest.mark.parametrize("window", [0, 700, 1025, 1100, 1281, 1700])
 def test_many_tiles_that_see_many_keys(csa, window):
-    """... and two tiles a CTA where they see more than 640 keys."""
-    many_tiles(csa, 128, window, [(1500, 1500), (300, 1300), (129, 40), (257, 900)])
+    """... and two tiles a CTA where they see more than 1024 keys."""
+    many_tiles(csa, 128, window, [(2000, 2000), (300, 2300), (129, 40), (257, 1900)])
 
 
 def many_tiles(csa, D, window, lens):
     x = make(lens, 48, 2, D, seed=window, pad=9)
     check(csa, x, "many tiles", heads=[0, 29, 47], window=window, sink=window % 2 == 0)
-    if window in (0, 300, 700):  # a value that is not finite: seen or not as the formula has it
+    if window in (0, 300, 700, 1100):  # a value that is not finite: seen or not as the formula has it
         clean = run(csa, x, window=window)[0]
         y = {k: v.clone() for k, v in x.items()}
         key = lens[0][1] - 60
@@ -317,7 +317,7 @@ def test_bad_offsets(csa):
 def test_a_wait_that_runs_out(csa):
     """The products never announce the first scores: the call ends, reports the timeout, and the next one is right."""
     for D, Hq, lens in ((128, 4, [(500, 500)]), (128, 48, [(700, 700)]), (64, 48, [(700, 700)]), (64, 2, [(20, 3000)]),
-                        (128, 48, [(100, 100)] * 8)):
+                        (128, 48, [(100, 100)] * 8), (128, 48, [(1100, 1100)])):
         x = make(lens, Hq, 2, D, seed=10)
         good = run(csa, x)[0]
         csa.csa_test_set_wait_fault(200, csa.CSA_TEST_FAULT_ATTN)
