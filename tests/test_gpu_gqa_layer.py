@@ -164,3 +164,57 @@ def test_prompts_then_decoding(csa, Hq, Hkv, D, page, window, sink):
     assert torch.equal(twin.k.view(torch.uint8), layer.k.view(torch.uint8))
     assert torch.equal(twin.vs, layer.vs)
     assert csa.csa_check_status() == 0
+
+
+def test_calls_on_several_streams(csa):
+    """Prompts in every form of the kernel, decode attention and appends replayed on five streams at once: the bits of
+    the same calls one after the other."""
+    g = torch.Generator(DEV).manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, device=DEV, generator=g).bfloat16()  # noqa: E731
+    work = []
+
+    def prompts(lens, Hq, D):
+        cu = torch.tensor([0] + lens).cumsum(0).int().to(DEV)
+        q, k, v = rnd(sum(lens), Hq, D), rnd(sum(lens), 2, D), rnd(sum(lens), 2, D)
+        out, lse = torch.empty_like(q), torch.empty(sum(lens), Hq, device=DEV)
+        work.append(((lambda: csa.csa_prompt_attn(cu, cu, q, k, v, D ** -0.5, True, 0, None, out, lse)), (out, lse)))
+
+    prompts([1700, 1300], 32, 128)      # two tiles of queries a CTA
+    prompts([300] * 9, 32, 64)          # two CTAs an SM
+    prompts([200], 8, 128)              # a cluster a tile
+    for D in (64, 128):
+        layer = Layer(csa, 12, 16, 2, D, 32, 40, 0, False, csa.rope_params(rope_dim=64), 5)
+        lens = torch.randint(1, 1000, (12,), device=DEV, generator=g).int()
+        x, pos = rnd(12, 20, D), lens - 1
+        cu = torch.cat([torch.zeros(1, device=DEV), lens.cumsum(0)]).int()
+        n = int(lens.sum())
+        csa.csa_kv_append(layer.cache, layer.rope, layer.turns, cu, torch.zeros_like(lens), rnd(n, 2, D), rnd(n, 2, D))
+        q, o = (torch.empty(12, 16, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        l = torch.empty(12, 16, device=DEV)
+        work.append(((lambda y=layer, x=x, p=pos, n=lens, q=q, o=o, l=l: y.decode(x, p, n, q, o, l)),
+                     (q, o, l, layer.k.view(torch.uint8), layer.vs)))
+    want = []
+    for call, outs in work:
+        call()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    graphs = []
+    for call, _ in work:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                call()
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in work]
+    for _, outs in work:
+        outs[0].zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(work, want):
+        for a, b in zip(outs, w):
+            assert torch.equal(a, b)
+    assert csa.csa_check_status() == 0
