@@ -143,18 +143,16 @@ __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
 __device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
 }
-// From a row's reference (in log2) and sum of weights to the factor of its
-// weighted values and its lse, the sink's weight in.
-__device__ __forceinline__ float finish_row(float m, float l, const float* sink, int head, float* lse) {
-  float f = 1.f;
+// From a row's sum of weights l in units of 2^m to the factor of its weighted
+// values, which are in units of 2^unit, and its lse, the sink's weight in.
+__device__ __forceinline__ float finish_row(float m, float unit, float l, const float* sink, int head, float* lse) {
   if (sink) {
     const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
-    f = ex2(m - m1);
-    l = l * f + ex2(s2 - m1);
+    l = l * ex2(m - m1) + ex2(s2 - m1);
     m = m1;
   }
   *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  return l == 0.f ? 0.f : f / l;
+  return l == 0.f ? 0.f : ex2(unit - m) / l;
 }
 
 // Finds the sequence that work item w belongs to, where sequence b has

@@ -41,6 +41,12 @@ constexpr int kRows = 16;                 // query heads a warp
 // more, so weights down to 2^-25 of the largest keep f16's full precision.
 constexpr float kLag = 4.f;
 constexpr float kWeightExp = 11.f;
+// A weight is the product of e^(l - m), which the sum takes, and a factor for
+// the value scale and f16's exponents.  Where the factor passes 2^64 (value
+// scales or logits far apart: a page of zero values has the scale 2^-126) the
+// weight is one exponential instead: the factor could pass fp32, and up to
+// here no weight that f16 holds (2^-24 and more) has an e^(l - m) that fp32 flushes.
+constexpr float kFar = 64.f - kWeightExp;
 constexpr float kNone = -1e30f;           // running maximum before the first token
 
 // H: halves of the 16 rows that hold query heads (1: groups of up to 8).
@@ -58,7 +64,8 @@ struct Cfg {
 };
 
 template <int D>
-constexpr int kRecord = kRows * (D + 2);  // floats of a partial result: sums, maxima, weights' sums
+constexpr int kRecord = kRows * (D + 4);  // floats of a partial result: sums, and a float4 a row: m, the weights'
+                                          // sum (in units of 2^m), the sums' unit (log2), nothing
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
     float o[kN][4];
 #pragma unroll
     for (int j = 0; j < kN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[H], mv[H];
+    float m[H], mv[H], room = 0.f;  // room: the value scale up to which no weight is far
     uint64_t l2[H];  // sums of weights, as pairs of partial sums
 #pragma unroll
     for (int h = 0; h < H; ++h) {
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
       __syncwarp();
       const int t0 = (sp.unit0() + c.u + it) << kUnitShift, st = c_stage;
       c_stage = c_stage + 1 == C::kStages ? 0 : c_stage + 1;
-      {
+      do {
         const uint32_t ks = ring + st * C::kStageBytes, vs = ks + C::kTileBytes;
         // logits of 32 tokens: 4 tiles of 8
         float x[4][4];
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
         // maxima of the logits, and of logit + log2(v_scale), the weights' exponents
         const float lv[2] = {__log2f(sc.z), __log2f(sc.w)};
         float top[H], topv[H];
-        bool grown = false;
+        bool grown = sc.z > room || sc.w > room;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           const float a0 = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
@@ -445,6 +452,68 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
           topv[h] = fmaxf(a0 + lv[0], a1 + lv[1]);
           grown |= top[h] > m[h] + kLag || topv[h] > mv[h] + kLag;
         }
+        uint32_t pf[2][2 * H];
+        auto weights = [&](auto apart) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const uint64_t mm = pair_of(-m[h], -m[h]);
+              float p0, p1, p2, p3;
+              split(add2(pair_of(x[2 * s][2 * h], x[2 * s][2 * h + 1]), mm), &p0, &p1);
+              split(add2(pair_of(x[2 * s + 1][2 * h], x[2 * s + 1][2 * h + 1]), mm), &p2, &p3);
+              const uint64_t p01 = pair_of(ex2(p0), ex2(p1)), p23 = pair_of(ex2(p2), ex2(p3));
+              l2[h] = add2(l2[h], add2(p01, p23));
+              if constexpr (apart) {
+                const float up = lv[s] + kWeightExp;
+                p0 = ex2(x[2 * s][2 * h] - mv[h] + up);
+                p1 = ex2(x[2 * s][2 * h + 1] - mv[h] + up);
+                p2 = ex2(x[2 * s + 1][2 * h] - mv[h] + up);
+                p3 = ex2(x[2 * s + 1][2 * h + 1] - mv[h] + up);
+              } else {
+                const float w = ex2(lv[s] + (m[h] - mv[h]) + kWeightExp);
+                const uint64_t ww = pair_of(w, w);
+                split(mul2(p01, ww), &p0, &p1);
+                split(mul2(p23, ww), &p2, &p3);
+              }
+              pf[s][h] = pack_f16(p0, p1);
+              pf[s][H + h] = pack_f16(p2, p3);
+            }
+        };
+        // out += weights . V: tokens 2cq, 2cq+1, 2cq+8, 2cq+9 of each 16, the
+        // bytes of two tokens paired by channel; lane group g holds channels
+        // g * D/8 .. + D/8
+        auto product = [&]() {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 16 * s + 2 * cq + (i & 1) + 8 * (i >> 1);
+              if constexpr (D == 128) {
+                const uint4 q4 = lds128(vs + chunk_at<D>(r, g));
+                v[i][0] = q4.x; v[i][1] = q4.y; v[i][2] = q4.z; v[i][3] = q4.w;
+              } else {
+                const uint2 q2 = lds64(vs + chunk_at<D>(r, g >> 1) + 8 * (g & 1));
+                v[i][0] = q2.x; v[i][1] = q2.y;
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+              const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), a23 = __byte_perm(v[0][w], v[1][w], 0x7362);
+              const uint32_t b01 = __byte_perm(v[2][w], v[3][w], 0x5140), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+              uint32_t p0, p1, q0, q1;
+              e4m3x4_to_f16(a01, p0, p1);
+              e4m3x4_to_f16(b01, q0, q1);
+              mma_f16_16816(o[4 * w], pf[s], p0, q0);
+              mma_f16_16816(o[4 * w + 1], pf[s], p1, q1);
+              e4m3x4_to_f16(a23, p0, p1);
+              e4m3x4_to_f16(b23, q0, q1);
+              mma_f16_16816(o[4 * w + 2], pf[s], p0, q0);
+              mma_f16_16816(o[4 * w + 3], pf[s], p1, q1);
+            }
+          }
+        };
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
           for (int h = 0; h < H; ++h) {
@@ -464,62 +533,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
             }
             m[h] = m1;
             mv[h] = mv1;
+            room = h == 0 ? mv1 - m1 : fminf(room, mv1 - m1);
+          }
+          room = ex2(room + kFar);
+          if (__any_sync(0xffffffffu, sc.z > room || sc.w > room)) {
+            // (a way of its own, so that the usual one is not cut by a branch: 96
+            // sequences of width 64 under a window 78.7 us with the branch)
+            weights(std::true_type{});
+            product();
+            break;
           }
         }
-        uint32_t pf[2][2 * H];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const float w = ex2(lv[s] + (m[h] - mv[h]) + kWeightExp);
-            const uint64_t ww = pair_of(w, w), mm = pair_of(-m[h], -m[h]);
-            float p0, p1, p2, p3;
-            split(add2(pair_of(x[2 * s][2 * h], x[2 * s][2 * h + 1]), mm), &p0, &p1);
-            split(add2(pair_of(x[2 * s + 1][2 * h], x[2 * s + 1][2 * h + 1]), mm), &p2, &p3);
-            const uint64_t p01 = pair_of(ex2(p0), ex2(p1)), p23 = pair_of(ex2(p2), ex2(p3));
-            l2[h] = add2(l2[h], add2(p01, p23));
-            split(mul2(p01, ww), &p0, &p1);
-            split(mul2(p23, ww), &p2, &p3);
-            pf[s][h] = pack_f16(p0, p1);
-            pf[s][H + h] = pack_f16(p2, p3);
-          }
-        // out += weights . V: tokens 2cq, 2cq+1, 2cq+8, 2cq+9 of each 16, the
-        // bytes of two tokens paired by channel; lane group g holds channels
-        // g * D/8 .. + D/8
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          uint32_t v[4][D / 32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 16 * s + 2 * cq + (i & 1) + 8 * (i >> 1);
-            if constexpr (D == 128) {
-              const uint4 q4 = lds128(vs + chunk_at<D>(r, g));
-              v[i][0] = q4.x; v[i][1] = q4.y; v[i][2] = q4.z; v[i][3] = q4.w;
-            } else {
-              const uint2 q2 = lds64(vs + chunk_at<D>(r, g >> 1) + 8 * (g & 1));
-              v[i][0] = q2.x; v[i][1] = q2.y;
-            }
-          }
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), a23 = __byte_perm(v[0][w], v[1][w], 0x7362);
-            const uint32_t b01 = __byte_perm(v[2][w], v[3][w], 0x5140), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-            uint32_t p0, p1, q0, q1;
-            e4m3x4_to_f16(a01, p0, p1);
-            e4m3x4_to_f16(b01, q0, q1);
-            mma_f16_16816(o[4 * w], pf[s], p0, q0);
-            mma_f16_16816(o[4 * w + 1], pf[s], p1, q1);
-            e4m3x4_to_f16(a23, p0, p1);
-            e4m3x4_to_f16(b23, q0, q1);
-            mma_f16_16816(o[4 * w + 2], pf[s], p0, q0);
-            mma_f16_16816(o[4 * w + 3], pf[s], p1, q1);
-          }
-        }
-      }
+        weights(std::false_type{});
+        product();
+      } while (false);
       __syncwarp();
       issue();
     }
-    // The pair's rows, or this share's part of them in units of 2^m.
+    // The pair's rows, or this share's part of them in units of 2^mv / 2^kWeightExp
+    // (not of 2^m: the two can be further apart than fp32's exponents).
     // Accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j.
     const bool whole = take == nt;
     const int slot = first ? 0 : 1;
@@ -532,12 +564,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
       l += other;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      float f = ex2(mv[h] - m[h] - kWeightExp);
+      const float unit = mv[h] - kWeightExp;
       if (r >= rows) continue;
       if (whole) {
         const int64_t row = static_cast<int64_t>(c.b) * a.n_heads + head0 + r;
         float lse;
-        f *= finish_row(m[h], l, a.sink, head0 + r, &lse);
+        const float f = finish_row(m[h], unit, l, a.sink, head0 + r, &lse);
         if (a.lse && cq == 0) a.lse[row] = lse;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -560,13 +592,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
           float4* dst = reinterpret_cast<float4*>(part + r * D + (2 * cq + e) * kN);
 #pragma unroll
           for (int k = 0; k < kN / 4; ++k)
-            dst[k] = make_float4(o[4 * k][2 * h + e] * f, o[4 * k + 1][2 * h + e] * f, o[4 * k + 2][2 * h + e] * f,
-                                 o[4 * k + 3][2 * h + e] * f);
+            dst[k] = make_float4(o[4 * k][2 * h + e], o[4 * k + 1][2 * h + e], o[4 * k + 2][2 * h + e],
+                                 o[4 * k + 3][2 * h + e]);
         }
-        if (cq == 0) {
-          part[kRows * D + r] = m[h];
-          part[kRows * D + kRows + r] = l;
-        }
+        if (cq == 0) *reinterpret_cast<float4*>(part + kRows * D + 4 * r) = make_float4(m[h], l, unit, 0.f);
       }
     }
     left -= take;
@@ -601,7 +630,7 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
   constexpr int kMergeWarps = merge_warps(SPLIT);
   constexpr int kPer = D / 32;  // channels a lane, neighbours
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
-  __shared__ float m_s[kMergeWarps], l_s[kMergeWarps];
+  __shared__ float m_s[kMergeWarps], u_s[kMergeWarps], l_s[kMergeWarps];
   __shared__ __align__(16) float n_s[kMergeWarps][D];
   pdl_launch_dependents();
   pdl_wait();
@@ -614,17 +643,25 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
   };
   for (int r = SPLIT == 1 ? warp : blockIdx.y; r < rows; r += SPLIT == 1 ? kMergeWarps : gridDim.y) {
     const int part = SPLIT == 1 ? 0 : warp;
-    float m = kNone, l = 0.f, n[kPer];
+    float m = kNone, unit = kNone, l = 0.f, n[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) n[j] = 0.f;
-    for (int k = part + lane * SPLIT; k < n_rec; k += 32 * SPLIT) m = fmaxf(m, record(k)[kRows * D + r]);
+    for (int k = part + lane * SPLIT; k < n_rec; k += 32 * SPLIT) {
+      const float4 y = *reinterpret_cast<const float4*>(record(k) + kRows * D + 4 * r);
+      m = fmaxf(m, y.x);
+      unit = fmaxf(unit, y.z);
+    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = 16; off > 0; off >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, off));
+    }
 #pragma unroll 4
     for (int k = part; k < n_rec; k += SPLIT) {
       const float* p = record(k);
-      const float f = ex2(p[kRows * D + r] - m);
-      l += p[kRows * D + kRows + r] * f;
+      const float4 w = *reinterpret_cast<const float4*>(p + kRows * D + 4 * r);
+      l += w.y * ex2(w.x - m);
+      const float f = ex2(w.z - unit);
       const Vec v = *reinterpret_cast<const Vec*>(p + r * D + lane * kPer);
       const float* y = reinterpret_cast<const float*>(&v);
 #pragma unroll
@@ -634,28 +671,32 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
       __syncthreads();
       if (lane == 0) {
         m_s[warp] = m;
+        u_s[warp] = unit;
         l_s[warp] = l;
       }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) n_s[warp][lane * kPer + j] = n[j];
       __syncthreads();
       if (part != 0) continue;
-      const float m0 = m;
-      for (int w = 1; w < SPLIT; ++w) m = fmaxf(m, m_s[w]);
-      const float f0 = ex2(m0 - m);
-      l *= f0;
+      const float m0 = m, unit0 = unit;
+      for (int w = 1; w < SPLIT; ++w) {
+        m = fmaxf(m, m_s[w]);
+        unit = fmaxf(unit, u_s[w]);
+      }
+      l *= ex2(m0 - m);
+      const float f0 = ex2(unit0 - unit);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) n[j] *= f0;
       for (int w = 1; w < SPLIT; ++w) {
-        const float f = ex2(m_s[w] - m);
-        l += l_s[w] * f;
+        l += l_s[w] * ex2(m_s[w] - m);
+        const float f = ex2(u_s[w] - unit);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) n[j] += n_s[w][lane * kPer + j] * f;
       }
     }
     const int64_t row = static_cast<int64_t>(cut.row) + r;
     float lse;
-    const float f = finish_row(m, l, a.sink, static_cast<int>(row % a.n_heads), &lse);
+    const float f = finish_row(m, unit, l, a.sink, static_cast<int>(row % a.n_heads), &lse);
     uint32_t y[kPer / 2];
 #pragma unroll
     for (int j = 0; j < kPer / 2; ++j) {
@@ -699,7 +740,7 @@ cudaError_t launch_dim(const PagedAttnArgs& a, int sms, cudaStream_t stream) {
 size_t paged_attn_bytes(int head_dim, int sms) {
   static_assert(Cfg<128, 1>::kCtas == Cfg<128, 2>::kCtas, "one size for both");
   const size_t ctas = static_cast<size_t>(sms) * (head_dim == 64 ? Cfg<64, 2>::kCtas : Cfg<128, 2>::kCtas);
-  return ctas * kWarps * (sizeof(Cut) + 2 * kRows * (head_dim + 2) * sizeof(float));
+  return ctas * kWarps * (sizeof(Cut) + 2 * kRows * (head_dim + 4) * sizeof(float));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int sms, cudaStream_t stream) {

@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           l = 1.f;
         } else {
           float lse;
-          l = finish_row(m * scale2, l, a.sink, w.head, &lse);
+          l = finish_row(m * scale2, m * scale2, l, a.sink, w.head, &lse);
           if (a.lse && r < rows) a.lse[row] = lse;
         }
         const int o2 = item % 3;
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         float sum = l * f;
         for (int off = 1; off < cluster; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         float lse;
-        g = f * finish_row(top, sum, a.sink, w.head, &lse);
+        g = f * finish_row(top, top, sum, a.sink, w.head, &lse);
         if (a.lse && lane < 16 && p == 0 && r < rows)
           a.lse[static_cast<int64_t>(w.sq.q0 + w.row0 + r) * a.n_heads + w.head] = lse;
       }

@@ -1,0 +1,101 @@
+"""The grouped-query calls at the edges of what they document: values that lie
+far apart, what a row does not see, offsets that are wrong."""
+import numpy as np
+import pytest
+import torch
+
+import _gqa as ref
+import test_gpu_kv_append as append
+import test_gpu_paged_attn as paged
+import test_gpu_prompt_attn as prompt
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+LN2 = 0.6931471805599453
+
+
+@pytest.fixture(scope="module")
+def csa():
+    import compressed_sparse_attention_02_gb300 as m
+    return m
+
+
+# ---- csa_paged_attn: logits and value scales far apart ---------------------------------
+
+def far_apart(L, B, Hq, Hkv, D, P, place):
+    """Sequences of L tokens with logits of about a binary order around 0, but for one page of each, whose logits
+    will be the queries' channel 0 (in binary orders)."""
+    x = paged.make([L] * B, Hq, Hkv, D, P, seed=D + P, scales=(0, 1))
+    page = x["table"][:, {"first": 0, "middle": L // P // 2, "last": (L - 1) // P}[place]].long()
+    x["q"][..., 1:] *= 2.0 ** -6
+    k = x["k"].float()
+    written = ~k.isnan()
+    k[..., 0] = 0.0
+    k[page, :, :, 0] = 1.0
+    k[~written] = float("nan")
+    x["k"] = k.to(torch.float8_e4m3fn)
+    x["ks"][page] = 1.0
+    return x, page
+
+
+def sample(x, csa, sm, sequences, **kw):
+    """The call on all sequences, checked on some."""
+    out, lse = paged.run(csa, x, sm=sm, **kw)
+    kw.pop("ws", None)
+    y = dict(x, q=x["q"][sequences], lens=x["lens"][sequences], table=x["table"][sequences])
+    ref.check_attention(out[sequences], lse[sequences], *paged.want(y, sm=sm, **kw), paged.STEP, "far apart")
+
+
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("B,Hq,Hkv,D,L", [
+    (1, 2, 1, 128, 3000), (1, 3, 1, 64, 3000),      # one pair: sixteen warps join its parts
+    (50, 1, 1, 128, 250), (70, 1, 1, 64, 250),      # some pairs: eight do
+    (60, 4, 4, 128, 250), (60, 4, 4, 64, 250),      # many pairs, each of several parts
+    (300, 16, 8, 128, 120), (300, 16, 8, 64, 120),  # ... and many of one part
+    (40, 16, 1, 128, 250),                          # groups of more than eight heads
+])
+def test_paged_attn_of_logits_and_scales_far_apart(csa, B, Hq, Hkv, D, L, P, place):
+    """A page whose logits stand 50 to 150 binary orders above all others: with values of zero (the append gives
+    such a page the scale 2^-126) or ordinary ones, beside values of ordinary size and of 2^119."""
+    x, page = far_apart(L, B, Hq, Hkv, D, P, place)
+    codes, scales = x["v"].view(torch.uint8).clone(), x["vs"].clone()
+    some = torch.tensor(sorted({0, B // 2, B - 1}), device=DEV)
+    for orders in (50, 100, 116, 120, 127, 150):
+        x["q"][..., 0] = orders
+        for others in (-6, 119):
+            for top in (None, 0, -126):
+                x["v"].view(torch.uint8).copy_(codes)
+                x["vs"].copy_(scales * 2.0 ** others)
+                x["vs"][page] = 2.0 ** (-126 if top is None else top)
+                if top is None:  # (what lies behind the sequence's end stays NaN)
+                    at = x["v"].view(torch.uint8)[page]
+                    x["v"].view(torch.uint8)[page] = torch.where(at == 0x7F, at, 0)
+                sample(x, csa, LN2, some, sink=others == 119 and orders == 100)
+    # one query head after the other far from the page's keys, and a window's border inside its tile
+    x["q"][..., 0] = torch.tensor([0, 150, 60, 120], device=DEV).repeat(Hq)[:Hq].bfloat16()
+    sample(x, csa, LN2, some, window=L - 5)
+    assert csa.csa_check_status() == 0
+
+
+def test_paged_attn_of_what_the_append_stored(csa):
+    """Tokens appended one page after the other, one page's values all zero and its keys far above the others'."""
+    H, D, P, T = 2, 128, 16, 80
+    k, v = (torch.zeros(8, H, P, D, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros(8, H, device=DEV) for _ in range(2))
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None]
+    cache = csa.paged_cache(k, v, ks, vs, table)
+    g = torch.Generator(DEV).manual_seed(0)
+    a, c = (torch.randn(T, H, D, device=DEV, generator=g).bfloat16() for _ in range(2))
+    a[:, :, 0] = 0
+    a[32:48, :, 0], c[32:48] = 8.0, 0.0
+    csa.csa_kv_append(cache, None, None, torch.tensor([0, T], dtype=torch.int32, device=DEV),
+                      torch.zeros(1, dtype=torch.int32, device=DEV), a, c)
+    assert (vs[2] == 2.0 ** -126).all()
+    q = (torch.randn(1, 8, D, device=DEV, generator=g) * 2.0 ** -6).bfloat16()
+    q[..., 0] = 16.0
+    x = dict(k=k.view(torch.float8_e4m3fn), v=v.view(torch.float8_e4m3fn), ks=ks, vs=vs, table=table, q=q,
+             lens=torch.tensor([T], dtype=torch.int32, device=DEV), sink=None)
+    out, lse = paged.run(csa, x, sm=1.0)  # 128 nats, 185 binary orders
+    ref.check_attention(out, lse, *paged.want(x, sm=1.0), paged.STEP, "appended")
+    assert csa.csa_check_status() == 0
