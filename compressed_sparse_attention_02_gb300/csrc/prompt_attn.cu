@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
       }
       float m = kNone, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
       bool large = false;        // of the warp: some row's logits are large (see below)
+      auto is_large = [&]() { return m > kNone && fabsf(m * scale2) > 65536.f; };
       for (int part = 0; part < n_tiles * C::kParts; ++part) {
         const int n = part / C::kParts, h = part % C::kParts, j = j_top - n;
         ok = wait_or_abort(&s_full[t][h], (n_s + n) & 1, abort_flag, a.status);
@@ -649,11 +650,14 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         float top1 = top[0];
 #pragma unroll
         for (int c = 1; c < kC; ++c) top1 = fmaxf(top1, top[c]);
-        if (__any_sync(0xffffffffu, (top1 - m) * scale2 > kLag)) {
-          const float m1 = fmaxf(m, top1), f = ex2((m - m1) * scale2);
-          m = m1;
+        // (a row whose own maximum has not grown keeps its reference, so that no bit
+        // of it depends on what only the warp's other rows see)
+        const bool grown = (top1 - m) * scale2 > kLag;
+        if (__any_sync(0xffffffffu, grown)) {
+          const float f = grown ? ex2((m - top1) * scale2) : 1.f;
+          if (grown) m = top1;
           l *= f;
-          large = __any_sync(0xffffffffu, m > kNone && fabsf(m * scale2) > 65536.f);
+          large = __any_sync(0xffffffffu, is_large());
           if (part > 0) {
             // the products of the parts before have finished: these scores were
             // issued after them, but for the last one's where parts alternate
@@ -679,11 +683,12 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         // the rounding of scale m shows, s - m first
         float offset = -m * scale2;
         if (large) {
-          offset = 0.f;
+          const float less = is_large() ? m : 0.f;
+          if (is_large()) offset = 0.f;
 #pragma unroll
           for (int c = 0; c < kC; ++c)
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - m);
+            for (int k = 0; k < 32; ++k) s[c][k] = __float_as_uint(__uint_as_float(s[c][k]) - less);
         }
         const uint64_t minus_m = pair_of(offset, offset);
         uint64_t sum[2] = {0ull, 0ull};

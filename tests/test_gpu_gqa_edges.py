@@ -99,3 +99,42 @@ def test_paged_attn_of_what_the_append_stored(csa):
     out, lse = paged.run(csa, x, sm=1.0)  # 128 nats, 185 binary orders
     ref.check_attention(out, lse, *paged.want(x, sm=1.0), paged.STEP, "appended")
     assert csa.csa_check_status() == 0
+
+
+# ---- csa_prompt_attn: what a row does not see ------------------------------------------
+
+@pytest.mark.parametrize("heads", [3, 48])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,window", [([(300, 300), (170, 170)], 0), ([(300, 300), (170, 170)], 150),
+                                         ([(40, 700), (30, 900)], 0), ([(2000, 2000), (257, 1900)], 700),
+                                         ([(2000, 2000), (257, 2300)], 1500)])
+def test_prompt_attn_rows_are_those_of_what_they_see(csa, heads, D, lens, window):
+    """Large and infinite keys where a row does not see them, and a neighbour's queries in the rows that its last
+    tile leaves empty, change no bit of it."""
+    x = prompt.make(lens, heads, 1, D, seed=D + window)
+    clean, clean_lse = prompt.run(csa, x, window=window)
+    first = 0
+    for b, (nq, nk) in enumerate(lens):
+        k0 = sum(m for _, m in lens[:b])
+        pos = torch.arange(nq) + nk - nq
+        for j in (nk - 2, nk - nq // 2, nk - nq + 3, nk - nq - (window or nk) + 1 + nq // 3, 5):
+            if not 0 <= j < nk:
+                continue
+            for value in (3e4, -3e4, float("inf"), float("nan")):
+                y = dict(x, k=x["k"].clone())
+                y["k"][k0 + j] = torch.where(x["k"][k0 + j] < 0, -value, value).bfloat16()
+                out, lse = prompt.run(csa, y, window=window)
+                blind = torch.ones(x["q"].shape[0], dtype=torch.bool)
+                blind[first:first + nq] = (pos < j) | (pos >= j + (window or nk))
+                blind = blind.to(DEV)
+                assert torch.equal(out[blind], clean[blind]), (b, j, value)
+                assert torch.equal(lse[blind], clean_lse[blind]), (b, j, value)
+        for value in (0.0, 1e4, float("inf")):
+            y = dict(x, q=x["q"].clone())
+            y["q"][first:first + nq] *= value
+            out, lse = prompt.run(csa, y, window=window)
+            others = torch.ones(x["q"].shape[0], dtype=torch.bool, device=DEV)
+            others[first:first + nq] = False
+            assert torch.equal(out[others], clean[others]) and torch.equal(lse[others], clean_lse[others])
+        first += nq
+    assert csa.csa_check_status() == 0
