@@ -116,6 +116,22 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
+// The scale's reciprocal, by which a power of two divides exactly.  A page that
+// another program began can have any scale: its rows are divided here, and 1 is
+// returned.
+template <int NI>
+__device__ __forceinline__ float divide_by(float s, float (&lo)[NI][8], float (&hi)[NI][8]) {
+  if ((__float_as_uint(s) & 0x007FFFFFu) == 0u) return __frcp_rn(s);
+#pragma unroll
+  for (int k = 0; k < NI; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      lo[k][j] = __fdiv_rn(lo[k][j], s);
+      hi[k][j] = __fdiv_rn(hi[k][j], s);
+    }
+  return 1.f;
+}
+
 // An item's 16 codes.
 __device__ __forceinline__ void store_item(uint8_t* row, int cl, int ch, const float (&lo)[8], const float (&hi)[8],
                                            float inv) {
@@ -269,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, kPagesCtas<THREADS, NI>)
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) amax = fmaxf(amax, top[k]);
     }
-    const float s = scale_of(amax, was), inv = __frcp_rn(s);  // exact for a power of two
+    const float s = scale_of(amax, was), inv = divide_by(s, lo, hi);
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
       if (tid + k * THREADS < n_items) store_item(sl.codes, dst[k], dst[k] + gap[k], lo[k], hi[k], inv);
@@ -301,11 +317,11 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvApp
   int cl, ch;
   item_chunks(rope, it, &cl, &ch);
   const int n = p.last - p.first;
-  float lo[8], hi[8];
+  float lo[1][8], hi[1][8];
   auto load = [&](int r) {
     const uint16_t* row = sl.src + r * sl.src_stride;
-    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + cl)), lo);
-    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + ch)), hi);
+    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + cl)), lo[0]);
+    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(row + ch)), hi[0]);
     if (it < (rope.rope_dim >> 4)) {
       float2 sc[8];
 #pragma unroll
@@ -314,19 +330,20 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvApp
         sc[j].x *= rope.mscale;
         sc[j].y *= rope.mscale;
       }
-      rotate_item(rope.half != 0, sc, lo, hi);
+      rotate_item(rope.half != 0, sc, lo[0], hi[0]);
     }
   };
   float amax = 0.f;
   for (int r = lane / items; r < n; r += at_once) {
     load(r);
-    amax = finite_max(lo, hi, amax);
+    amax = finite_max(lo[0], hi[0], amax);
   }
   amax = warp_max(amax);
-  const float s = scale_of(amax, was), inv = __frcp_rn(s);
+  const float s = scale_of(amax, was);
   for (int r = lane / items; r < n; r += at_once) {
     if (n > at_once) load(r);  // (else still in registers)
-    store_item(sl.codes + (p.first + r) * a.cache.head_dim, cl, ch, lo, hi, inv);
+    const float inv = divide_by(s, lo, hi);
+    store_item(sl.codes + (p.first + r) * a.cache.head_dim, cl, ch, lo[0], hi[0], inv);
   }
   if (p.first > 0 && s != was) round_again(sl.codes, p.first * a.cache.head_dim, __fdiv_rn(was, s), lane, 32);
   if (lane == 0 && (p.first == 0 || s != was)) *sl.scale = s;

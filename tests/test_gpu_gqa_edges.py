@@ -138,3 +138,38 @@ def test_prompt_attn_rows_are_those_of_what_they_see(csa, heads, D, lens, window
             assert torch.equal(out[others], clean[others]) and torch.equal(lse[others], clean_lse[others])
         first += nq
     assert csa.csa_check_status() == 0
+
+
+# ---- csa_kv_append: pages that another program began -----------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows_a_sequence", [1, 14])
+def test_append_to_a_scale_that_is_no_power_of_two(csa, D, rows_a_sequence):
+    """Codes are those of the quotient in binary32, also where the reciprocal's product is another number."""
+    H, P = 2, 16
+    n = 896 // D  # rows that hold every bf16 magnitude of seven binary orders, up to 16
+    bf = np.float32([m * 2.0 ** e for e in range(-10, -3) for m in range(128, 256)])
+    differ = 0
+    for scale in map(float.fromhex, ("0x1.cp-4", "0x1.eb851ep-4", "0x1.fca1bp-4", "0x1.fa6f4ep-4", "0x1.f9e79ep-4")):
+        s = np.float32(scale)
+        quotient, product = (torch.from_numpy(y.astype(np.float64)) for y in (bf / s, bf * (np.float32(1) / s)))
+        differ += int((ref.e4m3(quotient) != ref.e4m3(product)).sum())
+        want = ref.e4m3(quotient).view(n, 1, D).expand(n, H, D)
+        rows = torch.from_numpy(bf).view(n, 1, D).expand(n, H, D).contiguous().to(DEV).bfloat16()
+        rows[:, 1] *= -1
+        want = torch.stack([want[:, 0], -want[:, 1]], 1)
+        B = n if rows_a_sequence == 1 else 1
+        k, v, ks, vs, table = append.pool(B, 1, H, D, P)
+        ks.fill_(scale), vs.fill_(scale)
+        k[:, :, 0], v[:, :, 0] = 0x38, 0x38  # the token that was there: ones
+        cu = None if B == n else torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        csa.csa_kv_append(csa.paged_cache(k, v, ks, vs, table), None, None, cu,
+                          torch.ones(B, dtype=torch.int32, device=DEV), rows, rows)
+        for codes, sc in ((k, ks), (v, vs)):
+            assert (sc == float(s)).all()
+            at = codes[table[:, 0].long()]
+            got = at[:, :, 1].contiguous() if B == n else at[0, :, 1:1 + n].transpose(0, 1).contiguous()
+            assert torch.equal(append.values(got), want)
+            assert (at[:, :, 0] == 0x38).all()
+    assert differ > 10
+    assert csa.csa_check_status() == 0
