@@ -173,3 +173,51 @@ def test_append_to_a_scale_that_is_no_power_of_two(csa, D, rows_a_sequence):
             assert (at[:, :, 0] == 0x38).all()
     assert differ > 10
     assert csa.csa_check_status() == 0
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_append_under_wrong_offsets_and_positions(csa, many):
+    """Negative positions store nothing at all; offsets that fall or pass the rows, and tokens past the table, store
+    nothing but the other sequences' tokens (a warp a head, and a block a page)."""
+    H, D, P, B = 2, 64, 16, 6
+    scale = 20 if many else 1
+    n = 6 * scale
+    a, c = append.rows(n, H, D, 3)
+    cu = [0, 3 * scale, 2 * scale, 4 * scale, 9999, 9999, n]  # good: sequences 0 and 2
+    k, v, ks, vs, table = append.pool(B, 2, H, D, P)
+    g = torch.Generator(DEV).manual_seed(1)
+    for x in (k, v):  # every page holds something
+        x.copy_(torch.randint(0, 0x7F, x.shape, device=DEV, generator=g, dtype=torch.uint8))
+    ks.fill_(2.0 ** -9), vs.fill_(2.0 ** -9)
+    cache = csa.paged_cache(k, v, ks, vs, table)
+    before = [t.clone() for t in (k, v, ks, vs)]
+    cu_t = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    csa.csa_kv_append(cache, None, None, cu_t, torch.full((B,), -1, dtype=torch.int32, device=DEV), a, c)
+    assert csa.csa_check_status() == 5
+    for t, was in zip((k, v, ks, vs), before):
+        assert torch.equal(t, was)
+    m = append.Model(k, v, ks, vs, table)
+    csa.csa_kv_append(cache, None, None, cu_t, torch.full((B,), 2 * P - 1, dtype=torch.int32, device=DEV), a, c)
+    assert csa.csa_check_status() == 5
+    for b in (0, 2):  # token 31 is the table's last
+        r = slice(cu[b], cu[b] + 1)
+        m.append(b, 2 * P - 1, {"k": a[r].double().cpu(), "v": c[r].double().cpu()})
+    m.check(k, v, ks, vs)
+    # pages outside the pool and negative ones, under offsets that are right
+    table[0, 0], table[3, 1] = -5, k.shape[0]
+    m = append.Model(k, v, ks, vs, table)
+    cu = [b * scale for b in range(B + 1)]
+    csa.csa_kv_append(cache, None, None, torch.tensor(cu, dtype=torch.int32, device=DEV),
+                      torch.full((B,), P - 1, dtype=torch.int32, device=DEV), a, c)
+    assert csa.csa_check_status() == 5
+    for b in range(B):
+        for t in range(scale):
+            p, r = P - 1 + t, slice(cu[b] + t, cu[b] + t + 1)
+            if p >= 2 * P or not 0 <= int(table[b, p // P]) < k.shape[0]:
+                continue
+            take = min(scale - t, P - p % P)
+            if t and p % P:
+                continue  # (stored with its page's first)
+            r = slice(cu[b] + t, cu[b] + t + take)
+            m.append(b, p, {"k": a[r].double().cpu(), "v": c[r].double().cpu()})
+    m.check(k, v, ks, vs)
