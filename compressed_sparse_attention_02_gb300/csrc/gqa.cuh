@@ -157,32 +157,31 @@ __device__ __forceinline__ float finish_row(float m, float unit, float l, const 
 
 // Finds the sequence that work item w belongs to, where sequence b has
 // count(b) >= 0 items: returns b and the item's index in it, or -1 when w is
-// past the last.  T holds the sum of all counts.  Every thread of the CTA
-// calls it (THREADS threads, a multiple of 32); sh holds THREADS / 32 + 2
-// values.
-template <int THREADS, typename T, typename Count>
-__device__ __forceinline__ int find_item(int B, T w, Count count, T* sh, T* index) {
+// past the last.  Every thread of the CTA calls it (THREADS threads, a multiple
+// of 32); sh holds THREADS / 32 + 2 values.
+template <int THREADS, typename Count>
+__device__ __forceinline__ int find_item(int B, int w, Count count, int* sh, int* index) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWarps = THREADS / 32;
   if (threadIdx.x == 0) sh[kWarps] = -1;
-  T base = 0;
+  int base = 0;
   for (int b0 = 0; b0 < B; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    const T n = b < B ? count(b) : 0;
-    T x = n;
+    const int n = b < B ? count(b) : 0;
+    int x = n;
     if (B - b0 > 1) {
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, off);
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
         if (lane >= off) x += y;
       }
     }
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    T before = base, all = 0;
+    int before = base, all = 0;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      const T t = sh[k];
+      const int t = sh[k];
       if (k < warp) before += t;
       all += t;
     }
@@ -196,7 +195,7 @@ __device__ __forceinline__ int find_item(int B, T w, Count count, T* sh, T* inde
     if (sh[kWarps] >= 0) break;
   }
   *index = sh[kWarps + 1];
-  return static_cast<int>(sh[kWarps]);
+  return sh[kWarps];
 }
 
 }  // namespace csa
