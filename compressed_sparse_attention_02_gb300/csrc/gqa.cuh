@@ -158,9 +158,10 @@ __device__ __forceinline__ float finish_row(float m, float unit, float l, const 
 // Finds the sequence that work item w belongs to, where sequence b has
 // count(b) >= 0 items: returns b and the item's index in it, or -1 when w is
 // past the last.  Every thread of the CTA calls it (THREADS threads, a multiple
-// of 32); sh holds THREADS / 32 + 2 values.
+// of 32); sh holds THREADS / 32 + 2 values.  With `every` the sequences behind
+// b are counted too (count() reports bad ones).
 template <int THREADS, typename Count>
-__device__ __forceinline__ int find_item(int B, int w, Count count, int* sh, int* index) {
+__device__ __forceinline__ int find_item(int B, int w, bool every, Count count, int* sh, int* index) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWarps = THREADS / 32;
   if (threadIdx.x == 0) sh[kWarps] = -1;
@@ -192,7 +193,7 @@ __device__ __forceinline__ int find_item(int B, int w, Count count, int* sh, int
     }
     base += all;
     __syncthreads();
-    if (sh[kWarps] >= 0) break;
+    if (sh[kWarps] >= 0 && !every) break;
   }
   *index = sh[kWarps + 1];
   return sh[kWarps];

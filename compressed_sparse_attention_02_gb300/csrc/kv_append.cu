@@ -78,7 +78,8 @@ __device__ __forceinline__ bool find_page(const KvAppendArgs& a, int* sh, PageRo
   int b = blockIdx.x, index = 0;
   if (a.cu_rows) {
     b = find_item<THREADS>(
-        a.B, b, [&](int s) { return static_cast<int>(pages_of(__ldg(a.pos0 + s), rows_of(a, s), c.page_shift)); }, sh,
+        a.B, b, b + 1 == static_cast<int>(gridDim.x),
+        [&](int s) { return static_cast<int>(pages_of(__ldg(a.pos0 + s), rows_of(a, s), c.page_shift)); }, sh,
         &index);
     if (b < 0) return false;
   }

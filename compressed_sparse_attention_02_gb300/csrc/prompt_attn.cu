@@ -189,8 +189,12 @@ struct Walker {
     return at(a, place, w);
   }
   __device__ __forceinline__ bool at(const PromptAttnArgs& a, int place, Work* w) {
-    const int item = place / a.n_heads, lane = threadIdx.x & 31;
+    const int item = place / a.n_heads;
     w->head = place - item * a.n_heads;
+    return find(a, item, w);
+  }
+  __device__ __forceinline__ bool find(const PromptAttnArgs& a, int item, Work* w) {
+    const int lane = threadIdx.x & 31;
     for (; b0 < a.B; b0 += 32) {
       Seq s = {0, 0, 0, 0};
       if (b0 + lane < a.B) {
@@ -381,6 +385,11 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
           for (; ok && s < 2 * walk.n_it; ++s) load(s);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      // (the offsets behind the last item are looked at too)
+      if (C::kCluster && static_cast<int>(blockIdx.x) + 1 == static_cast<int>(gridDim.x)) {
+        Work none;
+        walker.find(a, 1 << 30, &none);
       }
       if (lane == 0) {  // every copy lands before the CTA ends (also after an abort)
         for (int t = 0; t < QT; ++t)
@@ -903,6 +912,13 @@ bool encode_rows(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 encode, const
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tiles of `rows` queries that the sequences have at most: n rows are at most
+// n / R + 1 tiles of R rows, and at most n.
+int64_t max_items(const PromptAttnArgs& a, int rows) {
+  const int64_t most = a.n_q / rows + a.B;
+  return most < a.n_q ? most : a.n_q;
+}
+
 template <int D, int QT, int CTAS>
 cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int sms,
                        int cluster, cudaStream_t stream) {
@@ -919,9 +935,7 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
   const cudaError_t e = kernel_limits(reinterpret_cast<const void*>(kernel), C::kSmem, C::kSplit ? C::kLaunchRegs : 0,
                                       &done);
   if (e != cudaSuccess) return e;
-  // n rows are at most n / R + 1 tiles of R rows, and at most n
-  const int64_t most = a.n_q / (QT * kTile) + a.B;
-  int64_t grid = (most < a.n_q ? most : a.n_q) * a.n_heads;
+  int64_t grid = max_items(a, QT * kTile) * a.n_heads;
   if (grid > 0x3fffffff) return cudaErrorInvalidValue;
   if (C::kCluster)
     grid *= cluster;  // an item a cluster
@@ -935,7 +949,7 @@ template <int D>
 cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
   const int sms = current_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int64_t most = a.n_q / kTile + a.B, tiles = (most < a.n_q ? most : a.n_q) * a.n_heads;
+  const int64_t tiles = max_items(a, kTile) * a.n_heads;
   if (tiles <= sms) {
     // Few tiles, an SM each; a cluster shares out the keys of a tile while
     // SMs are left and a CTA has two tiles of keys at least.

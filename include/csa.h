@@ -759,7 +759,8 @@ typedef struct {
  * above are not written.  Sequences with pos0[b] < 0 or no rows store
  * nothing.  A token past the table or in a page outside the pool, and a
  * cu_rows entry that falls or passes n_rows, record CSA_ERR_INDEX_RANGE and
- * store nothing.  Pages that several sequences of one call append to hold
+ * store nothing (of sequences that such entries make overlap, any part may be
+ * left out).  Pages that several sequences of one call append to hold
  * unspecified tokens afterwards (nothing outside them is touched).
  */
 csa_status csa_kv_append(const csa_paged_cache *c, const csa_rope_params *r,
@@ -810,7 +811,8 @@ csa_status csa_paged_attn(const csa_paged_cache *c, int32_t B, int32_t n_heads,
  * n_heads below 2^30); rows behind the last sequence are left as they are in
  * out.  out: [n_q][n_heads][head_dim], lse [n_q][n_heads],
  * contiguous.  head_dim: 64 or 128.  A sequence with a cu_q or cu_k entry
- * that falls or passes its rows records CSA_ERR_INDEX_RANGE and is left out.
+ * that falls or passes its rows records CSA_ERR_INDEX_RANGE and is left out
+ * (of sequences that such entries make overlap, any part may be).
  * No workspace.  Weights are rounded to bf16 for the product with the values.
  */
 csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads,

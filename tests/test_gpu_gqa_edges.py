@@ -221,3 +221,36 @@ def test_append_under_wrong_offsets_and_positions(csa, many):
             r = slice(cu[b] + t, cu[b] + t + take)
             m.append(b, p, {"k": a[r].double().cpu(), "v": c[r].double().cpu()})
     m.check(k, v, ks, vs)
+
+
+# ---- offsets that fall far behind, and that overlap ------------------------------------
+
+def test_a_fall_behind_the_last_row_is_reported(csa):
+    """Sequences of one row each take as many places as a launch can have; offsets that fall after them (in another
+    block of the search) are reported all the same."""
+    n, H, D, P = 300, 1, 64, 16
+    k, v, ks, vs, table = append.pool(2 * n, 1, H, D, P)
+    cache = csa.paged_cache(k, v, ks, vs, table)
+    a, c = append.rows(n, H, D, 0)
+    for last in ([n] * n, list(range(1, n + 1))):  # no more rows; the same rows again
+        for fall in (False, True):
+            cu = list(range(n + 1)) + last
+            if fall:
+                cu[-2] = 7
+            elif last[0] != n:
+                continue
+            csa.csa_kv_append(cache, None, None, torch.tensor(cu, dtype=torch.int32, device=DEV),
+                              torch.zeros(2 * n, dtype=torch.int32, device=DEV), a, c)
+            assert csa.csa_check_status() == (5 if fall else 0)
+    for n, heads, D in ((36, 1, 64), (36, 4, 128), (70, 2, 128), (70, 16, 64)):
+        x = prompt.make([(1, 1)] * n, heads, 1, D, seed=n)
+        good = prompt.run(csa, x)[0]
+        assert csa.csa_check_status() == 0
+        more = torch.full((41,), n, dtype=torch.int32, device=DEV)
+        for fall in (False, True):
+            cu = torch.cat([x["cu_q"], more])
+            if fall:
+                cu[-2] = 7
+            y = dict(x, cu_q=cu, cu_k=torch.cat([x["cu_k"], more]))
+            assert torch.equal(prompt.run(csa, y)[0][:7], good[:7])  # (the rows behind may be the overlapping ones' too)
+            assert csa.csa_check_status() == (5 if fall else 0)
