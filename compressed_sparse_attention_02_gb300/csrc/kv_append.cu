@@ -64,7 +64,8 @@ __device__ __forceinline__ int64_t rows_of(const KvAppendArgs& a, int b) {
 }
 
 // A page touched by the call: new rows [first, last) of it, from row src_row
-// of k / v on.
+// of k / v on.  (None, last <= first, only where overlapping sequences have more
+// pages in all than an int counts.)
 struct PageRows {
   int64_t page, pos0, src_row;  // pos0: position of the page's row 0
   int first, last;
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, kPagesCtas<THREADS, NI>)
       if (tid + k * THREADS < n_items) store_item(sl.codes, dst[k], dst[k] + gap[k], lo[k], hi[k], inv);
     }
     if (p.first > 0 && s != was) round_again(sl.codes, p.first * a.cache.head_dim, __fdiv_rn(was, s), tid, THREADS);
-    if (tid == 0 && (p.first == 0 || s != was)) *sl.scale = s;
+    if (tid == 0 && n_items > 0 && (p.first == 0 || s != was)) *sl.scale = s;
     sl.codes += a.cache.page * a.cache.head_dim;
     ++sl.scale;
   }
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_rows_kernel(const KvApp
     store_item(sl.codes + (p.first + r) * a.cache.head_dim, cl, ch, lo[0], hi[0], inv);
   }
   if (p.first > 0 && s != was) round_again(sl.codes, p.first * a.cache.head_dim, __fdiv_rn(was, s), lane, 32);
-  if (lane == 0 && (p.first == 0 || s != was)) *sl.scale = s;
+  if (lane == 0 && n > 0 && (p.first == 0 || s != was)) *sl.scale = s;
 }
 
 constexpr int kMaxAngles = 128 * 64 * static_cast<int>(sizeof(float2));  // of 128 rows of width 128

@@ -178,7 +178,8 @@ struct Walk {
 // the later ones first: under the causal mask they see more keys) times
 // heads.  CTA c of G takes c, 2G - 1 - c, 2G + c, ...: forward and backward in
 // turn, so that no CTA gets the longer one of every G.  The places grow, so
-// it never looks back.
+// it never looks back.  Offsets that fall can make sequences overlap, whose
+// items could pass 32 bits: a CTA takes no more turns than others can need.
 template <int ROWS>
 struct Walker {
   int b0 = 0, base = 0, round = 0;  // sequences before b0 hold `base` items
@@ -244,7 +245,8 @@ struct Order {
 template <int D, int QT, int CTAS>
 __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a, const int cluster_size) {
+                       const __grid_constant__ CUtensorMap tm_v, const PromptAttnArgs a, const int cluster_size,
+                       const int max_turns) {
   using C = Cfg<D, QT, CTAS>;
   constexpr int kTmaWarp = 4 * QT, kMmaWarp = 4 * QT + 1, kCleanWarp = 4 * QT + 2;
   constexpr int kRowsCta = QT * kTile;
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         if (C::kCluster)
           there = item == 0 && walker.at(a, cta, &o.w);
         else
-          there = walker.next(a, cta, static_cast<int>(gridDim.x), &o.w);
+          there = item <= max_turns && walker.next(a, cta, static_cast<int>(gridDim.x), &o.w);
         o.there = there;
         if (there) {
           o.walk.set(a, w, rank, cluster);
@@ -935,14 +937,17 @@ cudaError_t launch_dim(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v1200
   const cudaError_t e = kernel_limits(reinterpret_cast<const void*>(kernel), C::kSmem, C::kSplit ? C::kLaunchRegs : 0,
                                       &done);
   if (e != cudaSuccess) return e;
-  int64_t grid = max_items(a, QT * kTile) * a.n_heads;
+  int64_t grid = max_items(a, QT * kTile) * a.n_heads, turns = 1;
   if (grid > 0x3fffffff) return cudaErrorInvalidValue;
   if (C::kCluster)
     grid *= cluster;  // an item a cluster
-  else if (grid > static_cast<int64_t>(sms) * CTAS)
+  else if (grid > static_cast<int64_t>(sms) * CTAS) {
+    turns = grid;
     grid = static_cast<int64_t>(sms) * CTAS;  // resident CTAs, that walk through the items
+    turns = (turns + grid - 1) / grid;
+  }
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream,
-                            static_cast<unsigned>(cluster), tm_q, tm_k, tm_v, a, cluster);
+                            static_cast<unsigned>(cluster), tm_q, tm_k, tm_v, a, cluster, static_cast<int>(turns));
 }
 
 template <int D>

@@ -254,3 +254,23 @@ def test_a_fall_behind_the_last_row_is_reported(csa):
             y = dict(x, cu_q=cu, cu_k=torch.cat([x["cu_k"], more]))
             assert torch.equal(prompt.run(csa, y)[0][:7], good[:7])  # (the rows behind may be the overlapping ones' too)
             assert csa.csa_check_status() == (5 if fall else 0)
+
+
+def test_prompt_attn_of_offsets_that_overlap_a_million_times(csa):
+    """Sequences that all begin at row 0 again: the call does no more work than one of as many rows could ask for
+    (the items of all of them would pass 32 bits), stays inside its rows and reports the falls."""
+    B, n = 1 << 20, 1 << 20
+    cu = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    cu[1::2] = n
+    for D, heads in ((64, 1), (128, 1)):
+        wide = torch.full((n + 512, heads, D), 3.0, dtype=torch.bfloat16, device=DEV)
+        q = wide[256:-256]
+        k = torch.zeros(256, 1, D, dtype=torch.bfloat16, device=DEV)
+        for keys in (0, 256):
+            cu_k = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+            cu_k[1::2] = keys
+            out = torch.full_like(wide, 3.0)
+            csa.csa_prompt_attn(cu, cu_k, q, k, k, 0.1, keys == 0, 0, None, out[256:-256])
+            assert csa.csa_check_status() == 5
+            assert (out[:256] == 3).all() and (out[-256:] == 3).all()
+            assert (out[256:-256] == 0).all()
