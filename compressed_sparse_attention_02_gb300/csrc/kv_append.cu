@@ -190,7 +190,7 @@ template <int THREADS, int NI>
 __global__ void __launch_bounds__(THREADS, kPagesCtas<THREADS, NI>)
     kv_append_pages_kernel(const KvAppendArgs a, const int heads) {
   constexpr int kWarps = THREADS / 32;
-  extern __shared__ float2 sc_s[];  // K: the rows' (sin, cos), rope_dim / 2 each
+  extern __shared__ __align__(16) float2 sc_s[];  // K: the rows' (sin, cos), rope_dim / 2 each
   __shared__ int sh[kWarps + 2];
   __shared__ float max_s[2][kWarps];
   pdl_launch_dependents();

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sh[kWarps], found_at[kWarps];
   __shared__ int found_b[kWarps];
-  __shared__ float scale_s[kWarps][C::kStages][4];  // k, k, v, v scales of the unit's two halves
+  __shared__ float4 scale_s[kWarps][C::kStages];    // k, k, v, v scales of the unit's two halves
   __shared__ int bad_s[kWarps][C::kStages];         // halves whose page is outside the cache
   pdl_launch_dependents();
   pdl_wait();
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
             cp_async_16(vs + dst, (i < kChunks / 2 ? va : vb) + off);
           }
           if (lane < 4)
-            cp_async_4_or_zero(smem_u32(&scale_s[warp][st][lane]),
+            cp_async_4_or_zero(smem_u32(&scale_s[warp][st]) + 4 * lane,
                                ((lane & 2) ? cache.v_scale : cache.k_scale) + ((lane & 1) ? slab_b : slab_a), true);
         } else {
 #pragma unroll 1
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
           if (lane < 4) {
             const bool there = (lane & 1) ? ok_b : ok_a;
             const float* from = ((lane & 2) ? cache.v_scale : cache.k_scale) + ((lane & 1) ? slab_b : slab_a);
-            cp_async_4_or_zero(smem_u32(&scale_s[warp][st][lane]), from, there);
+            cp_async_4_or_zero(smem_u32(&scale_s[warp][st]) + 4 * lane, from, there);
           }
         }
         if (lane == 0) bad_s[warp][st] = (bads & 1u) | ((bads >> 31) << 1);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
             mma_f16_16816(x[n], qf[s], b0, b1);
           }
         }
-        const float4 sc = *reinterpret_cast<const float4*>(scale_s[warp][st]);
+        const float4 sc = scale_s[warp][st];
         const int bad = bad_s[warp][st];
 #pragma unroll
         for (int n = 0; n < 4; ++n)

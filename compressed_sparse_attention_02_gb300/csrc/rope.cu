@@ -48,7 +48,7 @@ constexpr int kFlight = 3;
 constexpr int kRopeCtas = 4;
 
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeRowsArgs a, const RopeGrid g) {
-  extern __shared__ float2 sc_s[];  // the tokens' (sin, cos), rope_dim / 2 each
+  extern __shared__ __align__(16) float2 sc_s[];  // the tokens' (sin, cos), rope_dim / 2 each
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
