@@ -274,3 +274,30 @@ def test_prompt_attn_of_offsets_that_overlap_a_million_times(csa):
             assert csa.csa_check_status() == 5
             assert (out[:256] == 3).all() and (out[-256:] == 3).all()
             assert (out[256:-256] == 0).all()
+
+
+# ---- csa_rope on the compressed layer's rows --------------------------------------------
+
+def test_rope_turns_the_compressed_layers_queries(csa):
+    """The rotation that the layer calls expect their queries to have (the last 64 of 512 channels, interleaved
+    pairs), and the one that inverse_rope takes back: csa_rope gives both, over the library's own oracle.
+
+    The tolerance: an angle is right to 8e-8 rad and the polynomials to 2e-9, their steps' roundings stay below 2^-23,
+    and a channel is two products and a sum of 2^-24 each: below 2^-21 of its pair, and one rounding to bf16."""
+    import oracle
+    T, H, D, R = 24, 64, 512, 64
+    r = csa.rope_params(rope_dim=R, offset=D - R, layout=csa.CSA_ROPE_INTERLEAVED, theta=1e4)
+    turns = csa.rope_table(r)
+    g = torch.Generator(DEV).manual_seed(0)
+    x = torch.randn(T, H, D, device=DEV, generator=g).bfloat16()
+    pos = torch.randint(0, 1 << 18, (T,), device=DEV, generator=g, dtype=torch.int32)
+    for inverse in (False, True):
+        got = csa.csa_rope(r, turns, pos, x, inverse=inverse).double().cpu()
+        rows = x.double().cpu().numpy()
+        want = np.stack([oracle.inverse_rope(rows[t], int(pos[t]), rope_dim=R) if inverse else
+                         np.stack([oracle.rope(h, R, 1e4, int(pos[t])) for h in rows[t]]) for t in range(T)])
+        want = torch.from_numpy(want)
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -21 * ref.pair_size(r, x)
+        assert ((got - want).abs() <= tol).all()
+        assert torch.equal(got[..., :D - R], x[..., :D - R].double().cpu())
+    assert csa.csa_check_status() == 0
