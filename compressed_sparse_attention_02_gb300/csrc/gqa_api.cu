@@ -320,6 +320,7 @@ csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32
   a.v_stride = v_stride;
   a.v_stride_h = v_stride_h;
   a.sm_scale = sm_scale;
+  a.no_key = -1e30f / fmaxf(1.5f * sm_scale, 1.f);  // (the kernel's scale has a factor log2(e) more)
   a.causal = causal;
   a.window = window;
   a.sink = sink;

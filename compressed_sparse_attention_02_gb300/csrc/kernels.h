@@ -364,6 +364,7 @@ struct PromptAttnArgs {
   const uint16_t *q, *k, *v;
   int64_t q_stride, q_stride_h, k_stride, k_stride_h, v_stride, v_stride_h;
   float sm_scale;
+  float no_key;              // a row's maximum of q . k before its first key: what the scale takes to -1e30 at most
   int causal, window;
   const float* sink;
   uint16_t* out;             // [n_q][n_heads][head_dim]

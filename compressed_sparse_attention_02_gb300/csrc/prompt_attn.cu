@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kTileShift = 7;
 constexpr int kTile = 1 << kTileShift;   // queries and keys a tile
-constexpr float kNone = -1e30f;          // running maximum before the first key
 // The accumulators are rescaled only when a row's maximum has grown by more
 // than 2^8 since (weights up to 256 are exact in range for bf16 and fp32).
 constexpr float kLag = 8.f;
@@ -625,9 +624,9 @@ __global__ void __launch_bounds__(Cfg<D, QT, CTAS>::kThreads, CTAS)
         first_key = a.window > 0 && at_key >= a.window ? at_key - a.window + 1 : 0;
         loaded = n_tiles > 0;
       }
-      float m = kNone, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
+      float m = a.no_key, l = 0.f;  // the reference of the weights e^(scale (s - m)), in the products' units
       bool large = false;        // of the warp: some row's logits are large (see below)
-      auto is_large = [&]() { return m > kNone && fabsf(m * scale2) > 65536.f; };
+      auto is_large = [&]() { return m > a.no_key && fabsf(m * scale2) > 65536.f; };
       for (int part = 0; part < n_tiles * C::kParts; ++part) {
         const int n = part / C::kParts, h = part % C::kParts, j = j_top - n;
         ok = wait_or_abort(&s_full[t][h], (n_s + n) & 1, abort_flag, a.status);

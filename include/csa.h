@@ -780,6 +780,7 @@ csa_status csa_kv_append(const csa_paged_cache *c, const csa_rope_params *r,
  * sequence of length 0 (or less) gives 0 and lse = sink, or -inf without one.
  * q: [B][n_heads][head_dim] with strides.  out: [B][n_heads][head_dim], lse
  * [B][n_heads], contiguous.  sink: [n_heads] fp32, finite or -inf.
+ * Logits are held in fp32, up to 1e30 in magnitude.
  * Scales and logits may lie as far apart as fp32 reaches; a result below 2^-100
  * may come out as 0.
  * A length past the table is clamped, and tokens in a page outside the pool

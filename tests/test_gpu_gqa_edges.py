@@ -139,6 +139,22 @@ def test_prompt_attn_rows_are_those_of_what_they_see(csa, heads, D, lens, window
         first += nq
     assert csa.csa_check_status() == 0
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [2, 48])
+def test_prompt_attn_of_a_large_scale(csa, D, heads):
+    """sm_scale of 2^28 and 2^60 over rows so small that their logits are ordinary ones: the same bits as with the
+    power of two in the queries, rows that see nothing at first or at all among them."""
+    lens = [(200, 90), (130, 130), (33, 500), (257, 1900), (40, 0)]
+    x = prompt.make(lens, heads, 1, D, seed=D)
+    x["sink"][0] = -float("inf")
+    for window, sink in ((0, False), (0, True), (129, True)):
+        want, want_lse = prompt.run(csa, x, window=window, sink=sink, sm=2.0 ** -3)
+        for e in (28, 60):
+            y = dict(x, q=x["q"] * 2.0 ** (-3 - e))
+            out, lse = prompt.run(csa, y, window=window, sink=sink, sm=2.0 ** e)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert csa.csa_check_status() == 0
+
 
 # ---- csa_kv_append: pages that another program began -----------------------------------
 
