@@ -373,15 +373,29 @@ def _bad(where, name, t=None, expected=""):
 
 def _flat(where, name, t, dtype, shape, dev):
     """A contiguous tensor of this type and shape on the current device: its address."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _bad(where, name, t, "contiguous %s %s on the current device" % (dtype, tuple(shape)))
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        pass
+    _bad(where, name, t, "contiguous %s %s on the current device" % (dtype, tuple(shape)))
+
+
+def _count(where, name, t):
+    try:
+        return t.numel()
+    except AttributeError:
+        _bad(where, name, t, "a tensor")
 
 
 def _rows(where, name, t, shape, dev):
     """[rows][heads][channels] bf16 with contiguous channels on the current device: address, row and head stride (of
     a dimension of size one, whose stride has no meaning, a valid one)."""
-    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+    try:
+        bad = t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev
+    except AttributeError:  # no tensor
+        bad = True
+    if bad:
         _bad(where, name, t, "bfloat16 %s on the current device" % (tuple(shape),))
     rows, heads, dim = shape
     row, head, one = t.stride()
@@ -437,10 +451,10 @@ def paged_cache(k, v, k_scale, v_scale, table) -> CsaPagedCache:
     k_scale, v_scale [pages][kv heads] fp32, table [sequences][pages] int32.  It keeps the tensors."""
     w = "paged_cache"
     for name, t in (("k", k), ("v", v)):
-        if t.dim() != 4 or t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_cuda:
+        if not torch.is_tensor(t) or t.dim() != 4 or t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_cuda:
             _bad(w, name, t, "E4M3 or uint8 [pages][kv heads][page size][channels] in device memory")
     dev = torch.cuda.current_device()
-    if table.dim() != 2:
+    if not torch.is_tensor(table) or table.dim() != 2:
         _bad(w, "table", table, "[sequences][pages]")
     n, heads, page, dim = k.shape
     c = CsaPagedCache(heads, dim, page, n, _flat(w, "k", k, k.dtype, k.shape, dev),
@@ -455,7 +469,7 @@ def csa_kv_append(cache, r, turns, cu_rows, pos0, k, v, stream=None):
     """Appends rows of k and v [rows][kv heads][channels] to the cache from positions pos0 [B] on; sequence b's rows
     are cu_rows[b] .. cu_rows[b+1]-1 (cu_rows [B+1], or None: one row each).  r and turns None: keys as they are."""
     w = "csa_kv_append"
-    B, shape = pos0.numel(), _shape3(w, "k", k)
+    B, shape = _count(w, "pos0", pos0), _shape3(w, "k", k)
     dev = torch.cuda.current_device()
     n, heads, dim = shape
     if heads != cache.n_kv_heads or dim != cache.head_dim or (cu_rows is None and n != B):
@@ -487,7 +501,7 @@ def csa_paged_attn(cache, lens, q, sm_scale, window, sink, out, lse, ws, stream=
     if dim != cache.head_dim or B > cache.n_seqs or cache.device != dev:
         _bad(w, "q", q, "at most %d sequences, heads of %d, the cache on the current device" %
              (cache.n_seqs, cache.head_dim))
-    size = 0 if ws is None else ws.numel()
+    size = 0 if ws is None else _count(w, "ws", ws)
     _check(_lib.csa_paged_attn(ctypes.byref(cache), B, heads, _flat(w, "lens", lens, _I32, (B,), dev),
                                *_rows(w, "q", q, shape, dev), sm_scale, window,
                                None if sink is None else _flat(w, "sink", sink, _F32, (heads,), dev),
@@ -506,7 +520,7 @@ def csa_prompt_attn(cu_q, cu_k, q, k, v, sm_scale, causal, window, sink, out, ls
     n, heads, dim = shape
     if kv_shape[2] != dim:
         _bad(w, "k", k, "heads of %d" % dim)
-    B = cu_q.numel() - 1
+    B = _count(w, "cu_q", cu_q) - 1
     if B < 0:
         _bad(w, "cu_q", cu_q, "sequences + 1 offsets")
     _check(_lib.csa_prompt_attn(B, heads, kv_shape[1], dim, n, kv_shape[0],

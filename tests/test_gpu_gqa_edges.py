@@ -317,3 +317,35 @@ def test_rope_turns_the_compressed_layers_queries(csa):
         assert ((got - want).abs() <= tol).all()
         assert torch.equal(got[..., :D - R], x[..., :D - R].double().cpu())
     assert csa.csa_check_status() == 0
+
+
+# ---- arguments that are no tensors ------------------------------------------------------
+
+def test_what_is_no_tensor_is_refused(csa):
+    """Every tensor argument as None or a list: CSA_ERR_INVALID_ARG, as for one of another type."""
+    x = paged.make([40, 9], 4, 2, 64, 16)
+    cache = csa.paged_cache(x["k"], x["v"], x["ks"], x["vs"], x["table"])
+    r = csa.rope_params(rope_dim=64)
+    turns, pos = csa.rope_table(r), torch.zeros(2, dtype=torch.int32, device=DEV)
+    kv, out = x["q"][:, :2].contiguous(), torch.empty_like(x["q"])
+    y = prompt.make([(5, 5)], 4, 2, 64)
+    calls = (
+        (csa.paged_cache, dict(k=x["k"], v=x["v"], k_scale=x["ks"], v_scale=x["vs"], table=x["table"]), ()),
+        (csa.csa_rope, dict(r=r, turns=turns, pos=pos, x=x["q"], out=out), ("r", "out")),
+        (csa.csa_kv_append, dict(cache=cache, r=r, turns=turns, cu_rows=None, pos0=pos, k=kv, v=kv),
+         ("cache", "r", "cu_rows")),
+        (csa.csa_paged_attn, dict(cache=cache, lens=x["lens"], q=x["q"], sm_scale=0.1, window=0, sink=None, out=out,
+                                  lse=None, ws=csa.paged_attn_workspace(cache, 2, 4)),
+         ("cache", "sm_scale", "window", "sink", "lse", "ws")),
+        (csa.csa_prompt_attn, dict(cu_q=y["cu_q"], cu_k=y["cu_k"], q=y["q"], k=y["k"], v=y["v"], sm_scale=0.1,
+                                   causal=True, window=0, sink=None, out=torch.empty_like(y["q"])),
+         ("sm_scale", "causal", "window", "sink")))
+    for call, args, free in calls:
+        call(**args)
+        for name in args:
+            for bad in ([1.0, 2.0],) if name in ("sink", "lse", "ws", "cu_rows") else (None, [1.0, 2.0]):
+                if name in free and name not in ("sink", "lse", "ws", "cu_rows"):
+                    continue
+                with pytest.raises(csa.CsaError) as e:
+                    call(**dict(args, **{name: bad}))
+                assert e.value.status == 1, (call, name)
