@@ -12,9 +12,10 @@ namespace csa {
 // Sine and cosine of position p at the frequency whose table entry is turns
 // (2^-64 turns a position): the angle's fraction of a turn is the low 64 bits
 // of p * turns, exact.  The nearest quarter turn is taken off as an integer,
-// so the remainder, at most an eighth of a turn, keeps 24 bits of its own:
-// the angle is right to 2e-8 rad whatever p is (a quarter of what rounding
-// the whole fraction to binary32 would leave).
+// so the remainder, at most an eighth of a turn, keeps 24 bits of its own: its
+// rounding is at most 2.3e-8 rad (an eighth of the whole fraction's), the
+// constant's and the product's add 2.2e-8 and 3.0e-8.  The angle is right to
+// 8e-8 rad of the table's whatever p is.
 // Both functions there are their Taylor polynomials, cut where the next term
 // is below 2e-9 and 2e-10 of an angle of pi/4.
 __device__ __forceinline__ void rope_sincos_exact(int64_t p, uint64_t turns, float* s, float* c) {

@@ -17,8 +17,9 @@
 // crosses threads.  Keys are walked from the diagonal down: the masked tiles
 // come first.  With one tile a CTA its keys are worked on in halves, one's
 // scores under the other's softmax.  16384 queries of 32 heads of width 128:
-// 1.39 ms, 1580 TFLOP/s, 83% of the matrix product's rate; 16 prompts of 237 to
-// 2500 under a window of 1024 at width 64: 204 us, 555 TFLOP/s.
+// 1.42 ms (1550 TFLOP/s, 82% of the matrix product's rate) in a few passes, 1.48
+// ms in calls that follow each other for seconds; 16 prompts of 237 to 2500 under
+// a window of 1024 at width 64: 206 us, 550 TFLOP/s.
 //
 // P is rounded to bf16 (the products take one type for both operands, and V
 // is bf16); sums and maxima are fp32, over the unrounded weights.
@@ -54,10 +55,10 @@ struct Cfg {
   static constexpr int kBlockBytes = kTile * 128;
   static constexpr int kStages = CTAS == 2 && D == 128 ? 2 : 4;  // K and V tiles in flight, alternating; a power of two
   // The output is staged 32 channels at a time in a place of its own, so that
-  // the next queries are copied and multiplied under it; two tiles of them, of
-  // which one's softmax runs under the other's end anyway, stage it whole where
-  // their queries were (32 prompts of 500 131 us, 143 so; 16 of 1000 with two
-  // tiles a CTA 183 us, 210 otherwise).
+  // the next queries are copied and multiplied under it (32 prompts of 500 131
+  // us, 143 where the queries were).  Two tiles a CTA stage it whole where their
+  // queries were, and the next ones wait for it: in a place of its own, 32
+  // channels at a time, 16 of 1000 took 210 us instead of 183.
   static constexpr bool kOwnStage = QT == 1;
   static constexpr int kOutBytes = kOwnStage ? kTile * 64 : 0;
   static constexpr int kSmem = (QT + kStages) * kTileBytes + kOutBytes + 1024;
@@ -971,7 +972,10 @@ cudaError_t launch_tiles(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12
   // under a window of 512 684 and 775, of 1024 1003 and 999; 64 times 200
   // queries over 1200 keys 326 and 297, 64 times 120 over 1120 167 and 239.  At
   // width 64 one tile was never slower (16 packed prompts, window 1024: 206 and
-  // 281; 8 of 2048 185 and 232).
+  // 281; 8 of 2048 185 and 232).  The rule knows the totals only: among many
+  // short sequences, or ones without rows, a few long ones get one tile a CTA
+  // (one of 8000 and 60 of 200 533 us, 473 with two; 16 of 2000 and 48 empty ones
+  // 542 and 520; two of 4000 and 32 of 300 339 and 344).
   constexpr int64_t kFewKeys = 1024;
   const int64_t in_windows = static_cast<int64_t>(a.window) * a.B;
   const int64_t keys = a.window > 0 && in_windows < a.n_k ? in_windows : a.n_k;

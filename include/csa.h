@@ -662,12 +662,15 @@ csa_status csa_hca_layer_decode(const csa_params *p, int32_t B,
 
 /*
  * ---- Grouped-query attention layers ------------------------------------------
- * Hybrid models place ordinary attention layers beside the compressed ones:
- * query heads that share key / value heads in groups ([结构对比] "MHA、GQA",
- * the layers that CSA and HCA are compared with).  The calls below serve such
- * a layer: rotate queries and keys, attend over packed prompts, append keys
- * and values to a paged 8-bit cache, and attend to it one token at a time.
- * They take no csa_params.  Conventions are those at the top, with these
+ * For programs that also have ordinary attention layers, with query heads that
+ * share key / value heads in groups ([结构对比] "MHA、GQA" compares CSA and HCA
+ * with such layers; the pages describe no model that mixes the two).  The calls
+ * below serve such a layer: rotate queries and keys, attend over packed
+ * prompts, append keys and values to a paged 8-bit cache, and attend to it one
+ * token at a time.  The layer calls above use none of them, and the cache and
+ * both attentions stop at width 128; csa_rope also turns the compressed
+ * layers' own rows (rope_dim 64, offset 448, CSA_ROPE_INTERLEAVED), which the
+ * layer calls expect of their queries.  They take no csa_params.  Conventions are those at the top, with these
  * additions: rows are [rows][heads][head_dim] bf16 with strides in elements
  * for rows and heads (multiples of 8, at least head_dim; the channels are
  * contiguous), so views of a fused projection pass as they are; row pointers
@@ -788,7 +791,9 @@ csa_status csa_kv_append(const csa_paged_cache *c, const csa_rope_params *r,
  * Workspace: csa_paged_attn_workspace_size bytes (a constant of the device
  * and head_dim), of the call's own while it runs: calls that can overlap on
  * the GPU, replayed graphs among them, need one each.
- * Equal calls give equal bits.
+ * Equal calls give equal bits.  Queries are rounded to f16 after a power of two
+ * takes their row's largest to [2^14, 2^15): exact but for values 2^-28 below
+ * it.  Weights are rounded to f16 for the product with the values.
  */
 size_t csa_paged_attn_workspace_size(const csa_paged_cache *c, int32_t B,
                                      int32_t n_heads);
