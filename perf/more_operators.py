@@ -240,7 +240,7 @@ def prepare(case, seed):
         cap = max(pages(x, P) for x in before + after + [1])
         s.update(_book(before, cap, P, case["pool"], seed))
         s["before"], s["after"] = _i32(before), _i32(after)
-        s["pos0"] = torch.empty(case["seqs"], dtype=I32, device="cuda")
+        s["pos0"], s["src"], s["dst"] = (torch.empty(case["seqs"], dtype=I32, device="cuda") for _ in range(3))
     elif op == "fork":
         L = parent_lengths(case) + [0] * case["children"]
         s.update(_book(L, max(pages(x, P) for x in L), P, case["pool"], seed))
@@ -299,15 +299,15 @@ def run(s):
         return {"k": s["k"], "v": s["v"], "k_scale": s["k_scale"], "v_scale": s["v_scale"]}
     if op == "resize":  # back to where they were, and on again: every pass leaves the same
         if own:
-            s["csa"].csa_pages_resize(s["book"], s["before"], None, s["ws"])
-            s["csa"].csa_pages_resize(s["book"], s["after"], s["pos0"], s["ws"])
+            s["csa"].csa_pages_resize(s["book"], s["before"], None, None, None, s["ws"])
+            s["csa"].csa_pages_resize(s["book"], s["after"], s["pos0"], s["src"], s["dst"], s["ws"])
         else:
             _resize(s, s["before"], c["page"])
-            s["pos0"] = _resize(s, s["after"], c["page"])
-        return {x: s[x] for x in ("table", "lens", "refs", "pos0")}
+            s["pos0"], s["src"], s["dst"] = _resize(s, s["after"], c["page"])
+        return {x: s[x] for x in ("table", "lens", "refs", "pos0", "src", "dst")}
     if op == "fork":  # the last step's children end, new ones start
         if own:
-            s["csa"].csa_pages_resize(s["book"], s["none"], None, s["ws"])
+            s["csa"].csa_pages_resize(s["book"], s["none"], None, None, None, s["ws"])
             s["csa"].csa_pages_fork(s["book"], s["parent"], s["src"], s["dst"], s["ws"])
         else:
             _resize(s, s["none"], c["page"])
@@ -369,20 +369,25 @@ def _resize(s, target, P):
     n0 = (lens + P - 1) // P
     n1 = torch.where(target >= 0, (target + P - 1) // P, n0)
     free, count = _free_pages(refs)
-    need = (n1 - n0).clamp(min=0).long()
+    # a last page that is partly filled and has other holders is left to them
+    last = table.gather(1, (lens // P).clamp(max=table.shape[1] - 1).long()[:, None])[:, 0]
+    apart = (target > lens) & (lens % P > 0) & (refs[last.clamp(min=0).long()] > 1)
+    from_ = n0 - apart.int()
+    need = (n1 - from_).clamp(min=0).long()
     upto = need.cumsum(0)
     served = (upto <= count) | (need == 0)
+    apart = apart & served
     j = torch.arange(table.shape[1], device="cuda")
-    gone = (j >= n1[:, None]) & (j < n0[:, None])
-    taken = (j >= n0[:, None]) & (j < n1[:, None]) & served[:, None]
-    page = free[torch.where(taken, (upto - need)[:, None] + j - n0[:, None], 0)]
+    gone = (j >= n1[:, None]) & (j < n0[:, None]) | apart[:, None] & (j == from_[:, None])
+    taken = (j >= from_[:, None]) & (j < n1[:, None]) & served[:, None]
+    page = free[torch.where(taken, (upto - need)[:, None] + j - from_[:, None], 0)]
     refs.index_add_(0, torch.where(gone, table, 0).flatten().long(), -gone.flatten().int())
     refs.index_add_(0, torch.where(taken, page, 0).flatten().long(), taken.flatten().int())
     table.copy_(torch.where(taken, page, torch.where(gone, -1, table)))
     grown = (target > lens) & served
     pos0 = torch.where(grown, lens, -1)
     lens.copy_(torch.where((target >= 0) & served, target, lens))
-    return pos0
+    return pos0, torch.where(apart, last, -1), torch.where(apart, free[torch.where(apart, upto - need, 0)], -1)
 
 
 def _fork(s, P):
@@ -455,7 +460,9 @@ def exact(case, seed):
     if op == "resize":
         _walk_resize(s, s["before"], P)
         pos0 = _walk_resize(s, s["after"], P)
-        return dict({x: torch.from_numpy(s[x]) for x in ("table", "lens", "refs")}, pos0=torch.tensor(pos0, dtype=I32))
+        none = torch.full((len(pos0),), -1, dtype=I32)  # (no two sequences share a page)
+        return dict({x: torch.from_numpy(s[x]) for x in ("table", "lens", "refs")}, pos0=torch.tensor(pos0, dtype=I32),
+                    src=none, dst=none)
     if op == "fork":
         _walk_resize(s, s["none"], P)
         free = [int(p) for p in np.flatnonzero(s["refs"] == 0)][::-1]
@@ -491,7 +498,7 @@ def exact(case, seed):
 
 
 def _walk_resize(s, target, P):
-    """Page by page; there is room for all."""
+    """Page by page; there is room for all, and no page is shared but for whole ones."""
     free = [int(p) for p in np.flatnonzero(s["refs"] == 0)][::-1]
     pos0 = []
     for b, t in enumerate(int(t) for t in target):
