@@ -344,7 +344,14 @@ class CsaPagedCache(ctypes.Structure):
                 ("table_stride", ctypes.c_int64)]
 
 
-_R, _C = ctypes.POINTER(CsaRopeParams), ctypes.POINTER(CsaPagedCache)
+class CsaPageBook(ctypes.Structure):
+    """Mirror of ``csa_page_book`` (device pointers; see page_book)."""
+    _fields_ = [("n_seqs", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
+
+
+_R, _C, _K = ctypes.POINTER(CsaRopeParams), ctypes.POINTER(CsaPagedCache), ctypes.POINTER(CsaPageBook)
 _lib.csa_default_rope.argtypes = [_R]
 _lib.csa_default_rope.restype = None
 _lib.csa_rope_table.argtypes = [_R, _vp]
@@ -356,7 +363,18 @@ _lib.csa_paged_attn.argtypes = [_C, _i32, _i32, _vp, _vp, _i64, _i64, ctypes.c_f
                                 _vp]
 _lib.csa_prompt_attn.argtypes = ([_i32] * 4 + [_i64] * 2 + [_vp] * 2 + [_vp, _i64, _i64] * 3 +
                                  [ctypes.c_float, _i32, _i32] + [_vp] * 4)
-for _f in ("csa_rope_table", "csa_rope", "csa_kv_append", "csa_paged_attn", "csa_prompt_attn"):
+_lib.csa_chunk_attn_workspace_size.argtypes = [_C, _i32]
+_lib.csa_chunk_attn_workspace_size.restype = _sz
+_lib.csa_chunk_attn.argtypes = [_C, _i32, _i32, _i64, _vp, _vp, _vp, _i64, _i64, ctypes.c_float, _i32, _vp, _vp, _vp,
+                                _vp, _sz, _vp]
+_lib.csa_pages_workspace_size.argtypes = [_K]
+_lib.csa_pages_workspace_size.restype = _sz
+_lib.csa_pages_resize.argtypes = [_K] + [_vp] * 5 + [_sz, _vp]
+_lib.csa_pages_fork.argtypes = [_K] + [_vp] * 4 + [_sz, _vp]
+_lib.csa_pages_compact.argtypes = [_K] + [_vp] * 6 + [_sz, _vp]
+_lib.csa_pages_copy.argtypes = [_C, _i64, _vp, _vp, _vp]
+for _f in ("csa_rope_table", "csa_rope", "csa_kv_append", "csa_paged_attn", "csa_prompt_attn", "csa_chunk_attn",
+           "csa_pages_resize", "csa_pages_fork", "csa_pages_compact", "csa_pages_copy"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -532,6 +550,110 @@ def csa_prompt_attn(cu_q, cu_k, q, k, v, sm_scale, causal, window, sink, out, ls
                                 _flat(w, "out", out, _BF16, shape, dev),
                                 None if lse is None else _flat(w, "lse", lse, _F32, (n, heads), dev),
                                 _stream(stream, dev)), w)
+
+
+def chunk_attn_workspace(cache, n_heads: int) -> torch.Tensor:
+    """Allocates (through torch) a workspace for csa_chunk_attn."""
+    n = int(_lib.csa_chunk_attn_workspace_size(ctypes.byref(cache), n_heads))
+    if n == 0:
+        raise CsaError(2, "csa_chunk_attn_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def csa_chunk_attn(cache, cu_q, lens, q, sm_scale, window, sink, out, lse, ws, stream=None):
+    """Packed queries q [rows][heads][channels] by cu_q [B+1], each sequence's at the last of its cached tokens
+    0 .. lens[b]-1, into out (like q, contiguous) and lse [rows][heads] fp32 or None."""
+    w = "csa_chunk_attn"
+    shape, B = _shape3(w, "q", q), _count(w, "lens", lens)
+    dev = torch.cuda.current_device()
+    n, heads, dim = shape
+    if dim != cache.head_dim or B > cache.n_seqs or cache.device != dev:
+        _bad(w, "q", q, "at most %d sequences, heads of %d, the cache on the current device" %
+             (cache.n_seqs, cache.head_dim))
+    size = 0 if ws is None else _count(w, "ws", ws)
+    _check(_lib.csa_chunk_attn(ctypes.byref(cache), B, heads, n, _flat(w, "cu_q", cu_q, _I32, (B + 1,), dev),
+                               _flat(w, "lens", lens, _I32, (B,), dev), *_rows(w, "q", q, shape, dev), sm_scale,
+                               window, None if sink is None else _flat(w, "sink", sink, _F32, (heads,), dev),
+                               _flat(w, "out", out, _BF16, shape, dev),
+                               None if lse is None else _flat(w, "lse", lse, _F32, (n, heads), dev),
+                               None if ws is None else _flat(w, "ws", ws, torch.uint8, (size,), dev), size,
+                               _stream(stream, dev)), w)
+
+
+def page_book(table, lens, refs, page_size) -> CsaPageBook:
+    """A ``csa_page_book`` over device tensors: table [sequences][pages], lens [sequences] and refs [pages of the
+    pool], all int32.  It keeps the tensors."""
+    w = "page_book"
+    if not torch.is_tensor(table) or table.dim() != 2 or not table.is_cuda:
+        _bad(w, "table", table, "[sequences][pages] in device memory")
+    dev = torch.cuda.current_device()
+    n = _count(w, "refs", refs)
+    k = CsaPageBook(table.shape[0], page_size, n, _flat(w, "table", table, _I32, table.shape, dev), table.shape[1],
+                    _flat(w, "lens", lens, _I32, (table.shape[0],), dev), _flat(w, "refs", refs, _I32, (n,), dev))
+    k.tensors, k.device = (table, lens, refs), dev
+    return k
+
+
+def pages_workspace(book) -> torch.Tensor:
+    """Allocates (through torch) a workspace for the csa_pages calls."""
+    n = int(_lib.csa_pages_workspace_size(ctypes.byref(book)))
+    if n == 0:
+        raise CsaError(2, "csa_pages_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def _book_call(where, book, ws):
+    """The current device, the book's on it, and the workspace's address and size."""
+    dev = torch.cuda.current_device()
+    if book.device != dev:
+        _bad(where, "book: on another device than the current one")
+    size = 0 if ws is None else _count(where, "ws", ws)
+    return dev, None if ws is None else _flat(where, "ws", ws, torch.uint8, (size,), dev), size
+
+
+def csa_pages_resize(book, target, pos0, src, dst, ws, stream=None):
+    """The sequences' lengths become target [sequences] (negative: as it is); pos0 (or None) receives the length
+    before of those that have grown and -1; src and dst (or None, both) the pages to copy.  All int32."""
+    w, n = "csa_pages_resize", (book.n_seqs,)
+    dev, at, size = _book_call(w, book, ws)
+    _check(_lib.csa_pages_resize(ctypes.byref(book), _flat(w, "target", target, _I32, n, dev),
+                                 *[None if t is None else _flat(w, name, t, _I32, n, dev)
+                                   for name, t in (("pos0", pos0), ("src", src), ("dst", dst))],
+                                 at, size, _stream(stream, dev)), w)
+
+
+def csa_pages_fork(book, parent, src, dst, ws, stream=None):
+    """Sequence b becomes a copy of parent[b] (negative: it is left alone); src and dst receive the pages to copy.
+    All [sequences] int32."""
+    w, n = "csa_pages_fork", (book.n_seqs,)
+    dev, at, size = _book_call(w, book, ws)
+    _check(_lib.csa_pages_fork(ctypes.byref(book), _flat(w, "parent", parent, _I32, n, dev),
+                               _flat(w, "src", src, _I32, n, dev), _flat(w, "dst", dst, _I32, n, dev), at, size,
+                               _stream(stream, dev)), w)
+
+
+def csa_pages_compact(book, src, dst, used, table_out, refs_out, ws, stream=None):
+    """New numbers for the used pages, 0 .. used-1: src and dst [pages // 2] receive the moves, table_out and refs_out
+    (which may be the book's own) the table and the counts afterwards.  All int32."""
+    w = "csa_pages_compact"
+    dev, at, size = _book_call(w, book, ws)
+    half = (book.n_pages // 2,)
+    _check(_lib.csa_pages_compact(ctypes.byref(book), _flat(w, "src", src, _I32, half, dev),
+                                  _flat(w, "dst", dst, _I32, half, dev), _flat(w, "used", used, _I32, (1,), dev),
+                                  _flat(w, "table_out", table_out, _I32, (book.n_seqs, book.table_stride), dev),
+                                  _flat(w, "refs_out", refs_out, _I32, (book.n_pages,), dev), at, size,
+                                  _stream(stream, dev)), w)
+
+
+def csa_pages_copy(cache, src, dst, stream=None):
+    """The contents of the cache's pages src into its pages dst (int32, as many; negative: none)."""
+    w = "csa_pages_copy"
+    n = _count(w, "src", src)
+    dev = torch.cuda.current_device()
+    if cache.device != dev:
+        _bad(w, "cache: on another device than the current one")
+    _check(_lib.csa_pages_copy(ctypes.byref(cache), n, _flat(w, "src", src, _I32, (n,), dev),
+                               _flat(w, "dst", dst, _I32, (n,), dev), _stream(stream, dev)), w)
 
 
 CSA_TEST_FAULT_INDEXER, CSA_TEST_FAULT_TOPK, CSA_TEST_FAULT_ATTN = 1, 2, 4

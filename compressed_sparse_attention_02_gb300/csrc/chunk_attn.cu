@@ -1,0 +1,1282 @@
+// Attention of a chunk of new tokens a sequence over its pages of E4M3 codes,
+// grouped heads, causal (the chunk's tokens are the sequence's last), optionally
+// windowed, with an optional attention sink:
+//   l_ij = sm_scale k_scale(page of j) q_i . codes_j,   p_ij = e^(l_ij - m_i)
+//   out_i = sum_j p_ij v_scale(page) codes^v_j / (sum_j p_ij + e^(sink - m_i))
+// over j <= len - n + i and, with a window W, j > len - n + i - W.
+//
+// The heads that share a key head are rows of one problem: row r of a key head
+// is head r % group of query r / group, so that the keys are read once for all
+// of them and few queries fill a tile.  A tile is 256 rows, two halves of 128
+// that work in turn on each block of 128 keys, one's softmax under the other's
+// products; one of at most 128 rows has its blocks shared out to the two halves,
+// whose sums are joined at its end.
+//
+// The blocks of all tiles form one line that is cut into equal shares, one a
+// CTA, whatever the lengths are; a tile that a cut divides is finished by the
+// merge kernel from fp32 partial results in a fixed order.
+//
+// S = Q K^T takes the codes as they are: a query row, scaled by a power of two,
+// is the sum of two E4M3 rows (a bf16 value has 8 significant bits, each part
+// holds 4), two products at twice the 16-bit rate.  The scales of keys are
+// factors of the logits.  The codes of values become f16, exactly, written by
+// four warps for the product O += P V; their scales go into the weights, whose
+// exponents they shift.  S and O are in tensor memory, P is written over S as
+// f16 and read from there.  The softmax has one thread a row, so no value
+// crosses threads.
+//
+// A masked weight is 0, and 0 * NaN is NaN: in blocks that some row of the tile
+// masks, NaN codes of values are taken out as they become f16, and the rows that
+// do see such a key get its NaN at the end.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <float.h>
+
+#include "gqa.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kTileShift = 7;
+constexpr int kTile = 1 << kTileShift;      // rows of a half, keys of a block
+constexpr int kTileRows = 2 * kTile;
+constexpr int kGroups = kTile / 16;         // groups of 16 keys, whose page is one
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 8, kLoadWarp = 12, kMmaWarp = 13, kWarpsUsed = 14;
+constexpr int kConvThreads = 128;
+// A maximum may lag behind by this much (in log2) before the sums are rescaled:
+// weights are then at most 2^8 times 1, and as f16 they carry 2^7 more, so that
+// weights down to 2^-21 of the largest keep f16's full precision.
+constexpr float kLag = 8.f;
+constexpr float kWeightExp = 7.f;
+// The weights' sum is taken from the weights, value scale in, a group of keys
+// at a time.  Where that scale takes weights further down than this, they may
+// pass fp32 while e^(l - m) counts: the sum then has exponentials of its own.
+constexpr float kFar = -64.f;
+constexpr float kLarge = 65536.f;           // a maximum whose half step, 2^-8, may show in a weight
+constexpr float kNone = -1e30f;             // running maximum before the first key
+// Blocks that some row of a tile masks: the causal edge of 256 rows crosses at
+// most 3, the window's edge 3.
+constexpr int kMaxMasked = 8;
+// What a tile costs, in the units of the shares: a block for two halves, for
+// one, and the tile itself.
+constexpr int kCostTwo = 3, kCostOne = 2, kCostTile = 4;
+
+template <int D>
+struct Cfg {
+  static constexpr int kQBytes = kTile * D * 2;     // of a half: two E4M3 parts
+  static constexpr int kCodeBytes = kTile * D;      // of a block's keys or values
+  static constexpr int kVBytes = kTile * D * 2;     // of a block's values as f16
+  static constexpr int kKStages = D == 128 ? 3 : 6;
+  static constexpr int kRawStages = D == 128 ? 2 : 4;
+  static constexpr int kVStages = 2;
+  static constexpr int kMeta = 2 * kKStages;
+  static constexpr int kStageOut = 8 * 1024;        // 32 rows of 16 channels a warp
+  static constexpr int kSmem =
+      2 * kQBytes + kKStages * kCodeBytes + kRawStages * kCodeBytes + kVStages * kVBytes + kStageOut + 1024;
+  static constexpr int kSCol(int t) { return t * kTile; }
+  static constexpr int kOCol(int t) { return 2 * kTile + t * D; }
+  static constexpr int kCols = 512;
+  static constexpr int64_t kRecord = static_cast<int64_t>(kTileRows) * (D + 4);  // floats of a partial result
+};
+// Registers a thread: 512 are launched with 128 each.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kConvRegs = 72, kOtherRegs = 56;
+static_assert(2 * kSoftmaxRegs + kConvRegs + kOtherRegs <= 4 * kLaunchRegs, "registers of the block");
+
+// A tile that a share's end divides, for the merge.
+struct __align__(16) Cut {
+  int32_t q0, row0, head0, rows;  // rows 0: no such tile
+  int32_t first, last, pad0, pad1;
+};
+
+struct Seq {
+  int q0, n, len;  // rows of q from q0 on, cached tokens
+};
+// A sequence as its arrays have it: n is 0 where its offsets are wrong.
+__device__ __forceinline__ Seq read_seq(const ChunkAttnArgs& a, int b) {
+  const int32_t q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+  const int64_t len = __ldg(a.lens + b), cap = a.cache.table_stride << a.cache.page_shift;
+  Seq s;
+  s.q0 = q0;
+  s.n = q1 - q0;
+  if (q0 < 0 || q1 < q0 || q1 > a.n_q) {
+    record_error(a.status, kErrIndexRange);
+    s.q0 = s.n = 0;
+  }
+  if (len > cap) record_error(a.status, kErrIndexRange);
+  s.len = static_cast<int>(len < 0 ? 0 : len > cap ? cap : len);
+  return s;
+}
+
+// A tile of a sequence: its rows (of one key head) and the keys they see.
+struct Tile {
+  int rows, lo, hi;  // keys [lo, hi)
+  int j_hi, blocks;  // blocks j_hi - 1 downwards; one at least
+  __device__ __forceinline__ int unit() const { return rows > kTile ? kCostTwo : kCostOne; }
+  __device__ __forceinline__ int64_t cost() const { return kCostTile + static_cast<int64_t>(unit()) * blocks; }
+};
+__device__ __forceinline__ Tile tile_of(const Seq& s, int group, int window, int t) {
+  Tile x;
+  const uint32_t row0 = static_cast<uint32_t>(t) * kTileRows, all = static_cast<uint32_t>(s.n) * group;
+  x.rows = static_cast<int>(min(all - row0, static_cast<uint32_t>(kTileRows)));
+  const int shift = s.len - s.n;  // (lengths and rows are below 2^30 and 2^27: no overflow)
+  const int first = shift + static_cast<int>(row0 / group);
+  const int last = shift + static_cast<int>((row0 + x.rows - 1) / group);
+  x.hi = last + 1;
+  x.lo = window > 0 && first >= window ? first - window + 1 : 0;
+  if (x.hi <= 0) x.hi = x.lo = 0;
+  x.j_hi = x.hi > 0 ? (x.hi + kTile - 1) >> kTileShift : 1;
+  x.blocks = x.j_hi - (x.lo >> kTileShift);
+  return x;
+}
+__device__ __forceinline__ int tiles_of(const Seq& s, int group) {
+  return static_cast<int>((static_cast<uint32_t>(s.n) * group + kTileRows - 1) / kTileRows);
+}
+
+// What a warp of a CTA has to know of a tile that it works on.
+struct Order {
+  int there;                    // 0: no more
+  int b, q0, row0, rows, head0, kv_head;
+  int shift;                    // query i stands at key i + shift
+  int lo, hi, from, upto;       // the tile's keys; its masked blocks: from `from` on, and up to `upto`
+  int j_top, blocks;            // this share's blocks: j_top downwards
+  int split;                    // the halves share out the blocks
+  int record;                   // -1: the tile is whole, else which of the share's records takes it
+  __device__ __forceinline__ bool masked(int j) const { return j >= from || j <= upto; }
+};
+
+// Two fp32 values as f16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four E4M3 codes (low byte first) as two pairs of f16, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+// The nearest E4M3 codes of four values, the first in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x4(float x, float y, float z, float w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(x), "f"(y), "f"(z), "f"(w));
+  return r;
+}
+// Non-zero where a byte is a NaN code (magnitude 0x7F, which carries into the
+// byte's top bit).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// What every CTA finds out first: its share of the line, and where it begins.
+struct Start {
+  int64_t per, total, offset;  // offset: units of sequence b before the share's first
+  int b, top;                  // rows of q below `top` belong to earlier sequences
+};
+
+// The cost of a sequence's tiles of one key head, and the largest row of q that
+// sequences whose offsets are right reach, by every thread of a warp for its own
+// sequence.  Sequences with more than two tiles are summed up by the whole warp.
+__device__ __forceinline__ int64_t head_cost(const Seq& s, int group, int window) {
+  const int tiles = tiles_of(s, group), lane = threadIdx.x & 31;
+  int64_t c = 0;
+  if (tiles > 0 && tiles <= 2) {
+    c = tile_of(s, group, window, 0).cost();
+    if (tiles == 2) c += tile_of(s, group, window, 1).cost();
+  }
+  for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+    const int from = __ffs(many) - 1;
+    Seq x;
+    x.q0 = 0;
+    x.n = __shfl_sync(0xffffffffu, s.n, from);
+    x.len = __shfl_sync(0xffffffffu, s.len, from);
+    const int nt = __shfl_sync(0xffffffffu, tiles, from);
+    int64_t sum = 0;
+    for (int t = lane; t < nt; t += 32) sum += tile_of(x, group, window, t).cost();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == from) c = sum;
+  }
+  return c;
+}
+
+// Walks the tiles of a share; one warp.
+struct Walker {
+  Seq s;
+  int b, top, head, t, tiles;
+  int64_t x0, left, tile_at;  // units of the tile before the share, units to go, the tile's place on the line
+  Tile tile;
+
+  // The sequence from b on that has rows; false: none.
+  __device__ __forceinline__ bool seek(const ChunkAttnArgs& a) {
+    const int lane = threadIdx.x & 31;
+    for (; b < a.B; b += 32) {
+      Seq mine = {0, 0, 0};
+      if (b + lane < a.B) mine = read_seq(a, b + lane);
+      int before = mine.q0 + mine.n;  // the largest end so far, this sequence's not counted
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before = max(before, y);
+      }
+      const int through = __shfl_sync(0xffffffffu, before, 31);
+      before = __shfl_up_sync(0xffffffffu, before, 1);
+      before = lane == 0 ? top : max(before, top);
+      const unsigned ok = __ballot_sync(0xffffffffu, mine.n > 0 && mine.q0 >= before);
+      if (ok) {
+        const int from = __ffs(ok) - 1;
+        s.q0 = __shfl_sync(0xffffffffu, mine.q0, from);
+        s.n = __shfl_sync(0xffffffffu, mine.n, from);
+        s.len = __shfl_sync(0xffffffffu, mine.len, from);
+        top = s.q0 + s.n;
+        b += from;
+        return true;
+      }
+      top = max(top, through);
+    }
+    return false;
+  }
+
+  // To the share's first tile.
+  __device__ __forceinline__ bool begin(const ChunkAttnArgs& a, const Start& st, int group) {
+    left = min(st.per, st.total - blockIdx.x * st.per);
+    if (left <= 0) return false;
+    b = st.b;
+    top = st.top;
+    if (!seek(a)) return false;
+    tiles = tiles_of(s, group);
+    const int lane = threadIdx.x & 31;
+    Seq one = {0, 0, 0};
+    if (lane == 0) one = s;
+    const int64_t per_head = __shfl_sync(0xffffffffu, head_cost(one, group, a.window), 0);
+    head = static_cast<int>(st.offset / per_head);
+    x0 = st.offset - head * per_head;
+    for (t = 0; t < tiles; t += 32) {  // the tile that x0 lies in
+      const int64_t c = t + lane < tiles ? tile_of(s, group, a.window, t + lane).cost() : 0;
+      int64_t x = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, x > x0);
+      if (in) {
+        const int from = __ffs(in) - 1;
+        x0 -= __shfl_sync(0xffffffffu, x - c, from);
+        t += from;
+        break;
+      }
+      x0 -= __shfl_sync(0xffffffffu, x, 31);
+    }
+    tile = tile_of(s, group, a.window, t);
+    tile_at = blockIdx.x * st.per - x0;
+    return true;
+  }
+
+  // To the next tile, whose units before the share are none.
+  __device__ __forceinline__ bool next(const ChunkAttnArgs& a, int group) {
+    tile_at += tile.cost();
+    x0 = 0;
+    if (++t == tiles) {
+      t = 0;
+      if (++head == a.cache.n_kv_heads) {
+        head = 0;
+        ++b;
+        if (!seek(a)) return false;
+        tiles = tiles_of(s, group);
+      }
+    }
+    tile = tile_of(s, group, a.window, t);
+    return true;
+  }
+};
+
+// The block, counted from the tile's first, at or behind place x of a tile.
+__device__ __forceinline__ int block_at(const Tile& t, int64_t x) {
+  const int64_t y = x - kCostTile, u = t.unit();
+  return y <= 0 ? 0 : static_cast<int>((y + u - 1) / u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const ChunkAttnArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t order_full[2], order_empty[2], q_full, q_empty;
+  __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages], raw_full[C::kRawStages], raw_empty[C::kRawStages];
+  __shared__ uint64_t v_full[C::kVStages], v_empty[C::kVStages], meta_full[C::kMeta];
+  __shared__ uint64_t s_full[2], p_full[2], o_full[2], joined, left_off, drain;
+  __shared__ Order orders[2];
+  __shared__ __align__(16) float k_scale_s[C::kMeta][kGroups], v_log_s[C::kMeta][kGroups];
+  __shared__ float v_min_s[C::kMeta];          // the least of the block's value scales, in log2
+  __shared__ uint32_t bad_s[C::kMeta];         // groups whose page is outside the pool
+  __shared__ float q_scale_s[2][kTile];
+  __shared__ float m_s[2][kTile], mv_s[2][kTile], l_s[2][kTile];
+  // keys of masked blocks whose values had NaN codes, as each converting warp
+  // found them, of three tiles (who converts for tile n + 2 knows that every warp
+  // has begun tile n): those of tile number n are valid if odd_item[n % 3] is n + 1
+  __shared__ uint32_t odd_rows[3][4][kMaxMasked][4];
+  __shared__ int odd_block[3][4][kMaxMasked], odd_item[3][4];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_s;
+  __shared__ int64_t sum_sh[kThreads / 32];
+  __shared__ int max_sh[kThreads / 32];
+  __shared__ Start start_s;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* q_s = smem;
+  uint8_t* k_ring = q_s + 2 * C::kQBytes;
+  uint8_t* v_ring = k_ring + C::kKStages * C::kCodeBytes;
+  uint8_t* raw_ring = v_ring + C::kVStages * C::kVBytes;
+  uint8_t* out_s = raw_ring + C::kRawStages * C::kCodeBytes;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.n_heads / a.cache.n_kv_heads;
+  volatile int* abort_flag = &abort_s;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(order_full + i, 1);
+      mbar_init(order_empty + i, kWarpsUsed - 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, kTile);
+      mbar_init(o_full + i, 1);
+    }
+    mbar_init(&q_full, kConvThreads);
+    mbar_init(&q_empty, kTileRows + 1);
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < C::kRawStages; ++i) {
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, kConvThreads);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(v_full + i, kConvThreads);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < C::kMeta; ++i) mbar_init(meta_full + i, 1);
+    mbar_init(&joined, kTileRows);
+    mbar_init(&left_off, kTileRows);
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+    abort_s = 0;
+    start_s.b = -1;
+    for (int i = 0; i < 12; ++i) odd_item[i >> 2][i & 3] = 0;
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  // Tensor memory is taken after the kernel before has ended and before the
+  // one after may start: no CTA of either can then hold what this one, or
+  // what it waits for, still needs.
+  pdl_wait();
+  if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
+
+  // ---------------- the CTA's share ----------------
+  // prefix sums of the sequences' costs; more than a block of sequences takes a
+  // pass for the total first
+  {
+    int64_t per = 1, total = 0;
+    for (int pass = a.B > kThreads ? 0 : 1; pass < 2; ++pass) {
+      int64_t base = 0;
+      int top = 0;  // rows of q that sequences so far reach
+      for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        Seq s = {0, 0, 0};
+        if (b < a.B) s = read_seq(a, b);
+        int end = s.q0 + s.n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, end, off);
+          if (lane >= off) end = max(end, y);
+        }
+        if (lane == 31) max_sh[warp] = end;
+        __syncthreads();
+        int before_top = __shfl_up_sync(0xffffffffu, end, 1), through = top;
+        before_top = lane == 0 ? top : max(before_top, top);
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) {
+          const int y = max_sh[k];
+          if (k < warp) before_top = max(before_top, y);
+          through = max(through, y);
+        }
+        top = through;
+        if (s.q0 < before_top) s.n = 0;  // offsets that fall: rows that an earlier sequence has
+        const int64_t n = head_cost(s, group, a.window) * a.cache.n_kv_heads;
+        int64_t x = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+          if (lane >= off) x += y;
+        }
+        if (lane == 31) sum_sh[warp] = x;
+        __syncthreads();
+        int64_t before = base + x - n;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) {
+          const int64_t y = sum_sh[k];
+          if (k < warp) before += y;
+          base += y;
+        }
+        if (a.B <= kThreads) total = base;
+        if (pass == 1) {
+          // (a share holds a block at least, so that no CTA between a tile's first and last has none)
+          per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kCostTwo));
+          const int64_t target = blockIdx.x * per;
+          if (target >= before && target < before + n) {  // one thread at most
+            start_s.b = b;
+            start_s.offset = target - before;
+            start_s.top = before_top;
+          }
+        }
+        __syncthreads();
+      }
+      total = base;
+    }
+    if (tid == 0) {
+      start_s.per = per;
+      start_s.total = total;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = tmem_slot;
+
+  // the next tile, of every warp but the loading one; false at the end and after an abort
+  auto take = [&](int item, Order* o) {
+    const bool ok = wait_or_abort(order_full + (item & 1), (item >> 1) & 1, abort_flag, a.status);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    *o = orders[item & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(order_empty + (item & 1));
+    return o->there != 0;
+  };
+
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      // ---------------- loads ----------------
+      Walker w;
+      const Start st = start_s;
+      bool there = st.b >= 0 && w.begin(a, st, group), ok = true;
+      int n_k = 0;  // blocks so far
+      Cut cut = {};
+      for (int item = 0; ok; ++item) {
+        Order o = {};
+        while (there) {
+          const int64_t x1 = min(w.tile.cost(), w.x0 + w.left);
+          const int k0 = block_at(w.tile, w.x0), k1 = block_at(w.tile, x1);
+          const bool done = x1 - w.x0 == w.left;
+          if (k1 > k0) {
+            const Tile& t = w.tile;
+            o.there = 1;
+            o.b = w.b;
+            o.q0 = w.s.q0;
+            o.row0 = w.t * kTileRows;
+            o.rows = t.rows;
+            o.kv_head = w.head;
+            o.head0 = w.head * group;
+            o.shift = w.s.len - w.s.n;
+            o.lo = t.lo;
+            o.hi = t.hi;
+            const int first = o.shift + static_cast<int>(static_cast<uint32_t>(o.row0) / group);
+            const int last = o.shift + static_cast<int>(static_cast<uint32_t>(o.row0 + o.rows - 1) / group);
+            o.from = first < 0 ? 0 : (first + 1) >> kTileShift;
+            o.upto = a.window > 0 && last >= a.window ? (last - a.window) >> kTileShift : -1;
+            o.j_top = t.j_hi - 1 - k0;
+            o.blocks = k1 - k0;
+            o.split = t.rows <= kTile;
+            o.record = k0 == 0 && k1 == t.blocks ? -1 : k0 == 0 ? 1 : 0;
+            if (o.record == 1) {
+              cut.q0 = o.q0;
+              cut.row0 = o.row0;
+              cut.head0 = o.head0;
+              cut.rows = o.rows;
+              cut.first = blockIdx.x;
+              cut.last = static_cast<int>(
+                  (w.tile_at + kCostTile + static_cast<int64_t>(t.unit()) * (t.blocks - 1)) / st.per);
+            }
+          }
+          w.left -= x1 - w.x0;
+          there = !done && w.next(a, group);
+          if (o.there) break;
+        }
+        if (lane == 0) {
+          if (item >= 2) ok = wait_or_abort(order_empty + (item & 1), ((item >> 1) - 1) & 1, abort_flag, a.status);
+          if (ok) {
+            orders[item & 1] = o;
+            mbar_arrive(order_full + (item & 1));
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok || !o.there) break;
+        // a lane looks after a group of 16 keys of one of four blocks
+        const int32_t* row = a.cache.table + static_cast<int64_t>(o.b) * a.cache.table_stride;
+        const int ps = a.cache.page_shift, g = lane & 7;
+        auto token_of = [&](int q) { return (o.j_top - q) * kTile + 16 * g; };
+        constexpr int32_t kNotNeeded = INT32_MIN;
+        auto entry = [&](int q0) -> int32_t {
+          const int q = q0 + (lane >> 3), t = token_of(q), p0 = (t >> ps) << ps;
+          if (q >= o.blocks || p0 >= o.hi || p0 + a.cache.page <= o.lo) return kNotNeeded;
+          return max(__ldg(row + (t >> ps)), -1);
+        };
+        int32_t next = entry(0);
+        for (int q0 = 0; q0 < o.blocks && ok; q0 += 4) {
+          const int32_t page = next;
+          const bool in = page >= 0 && page < a.cache.n_pages;
+          const bool bad = page != kNotNeeded && !in;
+          if (bad) record_error(a.status, kErrIndexRange);
+          float ks = 1.f, vs = 0.f;
+          if (in) {
+            const int64_t at = static_cast<int64_t>(page) * a.cache.n_kv_heads + o.kv_head;
+            ks = __ldg(a.cache.k_scale + at);
+            vs = __ldg(a.cache.v_scale + at);
+          }
+          next = entry(q0 + 4);
+          const unsigned bads = __ballot_sync(0xffffffffu, bad);
+          const int n_q = min(4, o.blocks - q0);
+          for (int i = 0; i < n_q && ok; ++i, ++n_k) {
+            const bool mine = (lane >> 3) == i;
+            const bool copies = mine && in && ((16 * g) & (a.cache.page - 1)) == 0;
+            const unsigned bytes = __popc(__ballot_sync(0xffffffffu, copies)) * a.cache.page * D;
+            const int ks_slot = n_k % C::kKStages, vs_slot = n_k % C::kRawStages, meta = n_k % C::kMeta;
+            if (n_k >= C::kKStages)
+              ok = wait_or_abort(k_empty + ks_slot, (n_k / C::kKStages - 1) & 1, abort_flag, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            float lv = in ? __log2f(vs) : 1e30f, least = lv;
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
+            if (mine) {
+              k_scale_s[meta][g] = ks;
+              v_log_s[meta][g] = lv;
+              if (g == 0) {
+                v_min_s[meta] = least;
+                bad_s[meta] = (bads >> (8 * i)) & 0xFFu;
+              }
+            }
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(meta_full + meta);
+              mbar_arrive_expect_tx(k_full + ks_slot, bytes);
+            }
+            __syncwarp();
+            if (copies)
+              tma_load_3d(k_ring + ks_slot * C::kCodeBytes + 16 * g * D, &tm_k, 0, o.kv_head << ps, page,
+                          k_full + ks_slot);
+            if (n_k >= C::kRawStages)
+              ok = wait_or_abort(raw_empty + vs_slot, (n_k / C::kRawStages - 1) & 1, abort_flag, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {  // (this block's keys are on their way)
+              if (lane == 0) mbar_wait(k_full + ks_slot, (n_k / C::kKStages) & 1, a.status);
+              __syncwarp();
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(raw_full + vs_slot, bytes);
+            __syncwarp();
+            if (copies)
+              tma_load_3d(raw_ring + vs_slot * C::kCodeBytes + 16 * g * D, &tm_v, 0, o.kv_head << ps, page,
+                          raw_full + vs_slot);
+          }
+        }
+      }
+      if (lane == 0) {
+        reinterpret_cast<Cut*>(a.part)[blockIdx.x] = cut;
+        // every copy lands before the CTA ends (also after an abort)
+        for (int k = max(0, n_k - C::kKStages); k < n_k; ++k)
+          mbar_wait(k_full + k % C::kKStages, (k / C::kKStages) & 1, a.status);
+        for (int k = max(0, n_k - C::kRawStages); k < n_k; ++k)
+          mbar_wait(raw_full + k % C::kRawStages, (k / C::kRawStages) & 1, a.status);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---------------- products ----------------
+      // (the whole warp walks the loop and one elected lane issues, so that the
+      // loop's values are uniform)
+      constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 0, 0, 0, 0);  // E4M3, K-major A and B
+      constexpr uint32_t idesc_o = instr_desc(kTile, D, 0, 0, 0, 1);     // f16, A from TMEM, B (= V) MN-major
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.status)) != 0;
+      };
+      auto wait_k = [&](int n) { return wait(k_full + n % C::kKStages, (n / C::kKStages) & 1); };
+      auto wait_v = [&](int n) { return wait(v_full + n % C::kVStages, (n / C::kVStages) & 1); };
+      // S of half t with the queries of slot qs and block n (one lane)
+      auto s_of = [&](int t, int qs, int n) {
+        const uint64_t k_desc = D == 128
+                                    ? smem_desc(smem_u32(k_ring) + (n % C::kKStages) * C::kCodeBytes, 16, 1024, kSwizzle128B)
+                                    : smem_desc(smem_u32(k_ring) + (n % C::kKStages) * C::kCodeBytes, 16, 512, kSwizzle64B);
+        const uint64_t q_desc = smem_desc(smem_u32(q_s) + qs * C::kQBytes, 16, 1024, kSwizzle128B);
+        // the high parts' products, then the low ones': at width 64 both parts
+        // are in one 128-byte line
+        constexpr int kLow = D == 128 ? kTile * 128 >> 4 : 64 >> 4;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int s = 0; s < D / 32; ++s)
+            mma_f8(tm + C::kSCol(t), q_desc + part * kLow + 2 * s, k_desc + 2 * s, idesc_s, part + s > 0 ? 1u : 0u);
+        if (!skip_s) tc_commit(s_full + t);
+      };
+      auto pv_of = [&](int t, int n, bool add) {
+        const uint64_t v_desc =
+            smem_desc(smem_u32(v_ring) + (n % C::kVStages) * C::kVBytes, kTile * 128, 1024, kSwizzle128B);
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (16 * s * 128 >> 4), idesc_o,
+                     add || s > 0 ? 1u : 0u);
+      };
+      bool ok = true;
+      int n0 = 0;               // blocks of the tiles before
+      uint32_t n_p[2] = {};     // weights taken so far, by half
+      Order o;
+      for (int item = 0; ok && take(item, &o); ++item) {
+        const int blocks = uniform(o.blocks);
+        const bool split = uniform(o.split) != 0;
+        ok = wait(&q_full, item & 1);
+        if (split) {
+          for (int t = 0; t < 2 && t < blocks && ok; ++t) {
+            ok = wait_k(n0 + t);
+            tc_fence_after();
+            if (ok && elect_one()) {
+              s_of(t, 0, n0 + t);
+              tc_commit(k_empty + (n0 + t) % C::kKStages);
+              if (t + 1 == blocks || t == 1)
+                if (blocks <= 2) tc_commit(&q_empty);
+            }
+            __syncwarp();
+          }
+          for (int it = 0; it < blocks && ok; ++it) {
+            const int t = it & 1;
+            const bool again = it + 2 < blocks;
+            ok = wait_v(n0 + it);
+            if (ok) ok = wait(p_full + t, n_p[t] & 1u);
+            if (ok && again) ok = wait_k(n0 + it + 2);
+            if (!ok) break;
+            ++n_p[t];
+            tc_fence_after();
+            if (elect_one()) {
+              pv_of(t, n0 + it, it >= 2);
+              if (!again) tc_commit(o_full + t);
+              tc_commit(v_empty + (n0 + it) % C::kVStages);
+              if (again) {
+                s_of(t, 0, n0 + it + 2);
+                tc_commit(k_empty + (n0 + it + 2) % C::kKStages);
+                if (it + 3 == blocks) tc_commit(&q_empty);
+              }
+            }
+            __syncwarp();
+          }
+        } else {
+          if (ok) ok = wait_k(n0);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            s_of(0, 0, n0);
+            s_of(1, 1, n0);
+            tc_commit(k_empty + n0 % C::kKStages);
+            if (blocks == 1) tc_commit(&q_empty);
+          }
+          __syncwarp();
+          for (int it = 0; it < blocks && ok; ++it) {
+            const bool again = it + 1 < blocks;
+            ok = wait_v(n0 + it);
+            if (ok && again) ok = wait_k(n0 + it + 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (ok) ok = wait(p_full + t, n_p[t] & 1u);
+              if (!ok) break;
+              ++n_p[t];
+              tc_fence_after();
+              if (elect_one()) {
+                pv_of(t, n0 + it, it > 0);
+                if (!again) tc_commit(o_full + t);
+                if (t == 1) tc_commit(v_empty + (n0 + it) % C::kVStages);
+                if (again) {
+                  s_of(t, t, n0 + it + 1);
+                  if (t == 1) {
+                    tc_commit(k_empty + (n0 + it + 1) % C::kKStages);
+                    if (it + 2 == blocks) tc_commit(&q_empty);
+                  }
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+        n0 += blocks;
+      }
+      // whatever was issued finishes before TMEM and shared memory are released
+      if (elect_one()) {
+        tc_commit(&drain);
+        mbar_wait(&drain, 0, a.status);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kConvWarp) {
+    // ---------------- queries into two parts, values into f16 ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    constexpr int kChunks = D / 16;               // 16-channel chunks a row
+    constexpr int kRowsAtOnce = kConvThreads / kChunks;
+    const int ct = tid - kConvWarp * 32, cw = warp - kConvWarp;
+    const int r0 = ct / kChunks, c = ct % kChunks;
+    const float scale2 = a.sm_scale * kLog2e;
+    int n0 = 0;
+    bool ok = true;
+    Order o;
+    for (int item = 0; ok && take(item, &o); ++item) {
+      if (item > 0) ok = __all_sync(0xffffffffu, wait_or_abort(&q_empty, (item - 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      for (int h = 0; h < (o.split ? 1 : 2); ++h) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < kChunks; k0 += 2) {
+          uint4 u[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = r0 + (k0 + i) * kRowsAtOnce, rr = h * kTile + r;
+            u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < o.rows) {
+              const uint32_t at = static_cast<uint32_t>(o.row0 + rr);
+              const int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  a.q + static_cast<int64_t>(o.q0 + qi) * a.q_stride + (o.head0 + hd) * a.q_stride_h + c * 16);
+              u[i][0] = __ldg(src);
+              u[i][1] = __ldg(src + 1);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = r0 + (k0 + i) * kRowsAtOnce;
+            float x[16];
+            {
+              float y[8];
+              unpack_bf16(u[i][0], y);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = y[j];
+              unpack_bf16(u[i][1], y);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[8 + j] = y[j];
+            }
+            // the largest magnitude; a value that is not finite shows as one past all others
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]) <= FLT_MAX ? fabsf(x[j]) : INFINITY);
+#pragma unroll
+            for (int off = 1; off < kChunks; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const bool finite = top <= FLT_MAX;
+            const int e = min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 126);
+            const float up = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.f;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float y[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) y[q] = x[4 * j + q] * up;
+              hi[j] = to_e4m3x4(y[0], y[1], y[2], y[3]);
+              uint32_t h01, h23;
+              e4m3x4_to_f16(hi[j], h01, h23);
+              const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+              const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+              lo[j] = to_e4m3x4(y[0] - f01.x, y[1] - f01.y, y[2] - f23.x, y[3] - f23.y);
+              if (!finite) {
+                hi[j] = 0x7F7F7F7Fu;
+                lo[j] = 0u;
+              }
+            }
+            uint8_t* line = q_s + h * C::kQBytes + r * 128;
+            *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            uint8_t* low = D == 128 ? line + kTile * 128 + ((c ^ (r & 7)) << 4) : line + (((c + 4) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (c == 0) q_scale_s[h][r] = finite ? scale2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full);
+      const int odd = item % 3;
+      int n_masked = 0;
+      odd_rows[odd][cw][lane >> 2][lane & 3] = 0u;  // (the tile three before, whose places these were, is done with)
+      static_assert(kMaxMasked * 4 == 32, "a word a lane");
+      __syncwarp();
+      for (int q = 0; q < o.blocks && ok; ++q) {
+        const int n = n0 + q, j = o.j_top - q;
+        const int raw_slot = n % C::kRawStages, v_slot = n % C::kVStages, meta = n % C::kMeta;
+        ok = wait_or_abort(meta_full + meta, (n / C::kMeta) & 1, abort_flag, a.status) &&
+             wait_or_abort(raw_full + raw_slot, (n / C::kRawStages) & 1, abort_flag, a.status);
+        if (ok && n >= C::kVStages)
+          ok = wait_or_abort(v_empty + v_slot, (n / C::kVStages - 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* raw = raw_ring + raw_slot * C::kCodeBytes;
+        uint8_t* to = v_ring + v_slot * C::kVBytes + (D == 128 ? (c >> 2) * (kTile * 128) : 0);
+        const uint32_t bad = bad_s[meta];
+        const bool masked = o.masked(j);
+        const int first = o.lo - j * kTile, past = o.hi - j * kTile;  // the block's keys that the tile sees
+#pragma unroll 1
+        for (int k0 = 0; k0 < kChunks; k0 += 4) {
+          uint4 u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0 + (k0 + i) * kRowsAtOnce;
+            u[i] = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
+          }
+          if (masked || bad) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + (k0 + i) * kRowsAtOnce;
+              if (r < first || r >= past || ((bad >> (r >> 4)) & 1u)) {
+                u[i] = make_uint4(0u, 0u, 0u, 0u);
+              } else if (masked) {
+                const uint32_t x = nan_codes(u[i].x), y = nan_codes(u[i].y), z = nan_codes(u[i].z), w = nan_codes(u[i].w);
+                if (x | y | z | w) {  // (0x80 of a NaN byte becomes all ones)
+                  u[i].x &= ~((x >> 7) * 255u);
+                  u[i].y &= ~((y >> 7) * 255u);
+                  u[i].z &= ~((z >> 7) * 255u);
+                  u[i].w &= ~((w >> 7) * 255u);
+                  if (n_masked < kMaxMasked) {
+                    atomicOr(&odd_rows[odd][cw][n_masked][r >> 5], 1u << (r & 31));
+                    odd_block[odd][cw][n_masked] = j;
+                    odd_item[odd][cw] = item + 1;
+                  }
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0 + (k0 + i) * kRowsAtOnce;
+            uint4 x, y;
+            e4m3x4_to_f16(u[i].x, x.x, x.y);
+            e4m3x4_to_f16(u[i].y, x.z, x.w);
+            e4m3x4_to_f16(u[i].z, y.x, y.y);
+            e4m3x4_to_f16(u[i].w, y.z, y.w);
+            // (chunks of the upper 64 channels store their second half first: the
+            // eight lanes of a row then write to eight different places of a line)
+            const int q0 = 2 * (c & 3), q1 = D == 128 ? c >> 2 : 0;
+            uint8_t* line = to + r * 128;
+            *reinterpret_cast<uint4*>(line + (((q0 + q1) ^ (r & 7)) << 4)) = q1 ? y : x;
+            *reinterpret_cast<uint4*>(line + (((q0 + 1 - q1) ^ (r & 7)) << 4)) = q1 ? x : y;
+          }
+        }
+        if (masked) ++n_masked;
+        fence_proxy_async_smem();
+        mbar_arrive(v_full + v_slot);
+        mbar_arrive(raw_empty + raw_slot);
+      }
+      n0 += o.blocks;
+    }
+  } else {
+    // ---------------- softmax: one thread a row ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int t = warp >> 2;                   // the half
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_base + C::kSCol(t), o_tmem = tmem + lane_base + C::kOCol(t);
+    uint32_t n_s = 0, n_o[2] = {}, n_split = 0;  // scores and sums taken so far, tiles whose halves were joined
+    int n0 = 0;
+    bool ok = true;
+    Order o;
+    for (int item = 0; ok && take(item, &o); ++item) {
+      ok = __all_sync(0xffffffffu, wait_or_abort(&q_full, item & 1, abort_flag, a.status));
+      if (!ok) break;
+      const bool split = o.split != 0;
+      const int half = split ? 0 : t;                    // of the queries
+      const int row = half * kTile + r;                  // in the tile
+      const float fac = q_scale_s[half][r];
+      mbar_arrive(&q_empty);
+      const uint32_t at = static_cast<uint32_t>(o.row0 + row);
+      const int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
+      // the row's keys [first_key, last_key]
+      const int last_key = row < o.rows ? qi + o.shift : -1;
+      const int first_key = a.window > 0 && last_key >= a.window ? last_key - a.window + 1 : 0;
+      float m = kNone, mv = kNone, l = 0.f;
+      const int step = split ? 2 : 1;
+      bool began = false;
+      for (int q = split ? t : 0; q < o.blocks; q += step) {
+        const int n = n0 + q, j = o.j_top - q, meta = n % C::kMeta;
+        ok = wait_or_abort(meta_full + meta, (n / C::kMeta) & 1, abort_flag, a.status) &&
+             wait_or_abort(s_full + t, n_s & 1u, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++n_s;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
+        float cf[kGroups];
+        {
+          const float4 x = *reinterpret_cast<const float4*>(&k_scale_s[meta][0]);
+          const float4 y = *reinterpret_cast<const float4*>(&k_scale_s[meta][4]);
+          const float ks[kGroups] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          // (not 0: a masked score is -inf, and stays so under the factor)
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) cf[g] = fmaxf(fac * ks[g], FLT_MIN);
+        }
+        const uint32_t bad = bad_s[meta];
+        tmem_wait_ld();
+        if (o.masked(j) || bad) {  // this row's keys among the block's, as a bit each
+          const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int hi = max(0, min(32, c_hi - 32 * c)), lo = max(0, min(32, c_lo - 32 * c));
+            uint32_t seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
+            if (bad & (1u << (2 * c))) seen &= 0xFFFF0000u;
+            if (bad & (2u << (2 * c))) seen &= 0x0000FFFFu;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
+          }
+        }
+        float lv[kGroups];
+        {
+          const float4 x = *reinterpret_cast<const float4*>(&v_log_s[meta][0]);
+          const float4 y = *reinterpret_cast<const float4*>(&v_log_s[meta][4]);
+          const float v[kGroups] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) lv[g] = v[g];
+        }
+        float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const int c = g >> 1, k0 = (g & 1) * 16;
+          float x = fmaxf(__uint_as_float(s[c][k0]), __uint_as_float(s[c][k0 + 1]));
+#pragma unroll
+          for (int k = 2; k < 16; k += 2) x = max3(x, __uint_as_float(s[c][k0 + k]), __uint_as_float(s[c][k0 + k + 1]));
+          x *= cf[g];
+          top = fmaxf(top, x);
+          topv = fmaxf(topv, x + lv[g]);
+        }
+        // (a row whose own maximum has not grown keeps its reference, so that no bit
+        // of it depends on what only the warp's other rows see)
+        const bool grown = top - m > kLag || topv - mv > kLag;
+        if (__any_sync(0xffffffffu, grown)) {
+          const float m1 = grown ? fmaxf(m, top) : m, mv1 = grown ? fmaxf(mv, topv) : mv;
+          l *= ex2(m - m1);
+          const float f = ex2(mv - mv1);
+          m = m1;
+          mv = mv1;
+          if (began) {  // (the half's products before have finished: these scores were issued after them)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32(o_tmem + 32 * c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+              tmem_st32(o_tmem + 32 * c, x);
+            }
+          }
+        }
+        began = true;
+        // exponents in one rounding, factor s - m; where logits are so large that the
+        // rounding of m shows, the products first
+        float minus_m = -m, up = kWeightExp - mv;
+        const float down = mv - kWeightExp - m;
+        const bool large = fmaxf(fabsf(m), fabsf(mv)) > kLarge && m > kNone;
+        if (__any_sync(0xffffffffu, large)) {
+          if (large) {
+            minus_m = 0.f;
+            up = kWeightExp + (m - mv);
+          }
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const float x = large ? cf[g] : 1.f, y = large ? m : 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              uint32_t& w = s[g >> 1][(g & 1) * 16 + k];
+              w = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(w), x), y));
+            }
+            if (large) cf[g] = 1.f;
+          }
+        }
+        const bool far = v_min_s[meta] - down < kFar;
+        if (__any_sync(0xffffffffu, far)) {
+          float sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum += ex2(fmaf(__uint_as_float(s[g >> 1][(g & 1) * 16 + k]), cf[g], minus_m));
+          if (far) l += sum;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int g = 2 * c + h;
+            const uint64_t cf2 = pair_of(cf[g], cf[g]), up2 = pair_of(lv[g] + up, lv[g] + up);
+            uint64_t sum = 0ull;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float x, y;
+              csa::split(fma2(pair_of(s[c][16 * h + 2 * k], s[c][16 * h + 2 * k + 1]), cf2, up2), &x, &y);
+              x = ex2(x);
+              y = ex2(y);
+              sum = add2(sum, pair_of(x, y));
+              p[8 * h + k] = pack_f16(x, y);
+            }
+            float sx, sy;
+            csa::split(sum, &sx, &sy);
+            if (!far) l = fmaf(sx + sy, ex2(down - lv[g]), l);
+          }
+          tmem_st16(s_tmem + 16 * c, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full + t);
+      }
+      if (!ok) break;
+      n0 += o.blocks;
+      // ---------------- the tile's rows, or this share's part of them ----------------
+      const bool have[2] = {true, !split || o.blocks > 1};
+      if (split) {
+        m_s[t][r] = m;
+        mv_s[t][r] = mv;
+        l_s[t][r] = l;
+        mbar_arrive(&joined);
+        ok = wait_or_abort(&joined, n_split & 1u, abort_flag, a.status) &&
+             wait_or_abort(o_full + 0, n_o[0] & 1u, abort_flag, a.status);
+        if (ok && have[1]) ok = wait_or_abort(o_full + 1, n_o[1] & 1u, abort_flag, a.status);
+      } else {
+        ok = wait_or_abort(o_full + t, n_o[t] & 1u, abort_flag, a.status);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ++n_o[0];
+      if (have[1]) ++n_o[1];
+      tc_fence_after();
+      float f0 = 1.f, f1 = 0.f;  // of the halves' sums
+      if (split) {
+        const float ma = m_s[0][r], mb = m_s[1][r], va = mv_s[0][r], vb = mv_s[1][r];
+        m = fmaxf(ma, mb);
+        mv = fmaxf(va, vb);
+        l = l_s[0][r] * ex2(ma - m) + l_s[1][r] * ex2(mb - m);
+        f0 = ex2(va - mv);
+        f1 = ex2(vb - mv);
+      }
+      const float unit = mv - kWeightExp;
+      const int64_t out_row = static_cast<int64_t>(o.q0 + qi) * a.n_heads + o.head0 + hd;
+      float* part = a.part + gridDim.x * (sizeof(Cut) / sizeof(float)) + (blockIdx.x * 2 + max(o.record, 0)) * C::kRecord;
+      float f = 1.f;
+      const bool writes = row < o.rows;
+      if (o.record < 0) {
+        float lse;
+        f = finish_row(m, unit, l, a.sink, o.head0 + hd, &lse);
+        if (a.lse && writes && (!split || t == 0)) a.lse[out_row] = lse;
+      } else if (!split || t == 0) {
+        *reinterpret_cast<float4*>(part + kTileRows * D + 4 * row) = make_float4(m, l, unit, 0.f);
+      }
+      f0 *= f;
+      f1 *= f;
+      const int odd = item % 3;
+      bool any_odd = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) any_odd |= *const_cast<volatile int*>(&odd_item[odd][k]) == item + 1;
+      uint8_t* stage = out_s + warp * 1024;
+      // the halves of a split tile take half of the channels each
+      const int c_lo = split ? t * (D / 32) : 0, c_hi = split ? (t + 1) * (D / 32) : D / 16;
+      const uint32_t oa = split ? tmem + lane_base + C::kOCol(0) : o_tmem, ob = tmem + lane_base + C::kOCol(1);
+#pragma unroll 1
+      for (int c = c_lo; c < c_hi; ++c) {
+        uint32_t x[16], y[16];
+        tmem_ld16(oa + 16 * c, x);
+        if (split && have[1]) tmem_ld16(ob + 16 * c, y);
+        tmem_wait_ld();
+        float z[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          z[k] = __uint_as_float(x[k]) * f0;
+          if (split && have[1]) z[k] = fmaf(__uint_as_float(y[k]), f1, z[k]);
+        }
+        if (any_odd && writes) {
+          for (int e = 0; e < 4 * kMaxMasked * kTile; ++e) {
+            const int cw = e / (kMaxMasked * kTile), i = (e / kTile) % kMaxMasked, k = e % kTile;
+            if (*const_cast<volatile int*>(&odd_item[odd][cw]) != item + 1) {
+              e += kMaxMasked * kTile - 1;
+              continue;
+            }
+            const uint32_t word = odd_rows[odd][cw][i][k >> 5];
+            if (word == 0u) {
+              e |= 31;
+              continue;
+            }
+            const int key = odd_block[odd][cw][i] * kTile + k;
+            if (!((word >> (k & 31)) & 1u) || key > last_key || key < first_key) continue;
+            const int64_t page = a.cache.table[o.b * a.cache.table_stride + (key >> a.cache.page_shift)];
+            const uint8_t* v = a.cache.v + (((page * a.cache.n_kv_heads + o.kv_head) << a.cache.page_shift) +
+                                            (key & (a.cache.page - 1))) * D + 16 * c;
+#pragma unroll
+            for (int d = 0; d < 16; ++d)
+              if ((v[d] & 0x7Fu) == 0x7Fu) z[d] = NAN;
+          }
+        }
+        if (o.record >= 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(part + ((4 * c + k) * kTileRows + row) * 4) =
+                make_float4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+          continue;
+        }
+        // the warp's 32 rows are staged, then stored with two lanes a row
+        uint8_t* line = stage + lane * 32;
+        const int sw = (lane >> 2) & 1;
+        *reinterpret_cast<uint4*>(line + (sw << 4)) =
+            make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+        *reinterpret_cast<uint4*>(line + ((sw ^ 1) << 4)) =
+            make_uint4(pack_bf16(z[8], z[9]), pack_bf16(z[10], z[11]), pack_bf16(z[12], z[13]), pack_bf16(z[14], z[15]));
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int rr = 16 * k + (lane >> 1), ch = lane & 1;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((ch ^ ((rr >> 2) & 1)) << 4));
+          const int64_t to = __shfl_sync(0xffffffffu, out_row, rr);
+          if (half * kTile + (warp & 3) * 32 + rr < o.rows)
+            *reinterpret_cast<uint4*>(a.out + to * D + 16 * c + 8 * ch) = v;
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      if (split) {  // the other half has read these sums, and its own, before either is written again
+        mbar_arrive(&left_off);
+        ok = __all_sync(0xffffffffu, wait_or_abort(&left_off, n_split & 1u, abort_flag, a.status));
+        ++n_split;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// Finishes the tiles that the shares' borders divide, from their records:
+// the first share's second one, the later shares' first.  CTA (x, y) takes 16
+// rows of the tile that begins in share x and goes on.
+constexpr int kMergeRows = 16;
+constexpr int kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkAttnArgs a, const int shares) {
+  using C = Cfg<D>;
+  extern __shared__ float fac_s[];  // [records][kMergeRows] m, l and unit, then the factor of each
+  __shared__ float f_s[kMergeRows];
+  __shared__ __align__(16) uint16_t out_s[kMergeRows][D + 8];
+  pdl_launch_dependents();
+  pdl_wait();
+  const Cut cut = reinterpret_cast<const Cut*>(a.part)[blockIdx.x];
+  const int row0 = blockIdx.y * kMergeRows;
+  if (row0 >= cut.rows) return;
+  const int rows = min(kMergeRows, cut.rows - row0), n = cut.last - cut.first + 1;
+  const int tid = threadIdx.x, r = tid % kMergeRows, k0 = tid / kMergeRows;
+  constexpr int kLanes = kMergeThreads / kMergeRows;
+  const float* records = a.part + shares * (sizeof(Cut) / sizeof(float));
+  auto record = [&](int k) { return records + (static_cast<int64_t>(cut.first + k) * 2 + (k == 0)) * C::kRecord; };
+  float* m_s = fac_s;
+  float* l_s = fac_s + n * kMergeRows;
+  float* u_s = fac_s + 2 * n * kMergeRows;
+  for (int k = k0; k < n; k += kLanes) {
+    const float4 x = *reinterpret_cast<const float4*>(record(k) + kTileRows * D + 4 * (row0 + r));
+    m_s[k * kMergeRows + r] = x.x;
+    l_s[k * kMergeRows + r] = x.y;
+    u_s[k * kMergeRows + r] = x.z;
+  }
+  __syncthreads();
+  const uint32_t at = static_cast<uint32_t>(cut.row0 + row0 + r), group = a.n_heads / a.cache.n_kv_heads;
+  float top = kNone, unit = kNone, l = 0.f;
+  for (int k = 0; k < n; ++k) {
+    top = fmaxf(top, m_s[k * kMergeRows + r]);
+    unit = fmaxf(unit, u_s[k * kMergeRows + r]);
+  }
+  for (int k = 0; k < n; ++k) l += l_s[k * kMergeRows + r] * ex2(m_s[k * kMergeRows + r] - top);
+  __syncthreads();
+  for (int k = k0; k < n; k += kLanes) u_s[k * kMergeRows + r] = ex2(u_s[k * kMergeRows + r] - unit);
+  if (k0 == 0 && r < rows) {
+    float lse;
+    f_s[r] = finish_row(top, unit, l, a.sink, cut.head0 + at % group, &lse);
+    if (a.lse) a.lse[static_cast<int64_t>(cut.q0 + at / group) * a.n_heads + cut.head0 + at % group] = lse;
+  }
+  __syncthreads();
+  if (r < rows) {
+    const float f = f_s[r];
+    for (int c = k0; c < D / 4; c += kLanes) {
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(record(k) + (c * kTileRows + row0 + r) * 4);
+        const float g = u_s[k * kMergeRows + r];
+        z.x = fmaf(x.x, g, z.x);
+        z.y = fmaf(x.y, g, z.y);
+        z.z = fmaf(x.z, g, z.z);
+        z.w = fmaf(x.w, g, z.w);
+      }
+      *reinterpret_cast<uint2*>(&out_s[r][4 * c]) = make_uint2(pack_bf16(z.x * f, z.y * f), pack_bf16(z.z * f, z.w * f));
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (D / 8); i += kMergeThreads) {
+    const int rr = i / (D / 8), ch = i % (D / 8);
+    const uint32_t x = static_cast<uint32_t>(cut.row0 + row0 + rr);
+    const int64_t to = static_cast<int64_t>(cut.q0 + x / group) * a.n_heads + cut.head0 + x % group;
+    *reinterpret_cast<uint4*>(a.out + to * D + 8 * ch) = *reinterpret_cast<const uint4*>(&out_s[rr][8 * ch]);
+  }
+}
+
+// The codes of a pool, [pages][kv heads * page size][channels], read a page of
+// one head at a time.
+bool encode_codes(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 encode, const PagedCache& c, uint8_t* base,
+                  CUtensorMapSwizzle swizzle) {
+  cuuint64_t size[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.n_kv_heads) * c.page,
+                        static_cast<cuuint64_t>(c.n_pages)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim), size[1] * c.head_dim};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(c.page), 1};
+  cuuint32_t ones[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, size, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_dim(const ChunkAttnArgs& a, int sms, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream) {
+  using C = Cfg<D>;
+  CUtensorMap tm_k, tm_v;
+  if (!encode ||
+      !encode_codes(&tm_k, encode, a.cache, a.cache.k, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !encode_codes(&tm_v, encode, a.cache, a.cache.v, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> done{0}, done_merge{0};
+  // (the split of registers assumes what the kernel is launched with)
+  cudaError_t e = kernel_limits(reinterpret_cast<const void*>(chunk_attn_kernel<D>), C::kSmem, kLaunchRegs, &done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(chunk_attn_kernel<D>, dim3(sms), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, a);
+  if (e != cudaSuccess || sms < 2) return e;
+  const int smem = sms * 3 * kMergeRows * static_cast<int>(sizeof(float));
+  e = kernel_limits(reinterpret_cast<const void*>(chunk_merge_kernel<D>), smem, 0, &done_merge);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_merge_kernel<D>, dim3(sms - 1, kTileRows / kMergeRows), dim3(kMergeThreads), smem, stream, a,
+                    sms);
+}
+
+}  // namespace
+
+size_t chunk_attn_bytes(int head_dim, int sms) {
+  const int64_t record = head_dim == 64 ? Cfg<64>::kRecord : Cfg<128>::kRecord;
+  return static_cast<size_t>(sms) * (sizeof(Cut) + 2 * record * sizeof(float));
+}
+
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, int sms, PFN_cuTensorMapEncodeTiled_v12000 encode,
+                              cudaStream_t stream) {
+  if (a.B <= 0 || a.n_q <= 0) return cudaSuccess;
+  return a.cache.head_dim == 128 ? launch_dim<128>(a, sms, encode, stream) : launch_dim<64>(a, sms, encode, stream);
+}
+
+}  // namespace csa

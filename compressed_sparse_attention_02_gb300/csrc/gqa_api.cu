@@ -1,6 +1,7 @@
 // C ABI of the grouped-query layer's calls (declared in include/csa.h):
-// rotary positions, the paged 8-bit cache's append and single-token attention,
-// and packed prompt attention.  Host-side argument checks and launches.
+// rotary positions, the paged 8-bit cache's append, single-token and chunk
+// attention, packed prompt attention, and the cache's pages.  Host-side argument
+// checks and launches.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -87,6 +88,36 @@ csa::PagedCache cache_args(const csa_paged_cache* c) {
   a.v_scale = c->v_scale;
   a.table = c->table;
   a.table_stride = c->table_stride;
+  return a;
+}
+
+// The pages' shape (for the workspace) and, for the calls, their arrays.
+csa_status check_book(const csa_page_book* k, bool pointers) {
+  if (!k) return CSA_ERR_INVALID_ARG;
+  if (k->page_size != 16 && k->page_size != 32 && k->page_size != 64 && k->page_size != 128)
+    return CSA_ERR_UNSUPPORTED;
+  if (k->n_seqs < 0 || k->n_seqs > kMaxSeqs || k->n_pages < 1 || k->n_pages > 0x7fffffff) return CSA_ERR_INVALID_ARG;
+  if (!pointers) return CSA_OK;
+  if (k->table_stride < 1 || k->table_stride > kMaxRows / k->page_size) return CSA_ERR_INVALID_ARG;
+  if (!words_ok(k->refs) || (k->n_seqs > 0 && (!words_ok(k->table) || !words_ok(k->lens)))) return CSA_ERR_INVALID_ARG;
+  return CSA_OK;
+}
+
+csa_status check_work(const csa_page_book* k, const void* workspace, size_t bytes) {
+  return workspace && aligned(workspace, 16) && bytes >= csa::pages_bytes(k->n_seqs, k->n_pages) ? CSA_OK
+                                                                                                 : CSA_ERR_WORKSPACE;
+}
+
+csa::PageBook book_args(const csa_page_book* k) {
+  csa::PageBook a;
+  a.n_seqs = k->n_seqs;
+  a.page = k->page_size;
+  a.page_shift = __builtin_ctz(static_cast<unsigned>(k->page_size));
+  a.n_pages = k->n_pages;
+  a.table = k->table;
+  a.table_stride = k->table_stride;
+  a.lens = k->lens;
+  a.refs = k->refs;
   return a;
 }
 
@@ -327,6 +358,113 @@ csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32
   a.out = out;
   a.lse = lse;
   return cuda_status(csa::launch_prompt_attn(a, csa::tensor_map_encoder(), static_cast<cudaStream_t>(stream)));
+}
+
+size_t csa_chunk_attn_workspace_size(const csa_paged_cache* c, int32_t n_heads) {
+  if (check_cache(c, false) != CSA_OK || !heads_ok(n_heads, c->n_kv_heads)) return 0;
+  const int sms = csa::current_sms();
+  return sms > 0 ? csa::chunk_attn_bytes(c->head_dim, sms) : 0;
+}
+
+csa_status csa_chunk_attn(const csa_paged_cache* c, int32_t B, int32_t n_heads, int64_t n_q, const int32_t* cu_q,
+                          const int32_t* lens, const uint16_t* q, int64_t q_stride, int64_t q_stride_h,
+                          float sm_scale, int32_t window, const float* sink, uint16_t* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  const csa_status s = check_cache(c, true);
+  if (s != CSA_OK) return s;
+  if (B < 0 || B > kMaxSeqs || !heads_ok(n_heads, c->n_kv_heads) || n_q < 0 || n_q > kMaxPromptRows || window < 0 ||
+      !isfinite(sm_scale) || !(sm_scale > 0.f))
+    return CSA_ERR_INVALID_ARG;
+  if (n_q * (n_heads / c->n_kv_heads) >= (int64_t(1) << 31)) return CSA_ERR_UNSUPPORTED;  // rows of a key head
+  if (B == 0 || n_q == 0) return CSA_OK;
+  if (!words_ok(cu_q) || !words_ok(lens) || !rows_ok(q) || !words_opt(sink) || !rows_ok(out) || !words_opt(lse) ||
+      !strides_ok(q_stride, q_stride_h, c->head_dim))
+    return CSA_ERR_INVALID_ARG;
+  csa::ChunkAttnArgs a = {};
+  a.status = csa::device_status();
+  const int sms = csa::current_sms();
+  if (!a.status || sms <= 0) return CSA_ERR_CUDA;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < csa::chunk_attn_bytes(c->head_dim, sms))
+    return CSA_ERR_WORKSPACE;
+  a.cache = cache_args(c);
+  a.B = B;
+  a.n_heads = n_heads;
+  a.n_q = n_q;
+  a.cu_q = cu_q;
+  a.lens = lens;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_stride_h = q_stride_h;
+  a.sm_scale = sm_scale;
+  a.window = window;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  return cuda_status(csa::launch_chunk_attn(a, sms, csa::tensor_map_encoder(), static_cast<cudaStream_t>(stream)));
+}
+
+size_t csa_pages_workspace_size(const csa_page_book* k) {
+  return check_book(k, false) == CSA_OK ? csa::pages_bytes(k->n_seqs, k->n_pages) : 0;
+}
+
+csa_status csa_pages_resize(const csa_page_book* k, const int32_t* target, int32_t* pos0, int32_t* src, int32_t* dst,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  csa_status s = check_book(k, true);
+  if (s != CSA_OK) return s;
+  if (k->n_seqs == 0) return CSA_OK;
+  if (!words_ok(target) || !words_opt(pos0) || !words_opt(src) || !words_opt(dst) || !src != !dst)
+    return CSA_ERR_INVALID_ARG;
+  if ((s = check_work(k, workspace, workspace_bytes)) != CSA_OK) return s;
+  unsigned* status = csa::device_status();
+  if (!status) return CSA_ERR_CUDA;
+  return cuda_status(csa::launch_pages_resize(book_args(k), target, pos0, src, dst, workspace, status,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_pages_fork(const csa_page_book* k, const int32_t* parent, int32_t* src, int32_t* dst, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  csa_status s = check_book(k, true);
+  if (s != CSA_OK) return s;
+  if (k->n_seqs == 0) return CSA_OK;
+  if (!words_ok(parent) || !words_ok(src) || !words_ok(dst)) return CSA_ERR_INVALID_ARG;
+  if ((s = check_work(k, workspace, workspace_bytes)) != CSA_OK) return s;
+  unsigned* status = csa::device_status();
+  if (!status) return CSA_ERR_CUDA;
+  return cuda_status(csa::launch_pages_fork(book_args(k), parent, src, dst, workspace, status,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_pages_compact(const csa_page_book* k, int32_t* src, int32_t* dst, int32_t* used, int32_t* table_out,
+                             int32_t* refs_out, void* workspace, size_t workspace_bytes, void* stream) {
+  csa_status s = check_book(k, true);
+  if (s != CSA_OK) return s;
+  if (!words_ok(used) || !words_ok(refs_out) || (k->n_seqs > 0 && !words_ok(table_out)) ||
+      (k->n_pages > 1 && (!words_ok(src) || !words_ok(dst))))
+    return CSA_ERR_INVALID_ARG;
+  if ((s = check_work(k, workspace, workspace_bytes)) != CSA_OK) return s;
+  unsigned* status = csa::device_status();
+  const int sms = csa::current_sms();
+  if (!status || sms <= 0) return CSA_ERR_CUDA;
+  return cuda_status(csa::launch_pages_compact(book_args(k), src, dst, used, table_out, refs_out, workspace, status,
+                                               sms, static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_pages_copy(const csa_paged_cache* c, int64_t n, const int32_t* src, const int32_t* dst, void* stream) {
+  if (!c) return CSA_ERR_INVALID_ARG;
+  csa_paged_cache pool = *c;  // (the table is not read)
+  pool.table = reinterpret_cast<const int32_t*>(16);
+  pool.table_stride = 1;
+  const csa_status s = check_cache(&pool, true);
+  if (s != CSA_OK) return s;
+  if (n < 0 || n > 0x7fffffff) return CSA_ERR_INVALID_ARG;
+  if (n == 0) return CSA_OK;
+  if (!words_ok(src) || !words_ok(dst)) return CSA_ERR_INVALID_ARG;
+  unsigned* status = csa::device_status();
+  const int sms = csa::current_sms();
+  if (!status || sms <= 0) return CSA_ERR_CUDA;
+  return cuda_status(csa::launch_pages_copy(cache_args(&pool), n, src, dst, status, sms,
+                                            static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

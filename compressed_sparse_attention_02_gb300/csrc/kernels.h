@@ -373,6 +373,46 @@ struct PromptAttnArgs {
 };
 cudaError_t launch_prompt_attn(const PromptAttnArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t stream);
 
+// A chunk of new tokens a sequence over the paged cache.
+struct ChunkAttnArgs {
+  PagedCache cache;
+  int B, n_heads;
+  int64_t n_q;               // rows of q
+  const int32_t* cu_q;       // [B+1]
+  const int32_t* lens;       // [B]
+  const uint16_t* q;
+  int64_t q_stride, q_stride_h;
+  float sm_scale;
+  int window;                // 0: none
+  const float* sink;         // [n_heads] or null
+  uint16_t* out;             // [n_q][n_heads][head_dim]
+  float* lse;                // [n_q][n_heads] or null
+  float* part;               // partial results (chunk_attn_bytes)
+  unsigned* status;
+};
+size_t chunk_attn_bytes(int head_dim, int sms);
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, int sms, PFN_cuTensorMapEncodeTiled_v12000 encode,
+                              cudaStream_t stream);
+
+// ---- pages of a paged cache: who holds them ------------------------------------------
+struct PageBook {
+  int n_seqs, page, page_shift;
+  int64_t n_pages;
+  int32_t* table;            // [n_seqs][table_stride]
+  int64_t table_stride;
+  int32_t* lens;             // [n_seqs]
+  int32_t* refs;             // [n_pages] table entries that hold a page
+};
+size_t pages_bytes(int n_seqs, int64_t n_pages);  // of workspace
+cudaError_t launch_pages_resize(const PageBook& k, const int32_t* target, int32_t* pos0, int32_t* src, int32_t* dst,
+                                void* workspace, unsigned* status, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PageBook& k, const int32_t* parent, int32_t* src, int32_t* dst, void* workspace,
+                              unsigned* status, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, int32_t* used, int32_t* table,
+                                 int32_t* refs, void* workspace, unsigned* status, int sms, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PagedCache& c, int64_t n, const int32_t* src, const int32_t* dst, unsigned* status,
+                              int sms, cudaStream_t stream);
+
 // Once per device and kernel: the shared memory a kernel may use and, where
 // min_regs is given, that it is launched with that many registers a thread.
 // `done` is the kernel's own mask of devices it was done for.

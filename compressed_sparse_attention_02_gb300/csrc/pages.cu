@@ -1,0 +1,571 @@
+// Bookkeeping of a paged cache's pages, and the copy of their contents.
+//
+// A page is free where its count is 0 (or less); pages are handed out lowest
+// number first, in the order of the sequences and of their tables, so that the
+// result is the same whatever runs when.  A call is two launches: the first
+// reads the counts once (4 bytes a page, all that grows with the pool), keeps a
+// bit a page and the free pages of each stretch, and sums up what the sequences
+// need; in the second a CTA a sequence finds its pages by their rank: the
+// stretch from the stretches' sums, the page from its bits.
+#include "gqa.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kScanThreads = 256;
+constexpr int kSumThreads = 1024;    // of the CTA that sums up what the sequences need
+constexpr int kSeqThreads = 128;     // of a sequence's CTA
+constexpr int kMaxStretches = 1024;
+constexpr int kMinStretch = 4096;    // pages
+
+// Stretches of 2^shift pages, at most kMaxStretches.
+__host__ __device__ __forceinline__ int stretch_shift(int64_t n_pages) {
+  int s = 12;
+  while ((n_pages + (int64_t(1) << s) - 1) >> s > kMaxStretches) ++s;
+  return s;
+}
+static_assert(kMinStretch == 1 << 12, "the first shift");
+
+// The workspace's parts.
+struct Work {
+  int32_t* free_of;    // [stretches] free pages of each
+  int64_t* before;     // [n_seqs + 1] pages that the sequences before need
+  int32_t* lens;       // [n_seqs] lengths before the call (fork: the parent's; -1: no child)
+  uint32_t* bits;      // [n_pages / 32] free pages
+  int32_t* rank;       // [n_pages] place of a page in the lists of a compaction
+};
+__host__ __device__ __forceinline__ size_t round16(size_t n) { return (n + 15) & ~size_t(15); }
+__host__ __device__ __forceinline__ size_t work_bytes(int n_seqs, int64_t n_pages, void* base, Work* w) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* x = p + at;
+    at += round16(bytes);
+    return x;
+  };
+  Work parts;
+  parts.free_of = reinterpret_cast<int32_t*>(take(kMaxStretches * 4));
+  parts.before = reinterpret_cast<int64_t*>(take((static_cast<size_t>(n_seqs) + 1) * 8));
+  parts.lens = reinterpret_cast<int32_t*>(take(static_cast<size_t>(n_seqs) * 4));
+  parts.bits = reinterpret_cast<uint32_t*>(take(static_cast<size_t>((n_pages + 31) / 32) * 4));
+  parts.rank = reinterpret_cast<int32_t*>(take(static_cast<size_t>(n_pages) * 4));
+  if (w) *w = parts;
+  return at;
+}
+
+enum Op { kResize = 0, kFork = 1, kCompact = 2 };
+
+__device__ __forceinline__ int64_t capacity(const PageBook& k) { return k.table_stride << k.page_shift; }
+__device__ __forceinline__ int pages_of(const PageBook& k, int tokens) {
+  return static_cast<int>((static_cast<int64_t>(tokens) + k.page - 1) >> k.page_shift);
+}
+// A sequence's length, within its table.
+__device__ __forceinline__ int length_of(const PageBook& k, int b, unsigned* status) {
+  const int64_t n = k.lens[b], cap = capacity(k);
+  if (n > cap) record_error(status, kErrIndexRange);
+  return static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
+}
+__device__ __forceinline__ bool in_pool(const PageBook& k, int32_t page) { return page >= 0 && page < k.n_pages; }
+
+// Pages that a sequence of L tokens takes from the free ones to grow to t (0:
+// it does not grow, or cannot): those of the new tokens, and one in the place
+// of a last page that is partly filled and that others hold too.
+__device__ __forceinline__ int growth(const PageBook& k, int b, int L, int t, unsigned* status) {
+  if (t <= L || t > capacity(k)) return 0;
+  int n = pages_of(k, t) - pages_of(k, L);
+  if (L & (k.page - 1)) {
+    const int32_t last = k.table[b * k.table_stride + (L >> k.page_shift)];
+    if (!in_pool(k, last))
+      record_error(status, kErrIndexRange);
+    else if (k.refs[last] > 1)
+      ++n;
+  }
+  return n;
+}
+
+// Sums over the CTA's threads before this one (of n), and the sum of all.
+template <int THREADS, typename T>
+__device__ __forceinline__ T sum_before(T n, T* sh, T* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T x = n;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  T before = x - n, sum = 0;
+#pragma unroll
+  for (int k = 0; k < THREADS / 32; ++k) {
+    const T y = sh[k];
+    if (k < warp) before += y;
+    sum += y;
+  }
+  *all = sum;
+  return before;
+}
+
+// CTAs 0 .. stretches - 1 look at a stretch of the counts each, the last one
+// at the sequences.
+template <int OP>
+__global__ void __launch_bounds__(OP == kCompact ? kScanThreads : kSumThreads)
+    pages_scan_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* want,
+                      unsigned* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kThreads = OP == kCompact ? kScanThreads : kSumThreads;
+  __shared__ int64_t sh[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (static_cast<int>(blockIdx.x) < stretches) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) << shift;
+    const int64_t end = min(first + (int64_t(1) << shift), k.n_pages);
+    int n = 0;
+    constexpr int kFlight = 4;  // words a warp
+    for (int64_t p0 = first + warp * 32; p0 < end; p0 += kFlight * kThreads) {
+      int32_t r[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int64_t p = p0 + i * kThreads + lane;
+        r[i] = p < end ? k.refs[p] : 1;
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const uint32_t word = __ballot_sync(0xffffffffu, r[i] <= 0);
+        const int64_t p = p0 + i * kThreads;
+        if (lane == 0 && p < end) w.bits[p >> 5] = word;
+        n += __popc(word);
+      }
+    }
+    int64_t all;
+    sum_before<kThreads, int64_t>(lane == 0 ? n : 0, sh, &all);
+    if (tid == 0) w.free_of[blockIdx.x] = static_cast<int32_t>(all);
+    return;
+  }
+  if (OP == kCompact) return;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < k.n_seqs; b0 += kThreads) {
+    const int b = b0 + tid;
+    int64_t n = 0;
+    if (b < k.n_seqs) {
+      const int t = want[b];
+      int L = 0;
+      if (OP == kResize) {
+        L = length_of(k, b, status);
+        if (t > capacity(k)) record_error(status, kErrIndexRange);
+        n = growth(k, b, L, t, status);
+      } else if (t < 0) {
+        L = -1;
+      } else if (t >= k.n_seqs || k.lens[b] > 0) {  // no such parent, or a sequence that has tokens
+        record_error(status, kErrIndexRange);
+        L = -1;
+      } else {
+        L = length_of(k, t, status);
+        n = (L & (k.page - 1)) != 0;
+      }
+      w.lens[b] = L;
+    }
+    int64_t all;
+    const int64_t before = base + sum_before<kThreads, int64_t>(n, sh, &all);
+    if (b < k.n_seqs) w.before[b] = before;
+    base += all;
+  }
+  if (tid == 0) w.before[k.n_seqs] = base;
+}
+
+// Free pages before each stretch, in shared memory (kMaxStretches + 1), and in
+// all; every thread of the CTA calls it.
+template <int THREADS>
+__device__ __forceinline__ int64_t free_before(const Work& w, int stretches, int32_t* before, int32_t* sh) {
+  int32_t base = 0;
+  for (int s0 = 0; s0 < stretches; s0 += THREADS) {
+    const int s = s0 + static_cast<int>(threadIdx.x);
+    const int32_t n = s < stretches ? w.free_of[s] : 0;
+    int32_t all;
+    const int32_t x = base + sum_before<THREADS, int32_t>(n, sh, &all);
+    if (s < stretches) before[s] = x;
+    base += all;
+  }
+  if (threadIdx.x == 0) before[stretches] = base;
+  __syncthreads();
+  return base;
+}
+
+// The free pages of ranks r0 .. r0 + n - 1, in order, by one warp: give(i, page).
+template <typename Give>
+__device__ __forceinline__ void free_pages(const PageBook& k, const Work& w, int shift, int stretches,
+                                           const int32_t* before, int32_t r0, int n, Give give) {
+  if (n <= 0) return;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = stretches - 1;  // the last stretch with at most r0 free pages before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] <= r0) lo = mid; else hi = mid - 1;
+  }
+  const int32_t r1 = r0 + n;
+  const int64_t words = (k.n_pages + 31) >> 5, per = int64_t(1) << (shift - 5);
+  for (int s = lo; s < stretches && before[s] < r1; ++s) {
+    int32_t rank = before[s];
+    const int64_t end = min((s + 1) * per, words);
+    for (int64_t i0 = s * per; i0 < end && rank < r1; i0 += 128) {
+      uint32_t word[4];
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // a lane holds four neighbours
+        const int64_t i = i0 + 4 * lane + j;
+        word[j] = i < end ? w.bits[i] : 0u;
+        c += __popc(word[j]);
+      }
+      int x = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      int32_t r = rank + x - c;
+      rank += __shfl_sync(0xffffffffu, x, 31);
+      if (r < r1 && r + c > r0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          for (uint32_t u = word[j]; u && r < r1; u &= u - 1, ++r)
+            if (r >= r0) give(r - r0, static_cast<int32_t>((i0 + 4 * lane + j) * 32 + __ffs(u) - 1));
+      }
+    }
+  }
+}
+
+// Takes one holder off a page.  (A count that is 0 already stays so.)
+__device__ __forceinline__ void drop(const PageBook& k, int32_t page, unsigned* status) {
+  if (in_pool(k, page)) {
+    if (atomicSub(k.refs + page, 1) > 0) return;
+    atomicAdd(k.refs + page, 1);
+  }
+  record_error(status, kErrIndexRange);
+}
+
+__global__ void __launch_bounds__(kSeqThreads)
+    pages_resize_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* target,
+                        int32_t* pos0, int32_t* src, int32_t* dst, unsigned* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int32_t before[kMaxStretches + 1], sh[kSeqThreads / 32];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int L = w.lens[b], t = target[b];
+  const int64_t r0 = w.before[b], need = w.before[b + 1] - r0;
+  int32_t* row = k.table + b * k.table_stride;
+  const int n0 = pages_of(k, L);
+  int now = L, first = -1, old = -1;
+  if (t > L && t <= capacity(k)) {
+    const int64_t all = need > 0 ? free_before<kSeqThreads>(w, stretches, before, sh) : 0;
+    const int n1 = pages_of(k, t), from = n1 - static_cast<int>(need);
+    const bool apart = from < n0;  // the last page is left to its other holders
+    if (r0 + need > all && need > 0) {
+      if (tid == 0) record_error(status, kErrIndexRange);
+    } else if (apart && !src) {
+      if (tid == 0) record_error(status, kErrIndexRange);
+    } else {
+      if (apart) old = row[from];
+      __syncthreads();
+      if (tid < 32)
+        free_pages(k, w, shift, stretches, before, static_cast<int32_t>(r0), static_cast<int>(need),
+                   [&](int i, int32_t page) {
+                     row[from + i] = page;
+                     k.refs[page] = 1;
+                     if (apart && i == 0) dst[b] = page;
+                   });
+      if (apart && tid == 0) drop(k, old, status);
+      now = t;
+      first = L;
+    }
+  } else if (t >= 0 && t < L) {
+    for (int j = pages_of(k, t) + tid; j < n0; j += kSeqThreads) {
+      drop(k, row[j], status);
+      row[j] = -1;
+    }
+    now = t;
+  }
+  if (tid == 0) {
+    k.lens[b] = now;
+    if (pos0) pos0[b] = first;
+    if (src) {
+      src[b] = old;
+      if (old < 0) dst[b] = -1;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSeqThreads)
+    pages_fork_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* parent,
+                      int32_t* src, int32_t* dst, unsigned* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int32_t before[kMaxStretches + 1], sh[kSeqThreads / 32];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int L = w.lens[b];
+  int32_t from = -1;
+  if (L > 0) {
+    const int64_t r0 = w.before[b];
+    const int whole = L >> k.page_shift, need = (L & (k.page - 1)) != 0;
+    const int32_t* theirs = k.table + static_cast<int64_t>(parent[b]) * k.table_stride;
+    int32_t* row = k.table + b * k.table_stride;
+    const int64_t all = need ? free_before<kSeqThreads>(w, stretches, before, sh) : 0;
+    if (need && r0 + need > all) {
+      if (tid == 0) record_error(status, kErrIndexRange);
+    } else {
+      for (int j = tid; j < whole; j += kSeqThreads) {
+        const int32_t page = theirs[j];
+        row[j] = page;
+        if (in_pool(k, page))
+          atomicAdd(k.refs + page, 1);
+        else
+          record_error(status, kErrIndexRange);
+      }
+      if (need) {
+        from = theirs[whole];
+        if (tid < 32)
+          free_pages(k, w, shift, stretches, before, static_cast<int32_t>(r0), 1, [&](int, int32_t page) {
+            row[whole] = page;
+            k.refs[page] = 1;
+            dst[b] = page;
+          });
+      }
+      if (tid == 0) k.lens[b] = L;
+    }
+  }
+  if (tid == 0) {
+    src[b] = from;
+    if (from < 0) dst[b] = -1;
+  }
+}
+
+// Lists of a compaction: with U used pages, the used ones from U on (src) and
+// the free ones below U (dst), as many, both in order; rank: each one's place.
+__global__ void __launch_bounds__(kScanThreads)
+    pages_list_kernel(const PageBook k, const Work w, const int shift, const int stretches, int32_t* src, int32_t* dst,
+                      int32_t* used) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int32_t before[kMaxStretches + 1], sh[kScanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t U = k.n_pages - free_before<kScanThreads>(w, stretches, before, sh);
+  if (blockIdx.x == 0 && tid == 0) *used = static_cast<int32_t>(U);
+  const int64_t words = (k.n_pages + 31) >> 5, per = int64_t(1) << (shift - 5);
+  // free pages below U
+  int64_t holes = 0;
+  if (U < k.n_pages) {
+    const int s = static_cast<int>(U >> shift);
+    int32_t n = 0;
+    for (int64_t i = s * per + tid; i <= U >> 5; i += kScanThreads) {
+      uint32_t u = w.bits[i];
+      if (i == U >> 5) u &= (1u << (U & 31)) - 1u;
+      n += __popc(u);
+    }
+    int32_t all;
+    sum_before<kScanThreads, int32_t>(n, sh, &all);
+    holes = before[s] + all;
+  }
+  int32_t rank = before[blockIdx.x];
+  const int64_t end = min((blockIdx.x + 1) * per, words);
+  for (int64_t i0 = blockIdx.x * per; i0 < end; i0 += kScanThreads) {
+    const int64_t i = i0 + tid;
+    const uint32_t word = i < end ? w.bits[i] : 0u;
+    int32_t all;
+    const int32_t mine = rank + sum_before<kScanThreads, int32_t>(__popc(word), sh, &all);
+    rank += all;
+    // a warp takes its lanes' words in turn, a lane a page
+    for (int l = 0; l < 32; ++l) {
+      const uint32_t u = __shfl_sync(0xffffffffu, word, l);
+      const int32_t free_here = __shfl_sync(0xffffffffu, mine, l);
+      const int64_t p = (i - lane + l) * 32 + lane;
+      if (i - lane + l >= end || p >= k.n_pages) continue;
+      const int32_t f = free_here + __popc(u & ((1u << lane) - 1u));  // free pages before p
+      const bool is_free = (u >> lane) & 1u;
+      if (is_free && p < U) {
+        dst[f] = static_cast<int32_t>(p);
+        w.rank[p] = f;
+      } else if (!is_free && p >= U) {
+        const int32_t r = static_cast<int32_t>(p - f - (U - holes));  // used pages before p, less those below U
+        src[r] = static_cast<int32_t>(p);
+        w.rank[p] = r;
+      }
+    }
+  }
+  for (int64_t r = holes + static_cast<int64_t>(blockIdx.x) * kScanThreads + tid; r < k.n_pages / 2;
+       r += static_cast<int64_t>(gridDim.x) * kScanThreads) {
+    src[r] = -1;
+    dst[r] = -1;
+  }
+}
+
+// The counts and the tables under the pages' new numbers.
+__global__ void __launch_bounds__(kScanThreads)
+    pages_renumber_kernel(const PageBook k, const Work w, const int page_ctas, const int32_t* src, const int32_t* dst,
+                          const int32_t* used, int32_t* table, int32_t* refs, unsigned* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t U = *used;
+  const auto is_free = [&](int64_t p) { return (w.bits[p >> 5] >> (p & 31)) & 1u; };
+  if (static_cast<int>(blockIdx.x) < page_ctas) {
+    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kScanThreads + threadIdx.x; p < k.n_pages;
+         p += static_cast<int64_t>(page_ctas) * kScanThreads) {
+      if (is_free(p)) {
+        if (p < U) {  // (both ends of a move by one thread: the counts may be written in place)
+          const int32_t from = src[w.rank[p]];
+          const int32_t n = k.refs[from];
+          refs[p] = n;
+          refs[from] = 0;
+        } else {
+          refs[p] = 0;
+        }
+      } else if (p < U) {
+        refs[p] = k.refs[p];
+      }
+    }
+    return;
+  }
+  const int64_t cta = blockIdx.x - page_ctas, ctas = gridDim.x - page_ctas;
+  for (int64_t b = cta; b < k.n_seqs; b += ctas) {
+    const int n = pages_of(k, length_of(k, static_cast<int>(b), status));
+    for (int64_t j = threadIdx.x; j < k.table_stride; j += kScanThreads) {
+      int32_t page = k.table[b * k.table_stride + j];
+      if (j < n) {
+        if (!in_pool(k, page))
+          record_error(status, kErrIndexRange);
+        else if (page >= U && !is_free(page))
+          page = dst[w.rank[page]];
+      }
+      table[b * k.table_stride + j] = page;
+    }
+  }
+}
+
+// Copies of pages' contents, bound by memory.  A unit is a slice of a pair;
+// a CTA looks at 256 of its units at a time, so that a long list of which most
+// is empty costs little, and copies the slices that are there.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyFlight = 4;  // 16-byte loads a thread on their way
+constexpr int kSliceBytes = kCopyThreads * kCopyFlight * 16 * 2;  // of k and of v together
+
+__global__ void __launch_bounds__(kCopyThreads)
+    pages_copy_kernel(const PagedCache c, const int64_t n, const int32_t* src, const int32_t* dst, const int slices,
+                      unsigned* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int64_t unit_s[kCopyThreads];
+  __shared__ int2 pair_s[kCopyThreads];
+  __shared__ int count_s;
+  const int tid = threadIdx.x;
+  const int64_t units = n * slices;
+  const int64_t page_bytes = static_cast<int64_t>(c.n_kv_heads) * c.page * c.head_dim;
+  for (int64_t u0 = blockIdx.x; u0 < units; u0 += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
+    __syncthreads();
+    if (tid == 0) count_s = 0;
+    __syncthreads();
+    const int64_t u = u0 + static_cast<int64_t>(tid) * gridDim.x;
+    if (u < units) {
+      const int64_t i = u / slices;
+      const int32_t from = src[i], to = dst[i];
+      if (from >= c.n_pages || to >= c.n_pages)
+        record_error(status, kErrIndexRange);
+      else if (from >= 0 && to >= 0 && from != to) {
+        const int at = atomicAdd(&count_s, 1);
+        unit_s[at] = u - i * slices;
+        pair_s[at] = make_int2(from, to);
+      }
+    }
+    __syncthreads();
+    const int count = count_s;
+    for (int q = 0; q < count; ++q) {
+      const int2 pair = pair_s[q];
+      const int64_t slice = unit_s[q];
+      const int64_t from = pair.x * page_bytes, to = pair.y * page_bytes;
+      const int64_t begin = slice * (kSliceBytes / 2) + tid * 16;
+      uint4 x[2][kCopyFlight];
+#pragma unroll
+      for (int i = 0; i < kCopyFlight; ++i) {
+        const int64_t at = begin + i * (kCopyThreads * 16);
+        if (at < page_bytes) {
+          x[0][i] = __ldcs(reinterpret_cast<const uint4*>(c.k + from + at));
+          x[1][i] = __ldcs(reinterpret_cast<const uint4*>(c.v + from + at));
+        }
+      }
+      if (slice == 0)
+        for (int h = tid; h < c.n_kv_heads; h += kCopyThreads) {
+          const int64_t a = static_cast<int64_t>(pair.x) * c.n_kv_heads + h;
+          const int64_t z = static_cast<int64_t>(pair.y) * c.n_kv_heads + h;
+          c.k_scale[z] = c.k_scale[a];
+          c.v_scale[z] = c.v_scale[a];
+        }
+#pragma unroll
+      for (int i = 0; i < kCopyFlight; ++i) {
+        const int64_t at = begin + i * (kCopyThreads * 16);
+        if (at < page_bytes) {
+          __stcs(reinterpret_cast<uint4*>(c.k + to + at), x[0][i]);
+          __stcs(reinterpret_cast<uint4*>(c.v + to + at), x[1][i]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+size_t pages_bytes(int n_seqs, int64_t n_pages) { return work_bytes(n_seqs, n_pages, nullptr, nullptr); }
+
+cudaError_t launch_pages_resize(const PageBook& k, const int32_t* target, int32_t* pos0, int32_t* src, int32_t* dst,
+                                void* workspace, unsigned* status, cudaStream_t stream) {
+  Work w;
+  work_bytes(k.n_seqs, k.n_pages, workspace, &w);
+  const int shift = stretch_shift(k.n_pages), stretches = static_cast<int>((k.n_pages + (int64_t(1) << shift) - 1) >> shift);
+  const cudaError_t e = launch_pdl(pages_scan_kernel<kResize>, dim3(stretches + 1), dim3(kSumThreads), 0, stream, k, w,
+                                   shift, stretches, target, status);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(pages_resize_kernel, dim3(k.n_seqs), dim3(kSeqThreads), 0, stream, k, w, shift, stretches, target,
+                    pos0, src, dst, status);
+}
+
+cudaError_t launch_pages_fork(const PageBook& k, const int32_t* parent, int32_t* src, int32_t* dst, void* workspace,
+                              unsigned* status, cudaStream_t stream) {
+  Work w;
+  work_bytes(k.n_seqs, k.n_pages, workspace, &w);
+  const int shift = stretch_shift(k.n_pages), stretches = static_cast<int>((k.n_pages + (int64_t(1) << shift) - 1) >> shift);
+  const cudaError_t e = launch_pdl(pages_scan_kernel<kFork>, dim3(stretches + 1), dim3(kSumThreads), 0, stream, k, w,
+                                   shift, stretches, parent, status);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(pages_fork_kernel, dim3(k.n_seqs), dim3(kSeqThreads), 0, stream, k, w, shift, stretches, parent,
+                    src, dst, status);
+}
+
+cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, int32_t* used, int32_t* table,
+                                 int32_t* refs, void* workspace, unsigned* status, int sms, cudaStream_t stream) {
+  Work w;
+  work_bytes(k.n_seqs, k.n_pages, workspace, &w);
+  const int shift = stretch_shift(k.n_pages), stretches = static_cast<int>((k.n_pages + (int64_t(1) << shift) - 1) >> shift);
+  cudaError_t e = launch_pdl(pages_scan_kernel<kCompact>, dim3(stretches), dim3(kScanThreads), 0, stream, k, w, shift,
+                             stretches, static_cast<const int32_t*>(nullptr), status);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(pages_list_kernel, dim3(stretches), dim3(kScanThreads), 0, stream, k, w, shift, stretches, src, dst,
+                 used);
+  if (e != cudaSuccess) return e;
+  const int64_t most = static_cast<int64_t>(sms) * 8;
+  const int64_t page_ctas = (k.n_pages + kScanThreads - 1) / kScanThreads, seq_ctas = k.n_seqs;
+  const int pc = static_cast<int>(page_ctas < most ? page_ctas : most);
+  const int sc = static_cast<int>(seq_ctas < most ? seq_ctas : most);
+  return launch_pdl(pages_renumber_kernel, dim3(pc + sc), dim3(kScanThreads), 0, stream, k, w, pc,
+                    static_cast<const int32_t*>(src), static_cast<const int32_t*>(dst),
+                    static_cast<const int32_t*>(used), table, refs, status);
+}
+
+cudaError_t launch_pages_copy(const PagedCache& c, int64_t n, const int32_t* src, const int32_t* dst, unsigned* status,
+                              int sms, cudaStream_t stream) {
+  if (n <= 0) return cudaSuccess;
+  const int64_t page_bytes = static_cast<int64_t>(c.n_kv_heads) * c.page * c.head_dim;
+  const int slices = static_cast<int>((page_bytes + kSliceBytes / 2 - 1) / (kSliceBytes / 2));
+  const int64_t units = n * slices, most = static_cast<int64_t>(sms) * 8;
+  return launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(units < most ? units : most)), dim3(kCopyThreads), 0,
+                    stream, c, n, src, dst, slices, status);
+}
+
+}  // namespace csa

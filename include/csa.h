@@ -666,8 +666,8 @@ csa_status csa_hca_layer_decode(const csa_params *p, int32_t B,
  * share key / value heads in groups ([结构对比] "MHA、GQA" compares CSA and HCA
  * with such layers; the pages describe no model that mixes the two).  The calls
  * below serve such a layer: rotate queries and keys, attend over packed
- * prompts, append keys and values to a paged 8-bit cache, and attend to it one
- * token at a time.  The layer calls above use none of them, and the cache and
+ * prompts, append keys and values to a paged 8-bit cache, attend to it one
+ * token or a chunk of tokens at a time, and keep its pages.  The layer calls above use none of them, and the cache and
  * both attentions stop at width 128; csa_rope also turns the compressed
  * layers' own rows (rope_dim 64, offset 448, CSA_ROPE_INTERLEAVED), which the
  * layer calls expect of their queries.  They take no csa_params.  Conventions are those at the top, with these
@@ -833,6 +833,136 @@ csa_status csa_prompt_attn(int32_t B, int32_t n_heads, int32_t n_kv_heads,
                            float *lse, void *stream);
 
 /*
+ * csa_chunk_attn — attention of a chunk of new tokens a sequence over its
+ * cached tokens, the chunk's own among them (they have been appended):
+ * sequence b's queries are rows cu_q[b] .. cu_q[b+1]-1 of q, n of them, and
+ * stand at its last positions: query i, at p = lens[b] - n + i, sees tokens
+ * t <= p, with window > 0 those with t > p - window.  The sums, sink and lse
+ * are csa_paged_attn's (so is a call with one query a sequence); a query that
+ * sees nothing, as one at a negative position, gives 0 and lse = sink, or -inf.
+ * Tokens that a query does not see have no effect on it, whatever they hold.
+ * n_q: rows of q, at most 2^27, and below 2^31 with the heads that share a key
+ * head counted; rows behind the last sequence are left as they
+ * are in out and lse.  out: [n_q][n_heads][head_dim], lse [n_q][n_heads] (or
+ * NULL), contiguous.
+ * A sequence with a cu_q entry that falls or passes n_q records
+ * CSA_ERR_INDEX_RANGE and is left out (of sequences that such entries make
+ * overlap, any part may be).  Lengths past the table and pages outside the pool
+ * are as for csa_paged_attn.
+ * Logits are held in fp32, up to 1e30 in magnitude; scales and logits may lie
+ * as far apart as fp32 reaches; a result below 2^-100 may come out as 0.
+ * Workspace: csa_chunk_attn_workspace_size bytes (a constant of the device and
+ * head_dim), of the call's own while it runs: calls that can overlap on the
+ * GPU, replayed graphs among them, need one each.
+ * Equal calls give equal bits.  Queries are held as a sum of two E4M3 values
+ * after a power of two takes their row's largest to [2^7, 2^8): exact for values
+ * down to 2^-10 of it, below that to 2^-18 of it.  A query row with a value
+ * that is not finite gives NaN.  Weights are rounded to f16 for the product with
+ * the values.
+ */
+size_t csa_chunk_attn_workspace_size(const csa_paged_cache *c, int32_t n_heads);
+csa_status csa_chunk_attn(const csa_paged_cache *c, int32_t B, int32_t n_heads,
+                          int64_t n_q, const int32_t *cu_q, const int32_t *lens,
+                          const uint16_t *q, int64_t q_stride,
+                          int64_t q_stride_h, float sm_scale, int32_t window,
+                          const float *sink, uint16_t *out, float *lse,
+                          void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * csa_page_book — who holds which page of the caches that share one table (the
+ * layers of a model): the table, the sequences' lengths and every page's count.
+ * A host struct of device pointers, read during the call; the arrays are read
+ * and written.
+ *   table [n_seqs][table_stride]  sequence b's pages are the entries
+ *                    0 .. ceil(lens[b] / page_size) - 1 of its row
+ *   lens  [n_seqs]   tokens (0 or less: none)
+ *   refs  [n_pages]  table entries that hold the page, and any other holders
+ *                    that the program counts (a kept prefix); 0: free
+ * page_size: 16, 32, 64 or 128; n_seqs at most 2^20, n_pages below 2^31,
+ * table_stride * page_size at most 2^30.
+ *
+ * A call's results follow from its inputs alone: free pages are taken lowest
+ * number first, in the order of the sequences and, in one, of its table.  Pages
+ * that a call gives back are free from the next call on.  Contents are not
+ * touched: where a page's contents have to be in another one too, the call
+ * lists the pair in src and dst (-1: none) for csa_pages_copy, once for each
+ * layer's cache, before anything is appended to.  Lengths past the table count
+ * up to it, and entries outside the pool are no pages; both record
+ * CSA_ERR_INDEX_RANGE.
+ * Workspace: csa_pages_workspace_size bytes, of the call's own while it runs.
+ */
+typedef struct {
+  int32_t n_seqs, page_size;
+  int64_t n_pages;
+  int32_t *table;
+  int64_t table_stride;
+  int32_t *lens;
+  int32_t *refs;
+} csa_page_book;
+
+size_t csa_pages_workspace_size(const csa_page_book *k);
+
+/*
+ * csa_pages_resize — sets the sequences' lengths to target [n_seqs] (negative:
+ * as it is).  A sequence that grows takes pages for its new tokens; if its last
+ * page is partly filled and has other holders, it takes one in its place, and
+ * src[b], dst[b] are the two.  One that shrinks, to 0 where it ends, gives back
+ * the pages behind its new length, whose entries become -1.
+ * pos0 [n_seqs] (or NULL): the length before of each sequence that has grown,
+ * the position of its first new token, and -1 for the others, as csa_kv_append
+ * takes it.
+ * A sequence whose pages are not all there stays as it is and records
+ * CSA_ERR_INDEX_RANGE: so does every one that takes pages while the sequences
+ * up to it, these counted, take more than are free.  So does one whose target
+ * is past the table, and, with src and dst NULL, one that needs them.
+ */
+csa_status csa_pages_resize(const csa_page_book *k, const int32_t *target,
+                            int32_t *pos0, int32_t *src, int32_t *dst,
+                            void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * csa_pages_fork — sequence b becomes a copy of sequence parent[b] as it was
+ * before the call (parent [n_seqs], negative: b is left alone): it holds the
+ * parent's full pages too, and takes a page of its own for a last one that is
+ * partly filled, whose pair is src[b], dst[b] ([n_seqs], -1: none).
+ * Sequence b must have no tokens; one that has, a parent past n_seqs, and a
+ * fork for whose page none is free (counted as for csa_pages_resize) record
+ * CSA_ERR_INDEX_RANGE and leave b as it is.
+ */
+csa_status csa_pages_fork(const csa_page_book *k, const int32_t *parent,
+                          int32_t *src, int32_t *dst, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * csa_pages_compact — new numbers for the used pages, so that the U of them are
+ * pages 0 .. U-1: the used ones from U on, in order, move to the free ones below
+ * U, in order; the others keep theirs.
+ * src, dst [n_pages / 2]: the moves, then -1.  used [1]: U.
+ * table_out, refs_out: the table and the counts afterwards, all of them; they
+ * may be the book's own arrays.  Entries behind a sequence's length are copied
+ * as they are, counts below 0 become 0.  The moved pages' contents stay where
+ * they were until something is written there, so work under way under the old
+ * table can end.
+ */
+csa_status csa_pages_compact(const csa_page_book *k, int32_t *src, int32_t *dst,
+                             int32_t *used, int32_t *table_out,
+                             int32_t *refs_out, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * csa_pages_copy — the contents (codes and scales) of pages src[i] of the pool
+ * into its pages dst[i], i < n.  Pairs with a negative number, or a page and
+ * itself, are passed over; pairs with a number past the pool record
+ * CSA_ERR_INDEX_RANGE and are too.  A page that is in several pairs may be src
+ * of all; one that is dst of a pair and in another one holds unspecified
+ * contents afterwards.  The table of *c is not read and may be NULL.
+ */
+csa_status csa_pages_copy(const csa_paged_cache *c, int64_t n,
+                          const int32_t *src, const int32_t *dst, void *stream);
+
+/*
  * Optional stage tracing, for profiling.  With events != NULL (n_events == 5
  * cudaEvent_t handles passed as void*), every csa_layer_decode(_append,
  * _with_keys) and csa_layer_prefill(_with_keys) call records events[0] on
@@ -874,7 +1004,7 @@ csa_status csa_check_status(void *stream);
  *              of more than 4096 keys);
  *     ATTN     the sparse attention's MMA thread never announces the first
  *              tile's scores (every form: single CTA, cluster, split-KV),
- *              nor does csa_prompt_attn's.
+ *              nor do csa_prompt_attn's and csa_chunk_attn's.
  *   A non-zero faults needs a non-zero wait_limit_us.
  * Synchronises the device first.  Process-wide per device: set it only while
  * no other call runs.  Errors: CSA_ERR_INVALID_ARG for unknown bits or faults
