@@ -45,6 +45,7 @@ constexpr int kGroups = kTile / 16;         // groups of 16 keys, whose page is 
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kLoadWarp = 12, kMmaWarp = 13, kWarpsUsed = 14;
 constexpr int kConvThreads = 128;
+constexpr int kOrders = 4;                  // tiles that the loading warp may be ahead
 // A maximum may lag behind by this much (in log2) before the sums are rescaled:
 // weights are then at most 2^8 times 1, and as f16 they carry 2^7 more, so that
 // weights down to 2^-21 of the largest keep f16's full precision.
@@ -63,6 +64,10 @@ constexpr int kMaxMasked = 8;
 // one, and the tile itself.
 constexpr int kCostTwo = 3, kCostOne = 2, kCostTile = 4;
 
+// Registers a thread: 512 threads are launched with 128 each.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvRegs = 56, kOtherRegs = 56;
+static_assert(2 * kSoftmaxRegs + kConvRegs + kOtherRegs <= 4 * kLaunchRegs, "registers of the block");
+
 template <int D>
 struct Cfg {
   static constexpr int kQBytes = kTile * D * 2;     // of a half: two E4M3 parts
@@ -80,9 +85,6 @@ struct Cfg {
   static constexpr int kCols = 512;
   static constexpr int64_t kRecord = static_cast<int64_t>(kTileRows) * (D + 4);  // floats of a partial result
 };
-// Registers a thread: 512 are launched with 128 each.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kConvRegs = 72, kOtherRegs = 56;
-static_assert(2 * kSoftmaxRegs + kConvRegs + kOtherRegs <= 4 * kLaunchRegs, "registers of the block");
 
 // A tile that a share's end divides, for the merge.
 struct __align__(16) Cut {
@@ -173,6 +175,17 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float x, float y, float z, float w
 // Non-zero where a byte is a NaN code (magnitude 0x7F, which carries into the
 // byte's top bit).
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Keeps what is computed from r behind the wait for its load.
+__device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               :);
+}
 
 // What every CTA finds out first: its share of the line, and where it begins.
 struct Start {
@@ -309,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const ChunkAttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t order_full[2], order_empty[2], q_full, q_empty;
+  __shared__ uint64_t order_full[kOrders], order_empty[kOrders], q_full, q_empty;
   __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages], raw_full[C::kRawStages], raw_empty[C::kRawStages];
   __shared__ uint64_t v_full[C::kVStages], v_empty[C::kVStages], meta_full[C::kMeta];
   __shared__ uint64_t s_full[2], p_full[2], o_full[2], joined, left_off, drain;
-  __shared__ Order orders[2];
+  __shared__ Order orders[kOrders];
   __shared__ __align__(16) float k_scale_s[C::kMeta][kGroups], v_log_s[C::kMeta][kGroups];
   __shared__ float v_min_s[C::kMeta];          // the least of the block's value scales, in log2
   __shared__ uint32_t bad_s[C::kMeta];         // groups whose page is outside the pool
@@ -340,9 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int group = a.n_heads / a.cache.n_kv_heads;
   volatile int* abort_flag = &abort_s;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kOrders; ++i) {
       mbar_init(order_full + i, 1);
       mbar_init(order_empty + i, kWarpsUsed - 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kTile);
       mbar_init(o_full + i, 1);
@@ -452,14 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   const uint32_t tmem = tmem_slot;
 
-  // the next tile, of every warp but the loading one; false at the end and after an abort
-  auto take = [&](int item, Order* o) {
-    const bool ok = wait_or_abort(order_full + (item & 1), (item >> 1) & 1, abort_flag, a.status);
-    if (!__all_sync(0xffffffffu, ok)) return false;
-    *o = orders[item & 1];
+  // the next tile, of every warp but the loading one (read where it lies, until
+  // `done` with it); false at the end and after an abort
+  auto take = [&](int item) {
+    const bool ok = wait_or_abort(order_full + item % kOrders, (item / kOrders) & 1, abort_flag, a.status);
+    return __all_sync(0xffffffffu, ok) && orders[item % kOrders].there != 0;
+  };
+  auto done = [&](int item) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(order_empty + (item & 1));
-    return o->there != 0;
+    if (lane == 0) mbar_arrive(order_empty + item % kOrders);
   };
 
   if (warp >= kLoadWarp) {
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (there) {
           const int64_t x1 = min(w.tile.cost(), w.x0 + w.left);
           const int k0 = block_at(w.tile, w.x0), k1 = block_at(w.tile, x1);
-          const bool done = x1 - w.x0 == w.left;
+          const bool last_one = x1 - w.x0 == w.left;
           if (k1 > k0) {
             const Tile& t = w.tile;
             o.there = 1;
@@ -508,14 +524,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           w.left -= x1 - w.x0;
-          there = !done && w.next(a, group);
+          there = !last_one && w.next(a, group);
           if (o.there) break;
         }
         if (lane == 0) {
-          if (item >= 2) ok = wait_or_abort(order_empty + (item & 1), ((item >> 1) - 1) & 1, abort_flag, a.status);
+          if (item >= kOrders)
+            ok = wait_or_abort(order_empty + item % kOrders, (item / kOrders - 1) & 1, abort_flag, a.status);
           if (ok) {
-            orders[item & 1] = o;
-            mbar_arrive(order_full + (item & 1));
+            orders[item % kOrders] = o;
+            mbar_arrive(order_full + item % kOrders);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -640,10 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int n0 = 0;               // blocks of the tiles before
       uint32_t n_p[2] = {};     // weights taken so far, by half
-      Order o;
-      for (int item = 0; ok && take(item, &o); ++item) {
+      for (int item = 0; ok && take(item); ++item) {
+        const Order& o = orders[item % kOrders];
         const int blocks = uniform(o.blocks);
         const bool split = uniform(o.split) != 0;
+        done(item);
         ok = wait(&q_full, item & 1);
         if (split) {
           for (int t = 0; t < 2 && t < blocks && ok; ++t) {
@@ -724,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp >= kConvWarp) {
-    // ---------------- queries into two parts, values into f16 ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    // ---------------- queries into two parts, values into f16 ----------------
     constexpr int kChunks = D / 16;               // 16-channel chunks a row
     constexpr int kRowsAtOnce = kConvThreads / kChunks;
     const int ct = tid - kConvWarp * 32, cw = warp - kConvWarp;
@@ -733,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale2 = a.sm_scale * kLog2e;
     int n0 = 0;
     bool ok = true;
-    Order o;
-    for (int item = 0; ok && take(item, &o); ++item) {
+    for (int item = 0; ok && take(item); ++item) {
+      const Order& o = orders[item % kOrders];
       if (item > 0) ok = __all_sync(0xffffffffu, wait_or_abort(&q_empty, (item - 1) & 1, abort_flag, a.status));
       if (!ok) break;
       for (int h = 0; h < (o.split ? 1 : 2); ++h) {
@@ -874,6 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(raw_empty + raw_slot);
       }
       n0 += o.blocks;
+      done(item);
     }
   } else {
     // ---------------- softmax: one thread a row ----------------
@@ -885,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n_s = 0, n_o[2] = {}, n_split = 0;  // scores and sums taken so far, tiles whose halves were joined
     int n0 = 0;
     bool ok = true;
-    Order o;
-    for (int item = 0; ok && take(item, &o); ++item) {
+    for (int item = 0; ok && take(item); ++item) {
+      const Order& o = orders[item % kOrders];
       ok = __all_sync(0xffffffffu, wait_or_abort(&q_full, item & 1, abort_flag, a.status));
       if (!ok) break;
       const bool split = o.split != 0;
@@ -904,8 +923,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool began = false;
       for (int q = split ? t : 0; q < o.blocks; q += step) {
         const int n = n0 + q, j = o.j_top - q, meta = n % C::kMeta;
-        ok = wait_or_abort(meta_full + meta, (n / C::kMeta) & 1, abort_flag, a.status) &&
-             wait_or_abort(s_full + t, n_s & 1u, abort_flag, a.status);
+        ok = wait_or_abort(meta_full + meta, (n / C::kMeta) & 1, abort_flag, a.status);
+        float cf[kGroups], lv[kGroups];  // the groups' factors and value scales (log2)
+        {
+          const float4 x = *reinterpret_cast<const float4*>(&k_scale_s[meta][0]);
+          const float4 y = *reinterpret_cast<const float4*>(&k_scale_s[meta][4]);
+          const float4 z = *reinterpret_cast<const float4*>(&v_log_s[meta][0]);
+          const float4 w = *reinterpret_cast<const float4*>(&v_log_s[meta][4]);
+          const float ks[kGroups] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          const float vs[kGroups] = {z.x, z.y, z.z, z.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            cf[g] = fmaxf(fac * ks[g], FLT_MIN);  // (not 0: a masked score is -inf, and stays so under it)
+            lv[g] = vs[g];
+          }
+        }
+        const float v_min = v_min_s[meta];
+        const uint32_t bad = bad_s[meta];
+        ok = ok && wait_or_abort(s_full + t, n_s & 1u, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++n_s;
@@ -913,17 +948,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
-        float cf[kGroups];
-        {
-          const float4 x = *reinterpret_cast<const float4*>(&k_scale_s[meta][0]);
-          const float4 y = *reinterpret_cast<const float4*>(&k_scale_s[meta][4]);
-          const float ks[kGroups] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          // (not 0: a masked score is -inf, and stays so under the factor)
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) cf[g] = fmaxf(fac * ks[g], FLT_MIN);
-        }
-        const uint32_t bad = bad_s[meta];
         tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) landed(s[c]);
         if (o.masked(j) || bad) {  // this row's keys among the block's, as a bit each
           const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
 #pragma unroll
@@ -937,21 +964,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
           }
         }
-        float lv[kGroups];
-        {
-          const float4 x = *reinterpret_cast<const float4*>(&v_log_s[meta][0]);
-          const float4 y = *reinterpret_cast<const float4*>(&v_log_s[meta][4]);
-          const float v[kGroups] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) lv[g] = v[g];
-        }
         float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          const int c = g >> 1, k0 = (g & 1) * 16;
-          float x = fmaxf(__uint_as_float(s[c][k0]), __uint_as_float(s[c][k0 + 1]));
+          const uint32_t* y = s[g >> 1] + (g & 1) * 16;
+          float x = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
-          for (int k = 2; k < 16; k += 2) x = max3(x, __uint_as_float(s[c][k0 + k]), __uint_as_float(s[c][k0 + k + 1]));
+          for (int k = 2; k < 16; k += 2) x = max3(x, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
           x *= cf[g];
           top = fmaxf(top, x);
           topv = fmaxf(topv, x + lv[g]);
@@ -966,40 +985,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m1;
           mv = mv1;
           if (began) {  // (the half's products before have finished: these scores were issued after them)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[32];
-              tmem_ld32(o_tmem + 32 * c, x);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t x[16];
+              tmem_ld16(o_tmem + 16 * c, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-              tmem_st32(o_tmem + 32 * c, x);
+              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+              tmem_st16(o_tmem + 16 * c, x);
             }
           }
         }
         began = true;
         // exponents in one rounding, factor s - m; where logits are so large that the
         // rounding of m shows, the products first
-        float minus_m = -m, up = kWeightExp - mv;
-        const float down = mv - kWeightExp - m;
         const bool large = fmaxf(fabsf(m), fabsf(mv)) > kLarge && m > kNone;
+        float up = kWeightExp - mv, minus_m = -m;
+        const float down = mv - kWeightExp - m;
         if (__any_sync(0xffffffffu, large)) {
+          const float less = large ? m : 0.f;
           if (large) {
-            minus_m = 0.f;
             up = kWeightExp + (m - mv);
+            minus_m = 0.f;
           }
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
-            const float x = large ? cf[g] : 1.f, y = large ? m : 0.f;
+            const float x = large ? cf[g] : 1.f;
+            if (large) cf[g] = 1.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               uint32_t& w = s[g >> 1][(g & 1) * 16 + k];
-              w = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(w), x), y));
+              w = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(w), x), less));
             }
-            if (large) cf[g] = 1.f;
           }
         }
-        const bool far = v_min_s[meta] - down < kFar;
+        const bool far = v_min - down < kFar;
         if (__any_sync(0xffffffffu, far)) {
           float sum = 0.f;
 #pragma unroll
@@ -1145,6 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      done(item);
       tc_fence_before();
       if (split) {  // the other half has read these sums, and its own, before either is written again
         mbar_arrive(&left_off);
