@@ -43,9 +43,9 @@ constexpr int kTile = 1 << kTileShift;      // rows of a half, keys of a block
 constexpr int kTileRows = 2 * kTile;
 constexpr int kGroups = kTile / 16;         // groups of 16 keys, whose page is one
 constexpr int kThreads = 512;
-constexpr int kConvWarp = 8, kLoadWarp = 12, kMmaWarp = 13, kWarpsUsed = 14;
+constexpr int kConvWarp = 8, kWalkWarp = 12, kMmaWarp = 13, kKeyWarp = 14, kValueWarp = 15;
 constexpr int kConvThreads = 128;
-constexpr int kOrders = 4;                  // tiles that the loading warp may be ahead
+constexpr int kOrders = 4;                  // tiles that the walking warp may be ahead
 // A maximum may lag behind by this much (in log2) before the sums are rescaled:
 // weights are then at most 2^8 times 1, and as f16 they carry 2^7 more, so that
 // weights down to 2^-21 of the largest keep f16's full precision.
@@ -148,6 +148,16 @@ struct Order {
   __device__ __forceinline__ bool masked(int j) const { return j >= from || j <= upto; }
 };
 
+// A copy of 16 bytes, or zeros without reading.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// Asks for a tile of a tensor map in L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
+               "r"(c2)
+               : "memory");
+}
 // Two fp32 values as f16, the first in the low half.
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -355,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kOrders; ++i) {
       mbar_init(order_full + i, 1);
-      mbar_init(order_empty + i, kWarpsUsed - 1);
+      mbar_init(order_empty + i, kThreads / 32 - 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
@@ -385,10 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     start_s.b = -1;
     for (int i = 0; i < 12; ++i) odd_item[i >> 2][i & 3] = 0;
   }
-  if (warp == kLoadWarp && lane == 0) {
-    prefetch_tensormap(&tm_k);
-    prefetch_tensormap(&tm_v);
-  }
+  if (warp == kKeyWarp && lane == 0) prefetch_tensormap(&tm_k);
+  if (warp == kValueWarp && lane == 0) prefetch_tensormap(&tm_v);
   // Tensor memory is taken after the kernel before has ended and before the
   // one after may start: no CTA of either can then hold what this one, or
   // what it waits for, still needs.
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   const uint32_t tmem = tmem_slot;
 
-  // the next tile, of every warp but the loading one (read where it lies, until
+  // the next tile, of every warp but the walking one (read where it lies, until
   // `done` with it); false at the end and after an abort
   auto take = [&](int item) {
     const bool ok = wait_or_abort(order_full + item % kOrders, (item / kOrders) & 1, abort_flag, a.status);
@@ -478,14 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(order_empty + item % kOrders);
   };
 
-  if (warp >= kLoadWarp) {
+  if (warp >= kWalkWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) {
-      // ---------------- loads ----------------
+    if (warp == kWalkWarp) {
+      // ---------------- the tiles of the share ----------------
       Walker w;
       const Start st = start_s;
       bool there = st.b >= 0 && w.begin(a, st, group), ok = true;
-      int n_k = 0;  // blocks so far
       Cut cut = {};
       for (int item = 0; ok; ++item) {
         Order o = {};
@@ -536,87 +543,93 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok || !o.there) break;
-        // a lane looks after a group of 16 keys of one of four blocks
+        if (!o.there) break;
+      }
+      if (lane == 0) reinterpret_cast<Cut*>(a.part)[blockIdx.x] = cut;
+    } else if (warp != kMmaWarp) {
+      // ---------------- loads: a warp for keys and scales, one for values ----------------
+      const bool keys = warp == kKeyWarp;
+      const CUtensorMap* tm = keys ? &tm_k : &tm_v;
+      uint64_t* full = keys ? k_full : raw_full;
+      uint64_t* empty = keys ? k_empty : raw_empty;
+      uint8_t* ring = keys ? k_ring : raw_ring;
+      const int stages = keys ? C::kKStages : C::kRawStages;
+      const int ps = a.cache.page_shift, g = lane & 7;
+      int n = 0, slot = 0, meta = 0;  // blocks so far, their places
+      uint32_t parity = 1;            // of the phase before the slot's
+      bool ok = true;
+      for (int item = 0; ok && take(item); ++item) {
+        const Order& o = orders[item % kOrders];
+        const int blocks = o.blocks, j_top = o.j_top, lo = o.lo, hi = o.hi, kv_head = o.kv_head;
+        // a lane looks after a group of 16 keys of one of four blocks; their pages
+        // are read eight blocks ahead, and their contents asked for four ahead
         const int32_t* row = a.cache.table + static_cast<int64_t>(o.b) * a.cache.table_stride;
-        const int ps = a.cache.page_shift, g = lane & 7;
-        auto token_of = [&](int q) { return (o.j_top - q) * kTile + 16 * g; };
         constexpr int32_t kNotNeeded = INT32_MIN;
         auto entry = [&](int q0) -> int32_t {
-          const int q = q0 + (lane >> 3), t = token_of(q), p0 = (t >> ps) << ps;
-          if (q >= o.blocks || p0 >= o.hi || p0 + a.cache.page <= o.lo) return kNotNeeded;
+          const int q = q0 + (lane >> 3), t = (j_top - q) * kTile + 16 * g, p0 = (t >> ps) << ps;
+          if (q >= blocks || p0 >= hi || p0 + a.cache.page <= lo) return kNotNeeded;
           return max(__ldg(row + (t >> ps)), -1);
         };
-        int32_t next = entry(0);
-        for (int q0 = 0; q0 < o.blocks && ok; q0 += 4) {
-          const int32_t page = next;
-          const bool in = page >= 0 && page < a.cache.n_pages;
-          const bool bad = page != kNotNeeded && !in;
-          if (bad) record_error(a.status, kErrIndexRange);
-          float ks = 1.f, vs = 0.f;
-          if (in) {
-            const int64_t at = static_cast<int64_t>(page) * a.cache.n_kv_heads + o.kv_head;
-            ks = __ldg(a.cache.k_scale + at);
-            vs = __ldg(a.cache.v_scale + at);
-          }
-          next = entry(q0 + 4);
-          const unsigned bads = __ballot_sync(0xffffffffu, bad);
-          const int n_q = min(4, o.blocks - q0);
-          for (int i = 0; i < n_q && ok; ++i, ++n_k) {
-            const bool mine = (lane >> 3) == i;
-            const bool copies = mine && in && ((16 * g) & (a.cache.page - 1)) == 0;
-            const unsigned bytes = __popc(__ballot_sync(0xffffffffu, copies)) * a.cache.page * D;
-            const int ks_slot = n_k % C::kKStages, vs_slot = n_k % C::kRawStages, meta = n_k % C::kMeta;
-            if (n_k >= C::kKStages)
-              ok = wait_or_abort(k_empty + ks_slot, (n_k / C::kKStages - 1) & 1, abort_flag, a.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            float lv = in ? __log2f(vs) : 1e30f, least = lv;
+        auto in_pool = [&](int32_t page) { return page >= 0 && page < a.cache.n_pages; };
+        auto scale = [&](int32_t page, const float* of, float none) {
+          return keys && in_pool(page) ? __ldg(of + static_cast<int64_t>(page) * a.cache.n_kv_heads + kv_head) : none;
+        };
+        const bool first_of_page = ((16 * g) & (a.cache.page - 1)) == 0;
+        int32_t page = entry(0), next = entry(4);
+        float ks = scale(page, a.cache.k_scale, 1.f), vs = scale(page, a.cache.v_scale, 0.f);
+        for (int q0 = 0; q0 < blocks && ok; q0 += 4) {
+          const int32_t after = entry(q0 + 8);
+          if (in_pool(next) && first_of_page) tma_prefetch_3d(tm, 0, kv_head << ps, next);
+          const float ks_next = scale(next, a.cache.k_scale, 1.f), vs_next = scale(next, a.cache.v_scale, 0.f);
+          const bool in = in_pool(page);
+          const unsigned bads = __ballot_sync(0xffffffffu, page != kNotNeeded && !in);
+          if (bads && keys) record_error(a.status, kErrIndexRange);
+          const float lv = in ? __log2f(vs) : 1e30f;
+          float least = lv;
 #pragma unroll
-            for (int off = 1; off < 8; off <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
-            if (mine) {
-              k_scale_s[meta][g] = ks;
-              v_log_s[meta][g] = lv;
-              if (g == 0) {
-                v_min_s[meta] = least;
-                bad_s[meta] = (bads >> (8 * i)) & 0xFFu;
+          for (int off = 1; off < 8; off <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
+          const unsigned copies = __ballot_sync(0xffffffffu, in && first_of_page);
+          const int n_q = min(4, blocks - q0);
+          for (int i = 0; i < n_q; ++i) {
+            const bool mine = (lane >> 3) == i;
+            if (n >= stages) ok = __all_sync(0xffffffffu, wait_or_abort(empty + slot, parity, abort_flag, a.status));
+            if (!ok) break;
+            if (keys) {
+              if (mine) {
+                k_scale_s[meta][g] = ks;
+                v_log_s[meta][g] = lv;
+                if (g == 0) {
+                  v_min_s[meta] = least;
+                  bad_s[meta] = (bads >> (8 * i)) & 0xFFu;
+                }
               }
-            }
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(meta_full + meta);
-              mbar_arrive_expect_tx(k_full + ks_slot, bytes);
-            }
-            __syncwarp();
-            if (copies)
-              tma_load_3d(k_ring + ks_slot * C::kCodeBytes + 16 * g * D, &tm_k, 0, o.kv_head << ps, page,
-                          k_full + ks_slot);
-            if (n_k >= C::kRawStages)
-              ok = wait_or_abort(raw_empty + vs_slot, (n_k / C::kRawStages - 1) & 1, abort_flag, a.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {  // (this block's keys are on their way)
-              if (lane == 0) mbar_wait(k_full + ks_slot, (n_k / C::kKStages) & 1, a.status);
               __syncwarp();
-              break;
+              if (lane == 0) mbar_arrive(meta_full + meta);
+              meta = meta + 1 == C::kMeta ? 0 : meta + 1;
             }
-            if (lane == 0) mbar_arrive_expect_tx(raw_full + vs_slot, bytes);
+            if (lane == 0)
+              mbar_arrive_expect_tx(full + slot, __popc(copies & (0xFFu << (8 * i))) * a.cache.page * D);
             __syncwarp();
-            if (copies)
-              tma_load_3d(raw_ring + vs_slot * C::kCodeBytes + 16 * g * D, &tm_v, 0, o.kv_head << ps, page,
-                          raw_full + vs_slot);
+            if (mine && in && first_of_page)
+              tma_load_3d(ring + slot * C::kCodeBytes + 16 * g * D, tm, 0, kv_head << ps, page, full + slot);
+            ++n;
+            if (++slot == stages) {
+              slot = 0;
+              parity ^= 1u;
+            }
           }
+          page = next;
+          next = after;
+          ks = ks_next;
+          vs = vs_next;
         }
+        if (!ok) break;
+        done(item);
       }
-      if (lane == 0) {
-        reinterpret_cast<Cut*>(a.part)[blockIdx.x] = cut;
-        // every copy lands before the CTA ends (also after an abort)
-        for (int k = max(0, n_k - C::kKStages); k < n_k; ++k)
-          mbar_wait(k_full + k % C::kKStages, (k / C::kKStages) & 1, a.status);
-        for (int k = max(0, n_k - C::kRawStages); k < n_k; ++k)
-          mbar_wait(raw_full + k % C::kRawStages, (k / C::kRawStages) & 1, a.status);
-      }
+      if (lane == 0)  // every copy lands before the CTA ends (also after an abort)
+        for (int k = max(0, n - stages); k < n; ++k) mbar_wait(full + k % stages, (k / stages) & 1, a.status);
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else {
       // ---------------- products ----------------
       // (the whole warp walks the loop and one elected lane issues, so that the
       // loop's values are uniform)
@@ -755,68 +768,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Order& o = orders[item % kOrders];
       if (item > 0) ok = __all_sync(0xffffffffu, wait_or_abort(&q_empty, (item - 1) & 1, abort_flag, a.status));
       if (!ok) break;
-      for (int h = 0; h < (o.split ? 1 : 2); ++h) {
-#pragma unroll 1
-        for (int k0 = 0; k0 < kChunks; k0 += 2) {
-          uint4 u[2][2];
+      // a thread's 16 channels of its rows are copied to where their two parts
+      // will be, and turned into these in place
+      const int halves = o.split ? 1 : 2;
+      auto q_at = [&](int h, int r, int part) {
+        uint8_t* line = q_s + h * C::kQBytes + r * 128;
+        return D == 128 ? line + part * (kTile * 128) + ((c ^ (r & 7)) << 4) : line + (((c + 4 * part) ^ (r & 7)) << 4);
+      };
+      for (int h = 0; h < halves; ++h) {
+#pragma unroll 4
+        for (int k = 0; k < kChunks; ++k) {
+          const int r = r0 + k * kRowsAtOnce, rr = h * kTile + r;
+          const bool there = rr < o.rows;
+          const uint32_t at = static_cast<uint32_t>(o.row0 + rr), qi = at / group;
+          const uint16_t* src = a.q;
+          if (there)
+            src += static_cast<int64_t>(o.q0 + static_cast<int>(qi)) * a.q_stride +
+                   (o.head0 + static_cast<int>(at - qi * group)) * a.q_stride_h + c * 16;
+          cp_async_16_or_zero(smem_u32(q_at(h, r, 0)), src, there);
+          cp_async_16_or_zero(smem_u32(q_at(h, r, 1)), src + 8, there);
+        }
+      }
+      cp_async_commit_wait_all();
+      for (int h = 0; h < halves; ++h) {
+#pragma unroll 2
+        for (int k = 0; k < kChunks; ++k) {
+          const int r = r0 + k * kRowsAtOnce;
+          uint4* part[2] = {reinterpret_cast<uint4*>(q_at(h, r, 0)), reinterpret_cast<uint4*>(q_at(h, r, 1))};
+          float x[16];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int r = r0 + (k0 + i) * kRowsAtOnce, rr = h * kTile + r;
-            u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < o.rows) {
-              const uint32_t at = static_cast<uint32_t>(o.row0 + rr);
-              const int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  a.q + static_cast<int64_t>(o.q0 + qi) * a.q_stride + (o.head0 + hd) * a.q_stride_h + c * 16);
-              u[i][0] = __ldg(src);
-              u[i][1] = __ldg(src + 1);
+            float y[8];
+            unpack_bf16(*part[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[8 * i + j] = y[j];
+          }
+          // the largest magnitude; a value that is not finite shows as one past all others
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]) <= FLT_MAX ? fabsf(x[j]) : INFINITY);
+#pragma unroll
+          for (int off = 1; off < kChunks; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const bool finite = top <= FLT_MAX;
+          const int e = min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 126);
+          const float up = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.f;
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = x[4 * j + i] * up;
+            hi[j] = to_e4m3x4(y[0], y[1], y[2], y[3]);
+            uint32_t h01, h23;
+            e4m3x4_to_f16(hi[j], h01, h23);
+            const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+            const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+            lo[j] = to_e4m3x4(y[0] - f01.x, y[1] - f01.y, y[2] - f23.x, y[3] - f23.y);
+            if (!finite) {
+              hi[j] = 0x7F7F7F7Fu;
+              lo[j] = 0u;
             }
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = r0 + (k0 + i) * kRowsAtOnce;
-            float x[16];
-            {
-              float y[8];
-              unpack_bf16(u[i][0], y);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = y[j];
-              unpack_bf16(u[i][1], y);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) x[8 + j] = y[j];
-            }
-            // the largest magnitude; a value that is not finite shows as one past all others
-            float top = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]) <= FLT_MAX ? fabsf(x[j]) : INFINITY);
-#pragma unroll
-            for (int off = 1; off < kChunks; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const bool finite = top <= FLT_MAX;
-            const int e = min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 126);
-            const float up = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.f;
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float y[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) y[q] = x[4 * j + q] * up;
-              hi[j] = to_e4m3x4(y[0], y[1], y[2], y[3]);
-              uint32_t h01, h23;
-              e4m3x4_to_f16(hi[j], h01, h23);
-              const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-              const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-              lo[j] = to_e4m3x4(y[0] - f01.x, y[1] - f01.y, y[2] - f23.x, y[3] - f23.y);
-              if (!finite) {
-                hi[j] = 0x7F7F7F7Fu;
-                lo[j] = 0u;
-              }
-            }
-            uint8_t* line = q_s + h * C::kQBytes + r * 128;
-            *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            uint8_t* low = D == 128 ? line + kTile * 128 + ((c ^ (r & 7)) << 4) : line + (((c + 4) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (c == 0) q_scale_s[h][r] = finite ? scale2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
-          }
+          *part[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *part[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (c == 0) q_scale_s[h][r] = finite ? scale2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
         }
       }
       fence_proxy_async_smem();
