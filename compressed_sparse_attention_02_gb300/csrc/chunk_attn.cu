@@ -173,14 +173,18 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint3
       : "=r"(lo), "=r"(hi)
       : "r"(four));
 }
-// The nearest E4M3 codes of four values, the first in the low byte.
-__device__ __forceinline__ uint32_t to_e4m3x4(float x, float y, float z, float w) {
+// The nearest E4M3 codes of four f16 values, the first in the low byte.
+__device__ __forceinline__ uint32_t f16x4_to_e4m3(uint32_t xy, uint32_t zw) {
   uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
       "mov.b32 %0, {l, h};\n\t}"
       : "=r"(r)
-      : "f"(x), "f"(y), "f"(z), "f"(w));
+      : "r"(xy), "r"(zw));
   return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
+  const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
 }
 // Non-zero where a byte is a NaN code (magnitude 0x7F, which carries into the
 // byte's top bit).
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const ChunkAttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t order_full[kOrders], order_empty[kOrders], q_full, q_empty;
+  __shared__ uint64_t order_full[kOrders], order_empty[kOrders], q_full[2], q_empty;
   __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages], raw_full[C::kRawStages], raw_empty[C::kRawStages];
   __shared__ uint64_t v_full[C::kVStages], v_empty[C::kVStages], meta_full[C::kMeta];
   __shared__ uint64_t s_full[2], p_full[2], o_full[2], joined, left_off, drain;
@@ -371,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kTile);
       mbar_init(o_full + i, 1);
+      mbar_init(q_full + i, kConvThreads);
     }
-    mbar_init(&q_full, kConvThreads);
     mbar_init(&q_empty, kTileRows + 1);
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(k_full + i, 1);
@@ -635,20 +639,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // loop's values are uniform)
       constexpr uint32_t idesc_s = instr_desc(kTile, kTile, 0, 0, 0, 0);  // E4M3, K-major A and B
       constexpr uint32_t idesc_o = instr_desc(kTile, D, 0, 0, 0, 1);     // f16, A from TMEM, B (= V) MN-major
-      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // A descriptor's upper half is the same for all operands of a kind; its lower
+      // half is the address, for values the distance of their channel blocks too.
+      constexpr uint32_t kLineHi = static_cast<uint32_t>(1024 >> 4) | 1u << 14 | kSwizzle128B << 29;
+      constexpr uint32_t kKeyHi = D == 128 ? kLineHi : static_cast<uint32_t>(512 >> 4) | 1u << 14 | kSwizzle64B << 29;
+      constexpr uint32_t kValueLo = static_cast<uint32_t>(kTile * 128 >> 4) << 16;
+      auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+      auto desc = [](uint32_t hi, uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
+      const uint32_t tm = uniform(tmem), q_lo = uniform(smem_u32(q_s) >> 4);
+      const uint32_t k_lo = uniform(smem_u32(k_ring) >> 4), v_lo = uniform(smem_u32(v_ring) >> 4 | kValueLo);
       const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.status)) != 0;
       };
-      auto wait_k = [&](int n) { return wait(k_full + n % C::kKStages, (n / C::kKStages) & 1); };
-      auto wait_v = [&](int n) { return wait(v_full + n % C::kVStages, (n / C::kVStages) & 1); };
-      // S of half t with the queries of slot qs and block n (one lane)
-      auto s_of = [&](int t, int qs, int n) {
-        const uint64_t k_desc = D == 128
-                                    ? smem_desc(smem_u32(k_ring) + (n % C::kKStages) * C::kCodeBytes, 16, 1024, kSwizzle128B)
-                                    : smem_desc(smem_u32(k_ring) + (n % C::kKStages) * C::kCodeBytes, 16, 512, kSwizzle64B);
-        const uint64_t q_desc = smem_desc(smem_u32(q_s) + qs * C::kQBytes, 16, 1024, kSwizzle128B);
+      // S of half t with the queries of half qs and the keys at slot (one lane)
+      auto s_of = [&](int t, int qs, uint32_t slot) {
+        const uint32_t kl = k_lo + slot * (C::kCodeBytes >> 4), ql = q_lo + qs * (C::kQBytes >> 4);
         // the high parts' products, then the low ones': at width 64 both parts
         // are in one 128-byte line
         constexpr int kLow = D == 128 ? kTile * 128 >> 4 : 64 >> 4;
@@ -656,96 +662,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int s = 0; s < D / 32; ++s)
-            mma_f8(tm + C::kSCol(t), q_desc + part * kLow + 2 * s, k_desc + 2 * s, idesc_s, part + s > 0 ? 1u : 0u);
+            mma_f8(tm + C::kSCol(t), desc(kLineHi, ql + part * kLow + 2 * s), desc(kKeyHi, kl + 2 * s), idesc_s,
+                   part + s > 0 ? 1u : 0u);
         if (!skip_s) tc_commit(s_full + t);
       };
-      auto pv_of = [&](int t, int n, bool add) {
-        const uint64_t v_desc =
-            smem_desc(smem_u32(v_ring) + (n % C::kVStages) * C::kVBytes, kTile * 128, 1024, kSwizzle128B);
+      auto pv_of = [&](int t, uint32_t slot, bool add) {
+        const uint32_t vl = v_lo + slot * (C::kVBytes >> 4);
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
-          mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, v_desc + (16 * s * 128 >> 4), idesc_o,
-                     add || s > 0 ? 1u : 0u);
+          mma_f16_ts(tm + C::kOCol(t), tm + C::kSCol(t) + s * 8, desc(kLineHi, vl + (16 * s * 128 >> 4)), idesc_o,
+                     s > 0 ? 1u : add ? 1u : 0u);
       };
       bool ok = true;
-      int n0 = 0;               // blocks of the tiles before
-      uint32_t n_p[2] = {};     // weights taken so far, by half
+      uint32_t k_slot = 0, k_parity = 0, v_slot = 0, v_parity = 0, p_parity = 0;  // (p_parity: a bit a half)
+      auto wait_k = [&]() { return wait(k_full + k_slot, k_parity); };
+      auto next_k = [&]() {
+        if (++k_slot == C::kKStages) {
+          k_slot = 0;
+          k_parity ^= 1u;
+        }
+      };
+      auto next_v = [&]() {
+        if (++v_slot == C::kVStages) {
+          v_slot = 0;
+          v_parity ^= 1u;
+        }
+      };
       for (int item = 0; ok && take(item); ++item) {
-        const Order& o = orders[item % kOrders];
-        const int blocks = uniform(o.blocks);
-        const bool split = uniform(o.split) != 0;
+        const int blocks = static_cast<int>(uniform(orders[item % kOrders].blocks));
+        const bool split = uniform(orders[item % kOrders].split) != 0;
         done(item);
-        ok = wait(&q_full, item & 1);
+        ok = wait(q_full, item & 1);
         if (split) {
-          for (int t = 0; t < 2 && t < blocks && ok; ++t) {
-            ok = wait_k(n0 + t);
+          // blocks in turn to the halves, both with the queries of the first
+          if (ok) ok = wait(q_full + 1, item & 1);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= blocks || !ok) break;
+            ok = wait_k();
             tc_fence_after();
             if (ok && elect_one()) {
-              s_of(t, 0, n0 + t);
-              tc_commit(k_empty + (n0 + t) % C::kKStages);
-              if (t + 1 == blocks || t == 1)
-                if (blocks <= 2) tc_commit(&q_empty);
+              s_of(t, 0, k_slot);
+              tc_commit(k_empty + k_slot);
+              if (t + 1 == blocks || (t == 1 && blocks == 2)) tc_commit(&q_empty);
             }
             __syncwarp();
+            next_k();
           }
-          for (int it = 0; it < blocks && ok; ++it) {
-            const int t = it & 1;
-            const bool again = it + 2 < blocks;
-            ok = wait_v(n0 + it);
-            if (ok) ok = wait(p_full + t, n_p[t] & 1u);
-            if (ok && again) ok = wait_k(n0 + it + 2);
-            if (!ok) break;
-            ++n_p[t];
-            tc_fence_after();
-            if (elect_one()) {
-              pv_of(t, n0 + it, it >= 2);
-              if (!again) tc_commit(o_full + t);
-              tc_commit(v_empty + (n0 + it) % C::kVStages);
-              if (again) {
-                s_of(t, 0, n0 + it + 2);
-                tc_commit(k_empty + (n0 + it + 2) % C::kKStages);
-                if (it + 3 == blocks) tc_commit(&q_empty);
+          for (int it0 = 0; it0 < blocks && ok; it0 += 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int it = it0 + t;
+              if (it >= blocks || !ok) break;
+              const bool again = it + 2 < blocks;
+              ok = wait(v_full + v_slot, v_parity);
+              if (ok) ok = wait(p_full + t, p_parity >> t & 1u);
+              if (ok && again) ok = wait_k();
+              if (!ok) break;
+              p_parity ^= 1u << t;
+              tc_fence_after();
+              if (elect_one()) {
+                pv_of(t, v_slot, it >= 2);
+                if (!again) tc_commit(o_full + t);
+                tc_commit(v_empty + v_slot);
+                if (again) {
+                  s_of(t, 0, k_slot);
+                  tc_commit(k_empty + k_slot);
+                  if (it + 3 == blocks) tc_commit(&q_empty);
+                }
               }
+              __syncwarp();
+              next_v();
+              if (again) next_k();
             }
-            __syncwarp();
           }
         } else {
-          if (ok) ok = wait_k(n0);
+          if (ok) ok = wait_k();
+          tc_fence_after();
+          if (ok && elect_one()) s_of(0, 0, k_slot);
+          __syncwarp();
+          if (ok) ok = wait(q_full + 1, item & 1);
           tc_fence_after();
           if (ok && elect_one()) {
-            s_of(0, 0, n0);
-            s_of(1, 1, n0);
-            tc_commit(k_empty + n0 % C::kKStages);
+            s_of(1, 1, k_slot);
+            tc_commit(k_empty + k_slot);
             if (blocks == 1) tc_commit(&q_empty);
           }
           __syncwarp();
+          next_k();
           for (int it = 0; it < blocks && ok; ++it) {
             const bool again = it + 1 < blocks;
-            ok = wait_v(n0 + it);
-            if (ok && again) ok = wait_k(n0 + it + 1);
+            ok = wait(v_full + v_slot, v_parity);
+            if (ok && again) ok = wait_k();
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              if (ok) ok = wait(p_full + t, n_p[t] & 1u);
+              if (ok) ok = wait(p_full + t, p_parity >> t & 1u);
               if (!ok) break;
-              ++n_p[t];
+              p_parity ^= 1u << t;
               tc_fence_after();
               if (elect_one()) {
-                pv_of(t, n0 + it, it > 0);
+                pv_of(t, v_slot, it > 0);
                 if (!again) tc_commit(o_full + t);
-                if (t == 1) tc_commit(v_empty + (n0 + it) % C::kVStages);
+                if (t == 1) tc_commit(v_empty + v_slot);
                 if (again) {
-                  s_of(t, t, n0 + it + 1);
+                  s_of(t, t, k_slot);
                   if (t == 1) {
-                    tc_commit(k_empty + (n0 + it + 1) % C::kKStages);
+                    tc_commit(k_empty + k_slot);
                     if (it + 2 == blocks) tc_commit(&q_empty);
                   }
                 }
               }
               __syncwarp();
             }
+            next_v();
+            if (again) next_k();
           }
         }
-        n0 += blocks;
       }
       // whatever was issued finishes before TMEM and shared memory are released
       if (elect_one()) {
@@ -770,72 +802,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // a thread's 16 channels of its rows are copied to where their two parts
       // will be, and turned into these in place
-      const int halves = o.split ? 1 : 2;
       auto q_at = [&](int h, int r, int part) {
         uint8_t* line = q_s + h * C::kQBytes + r * 128;
         return D == 128 ? line + part * (kTile * 128) + ((c ^ (r & 7)) << 4) : line + (((c + 4 * part) ^ (r & 7)) << 4);
       };
+      const int halves = o.split ? 1 : 2, step_q = kRowsAtOnce / group, step_h = kRowsAtOnce - step_q * group;
       for (int h = 0; h < halves; ++h) {
-#pragma unroll 4
-        for (int k = 0; k < kChunks; ++k) {
-          const int r = r0 + k * kRowsAtOnce, rr = h * kTile + r;
-          const bool there = rr < o.rows;
-          const uint32_t at = static_cast<uint32_t>(o.row0 + rr), qi = at / group;
-          const uint16_t* src = a.q;
-          if (there)
-            src += static_cast<int64_t>(o.q0 + static_cast<int>(qi)) * a.q_stride +
-                   (o.head0 + static_cast<int>(at - qi * group)) * a.q_stride_h + c * 16;
-          cp_async_16_or_zero(smem_u32(q_at(h, r, 0)), src, there);
-          cp_async_16_or_zero(smem_u32(q_at(h, r, 1)), src + 8, there);
-        }
-      }
-      cp_async_commit_wait_all();
-      for (int h = 0; h < halves; ++h) {
-#pragma unroll 2
+        const uint32_t at = static_cast<uint32_t>(o.row0 + h * kTile + r0);
+        int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
+#pragma unroll
         for (int k = 0; k < kChunks; ++k) {
           const int r = r0 + k * kRowsAtOnce;
-          uint4* part[2] = {reinterpret_cast<uint4*>(q_at(h, r, 0)), reinterpret_cast<uint4*>(q_at(h, r, 1))};
-          float x[16];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float y[8];
-            unpack_bf16(*part[i], y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[8 * i + j] = y[j];
+          const bool there = h * kTile + r < o.rows;
+          const uint16_t* src = a.q;
+          if (there) src += static_cast<int64_t>(o.q0 + qi) * a.q_stride + (o.head0 + hd) * a.q_stride_h + c * 16;
+          cp_async_16_or_zero(smem_u32(q_at(h, r, 0)), src, there);
+          cp_async_16_or_zero(smem_u32(q_at(h, r, 1)), src + 8, there);
+          qi += step_q;
+          hd += step_h;
+          if (hd >= group) {
+            hd -= group;
+            ++qi;
           }
-          // the largest magnitude; a value that is not finite shows as one past all others
-          float top = 0.f;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]) <= FLT_MAX ? fabsf(x[j]) : INFINITY);
-#pragma unroll
-          for (int off = 1; off < kChunks; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          const bool finite = top <= FLT_MAX;
-          const int e = min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 126);
-          const float up = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.f;
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = x[4 * j + i] * up;
-            hi[j] = to_e4m3x4(y[0], y[1], y[2], y[3]);
-            uint32_t h01, h23;
-            e4m3x4_to_f16(hi[j], h01, h23);
-            const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-            const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-            lo[j] = to_e4m3x4(y[0] - f01.x, y[1] - f01.y, y[2] - f23.x, y[3] - f23.y);
-            if (!finite) {
-              hi[j] = 0x7F7F7F7Fu;
-              lo[j] = 0u;
-            }
-          }
-          *part[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *part[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (c == 0) q_scale_s[h][r] = finite ? scale2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
         }
+        cp_async_commit();
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&q_full);
+      for (int h = 0; h < 2; ++h) {
+        if (h < halves) {
+          cp_async_wait_pending(halves - 1 - h);
+#pragma unroll 4
+          for (int k = 0; k < kChunks; ++k) {
+            const int r = r0 + k * kRowsAtOnce;
+            uint4* part[2] = {reinterpret_cast<uint4*>(q_at(h, r, 0)), reinterpret_cast<uint4*>(q_at(h, r, 1))};
+            const uint4 u = *part[0], v = *part[1];
+            const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            // the largest magnitude, two at a time as whole numbers (past 0x7F7F: not finite)
+            uint32_t both = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) both = __vmaxu2(both, w[j] & 0x7FFF7FFFu);
+#pragma unroll
+            for (int off = 1; off < kChunks; off <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, off));
+            const uint32_t top = max(both & 0xFFFFu, both >> 16);
+            const bool finite = top < 0x7F80u;
+            const int e = min(7 - (static_cast<int>(top >> 7) - 127), 126);
+            const float up = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 0.f;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // (exact in f16 but for what is below both parts)
+              const uint32_t y01 = pack_f16(__uint_as_float(w[2 * j] << 16) * up, __uint_as_float(w[2 * j] & 0xFFFF0000u) * up);
+              const uint32_t y23 =
+                  pack_f16(__uint_as_float(w[2 * j + 1] << 16) * up, __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * up);
+              hi[j] = f16x4_to_e4m3(y01, y23);
+              uint32_t h01, h23;
+              e4m3x4_to_f16(hi[j], h01, h23);
+              lo[j] = f16x4_to_e4m3(sub_f16x2(y01, h01), sub_f16x2(y23, h23));
+              if (!finite) {
+                hi[j] = 0x7F7F7F7Fu;
+                lo[j] = 0u;
+              }
+            }
+            *part[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *part[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (c == 0) q_scale_s[h][r] = finite ? scale2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(q_full + h);
+      }
       const int odd = item % 3;
       int n_masked = 0;
       odd_rows[odd][cw][lane >> 2][lane & 3] = 0u;  // (the tile three before, whose places these were, is done with)
@@ -921,10 +954,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int item = 0; ok && take(item); ++item) {
       const Order& o = orders[item % kOrders];
-      ok = __all_sync(0xffffffffu, wait_or_abort(&q_full, item & 1, abort_flag, a.status));
-      if (!ok) break;
       const bool split = o.split != 0;
       const int half = split ? 0 : t;                    // of the queries
+      ok = __all_sync(0xffffffffu, wait_or_abort(q_full + half, item & 1, abort_flag, a.status));
+      if (!ok) break;
       const int row = half * kTile + r;                  // in the tile
       const float fac = q_scale_s[half][r];
       mbar_arrive(&q_empty);
