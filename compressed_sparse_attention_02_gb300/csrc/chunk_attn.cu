@@ -62,10 +62,10 @@ constexpr float kNone = -1e30f;             // running maximum before the first 
 constexpr int kMaxMasked = 8;
 // What a tile costs, in the units of the shares: a block for two halves, for
 // one, and the tile itself.
-constexpr int kCostTwo = 3, kCostOne = 2, kCostTile = 4;
+constexpr int kCostTwo = 3, kCostOne = 2, kCostTile = 16;
 
 // Registers a thread: 512 threads are launched with 128 each.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvRegs = 56, kOtherRegs = 56;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvRegs = 48, kOtherRegs = 64;
 static_assert(2 * kSoftmaxRegs + kConvRegs + kOtherRegs <= 4 * kLaunchRegs, "registers of the block");
 
 template <int D>
@@ -116,9 +116,9 @@ struct Tile {
   int rows, lo, hi;  // keys [lo, hi)
   int j_hi, blocks;  // blocks j_hi - 1 downwards; one at least
   __device__ __forceinline__ int unit() const { return rows > kTile ? kCostTwo : kCostOne; }
-  __device__ __forceinline__ int64_t cost() const { return kCostTile + static_cast<int64_t>(unit()) * blocks; }
+  __device__ __forceinline__ int cost() const { return kCostTile + unit() * blocks; }  // (blocks: below 2^23)
 };
-__device__ __forceinline__ Tile tile_of(const Seq& s, int group, int window, int t) {
+__device__ __noinline__ Tile tile_of(const Seq& s, int group, int window, int t) {
   Tile x;
   const uint32_t row0 = static_cast<uint32_t>(t) * kTileRows, all = static_cast<uint32_t>(s.n) * group;
   x.rows = static_cast<int>(min(all - row0, static_cast<uint32_t>(kTileRows)));
@@ -201,6 +201,41 @@ __device__ __forceinline__ void landed(uint32_t (&r)[32]) {
                :);
 }
 
+// x, as something that the compiler cannot move out of a loop: it would copy the
+// loop for each value (the loading warps' loop had 25 KB of code, the product
+// warp's as much), and the kernel's hot code has to fit the instruction caches.
+__device__ __forceinline__ bool here(bool x) {
+  uint32_t y = x ? 1u : 0u;
+  asm volatile("" : "+r"(y));
+  return y != 0u;
+}
+
+// wait_or_abort in few instructions, its limit (ns) in shared memory: with all
+// waits in full and all loops unrolled the kernel's code was 160 KB, and the
+// softmax waited for its instructions.
+struct Watch {
+  volatile int abort;
+  uint32_t limit;
+  unsigned* status;
+};
+__device__ __forceinline__ uint32_t timer_low() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Watch* w) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = timer_low();
+  while (w->abort == 0) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (timer_low() - t0 > w->limit) {
+      record_error(w->status, kErrTimeout);
+      w->abort = 1;
+    }
+  }
+  return false;
+}
+
 // What every CTA finds out first: its share of the line, and where it begins.
 struct Start {
   int64_t per, total, offset;  // offset: units of sequence b before the share's first
@@ -210,13 +245,14 @@ struct Start {
 // The cost of a sequence's tiles of one key head, and the largest row of q that
 // sequences whose offsets are right reach, by every thread of a warp for its own
 // sequence.  Sequences with more than two tiles are summed up by the whole warp.
-__device__ __forceinline__ int64_t head_cost(const Seq& s, int group, int window) {
+__device__ __noinline__ int64_t head_cost(const Seq& s, int group, int window) {
   const int tiles = tiles_of(s, group), lane = threadIdx.x & 31;
   int64_t c = 0;
   if (tiles > 0 && tiles <= 2) {
     c = tile_of(s, group, window, 0).cost();
     if (tiles == 2) c += tile_of(s, group, window, 1).cost();
   }
+#pragma unroll 1
   for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
     const int from = __ffs(many) - 1;
     Seq x;
@@ -225,6 +261,7 @@ __device__ __forceinline__ int64_t head_cost(const Seq& s, int group, int window
     x.len = __shfl_sync(0xffffffffu, s.len, from);
     const int nt = __shfl_sync(0xffffffffu, tiles, from);
     int64_t sum = 0;
+#pragma unroll 1
     for (int t = lane; t < nt; t += 32) sum += tile_of(x, group, window, t).cost();
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -233,16 +270,21 @@ __device__ __forceinline__ int64_t head_cost(const Seq& s, int group, int window
   return c;
 }
 
+// (64-bit divisions are long: one copy for all)
+__device__ __noinline__ int64_t quotient(int64_t x, int64_t y) { return x / y; }
+
 // Walks the tiles of a share; one warp.
 struct Walker {
   Seq s;
   int b, top, head, t, tiles;
-  int64_t x0, left, tile_at;  // units of the tile before the share, units to go, the tile's place on the line
+  int x0;                 // units of the tile before the share
+  int64_t left, tile_at;  // units to go, the tile's place on the line
   Tile tile;
 
   // The sequence from b on that has rows; false: none.
-  __device__ __forceinline__ bool seek(const ChunkAttnArgs& a) {
+  __device__ __noinline__ bool seek(const ChunkAttnArgs& a) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
     for (; b < a.B; b += 32) {
       Seq mine = {0, 0, 0};
       if (b + lane < a.B) mine = read_seq(a, b + lane);
@@ -282,9 +324,10 @@ struct Walker {
     Seq one = {0, 0, 0};
     if (lane == 0) one = s;
     const int64_t per_head = __shfl_sync(0xffffffffu, head_cost(one, group, a.window), 0);
-    head = static_cast<int>(st.offset / per_head);
-    x0 = st.offset - head * per_head;
-    for (t = 0; t < tiles; t += 32) {  // the tile that x0 lies in
+    head = static_cast<int>(quotient(st.offset, per_head));
+    int64_t at = st.offset - head * per_head;  // units of the head's tiles before the share
+#pragma unroll 1
+    for (t = 0; t < tiles; t += 32) {  // the tile that it begins in
       const int64_t c = t + lane < tiles ? tile_of(s, group, a.window, t + lane).cost() : 0;
       int64_t x = c;
 #pragma unroll
@@ -292,16 +335,17 @@ struct Walker {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
         if (lane >= off) x += y;
       }
-      const unsigned in = __ballot_sync(0xffffffffu, x > x0);
+      const unsigned in = __ballot_sync(0xffffffffu, x > at);
       if (in) {
         const int from = __ffs(in) - 1;
-        x0 -= __shfl_sync(0xffffffffu, x - c, from);
+        at -= __shfl_sync(0xffffffffu, x - c, from);
         t += from;
         break;
       }
-      x0 -= __shfl_sync(0xffffffffu, x, 31);
+      at -= __shfl_sync(0xffffffffu, x, 31);
     }
     tile = tile_of(s, group, a.window, t);
+    x0 = static_cast<int>(at);
     tile_at = blockIdx.x * st.per - x0;
     return true;
   }
@@ -325,11 +369,10 @@ struct Walker {
 };
 
 // The block, counted from the tile's first, at or behind place x of a tile.
-__device__ __forceinline__ int block_at(const Tile& t, int64_t x) {
-  const int64_t y = x - kCostTile, u = t.unit();
-  return y <= 0 ? 0 : static_cast<int>((y + u - 1) / u);
+__device__ __forceinline__ int block_at(const Tile& t, int x) {
+  const int y = max(x - kCostTile, 0);
+  return t.rows > kTile ? (y + kCostTwo - 1) / kCostTwo : (y + kCostOne - 1) / kCostOne;
 }
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -352,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t odd_rows[3][4][kMaxMasked][4];
   __shared__ int odd_block[3][4][kMaxMasked], odd_item[3][4];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_s;
+  __shared__ Watch watch;
   __shared__ int64_t sum_sh[kThreads / 32];
   __shared__ int max_sh[kThreads / 32];
   __shared__ Start start_s;
@@ -365,12 +408,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.n_heads / a.cache.n_kv_heads;
-  volatile int* abort_flag = &abort_s;
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < kOrders; ++i) {
       mbar_init(order_full + i, 1);
       mbar_init(order_empty + i, kThreads / 32 - 1);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kTile);
@@ -378,25 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full + i, kConvThreads);
     }
     mbar_init(&q_empty, kTileRows + 1);
+#pragma unroll 1
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < C::kRawStages; ++i) {
       mbar_init(raw_full + i, 1);
       mbar_init(raw_empty + i, kConvThreads);
     }
+#pragma unroll 1
     for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(v_full + i, kConvThreads);
       mbar_init(v_empty + i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < C::kMeta; ++i) mbar_init(meta_full + i, 1);
     mbar_init(&joined, kTileRows);
     mbar_init(&left_off, kTileRows);
     mbar_init(&drain, 1);
     fence_mbar_init();
-    abort_s = 0;
+    watch.abort = 0;
+    watch.limit = static_cast<uint32_t>(min(wait_limit_ns(a.status), static_cast<uint64_t>(4000000000u)));
+    watch.status = a.status;
     start_s.b = -1;
+#pragma unroll 1
     for (int i = 0; i < 12; ++i) odd_item[i >> 2][i & 3] = 0;
   }
   if (warp == kKeyWarp && lane == 0) prefetch_tensormap(&tm_k);
@@ -412,9 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // pass for the total first
   {
     int64_t per = 1, total = 0;
+#pragma unroll 1
     for (int pass = a.B > kThreads ? 0 : 1; pass < 2; ++pass) {
       int64_t base = 0;
       int top = 0;  // rows of q that sequences so far reach
+#pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         Seq s = {0, 0, 0};
@@ -429,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         int before_top = __shfl_up_sync(0xffffffffu, end, 1), through = top;
         before_top = lane == 0 ? top : max(before_top, top);
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < kThreads / 32; ++k) {
           const int y = max_sh[k];
           if (k < warp) before_top = max(before_top, y);
@@ -447,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31) sum_sh[warp] = x;
         __syncthreads();
         int64_t before = base + x - n;
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < kThreads / 32; ++k) {
           const int64_t y = sum_sh[k];
           if (k < warp) before += y;
@@ -456,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.B <= kThreads) total = base;
         if (pass == 1) {
           // (a share holds a block at least, so that no CTA between a tile's first and last has none)
-          per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kCostTwo));
+          per = max(quotient(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(kCostTwo));
           const int64_t target = blockIdx.x * per;
           if (target >= before && target < before + n) {  // one thread at most
             start_s.b = b;
@@ -482,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the next tile, of every warp but the walking one (read where it lies, until
   // `done` with it); false at the end and after an abort
   auto take = [&](int item) {
-    const bool ok = wait_or_abort(order_full + item % kOrders, (item / kOrders) & 1, abort_flag, a.status);
+    const bool ok = await(order_full + item % kOrders, (item / kOrders) & 1, &watch);
     return __all_sync(0xffffffffu, ok) && orders[item % kOrders].there != 0;
   };
   auto done = [&](int item) {
@@ -498,10 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Start st = start_s;
       bool there = st.b >= 0 && w.begin(a, st, group), ok = true;
       Cut cut = {};
+#pragma unroll 1
       for (int item = 0; ok; ++item) {
         Order o = {};
         while (there) {
-          const int64_t x1 = min(w.tile.cost(), w.x0 + w.left);
+          const int x1 = static_cast<int>(min(static_cast<int64_t>(w.tile.cost()), w.x0 + w.left));
           const int k0 = block_at(w.tile, w.x0), k1 = block_at(w.tile, x1);
           const bool last_one = x1 - w.x0 == w.left;
           if (k1 > k0) {
@@ -530,8 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cut.head0 = o.head0;
               cut.rows = o.rows;
               cut.first = blockIdx.x;
-              cut.last = static_cast<int>(
-                  (w.tile_at + kCostTile + static_cast<int64_t>(t.unit()) * (t.blocks - 1)) / st.per);
+              cut.last = static_cast<int>(quotient(w.tile_at + kCostTile + t.unit() * (t.blocks - 1), st.per));
             }
           }
           w.left -= x1 - w.x0;
@@ -540,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
           if (item >= kOrders)
-            ok = wait_or_abort(order_empty + item % kOrders, (item / kOrders - 1) & 1, abort_flag, a.status);
+            ok = await(order_empty + item % kOrders, (item / kOrders - 1) & 1, &watch);
           if (ok) {
             orders[item % kOrders] = o;
             mbar_arrive(order_full + item % kOrders);
@@ -562,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0, slot = 0, meta = 0;  // blocks so far, their places
       uint32_t parity = 1;            // of the phase before the slot's
       bool ok = true;
+#pragma unroll 1
       for (int item = 0; ok && take(item); ++item) {
         const Order& o = orders[item % kOrders];
         const int blocks = o.blocks, j_top = o.j_top, lo = o.lo, hi = o.hi, kv_head = o.kv_head;
@@ -576,29 +630,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto in_pool = [&](int32_t page) { return page >= 0 && page < a.cache.n_pages; };
         auto scale = [&](int32_t page, const float* of, float none) {
-          return keys && in_pool(page) ? __ldg(of + static_cast<int64_t>(page) * a.cache.n_kv_heads + kv_head) : none;
+          return here(keys) && in_pool(page) ? __ldg(of + static_cast<int64_t>(page) * a.cache.n_kv_heads + kv_head) : none;
         };
         const bool first_of_page = ((16 * g) & (a.cache.page - 1)) == 0;
         int32_t page = entry(0), next = entry(4);
         float ks = scale(page, a.cache.k_scale, 1.f), vs = scale(page, a.cache.v_scale, 0.f);
+#pragma unroll 1
         for (int q0 = 0; q0 < blocks && ok; q0 += 4) {
           const int32_t after = entry(q0 + 8);
           if (in_pool(next) && first_of_page) tma_prefetch_3d(tm, 0, kv_head << ps, next);
           const float ks_next = scale(next, a.cache.k_scale, 1.f), vs_next = scale(next, a.cache.v_scale, 0.f);
           const bool in = in_pool(page);
           const unsigned bads = __ballot_sync(0xffffffffu, page != kNotNeeded && !in);
-          if (bads && keys) record_error(a.status, kErrIndexRange);
+          if (bads && here(keys)) record_error(a.status, kErrIndexRange);
           const float lv = in ? __log2f(vs) : 1e30f;
           float least = lv;
 #pragma unroll
           for (int off = 1; off < 8; off <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
           const unsigned copies = __ballot_sync(0xffffffffu, in && first_of_page);
           const int n_q = min(4, blocks - q0);
+#pragma unroll 1
           for (int i = 0; i < n_q; ++i) {
             const bool mine = (lane >> 3) == i;
-            if (n >= stages) ok = __all_sync(0xffffffffu, wait_or_abort(empty + slot, parity, abort_flag, a.status));
+            if (n >= stages) ok = __all_sync(0xffffffffu, await(empty + slot, parity, &watch));
             if (!ok) break;
-            if (keys) {
+            if (here(keys)) {
               if (mine) {
                 k_scale_s[meta][g] = ks;
                 v_log_s[meta][g] = lv;
@@ -631,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         done(item);
       }
       if (lane == 0)  // every copy lands before the CTA ends (also after an abort)
+#pragma unroll 1
         for (int k = max(0, n - stages); k < n; ++k) mbar_wait(full + k % stages, (k / stages) & 1, a.status);
       __syncwarp();
     } else {
@@ -650,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_lo = uniform(smem_u32(k_ring) >> 4), v_lo = uniform(smem_u32(v_ring) >> 4 | kValueLo);
       const bool skip_s = test_fault(a.status, kFaultAttn);  // test fault: S is never announced
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.status)) != 0;
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+               __all_sync(0xffffffffu, await(bar, parity, &watch));
       };
       // S of half t with the queries of half qs and the keys at slot (one lane)
       auto s_of = [&](int t, int qs, uint32_t slot) {
@@ -675,7 +733,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool ok = true;
       uint32_t k_slot = 0, k_parity = 0, v_slot = 0, v_parity = 0, p_parity = 0;  // (p_parity: a bit a half)
-      auto wait_k = [&]() { return wait(k_full + k_slot, k_parity); };
       auto next_k = [&]() {
         if (++k_slot == C::kKStages) {
           k_slot = 0;
@@ -688,92 +745,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           v_parity ^= 1u;
         }
       };
+#pragma unroll 1
       for (int item = 0; ok && take(item); ++item) {
-        const int blocks = static_cast<int>(uniform(orders[item % kOrders].blocks));
+        // The halves take turns, a step each: all blocks each, or, where they share
+        // them out, a block a step with the queries of the first half.
         const bool split = uniform(orders[item % kOrders].split) != 0;
+        const int steps = static_cast<int>(uniform(orders[item % kOrders].blocks)) << (split ? 0 : 1);
         done(item);
-        ok = wait(q_full, item & 1);
-        if (split) {
-          // blocks in turn to the halves, both with the queries of the first
-          if (ok) ok = wait(q_full + 1, item & 1);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t >= blocks || !ok) break;
-            ok = wait_k();
-            tc_fence_after();
-            if (ok && elect_one()) {
-              s_of(t, 0, k_slot);
-              tc_commit(k_empty + k_slot);
-              if (t + 1 == blocks || (t == 1 && blocks == 2)) tc_commit(&q_empty);
-            }
-            __syncwarp();
-            next_k();
-          }
-          for (int it0 = 0; it0 < blocks && ok; it0 += 2) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int it = it0 + t;
-              if (it >= blocks || !ok) break;
-              const bool again = it + 2 < blocks;
-              ok = wait(v_full + v_slot, v_parity);
-              if (ok) ok = wait(p_full + t, p_parity >> t & 1u);
-              if (ok && again) ok = wait_k();
-              if (!ok) break;
-              p_parity ^= 1u << t;
-              tc_fence_after();
-              if (elect_one()) {
-                pv_of(t, v_slot, it >= 2);
-                if (!again) tc_commit(o_full + t);
-                tc_commit(v_empty + v_slot);
-                if (again) {
-                  s_of(t, 0, k_slot);
-                  tc_commit(k_empty + k_slot);
-                  if (it + 3 == blocks) tc_commit(&q_empty);
-                }
-              }
-              __syncwarp();
-              next_v();
-              if (again) next_k();
-            }
-          }
-        } else {
-          if (ok) ok = wait_k();
-          tc_fence_after();
-          if (ok && elect_one()) s_of(0, 0, k_slot);
-          __syncwarp();
-          if (ok) ok = wait(q_full + 1, item & 1);
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+          ok = wait(q_full + t, item & 1);
+          if (t >= steps) break;
+          if (ok && (here(split) || t == 0)) ok = wait(k_full + k_slot, k_parity);
           tc_fence_after();
           if (ok && elect_one()) {
-            s_of(1, 1, k_slot);
-            tc_commit(k_empty + k_slot);
-            if (blocks == 1) tc_commit(&q_empty);
+            s_of(t, here(split) ? 0 : t, k_slot);
+            if (here(split) || t == 1) tc_commit(k_empty + k_slot);
+            if (steps <= t + 1 || (t == 1 && steps == 2)) tc_commit(&q_empty);
           }
           __syncwarp();
-          next_k();
-          for (int it = 0; it < blocks && ok; ++it) {
-            const bool again = it + 1 < blocks;
+          if (here(split) || t == 1) next_k();
+        }
+#pragma unroll 1
+        for (int i = 0; i < steps && ok; ++i) {
+          const int t = i & 1;
+          const bool again = i + 2 < steps, last_of_block = here(split) || t == 1;
+          if (here(split) || t == 0) {
             ok = wait(v_full + v_slot, v_parity);
-            if (ok && again) ok = wait_k();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (ok) ok = wait(p_full + t, p_parity >> t & 1u);
-              if (!ok) break;
-              p_parity ^= 1u << t;
-              tc_fence_after();
-              if (elect_one()) {
-                pv_of(t, v_slot, it > 0);
-                if (!again) tc_commit(o_full + t);
-                if (t == 1) tc_commit(v_empty + v_slot);
-                if (again) {
-                  s_of(t, t, k_slot);
-                  if (t == 1) {
-                    tc_commit(k_empty + k_slot);
-                    if (it + 2 == blocks) tc_commit(&q_empty);
-                  }
-                }
-              }
-              __syncwarp();
+            if (ok && again) ok = wait(k_full + k_slot, k_parity);
+          }
+          if (ok) ok = wait(p_full + t, p_parity >> t & 1u);
+          if (!ok) break;
+          p_parity ^= 1u << t;
+          tc_fence_after();
+          if (elect_one()) {
+            pv_of(t, v_slot, i >= 2);
+            if (!again) tc_commit(o_full + t);
+            if (last_of_block) tc_commit(v_empty + v_slot);
+            if (again) {
+              s_of(t, here(split) ? 0 : t, k_slot);
+              if (last_of_block) tc_commit(k_empty + k_slot);
+              if (i + 3 == steps) tc_commit(&q_empty);
             }
+          }
+          __syncwarp();
+          if (last_of_block) {
             next_v();
             if (again) next_k();
           }
@@ -796,9 +812,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale2 = a.sm_scale * kLog2e;
     int n0 = 0;
     bool ok = true;
+#pragma unroll 1
     for (int item = 0; ok && take(item); ++item) {
       const Order& o = orders[item % kOrders];
-      if (item > 0) ok = __all_sync(0xffffffffu, wait_or_abort(&q_empty, (item - 1) & 1, abort_flag, a.status));
+      if (item > 0) ok = __all_sync(0xffffffffu, await(&q_empty, (item - 1) & 1, &watch));
       if (!ok) break;
       // a thread's 16 channels of its rows are copied to where their two parts
       // will be, and turned into these in place
@@ -807,10 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return D == 128 ? line + part * (kTile * 128) + ((c ^ (r & 7)) << 4) : line + (((c + 4 * part) ^ (r & 7)) << 4);
       };
       const int halves = o.split ? 1 : 2, step_q = kRowsAtOnce / group, step_h = kRowsAtOnce - step_q * group;
+#pragma unroll 1
       for (int h = 0; h < halves; ++h) {
         const uint32_t at = static_cast<uint32_t>(o.row0 + h * kTile + r0);
         int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
-#pragma unroll
+#pragma unroll 1  // (code that runs once a tile waits for its instructions)
         for (int k = 0; k < kChunks; ++k) {
           const int r = r0 + k * kRowsAtOnce;
           const bool there = h * kTile + r < o.rows;
@@ -827,10 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cp_async_commit();
       }
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         if (h < halves) {
           cp_async_wait_pending(halves - 1 - h);
-#pragma unroll 4
+#pragma unroll 1
           for (int k = 0; k < kChunks; ++k) {
             const int r = r0 + k * kRowsAtOnce;
             uint4* part[2] = {reinterpret_cast<uint4*>(q_at(h, r, 0)), reinterpret_cast<uint4*>(q_at(h, r, 1))};
@@ -874,13 +893,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       odd_rows[odd][cw][lane >> 2][lane & 3] = 0u;  // (the tile three before, whose places these were, is done with)
       static_assert(kMaxMasked * 4 == 32, "a word a lane");
       __syncwarp();
+#pragma unroll 1
       for (int q = 0; q < o.blocks && ok; ++q) {
         const int n = n0 + q, j = o.j_top - q;
         const int raw_slot = n % C::kRawStages, v_slot = n % C::kVStages, meta = n % C::kMeta;
-        ok = wait_or_abort(meta_full + meta, (n / C::kMeta) & 1, abort_flag, a.status) &&
-             wait_or_abort(raw_full + raw_slot, (n / C::kRawStages) & 1, abort_flag, a.status);
+        ok = await(meta_full + meta, (n / C::kMeta) & 1, &watch) &&
+             await(raw_full + raw_slot, (n / C::kRawStages) & 1, &watch);
         if (ok && n >= C::kVStages)
-          ok = wait_or_abort(v_empty + v_slot, (n / C::kVStages - 1) & 1, abort_flag, a.status);
+          ok = await(v_empty + v_slot, (n / C::kVStages - 1) & 1, &watch);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint8_t* raw = raw_ring + raw_slot * C::kCodeBytes;
@@ -896,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = r0 + (k0 + i) * kRowsAtOnce;
             u[i] = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
           }
-          if (masked || bad) {
+          if (here(masked || bad)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = r0 + (k0 + i) * kRowsAtOnce;
@@ -952,11 +972,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n_s = 0, n_o[2] = {}, n_split = 0;  // scores and sums taken so far, tiles whose halves were joined
     int n0 = 0;
     bool ok = true;
+#pragma unroll 1
     for (int item = 0; ok && take(item); ++item) {
       const Order& o = orders[item % kOrders];
       const bool split = o.split != 0;
       const int half = split ? 0 : t;                    // of the queries
-      ok = __all_sync(0xffffffffu, wait_or_abort(q_full + half, item & 1, abort_flag, a.status));
+      ok = __all_sync(0xffffffffu, await(q_full + half, item & 1, &watch));
       if (!ok) break;
       const int row = half * kTile + r;                  // in the tile
       const float fac = q_scale_s[half][r];
@@ -969,9 +990,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = kNone, mv = kNone, l = 0.f;
       const int step = split ? 2 : 1;
       bool began = false;
+#pragma unroll 1
       for (int q = split ? t : 0; q < o.blocks; q += step) {
         const int n = n0 + q, j = o.j_top - q, meta = n % C::kMeta;
-        ok = wait_or_abort(meta_full + meta, (n / C::kMeta) & 1, abort_flag, a.status);
+        ok = await(meta_full + meta, (n / C::kMeta) & 1, &watch);
         float cf[kGroups], lv[kGroups];  // the groups' factors and value scales (log2)
         {
           const float4 x = *reinterpret_cast<const float4*>(&k_scale_s[meta][0]);
@@ -988,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float v_min = v_min_s[meta];
         const uint32_t bad = bad_s[meta];
-        ok = ok && wait_or_abort(s_full + t, n_s & 1u, abort_flag, a.status);
+        ok = ok && await(s_full + t, n_s & 1u, &watch);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++n_s;
@@ -1112,11 +1134,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mv_s[t][r] = mv;
         l_s[t][r] = l;
         mbar_arrive(&joined);
-        ok = wait_or_abort(&joined, n_split & 1u, abort_flag, a.status) &&
-             wait_or_abort(o_full + 0, n_o[0] & 1u, abort_flag, a.status);
-        if (ok && have[1]) ok = wait_or_abort(o_full + 1, n_o[1] & 1u, abort_flag, a.status);
+        ok = await(&joined, n_split & 1u, &watch) &&
+             await(o_full + 0, n_o[0] & 1u, &watch);
+        if (ok && have[1]) ok = await(o_full + 1, n_o[1] & 1u, &watch);
       } else {
-        ok = wait_or_abort(o_full + t, n_o[t] & 1u, abort_flag, a.status);
+        ok = await(o_full + t, n_o[t] & 1u, &watch);
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -1154,6 +1176,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the halves of a split tile take half of the channels each
       const int c_lo = split ? t * (D / 32) : 0, c_hi = split ? (t + 1) * (D / 32) : D / 16;
       const uint32_t oa = split ? tmem + lane_base + C::kOCol(0) : o_tmem, ob = tmem + lane_base + C::kOCol(1);
+      const uint64_t f00 = pair_of(f0, f0), f11 = pair_of(f1, f1);
+      // where the row that a lane stores goes: two lanes a row, 16 rows at a time
+      int64_t to[2];
+      bool in[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rr = 16 * k + (lane >> 1);
+        to[k] = __shfl_sync(0xffffffffu, out_row, rr) * D + 8 * (lane & 1);
+        in[k] = half * kTile + (warp & 3) * 32 + rr < o.rows;
+      }
+      const int swap = (lane >> 2) & 1;  // (the 16-byte places of every second four rows are exchanged)
+      uint8_t* mine = stage + lane * 32;
+      const uint8_t* theirs = stage + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4);
 #pragma unroll 1
       for (int c = c_lo; c < c_hi; ++c) {
         uint32_t x[16], y[16];
@@ -1161,12 +1196,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (split && have[1]) tmem_ld16(ob + 16 * c, y);
         tmem_wait_ld();
         float z[16];
+        uint64_t zz[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          z[k] = __uint_as_float(x[k]) * f0;
-          if (split && have[1]) z[k] = fmaf(__uint_as_float(y[k]), f1, z[k]);
+        for (int k = 0; k < 8; ++k) zz[k] = mul2(pair_of(x[2 * k], x[2 * k + 1]), f00);
+        if (split && have[1]) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) zz[k] = fma2(pair_of(y[2 * k], y[2 * k + 1]), f11, zz[k]);
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) csa::split(zz[k], &z[2 * k], &z[2 * k + 1]);
         if (any_odd && writes) {
+#pragma unroll 1
           for (int e = 0; e < 4 * kMaxMasked * kTile; ++e) {
             const int cw = e / (kMaxMasked * kTile), i = (e / kTile) % kMaxMasked, k = e % kTile;
             if (*const_cast<volatile int*>(&odd_item[odd][cw]) != item + 1) {
@@ -1196,20 +1236,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         // the warp's 32 rows are staged, then stored with two lanes a row
-        uint8_t* line = stage + lane * 32;
-        const int sw = (lane >> 2) & 1;
-        *reinterpret_cast<uint4*>(line + (sw << 4)) =
+        *reinterpret_cast<uint4*>(mine + (swap << 4)) =
             make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
-        *reinterpret_cast<uint4*>(line + ((sw ^ 1) << 4)) =
+        *reinterpret_cast<uint4*>(mine + ((swap ^ 1) << 4)) =
             make_uint4(pack_bf16(z[8], z[9]), pack_bf16(z[10], z[11]), pack_bf16(z[12], z[13]), pack_bf16(z[14], z[15]));
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int rr = 16 * k + (lane >> 1), ch = lane & 1;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((ch ^ ((rr >> 2) & 1)) << 4));
-          const int64_t to = __shfl_sync(0xffffffffu, out_row, rr);
-          if (half * kTile + (warp & 3) * 32 + rr < o.rows)
-            *reinterpret_cast<uint4*>(a.out + to * D + 16 * c + 8 * ch) = v;
+          const uint4 v = *reinterpret_cast<const uint4*>(theirs + k * 512);
+          if (in[k]) *reinterpret_cast<uint4*>(a.out + to[k] + 16 * c) = v;
         }
         __syncwarp();
       }
@@ -1217,7 +1252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       if (split) {  // the other half has read these sums, and its own, before either is written again
         mbar_arrive(&left_off);
-        ok = __all_sync(0xffffffffu, wait_or_abort(&left_off, n_split & 1u, abort_flag, a.status));
+        ok = __all_sync(0xffffffffu, await(&left_off, n_split & 1u, &watch));
         ++n_split;
       }
     }
@@ -1254,6 +1289,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
   float* m_s = fac_s;
   float* l_s = fac_s + n * kMergeRows;
   float* u_s = fac_s + 2 * n * kMergeRows;
+#pragma unroll 1
   for (int k = k0; k < n; k += kLanes) {
     const float4 x = *reinterpret_cast<const float4*>(record(k) + kTileRows * D + 4 * (row0 + r));
     m_s[k * kMergeRows + r] = x.x;
@@ -1263,12 +1299,15 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
   __syncthreads();
   const uint32_t at = static_cast<uint32_t>(cut.row0 + row0 + r), group = a.n_heads / a.cache.n_kv_heads;
   float top = kNone, unit = kNone, l = 0.f;
+#pragma unroll 1
   for (int k = 0; k < n; ++k) {
     top = fmaxf(top, m_s[k * kMergeRows + r]);
     unit = fmaxf(unit, u_s[k * kMergeRows + r]);
   }
+#pragma unroll 1
   for (int k = 0; k < n; ++k) l += l_s[k * kMergeRows + r] * ex2(m_s[k * kMergeRows + r] - top);
   __syncthreads();
+#pragma unroll 1
   for (int k = k0; k < n; k += kLanes) u_s[k * kMergeRows + r] = ex2(u_s[k * kMergeRows + r] - unit);
   if (k0 == 0 && r < rows) {
     float lse;
@@ -1278,6 +1317,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
   __syncthreads();
   if (r < rows) {
     const float f = f_s[r];
+#pragma unroll 1
     for (int c = k0; c < D / 4; c += kLanes) {
       float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -1293,6 +1333,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < rows * (D / 8); i += kMergeThreads) {
     const int rr = i / (D / 8), ch = i % (D / 8);
     const uint32_t x = static_cast<uint32_t>(cut.row0 + row0 + rr);
