@@ -77,9 +77,9 @@ struct Cfg {
   static constexpr int kRawStages = D == 128 ? 2 : 4;
   static constexpr int kVStages = 2;
   static constexpr int kMeta = 2 * kKStages;
-  static constexpr int kStageOut = 8 * 1024;        // 32 rows of 16 channels a warp
+  static constexpr int kSearch = kThreads * 12;     // of the sequences' costs, at the start
   static constexpr int kSmem =
-      2 * kQBytes + kKStages * kCodeBytes + kRawStages * kCodeBytes + kVStages * kVBytes + kStageOut + 1024;
+      2 * kQBytes + kKStages * kCodeBytes + kRawStages * kCodeBytes + kVStages * kVBytes + kSearch + 1024;
   static constexpr int kSCol(int t) { return t * kTile; }
   static constexpr int kOCol(int t) { return 2 * kTile + t * D; }
   static constexpr int kCols = 512;
@@ -201,6 +201,14 @@ __device__ __forceinline__ void landed(uint32_t (&r)[32]) {
                :);
 }
 
+__device__ __forceinline__ void landed(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               :);
+}
+
 // x, as something that the compiler cannot move out of a loop: it would copy the
 // loop for each value (the loading warps' loop had 25 KB of code, the product
 // warp's as much), and the kernel's hot code has to fit the instruction caches.
@@ -242,32 +250,15 @@ struct Start {
   int b, top;                  // rows of q below `top` belong to earlier sequences
 };
 
-// The cost of a sequence's tiles of one key head, and the largest row of q that
-// sequences whose offsets are right reach, by every thread of a warp for its own
-// sequence.  Sequences with more than two tiles are summed up by the whole warp.
+// The cost of a sequence's tiles of one key head, by a whole warp.
 __device__ __noinline__ int64_t head_cost(const Seq& s, int group, int window) {
-  const int tiles = tiles_of(s, group), lane = threadIdx.x & 31;
-  int64_t c = 0;
-  if (tiles > 0 && tiles <= 2) {
-    c = tile_of(s, group, window, 0).cost();
-    if (tiles == 2) c += tile_of(s, group, window, 1).cost();
-  }
+  const int tiles = tiles_of(s, group);
+  int64_t sum = 0;
 #pragma unroll 1
-  for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
-    const int from = __ffs(many) - 1;
-    Seq x;
-    x.q0 = 0;
-    x.n = __shfl_sync(0xffffffffu, s.n, from);
-    x.len = __shfl_sync(0xffffffffu, s.len, from);
-    const int nt = __shfl_sync(0xffffffffu, tiles, from);
-    int64_t sum = 0;
-#pragma unroll 1
-    for (int t = lane; t < nt; t += 32) sum += tile_of(x, group, window, t).cost();
+  for (int t = threadIdx.x & 31; t < tiles; t += 32) sum += tile_of(s, group, window, t).cost();
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == from) c = sum;
-  }
-  return c;
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  return sum;
 }
 
 // (64-bit divisions are long: one copy for all)
@@ -321,9 +312,7 @@ struct Walker {
     if (!seek(a)) return false;
     tiles = tiles_of(s, group);
     const int lane = threadIdx.x & 31;
-    Seq one = {0, 0, 0};
-    if (lane == 0) one = s;
-    const int64_t per_head = __shfl_sync(0xffffffffu, head_cost(one, group, a.window), 0);
+    const int64_t per_head = head_cost(s, group, a.window);
     head = static_cast<int>(quotient(st.offset, per_head));
     int64_t at = st.offset - head * per_head;  // units of the head's tiles before the share
 #pragma unroll 1
@@ -399,12 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int64_t sum_sh[kThreads / 32];
   __shared__ int max_sh[kThreads / 32];
   __shared__ Start start_s;
+  __shared__ int n_long;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_s = smem;
   uint8_t* k_ring = q_s + 2 * C::kQBytes;
   uint8_t* v_ring = k_ring + C::kKStages * C::kCodeBytes;
   uint8_t* raw_ring = v_ring + C::kVStages * C::kVBytes;
-  uint8_t* out_s = raw_ring + C::kRawStages * C::kCodeBytes;
+  int64_t* cost_s = reinterpret_cast<int64_t*>(raw_ring + C::kRawStages * C::kCodeBytes);
+  int* long_s = reinterpret_cast<int*>(cost_s + kThreads);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.n_heads / a.cache.n_kv_heads;
@@ -447,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     watch.limit = static_cast<uint32_t>(min(wait_limit_ns(a.status), static_cast<uint64_t>(4000000000u)));
     watch.status = a.status;
     start_s.b = -1;
+    n_long = 0;
 #pragma unroll 1
     for (int i = 0; i < 12; ++i) odd_item[i >> 2][i & 3] = 0;
   }
@@ -490,7 +482,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         top = through;
         if (s.q0 < before_top) s.n = 0;  // offsets that fall: rows that an earlier sequence has
-        const int64_t n = head_cost(s, group, a.window) * a.cache.n_kv_heads;
+        // Sequences of one tile or two are a thread's own, the others a warp's each.
+        const int tiles = tiles_of(s, group);
+        int64_t n = 0;
+        if (tiles > 2) {
+          long_s[atomicAdd(&n_long, 1)] = tid;
+        } else {
+#pragma unroll 1
+          for (int t = 0; t < tiles; ++t) n += tile_of(s, group, a.window, t).cost();
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = warp; i < n_long; i += kThreads / 32) {
+          const int64_t c = head_cost(read_seq(a, b0 + long_s[i]), group, a.window);
+          if (lane == 0) cost_s[long_s[i]] = c;
+        }
+        __syncthreads();
+        if (tiles > 2) n = cost_s[tid];
+        if (tid == 0) n_long = 0;
+        n *= a.cache.n_kv_heads;
         int64_t x = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -824,26 +834,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         return D == 128 ? line + part * (kTile * 128) + ((c ^ (r & 7)) << 4) : line + (((c + 4 * part) ^ (r & 7)) << 4);
       };
       const int halves = o.split ? 1 : 2, step_q = kRowsAtOnce / group, step_h = kRowsAtOnce - step_q * group;
+      {
+        const uint32_t at = static_cast<uint32_t>(o.row0 + r0);
+        const int qi = static_cast<int>(at / group);
+        int hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group), left = o.rows - r0;
+        const uint16_t* src = a.q + static_cast<int64_t>(o.q0 + qi) * a.q_stride + (o.head0 + hd) * a.q_stride_h + c * 16;
+        const int64_t step = step_q * a.q_stride + step_h * a.q_stride_h, wrap = a.q_stride - group * a.q_stride_h;
+        uint32_t to = smem_u32(q_at(0, r0, 0));
+        const uint32_t apart = smem_u32(q_at(0, r0, 1)) - to;
 #pragma unroll 1
-      for (int h = 0; h < halves; ++h) {
-        const uint32_t at = static_cast<uint32_t>(o.row0 + h * kTile + r0);
-        int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
-#pragma unroll 1  // (code that runs once a tile waits for its instructions)
-        for (int k = 0; k < kChunks; ++k) {
-          const int r = r0 + k * kRowsAtOnce;
-          const bool there = h * kTile + r < o.rows;
-          const uint16_t* src = a.q;
-          if (there) src += static_cast<int64_t>(o.q0 + qi) * a.q_stride + (o.head0 + hd) * a.q_stride_h + c * 16;
-          cp_async_16_or_zero(smem_u32(q_at(h, r, 0)), src, there);
-          cp_async_16_or_zero(smem_u32(q_at(h, r, 1)), src + 8, there);
-          qi += step_q;
-          hd += step_h;
-          if (hd >= group) {
-            hd -= group;
-            ++qi;
+        for (int h = 0; h < halves; ++h) {
+#pragma unroll 2
+          for (int k = 0; k < kChunks; ++k) {
+            const bool there = left > 0;
+            const uint16_t* from = there ? src : a.q;
+            cp_async_16_or_zero(to, from, there);
+            cp_async_16_or_zero(to + apart, from + 8, there);
+            to += kRowsAtOnce * 128;  // (rows 8 apart and more have their chunks in the same places)
+            left -= kRowsAtOnce;
+            hd += step_h;
+            src += step;
+            if (hd >= group) {
+              hd -= group;
+              src += wrap;
+            }
           }
+          to += C::kQBytes - kTile * 128;
+          cp_async_commit();
         }
-        cp_async_commit();
       }
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -1172,36 +1190,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any_odd = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) any_odd |= *const_cast<volatile int*>(&odd_item[odd][k]) == item + 1;
-      uint8_t* stage = out_s + warp * 1024;
       // the halves of a split tile take half of the channels each
       const int c_lo = split ? t * (D / 32) : 0, c_hi = split ? (t + 1) * (D / 32) : D / 16;
       const uint32_t oa = split ? tmem + lane_base + C::kOCol(0) : o_tmem, ob = tmem + lane_base + C::kOCol(1);
       const uint64_t f00 = pair_of(f0, f0), f11 = pair_of(f1, f1);
-      // where the row that a lane stores goes: two lanes a row, 16 rows at a time
-      int64_t to[2];
-      bool in[2];
+      uint16_t* out = a.out + out_row * D;
+      const bool two = split && have[1];
+      uint32_t x[16], y[16];
+      tmem_ld16(oa + 16 * c_lo, x);
+      if (two)
+        tmem_ld16(ob + 16 * c_lo, y);
+      else
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rr = 16 * k + (lane >> 1);
-        to[k] = __shfl_sync(0xffffffffu, out_row, rr) * D + 8 * (lane & 1);
-        in[k] = half * kTile + (warp & 3) * 32 + rr < o.rows;
-      }
-      const int swap = (lane >> 2) & 1;  // (the 16-byte places of every second four rows are exchanged)
-      uint8_t* mine = stage + lane * 32;
-      const uint8_t* theirs = stage + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4);
+        for (int k = 0; k < 16; ++k) y[k] = 0u;
 #pragma unroll 1
       for (int c = c_lo; c < c_hi; ++c) {
-        uint32_t x[16], y[16];
-        tmem_ld16(oa + 16 * c, x);
-        if (split && have[1]) tmem_ld16(ob + 16 * c, y);
         tmem_wait_ld();
+        landed(x);
+        landed(y);
         float z[16];
         uint64_t zz[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) zz[k] = mul2(pair_of(x[2 * k], x[2 * k + 1]), f00);
-        if (split && have[1]) {
+        if (two) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) zz[k] = fma2(pair_of(y[2 * k], y[2 * k + 1]), f11, zz[k]);
+        }
+        if (c + 1 < c_hi) {  // (the next ones, under what follows)
+          tmem_ld16(oa + 16 * (c + 1), x);
+          if (two) tmem_ld16(ob + 16 * (c + 1), y);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) csa::split(zz[k], &z[2 * k], &z[2 * k + 1]);
@@ -1235,18 +1252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
           continue;
         }
-        // the warp's 32 rows are staged, then stored with two lanes a row
-        *reinterpret_cast<uint4*>(mine + (swap << 4)) =
-            make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
-        *reinterpret_cast<uint4*>(mine + ((swap ^ 1) << 4)) =
-            make_uint4(pack_bf16(z[8], z[9]), pack_bf16(z[10], z[11]), pack_bf16(z[12], z[13]), pack_bf16(z[14], z[15]));
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(theirs + k * 512);
-          if (in[k]) *reinterpret_cast<uint4*>(a.out + to[k] + 16 * c) = v;
-        }
-        __syncwarp();
+        if (!writes) continue;
+        uint4* to = reinterpret_cast<uint4*>(out + 16 * c);
+        to[0] = make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+        to[1] = make_uint4(pack_bf16(z[8], z[9]), pack_bf16(z[10], z[11]), pack_bf16(z[12], z[13]), pack_bf16(z[14], z[15]));
       }
       done(item);
       tc_fence_before();
