@@ -148,10 +148,6 @@ struct Order {
   __device__ __forceinline__ bool masked(int j) const { return j >= from || j <= upto; }
 };
 
-// A copy of 16 bytes, or zeros without reading.
-__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 // Asks for a tile of a tensor map in L2.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
@@ -247,7 +243,9 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Watch* w) 
 // What every CTA finds out first: its share of the line, and where it begins.
 struct Start {
   int64_t per, total, offset;  // offset: units of sequence b before the share's first
-  int b, top;                  // rows of q below `top` belong to earlier sequences
+  int64_t per_head;            // units of a key head of it
+  Seq s;
+  int b;
 };
 
 // The cost of a sequence's tiles of one key head, by a whole warp.
@@ -262,7 +260,72 @@ __device__ __noinline__ int64_t head_cost(const Seq& s, int group, int window) {
 }
 
 // (64-bit divisions are long: one copy for all)
-__device__ __noinline__ int64_t quotient(int64_t x, int64_t y) { return x / y; }
+__device__ __noinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// What share each CTA has of `total` units.  (A share holds a block at least, so
+// that no CTA between a tile's first and last has none.)
+__device__ __forceinline__ int64_t share_of(int64_t total) {
+  return max(quotient(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(kCostTwo));
+}
+
+// The largest of the lanes' values up to this one, and their sum.
+__device__ __forceinline__ int max_upto(int x) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if ((threadIdx.x & 31) >= off) x = max(x, y);
+  }
+  return x;
+}
+__device__ __forceinline__ int64_t sum_upto(int64_t x) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if ((threadIdx.x & 31) >= off) x += y;
+  }
+  return x;
+}
+
+// The start of a CTA's share among at most 32 sequences, by one warp.
+constexpr int kFewSeqs = 32;
+__device__ __forceinline__ Start find_start(const ChunkAttnArgs& a, int group) {
+  const int lane = threadIdx.x & 31;
+  Seq s = {0, 0, 0};
+  if (lane < a.B) s = read_seq(a, lane);
+  const int top = __shfl_up_sync(0xffffffffu, max_upto(s.q0 + s.n), 1);
+  if (lane > 0 && s.q0 < top) s.n = 0;  // offsets that fall: rows that an earlier sequence has
+  const int tiles = tiles_of(s, group);
+  int64_t per_head = 0;
+#pragma unroll 1
+  for (int t = 0; t < min(tiles, 2); ++t) per_head += tile_of(s, group, a.window, t).cost();
+#pragma unroll 1
+  for (unsigned more = __ballot_sync(0xffffffffu, tiles > 2); more; more &= more - 1) {
+    const int from = __ffs(more) - 1;
+    Seq x;
+    x.q0 = 0;
+    x.n = __shfl_sync(0xffffffffu, s.n, from);
+    x.len = __shfl_sync(0xffffffffu, s.len, from);
+    const int64_t c = head_cost(x, group, a.window);
+    if (lane == from) per_head = c;
+  }
+  const int64_t n = per_head * a.cache.n_kv_heads, upto = sum_upto(n);
+  Start st;
+  st.total = __shfl_sync(0xffffffffu, upto, 31);
+  st.per = share_of(st.total);
+  const int64_t target = blockIdx.x * st.per;
+  const unsigned in = __ballot_sync(0xffffffffu, target < upto);
+  st.b = in ? __ffs(in) - 1 : -1;
+  const int from = max(st.b, 0);
+  st.offset = target - __shfl_sync(0xffffffffu, upto - n, from);
+  st.per_head = __shfl_sync(0xffffffffu, per_head, from);
+  st.s.q0 = __shfl_sync(0xffffffffu, s.q0, from);
+  st.s.n = __shfl_sync(0xffffffffu, s.n, from);
+  st.s.len = __shfl_sync(0xffffffffu, s.len, from);
+  return st;
+}
 
 // Walks the tiles of a share; one warp.
 struct Walker {
@@ -308,13 +371,12 @@ struct Walker {
     left = min(st.per, st.total - blockIdx.x * st.per);
     if (left <= 0) return false;
     b = st.b;
-    top = st.top;
-    if (!seek(a)) return false;
+    s = st.s;
+    top = s.q0 + s.n;
     tiles = tiles_of(s, group);
     const int lane = threadIdx.x & 31;
-    const int64_t per_head = head_cost(s, group, a.window);
-    head = static_cast<int>(quotient(st.offset, per_head));
-    int64_t at = st.offset - head * per_head;  // units of the head's tiles before the share
+    head = static_cast<int>(quotient(st.offset, st.per_head));
+    int64_t at = st.offset - head * st.per_head;  // units of the head's tiles before the share
 #pragma unroll 1
     for (t = 0; t < tiles; t += 32) {  // the tile that it begins in
       const int64_t c = t + lane < tiles ? tile_of(s, group, a.window, t + lane).cost() : 0;
@@ -399,49 +461,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.n_heads / a.cache.n_kv_heads;
-  if (tid == 0) {
+  // the barriers, a thread a kind
+  auto init = [&](int who, uint64_t* bars, int n, uint32_t count) {
+    if (tid == 32 * who)
 #pragma unroll 1
-    for (int i = 0; i < kOrders; ++i) {
-      mbar_init(order_full + i, 1);
-      mbar_init(order_empty + i, kThreads / 32 - 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, kTile);
-      mbar_init(o_full + i, 1);
-      mbar_init(q_full + i, kConvThreads);
-    }
-    mbar_init(&q_empty, kTileRows + 1);
-#pragma unroll 1
-    for (int i = 0; i < C::kKStages; ++i) {
-      mbar_init(k_full + i, 1);
-      mbar_init(k_empty + i, 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < C::kRawStages; ++i) {
-      mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, kConvThreads);
-    }
-#pragma unroll 1
-    for (int i = 0; i < C::kVStages; ++i) {
-      mbar_init(v_full + i, kConvThreads);
-      mbar_init(v_empty + i, 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < C::kMeta; ++i) mbar_init(meta_full + i, 1);
-    mbar_init(&joined, kTileRows);
-    mbar_init(&left_off, kTileRows);
-    mbar_init(&drain, 1);
-    fence_mbar_init();
+      for (int i = 0; i < n; ++i) mbar_init(bars + i, count);
+  };
+  init(0, order_full, kOrders, 1);
+  init(1, order_empty, kOrders, kThreads / 32 - 1);
+  init(2, q_full, 2, kConvThreads);
+  init(2, &q_empty, 1, kTileRows + 1);
+  init(3, k_full, C::kKStages, 1);
+  init(4, k_empty, C::kKStages, 1);
+  init(5, raw_full, C::kRawStages, 1);
+  init(6, raw_empty, C::kRawStages, kConvThreads);
+  init(7, v_full, C::kVStages, kConvThreads);
+  init(7, v_empty, C::kVStages, 1);
+  init(8, meta_full, C::kMeta, 1);
+  init(9, s_full, 2, 1);
+  init(9, p_full, 2, kTile);
+  init(10, o_full, 2, 1);
+  init(10, &joined, 1, kTileRows);
+  init(10, &left_off, 1, kTileRows);
+  init(10, &drain, 1, 1);
+  if (lane == 0 && warp <= 10) fence_mbar_init();
+  if (tid == 32 * 11) {
     watch.abort = 0;
     watch.limit = static_cast<uint32_t>(min(wait_limit_ns(a.status), static_cast<uint64_t>(4000000000u)));
     watch.status = a.status;
     start_s.b = -1;
     n_long = 0;
-#pragma unroll 1
-    for (int i = 0; i < 12; ++i) odd_item[i >> 2][i & 3] = 0;
   }
+  if (tid < 12) odd_item[tid >> 2][tid & 3] = 0;
   if (warp == kKeyWarp && lane == 0) prefetch_tensormap(&tm_k);
   if (warp == kValueWarp && lane == 0) prefetch_tensormap(&tm_v);
   // Tensor memory is taken after the kernel before has ended and before the
@@ -451,9 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_alloc(&tmem_slot, C::kCols);
 
   // ---------------- the CTA's share ----------------
-  // prefix sums of the sequences' costs; more than a block of sequences takes a
-  // pass for the total first
-  {
+  // Prefix sums of the sequences' costs; more than a block of sequences takes a
+  // pass for the total first.  Up to kFewSeqs the walking warp finds it by itself
+  // (one sequence, 5 tokens after 900: 19.3 us, 18.4 so).
+  if (a.B > kFewSeqs) {
     int64_t per = 1, total = 0;
 #pragma unroll 1
     for (int pass = a.B > kThreads ? 0 : 1; pass < 2; ++pass) {
@@ -464,12 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = b0 + tid;
         Seq s = {0, 0, 0};
         if (b < a.B) s = read_seq(a, b);
-        int end = s.q0 + s.n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, end, off);
-          if (lane >= off) end = max(end, y);
-        }
+        const int end = max_upto(s.q0 + s.n);
         if (lane == 31) max_sh[warp] = end;
         __syncthreads();
         int before_top = __shfl_up_sync(0xffffffffu, end, 1), through = top;
@@ -500,13 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         if (tiles > 2) n = cost_s[tid];
         if (tid == 0) n_long = 0;
+        const int64_t per_head = n;
         n *= a.cache.n_kv_heads;
-        int64_t x = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-          if (lane >= off) x += y;
-        }
+        const int64_t x = sum_upto(n);
         if (lane == 31) sum_sh[warp] = x;
         __syncthreads();
         int64_t before = base + x - n;
@@ -518,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (a.B <= kThreads) total = base;
         if (pass == 1) {
-          // (a share holds a block at least, so that no CTA between a tile's first and last has none)
-          per = max(quotient(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(kCostTwo));
+          per = share_of(total);
           const int64_t target = blockIdx.x * per;
           if (target >= before && target < before + n) {  // one thread at most
             start_s.b = b;
             start_s.offset = target - before;
-            start_s.top = before_top;
+            start_s.per_head = per_head;
+            start_s.s = s;
           }
         }
         __syncthreads();
@@ -558,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWalkWarp) {
       // ---------------- the tiles of the share ----------------
       Walker w;
-      const Start st = start_s;
+      const Start st = a.B > kFewSeqs ? start_s : find_start(a, group);
       bool there = st.b >= 0 && w.begin(a, st, group), ok = true;
       Cut cut = {};
 #pragma unroll 1
@@ -840,16 +883,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         int hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group), left = o.rows - r0;
         const uint16_t* src = a.q + static_cast<int64_t>(o.q0 + qi) * a.q_stride + (o.head0 + hd) * a.q_stride_h + c * 16;
         const int64_t step = step_q * a.q_stride + step_h * a.q_stride_h, wrap = a.q_stride - group * a.q_stride_h;
-        uint32_t to = smem_u32(q_at(0, r0, 0));
-        const uint32_t apart = smem_u32(q_at(0, r0, 1)) - to;
+        uint8_t* to = q_at(0, r0, 0);
+        const int apart = static_cast<int>(q_at(0, r0, 1) - to);
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {
 #pragma unroll 2
           for (int k = 0; k < kChunks; ++k) {
-            const bool there = left > 0;
-            const uint16_t* from = there ? src : a.q;
-            cp_async_16_or_zero(to, from, there);
-            cp_async_16_or_zero(to + apart, from + 8, there);
+            if (left > 0) {
+              cp_async_16(to, src);
+              cp_async_16(to + apart, src + 8);
+            }
             to += kRowsAtOnce * 128;  // (rows 8 apart and more have their chunks in the same places)
             left -= kRowsAtOnce;
             hd += step_h;
@@ -867,8 +910,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 2; ++h) {
         if (h < halves) {
           cp_async_wait_pending(halves - 1 - h);
+          // (rows past the tile's keep what was there: nothing of theirs is used)
+          const int n_rows = min(o.rows - h * kTile, kTile);
 #pragma unroll 1
-          for (int k = 0; k < kChunks; ++k) {
+          for (int k = 0; k * kRowsAtOnce < n_rows; ++k) {
             const int r = r0 + k * kRowsAtOnce;
             uint4* part[2] = {reinterpret_cast<uint4*>(q_at(h, r, 0)), reinterpret_cast<uint4*>(q_at(h, r, 1))};
             const uint4 u = *part[0], v = *part[1];
@@ -998,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, await(q_full + half, item & 1, &watch));
       if (!ok) break;
       const int row = half * kTile + r;                  // in the tile
-      const float fac = q_scale_s[half][r];
+      const float fac = row < o.rows ? q_scale_s[half][r] : 0.f;
       mbar_arrive(&q_empty);
       const uint32_t at = static_cast<uint32_t>(o.row0 + row);
       const int qi = static_cast<int>(at / group), hd = static_cast<int>(at - static_cast<uint32_t>(qi) * group);
