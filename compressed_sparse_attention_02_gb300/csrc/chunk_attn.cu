@@ -866,6 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- queries into two parts, values into f16 ----------------
     constexpr int kChunks = D / 16;               // 16-channel chunks a row
     constexpr int kRowsAtOnce = kConvThreads / kChunks;
+    // (at width 64 two chunks at a time: 48 mixed sequences 316 us, 306 so; at width
+    // 128 12 prompts 570 us, 595 so)
+    constexpr int kFlight = D == 128 ? 4 : 2;
     const int ct = tid - kConvWarp * 32, cw = warp - kConvWarp;
     const int r0 = ct / kChunks, c = ct % kChunks;
     const float scale2 = a.sm_scale * kLog2e;
@@ -978,16 +981,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool masked = o.masked(j);
         const int first = o.lo - j * kTile, past = o.hi - j * kTile;  // the block's keys that the tile sees
 #pragma unroll 1
-        for (int k0 = 0; k0 < kChunks; k0 += 4) {
-          uint4 u[4];
+        for (int k0 = 0; k0 < kChunks; k0 += kFlight) {
+          uint4 u[kFlight];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kFlight; ++i) {
             const int r = r0 + (k0 + i) * kRowsAtOnce;
             u[i] = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
           }
           if (here(masked || bad)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kFlight; ++i) {
               const int r = r0 + (k0 + i) * kRowsAtOnce;
               if (r < first || r >= past || ((bad >> (r >> 4)) & 1u)) {
                 u[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kFlight; ++i) {
             const int r = r0 + (k0 + i) * kRowsAtOnce;
             uint4 x, y;
             e4m3x4_to_f16(u[i].x, x.x, x.y);

@@ -108,46 +108,41 @@ __device__ __forceinline__ T sum_before(T n, T* sh, T* all) {
   return before;
 }
 
-// CTAs 0 .. stretches - 1 look at a stretch of the counts each, the last one
-// at the sequences.
-template <int OP>
-__global__ void __launch_bounds__(OP == kCompact ? kScanThreads : kSumThreads)
-    pages_scan_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* want,
-                      unsigned* status) {
-  pdl_launch_dependents();
-  pdl_wait();
-  constexpr int kThreads = OP == kCompact ? kScanThreads : kSumThreads;
-  __shared__ int64_t sh[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (static_cast<int>(blockIdx.x) < stretches) {
-    const int64_t first = static_cast<int64_t>(blockIdx.x) << shift;
-    const int64_t end = min(first + (int64_t(1) << shift), k.n_pages);
-    int n = 0;
-    constexpr int kFlight = 4;  // words a warp
-    for (int64_t p0 = first + warp * 32; p0 < end; p0 += kFlight * kThreads) {
-      int32_t r[kFlight];
+// Looks at a stretch of the counts: a bit a page and the free pages' number.  Every
+// thread of the CTA calls it; sh holds THREADS / 32 values.
+template <int THREADS>
+__device__ __forceinline__ void scan_stretch(const PageBook& k, const Work& w, int shift, int s, int64_t* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = static_cast<int64_t>(s) << shift, end = min(first + (int64_t(1) << shift), k.n_pages);
+  int n = 0;
+  constexpr int kFlight = 4;  // words a warp
+  for (int64_t p0 = first + warp * 32; p0 < end; p0 += kFlight * THREADS) {
+    int32_t r[kFlight];
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        const int64_t p = p0 + i * kThreads + lane;
-        r[i] = p < end ? k.refs[p] : 1;
-      }
-#pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        const uint32_t word = __ballot_sync(0xffffffffu, r[i] <= 0);
-        const int64_t p = p0 + i * kThreads;
-        if (lane == 0 && p < end) w.bits[p >> 5] = word;
-        n += __popc(word);
-      }
+    for (int i = 0; i < kFlight; ++i) {
+      const int64_t p = p0 + i * THREADS + lane;
+      r[i] = p < end ? k.refs[p] : 1;
     }
-    int64_t all;
-    sum_before<kThreads, int64_t>(lane == 0 ? n : 0, sh, &all);
-    if (tid == 0) w.free_of[blockIdx.x] = static_cast<int32_t>(all);
-    return;
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const uint32_t word = __ballot_sync(0xffffffffu, r[i] <= 0);
+      const int64_t p = p0 + i * THREADS;
+      if (lane == 0 && p < end) w.bits[p >> 5] = word;
+      n += __popc(word);
+    }
   }
-  if (OP == kCompact) return;
+  int64_t all;
+  sum_before<THREADS, int64_t>(lane == 0 ? n : 0, sh, &all);
+  if (threadIdx.x == 0) w.free_of[s] = static_cast<int32_t>(all);
+}
+
+// Sums up what the sequences need, by one CTA.
+template <int OP, int THREADS>
+__device__ __forceinline__ void sum_needs(const PageBook& k, const Work& w, const int32_t* want, unsigned* status,
+                                          int64_t* sh) {
   int64_t base = 0;
-  for (int b0 = 0; b0 < k.n_seqs; b0 += kThreads) {
-    const int b = b0 + tid;
+  for (int b0 = 0; b0 < k.n_seqs; b0 += THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
     int64_t n = 0;
     if (b < k.n_seqs) {
       const int t = want[b];
@@ -168,27 +163,26 @@ __global__ void __launch_bounds__(OP == kCompact ? kScanThreads : kSumThreads)
       w.lens[b] = L;
     }
     int64_t all;
-    const int64_t before = base + sum_before<kThreads, int64_t>(n, sh, &all);
+    const int64_t before = base + sum_before<THREADS, int64_t>(n, sh, &all);
     if (b < k.n_seqs) w.before[b] = before;
     base += all;
   }
-  if (tid == 0) w.before[k.n_seqs] = base;
+  if (threadIdx.x == 0) w.before[k.n_seqs] = base;
 }
 
 // Free pages before each stretch, in shared memory (kMaxStretches + 1), and in
 // all; every thread of the CTA calls it.
 template <int THREADS>
-__device__ __forceinline__ int64_t free_before(const Work& w, int stretches, int32_t* before, int32_t* sh) {
-  int32_t base = 0;
+__device__ __forceinline__ int64_t free_before(const Work& w, int stretches, int32_t* before, int64_t* sh) {
+  int64_t base = 0;
   for (int s0 = 0; s0 < stretches; s0 += THREADS) {
     const int s = s0 + static_cast<int>(threadIdx.x);
-    const int32_t n = s < stretches ? w.free_of[s] : 0;
-    int32_t all;
-    const int32_t x = base + sum_before<THREADS, int32_t>(n, sh, &all);
-    if (s < stretches) before[s] = x;
+    int64_t all;
+    const int64_t x = base + sum_before<THREADS, int64_t>(s < stretches ? w.free_of[s] : 0, sh, &all);
+    if (s < stretches) before[s] = static_cast<int32_t>(x);
     base += all;
   }
-  if (threadIdx.x == 0) before[stretches] = base;
+  if (threadIdx.x == 0) before[stretches] = static_cast<int32_t>(base);
   __syncthreads();
   return base;
 }
@@ -224,35 +218,61 @@ __device__ __forceinline__ void free_pages(const PageBook& k, const Work& w, int
         const int y = __shfl_up_sync(0xffffffffu, x, off);
         if (lane >= off) x += y;
       }
-      int32_t r = rank + x - c;
+      const int32_t mine = rank + x - c;
       rank += __shfl_sync(0xffffffffu, x, 31);
-      if (r < r1 && r + c > r0) {
+      // a word at a time, a lane a page
+      for (unsigned hit = __ballot_sync(0xffffffffu, mine < r1 && mine + c > r0); hit; hit &= hit - 1) {
+        const int l = __ffs(hit) - 1;
+        int32_t r = __shfl_sync(0xffffffffu, mine, l);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          for (uint32_t u = word[j]; u && r < r1; u &= u - 1, ++r)
-            if (r >= r0) give(r - r0, static_cast<int32_t>((i0 + 4 * lane + j) * 32 + __ffs(u) - 1));
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t u = __shfl_sync(0xffffffffu, word[j], l);
+          const int32_t q = r + __popc(u & ((1u << lane) - 1u));
+          if (((u >> lane) & 1u) && q >= r0 && q < r1)
+            give(q - r0, static_cast<int32_t>((i0 + 4 * l + j) * 32 + lane));
+          r += __popc(u);
+        }
       }
     }
   }
 }
 
-// Takes one holder off a page.  (A count that is 0 already stays so.)
-__device__ __forceinline__ void drop(const PageBook& k, int32_t page, unsigned* status) {
-  if (in_pool(k, page)) {
-    if (atomicSub(k.refs + page, 1) > 0) return;
-    atomicAdd(k.refs + page, 1);
+// Takes one holder off each of entries [from, to) of a row, which become -1; a CTA.
+// (A count that is 0 already stays so.)
+__device__ __forceinline__ void give_back(const PageBook& k, int32_t* row, int from, int to, unsigned* status) {
+  constexpr int kFlight = 4;
+  for (int j0 = from + static_cast<int>(threadIdx.x); j0 < to; j0 += kFlight * kSeqThreads) {
+    int32_t page[kFlight], held[kFlight];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) page[i] = j0 + i * kSeqThreads < to ? row[j0 + i * kSeqThreads] : -1;
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) held[i] = in_pool(k, page[i]) ? atomicSub(k.refs + page[i], 1) : 0;
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      if (j0 + i * kSeqThreads >= to) continue;
+      row[j0 + i * kSeqThreads] = -1;
+      if (held[i] > 0) continue;
+      if (in_pool(k, page[i])) atomicAdd(k.refs + page[i], 1);
+      record_error(status, kErrIndexRange);
+    }
   }
-  record_error(status, kErrIndexRange);
 }
 
+// What a call is given and gives beside the book.
+struct Lists {
+  const int32_t* want;         // targets, or parents
+  int32_t *pos0, *src, *dst;
+};
+
 __global__ void __launch_bounds__(kSeqThreads)
-    pages_resize_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* target,
-                        int32_t* pos0, int32_t* src, int32_t* dst, unsigned* status) {
+    pages_resize_kernel(const PageBook k, const Work w, const int shift, const int stretches, const Lists x,
+                        unsigned* status) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ int32_t before[kMaxStretches + 1], sh[kSeqThreads / 32];
+  __shared__ int32_t before[kMaxStretches + 1];
+  __shared__ int64_t sh[kSeqThreads / 32];
   const int b = blockIdx.x, tid = threadIdx.x;
-  const int L = w.lens[b], t = target[b];
+  const int L = w.lens[b], t = x.want[b];
   const int64_t r0 = w.before[b], need = w.before[b + 1] - r0;
   int32_t* row = k.table + b * k.table_stride;
   const int n0 = pages_of(k, L);
@@ -261,9 +281,7 @@ __global__ void __launch_bounds__(kSeqThreads)
     const int64_t all = need > 0 ? free_before<kSeqThreads>(w, stretches, before, sh) : 0;
     const int n1 = pages_of(k, t), from = n1 - static_cast<int>(need);
     const bool apart = from < n0;  // the last page is left to its other holders
-    if (r0 + need > all && need > 0) {
-      if (tid == 0) record_error(status, kErrIndexRange);
-    } else if (apart && !src) {
+    if ((need > 0 && r0 + need > all) || (apart && !x.src)) {
       if (tid == 0) record_error(status, kErrIndexRange);
     } else {
       if (apart) old = row[from];
@@ -273,54 +291,59 @@ __global__ void __launch_bounds__(kSeqThreads)
                    [&](int i, int32_t page) {
                      row[from + i] = page;
                      k.refs[page] = 1;
-                     if (apart && i == 0) dst[b] = page;
+                     if (apart && i == 0) x.dst[b] = page;
                    });
-      if (apart && tid == 0) drop(k, old, status);
+      if (apart && tid == 0) atomicSub(k.refs + old, 1);  // (it has other holders)
       now = t;
       first = L;
     }
   } else if (t >= 0 && t < L) {
-    for (int j = pages_of(k, t) + tid; j < n0; j += kSeqThreads) {
-      drop(k, row[j], status);
-      row[j] = -1;
-    }
+    give_back(k, row, pages_of(k, t), n0, status);
     now = t;
   }
   if (tid == 0) {
     k.lens[b] = now;
-    if (pos0) pos0[b] = first;
-    if (src) {
-      src[b] = old;
-      if (old < 0) dst[b] = -1;
+    if (x.pos0) x.pos0[b] = first;
+    if (x.src) {
+      x.src[b] = old;
+      if (old < 0) x.dst[b] = -1;
     }
   }
 }
 
 __global__ void __launch_bounds__(kSeqThreads)
-    pages_fork_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* parent,
-                      int32_t* src, int32_t* dst, unsigned* status) {
+    pages_fork_kernel(const PageBook k, const Work w, const int shift, const int stretches, const Lists x,
+                      unsigned* status) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ int32_t before[kMaxStretches + 1], sh[kSeqThreads / 32];
+  __shared__ int32_t before[kMaxStretches + 1];
+  __shared__ int64_t sh[kSeqThreads / 32];
   const int b = blockIdx.x, tid = threadIdx.x;
   const int L = w.lens[b];
   int32_t from = -1;
   if (L > 0) {
     const int64_t r0 = w.before[b];
     const int whole = L >> k.page_shift, need = (L & (k.page - 1)) != 0;
-    const int32_t* theirs = k.table + static_cast<int64_t>(parent[b]) * k.table_stride;
+    const int32_t* theirs = k.table + static_cast<int64_t>(x.want[b]) * k.table_stride;
     int32_t* row = k.table + b * k.table_stride;
     const int64_t all = need ? free_before<kSeqThreads>(w, stretches, before, sh) : 0;
     if (need && r0 + need > all) {
       if (tid == 0) record_error(status, kErrIndexRange);
     } else {
-      for (int j = tid; j < whole; j += kSeqThreads) {
-        const int32_t page = theirs[j];
-        row[j] = page;
-        if (in_pool(k, page))
-          atomicAdd(k.refs + page, 1);
-        else
-          record_error(status, kErrIndexRange);
+      constexpr int kFlight = 4;
+      for (int j0 = tid; j0 < whole; j0 += kFlight * kSeqThreads) {
+        int32_t page[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) page[i] = j0 + kSeqThreads * i < whole ? theirs[j0 + kSeqThreads * i] : 0;
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          if (j0 + kSeqThreads * i >= whole) continue;
+          row[j0 + kSeqThreads * i] = page[i];
+          if (in_pool(k, page[i]))
+            atomicAdd(k.refs + page[i], 1);
+          else
+            record_error(status, kErrIndexRange);
+        }
       }
       if (need) {
         from = theirs[whole];
@@ -328,117 +351,172 @@ __global__ void __launch_bounds__(kSeqThreads)
           free_pages(k, w, shift, stretches, before, static_cast<int32_t>(r0), 1, [&](int, int32_t page) {
             row[whole] = page;
             k.refs[page] = 1;
-            dst[b] = page;
+            x.dst[b] = page;
           });
       }
       if (tid == 0) k.lens[b] = L;
     }
   }
   if (tid == 0) {
-    src[b] = from;
-    if (from < 0) dst[b] = -1;
+    x.src[b] = from;
+    if (from < 0) x.dst[b] = -1;
   }
+}
+
+// CTAs 0 .. stretches - 1 look at a stretch of the counts each, the last one at
+// the sequences.
+template <int OP>
+__global__ void __launch_bounds__(kSumThreads)
+    pages_scan_kernel(const PageBook k, const Work w, const int shift, const int stretches, const int32_t* want,
+                      unsigned* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int64_t sh[kSumThreads / 32];
+  if (static_cast<int>(blockIdx.x) < stretches)
+    scan_stretch<kSumThreads>(k, w, shift, blockIdx.x, sh);
+  else if (OP != kCompact)
+    sum_needs<OP, kSumThreads>(k, w, want, status, sh);
 }
 
 // Lists of a compaction: with U used pages, the used ones from U on (src) and
 // the free ones below U (dst), as many, both in order; rank: each one's place.
-__global__ void __launch_bounds__(kScanThreads)
-    pages_list_kernel(const PageBook k, const Work w, const int shift, const int stretches, int32_t* src, int32_t* dst,
-                      int32_t* used) {
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ int32_t before[kMaxStretches + 1], sh[kScanThreads / 32];
+template <int THREADS>
+__device__ __forceinline__ void list_moves(const PageBook& k, const Work& w, int shift, int stretches, int cta,
+                                           int ctas, int32_t* src, int32_t* dst, int32_t* used, int32_t* before,
+                                           int64_t* sh) {
   const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t U = k.n_pages - free_before<kScanThreads>(w, stretches, before, sh);
-  if (blockIdx.x == 0 && tid == 0) *used = static_cast<int32_t>(U);
+  const int64_t U = k.n_pages - free_before<THREADS>(w, stretches, before, sh);
+  if (cta == 0 && tid == 0) *used = static_cast<int32_t>(U);
   const int64_t words = (k.n_pages + 31) >> 5, per = int64_t(1) << (shift - 5);
   // free pages below U
   int64_t holes = 0;
   if (U < k.n_pages) {
     const int s = static_cast<int>(U >> shift);
     int32_t n = 0;
-    for (int64_t i = s * per + tid; i <= U >> 5; i += kScanThreads) {
+    for (int64_t i = s * per + tid; i <= U >> 5; i += THREADS) {
       uint32_t u = w.bits[i];
       if (i == U >> 5) u &= (1u << (U & 31)) - 1u;
       n += __popc(u);
     }
-    int32_t all;
-    sum_before<kScanThreads, int32_t>(n, sh, &all);
+    int64_t all;
+    sum_before<THREADS, int64_t>(n, sh, &all);
     holes = before[s] + all;
   }
-  int32_t rank = before[blockIdx.x];
-  const int64_t end = min((blockIdx.x + 1) * per, words);
-  for (int64_t i0 = blockIdx.x * per; i0 < end; i0 += kScanThreads) {
-    const int64_t i = i0 + tid;
-    const uint32_t word = i < end ? w.bits[i] : 0u;
-    int32_t all;
-    const int32_t mine = rank + sum_before<kScanThreads, int32_t>(__popc(word), sh, &all);
-    rank += all;
-    // a warp takes its lanes' words in turn, a lane a page
-    for (int l = 0; l < 32; ++l) {
-      const uint32_t u = __shfl_sync(0xffffffffu, word, l);
-      const int32_t free_here = __shfl_sync(0xffffffffu, mine, l);
-      const int64_t p = (i - lane + l) * 32 + lane;
-      if (i - lane + l >= end || p >= k.n_pages) continue;
-      const int32_t f = free_here + __popc(u & ((1u << lane) - 1u));  // free pages before p
-      const bool is_free = (u >> lane) & 1u;
-      if (is_free && p < U) {
-        dst[f] = static_cast<int32_t>(p);
-        w.rank[p] = f;
-      } else if (!is_free && p >= U) {
-        const int32_t r = static_cast<int32_t>(p - f - (U - holes));  // used pages before p, less those below U
-        src[r] = static_cast<int32_t>(p);
-        w.rank[p] = r;
+  for (int s = cta; s < stretches; s += ctas) {
+    int64_t rank = before[s];
+    const int64_t end = min((s + 1) * per, words);
+    for (int64_t i0 = s * per; i0 < end; i0 += THREADS) {
+      const int64_t i = i0 + tid;
+      const uint32_t word = i < end ? w.bits[i] : 0u;
+      int64_t all;
+      const int32_t mine = static_cast<int32_t>(rank + sum_before<THREADS, int64_t>(__popc(word), sh, &all));
+      rank += all;
+      // a warp takes its lanes' words in turn, a lane a page
+      const int here = static_cast<int>(min(end - (i - lane), static_cast<int64_t>(32)));
+#pragma unroll 4
+      for (int l = 0; l < here; ++l) {
+        const uint32_t u = __shfl_sync(0xffffffffu, word, l);
+        const int32_t free_here = __shfl_sync(0xffffffffu, mine, l);
+        const int64_t p = (i - lane + l) * 32 + lane;
+        if (p >= k.n_pages) continue;
+        const int32_t f = free_here + __popc(u & ((1u << lane) - 1u));  // free pages before p
+        const bool is_free = (u >> lane) & 1u;
+        if (is_free && p < U) {
+          dst[f] = static_cast<int32_t>(p);
+          w.rank[p] = f;
+        } else if (!is_free && p >= U) {
+          const int32_t r = static_cast<int32_t>(p - f - (U - holes));  // used pages before p, less those below U
+          src[r] = static_cast<int32_t>(p);
+          w.rank[p] = r;
+        }
       }
     }
   }
-  for (int64_t r = holes + static_cast<int64_t>(blockIdx.x) * kScanThreads + tid; r < k.n_pages / 2;
-       r += static_cast<int64_t>(gridDim.x) * kScanThreads) {
+  for (int64_t r = holes + static_cast<int64_t>(cta) * THREADS + tid; r < k.n_pages / 2;
+       r += static_cast<int64_t>(ctas) * THREADS) {
     src[r] = -1;
     dst[r] = -1;
   }
 }
 
-// The counts and the tables under the pages' new numbers.
+__device__ __forceinline__ bool is_free(const Work& w, int64_t p) { return (w.bits[p >> 5] >> (p & 31)) & 1u; }
+
+// The counts under the pages' new numbers, by `threads` threads of which this is number i.
+__device__ __forceinline__ void renumber_counts(const PageBook& k, const Work& w, int64_t U, int64_t i,
+                                                int64_t threads, const int32_t* src, int32_t* refs) {
+  constexpr int kFlight = 4;
+  for (int64_t p0 = i; p0 < k.n_pages; p0 += kFlight * threads) {
+    int32_t n[kFlight];
+    int64_t from[kFlight];
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      const int64_t p = p0 + j * threads;
+      from[j] = -1;
+      if (p >= k.n_pages) continue;
+      from[j] = !is_free(w, p) ? (p < U ? p : -1) : p < U ? src[w.rank[p]] : -2;
+    }
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) n[j] = from[j] >= 0 ? k.refs[from[j]] : 0;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      const int64_t p = p0 + j * threads;
+      if (from[j] == -1) continue;  // (a page that moves: its count is written by the thread of its new place)
+      refs[p] = n[j];
+      if (from[j] >= 0 && from[j] != p) refs[from[j]] = 0;
+    }
+  }
+}
+
+// A sequence's table under the new numbers, by `threads` threads.
+__device__ __forceinline__ void renumber_table(const PageBook& k, const Work& w, int64_t U, int b, int i, int threads,
+                                               const int32_t* dst, int32_t* table, unsigned* status) {
+  const int n = pages_of(k, length_of(k, b, status));
+  constexpr int kFlight = 4;
+  for (int64_t j0 = i; j0 < k.table_stride; j0 += kFlight * threads) {
+    int32_t page[kFlight];
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      const int64_t j = j0 + q * threads;
+      page[q] = j < k.table_stride ? k.table[b * k.table_stride + j] : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      const int64_t j = j0 + q * threads;
+      if (j >= k.table_stride) continue;
+      if (j < n) {
+        if (!in_pool(k, page[q]))
+          record_error(status, kErrIndexRange);
+        else if (page[q] >= U && !is_free(w, page[q]))
+          page[q] = dst[w.rank[page[q]]];
+      }
+      table[b * k.table_stride + j] = page[q];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kScanThreads)
+    pages_list_kernel(const PageBook k, const Work w, const int shift, const int stretches, int32_t* src, int32_t* dst,
+                      int32_t* used) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int32_t before[kMaxStretches + 1];
+  __shared__ int64_t sh[kScanThreads / 32];
+  list_moves<kScanThreads>(k, w, shift, stretches, blockIdx.x, gridDim.x, src, dst, used, before, sh);
+}
+
 __global__ void __launch_bounds__(kScanThreads)
     pages_renumber_kernel(const PageBook k, const Work w, const int page_ctas, const int32_t* src, const int32_t* dst,
                           const int32_t* used, int32_t* table, int32_t* refs, unsigned* status) {
   pdl_launch_dependents();
   pdl_wait();
   const int64_t U = *used;
-  const auto is_free = [&](int64_t p) { return (w.bits[p >> 5] >> (p & 31)) & 1u; };
   if (static_cast<int>(blockIdx.x) < page_ctas) {
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kScanThreads + threadIdx.x; p < k.n_pages;
-         p += static_cast<int64_t>(page_ctas) * kScanThreads) {
-      if (is_free(p)) {
-        if (p < U) {  // (both ends of a move by one thread: the counts may be written in place)
-          const int32_t from = src[w.rank[p]];
-          const int32_t n = k.refs[from];
-          refs[p] = n;
-          refs[from] = 0;
-        } else {
-          refs[p] = 0;
-        }
-      } else if (p < U) {
-        refs[p] = k.refs[p];
-      }
-    }
+    renumber_counts(k, w, U, static_cast<int64_t>(blockIdx.x) * kScanThreads + threadIdx.x,
+                    static_cast<int64_t>(page_ctas) * kScanThreads, src, refs);
     return;
   }
-  const int64_t cta = blockIdx.x - page_ctas, ctas = gridDim.x - page_ctas;
-  for (int64_t b = cta; b < k.n_seqs; b += ctas) {
-    const int n = pages_of(k, length_of(k, static_cast<int>(b), status));
-    for (int64_t j = threadIdx.x; j < k.table_stride; j += kScanThreads) {
-      int32_t page = k.table[b * k.table_stride + j];
-      if (j < n) {
-        if (!in_pool(k, page))
-          record_error(status, kErrIndexRange);
-        else if (page >= U && !is_free(page))
-          page = dst[w.rank[page]];
-      }
-      table[b * k.table_stride + j] = page;
-    }
-  }
+  for (int b = blockIdx.x - page_ctas; b < k.n_seqs; b += gridDim.x - page_ctas)
+    renumber_table(k, w, U, b, threadIdx.x, kScanThreads, dst, table, status);
 }
 
 // Copies of pages' contents, bound by memory.  A unit is a slice of a pair;
@@ -514,43 +592,47 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 size_t pages_bytes(int n_seqs, int64_t n_pages) { return work_bytes(n_seqs, n_pages, nullptr, nullptr); }
 
-cudaError_t launch_pages_resize(const PageBook& k, const int32_t* target, int32_t* pos0, int32_t* src, int32_t* dst,
-                                void* workspace, unsigned* status, cudaStream_t stream) {
+namespace {
+
+int stretches_of(int64_t n_pages, int shift) { return static_cast<int>((n_pages + (int64_t(1) << shift) - 1) >> shift); }
+
+template <int OP>
+cudaError_t launch_change(const PageBook& k, const Lists& x, void* workspace, unsigned* status, cudaStream_t stream) {
   Work w;
   work_bytes(k.n_seqs, k.n_pages, workspace, &w);
-  const int shift = stretch_shift(k.n_pages), stretches = static_cast<int>((k.n_pages + (int64_t(1) << shift) - 1) >> shift);
-  const cudaError_t e = launch_pdl(pages_scan_kernel<kResize>, dim3(stretches + 1), dim3(kSumThreads), 0, stream, k, w,
-                                   shift, stretches, target, status);
+  const int shift = stretch_shift(k.n_pages), stretches = stretches_of(k.n_pages, shift);
+  const cudaError_t e = launch_pdl(pages_scan_kernel<OP>, dim3(stretches + 1), dim3(kSumThreads), 0, stream, k, w,
+                                   shift, stretches, x.want, status);
   if (e != cudaSuccess) return e;
-  return launch_pdl(pages_resize_kernel, dim3(k.n_seqs), dim3(kSeqThreads), 0, stream, k, w, shift, stretches, target,
-                    pos0, src, dst, status);
+  return launch_pdl(OP == kResize ? pages_resize_kernel : pages_fork_kernel, dim3(k.n_seqs), dim3(kSeqThreads), 0,
+                    stream, k, w, shift, stretches, x, status);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_resize(const PageBook& k, const int32_t* target, int32_t* pos0, int32_t* src, int32_t* dst,
+                                void* workspace, unsigned* status, cudaStream_t stream) {
+  return launch_change<kResize>(k, {target, pos0, src, dst}, workspace, status, stream);
 }
 
 cudaError_t launch_pages_fork(const PageBook& k, const int32_t* parent, int32_t* src, int32_t* dst, void* workspace,
                               unsigned* status, cudaStream_t stream) {
-  Work w;
-  work_bytes(k.n_seqs, k.n_pages, workspace, &w);
-  const int shift = stretch_shift(k.n_pages), stretches = static_cast<int>((k.n_pages + (int64_t(1) << shift) - 1) >> shift);
-  const cudaError_t e = launch_pdl(pages_scan_kernel<kFork>, dim3(stretches + 1), dim3(kSumThreads), 0, stream, k, w,
-                                   shift, stretches, parent, status);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(pages_fork_kernel, dim3(k.n_seqs), dim3(kSeqThreads), 0, stream, k, w, shift, stretches, parent,
-                    src, dst, status);
+  return launch_change<kFork>(k, {parent, nullptr, src, dst}, workspace, status, stream);
 }
 
 cudaError_t launch_pages_compact(const PageBook& k, int32_t* src, int32_t* dst, int32_t* used, int32_t* table,
                                  int32_t* refs, void* workspace, unsigned* status, int sms, cudaStream_t stream) {
   Work w;
   work_bytes(k.n_seqs, k.n_pages, workspace, &w);
-  const int shift = stretch_shift(k.n_pages), stretches = static_cast<int>((k.n_pages + (int64_t(1) << shift) - 1) >> shift);
-  cudaError_t e = launch_pdl(pages_scan_kernel<kCompact>, dim3(stretches), dim3(kScanThreads), 0, stream, k, w, shift,
+  const int shift = stretch_shift(k.n_pages), stretches = stretches_of(k.n_pages, shift);
+  cudaError_t e = launch_pdl(pages_scan_kernel<kCompact>, dim3(stretches), dim3(kSumThreads), 0, stream, k, w, shift,
                              stretches, static_cast<const int32_t*>(nullptr), status);
   if (e != cudaSuccess) return e;
   e = launch_pdl(pages_list_kernel, dim3(stretches), dim3(kScanThreads), 0, stream, k, w, shift, stretches, src, dst,
                  used);
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(sms) * 8;
-  const int64_t page_ctas = (k.n_pages + kScanThreads - 1) / kScanThreads, seq_ctas = k.n_seqs;
+  const int64_t page_ctas = (k.n_pages + 4 * kScanThreads - 1) / (4 * kScanThreads), seq_ctas = k.n_seqs;
   const int pc = static_cast<int>(page_ctas < most ? page_ctas : most);
   const int sc = static_cast<int>(seq_ctas < most ? seq_ctas : most);
   return launch_pdl(pages_renumber_kernel, dim3(pc + sc), dim3(kScanThreads), 0, stream, k, w, pc,

@@ -191,11 +191,12 @@ def test_forks_that_cannot_be(csa):
     y.host.check()
 
 
-def test_many_sequences(csa):
-    """More than one block of the sums, every kind of change at once, over several steps."""
-    r = np.random.default_rng(7)
-    n, P = 2500, 16
-    x = make(csa, r.integers(0, 200, n).tolist(), 30, 60000, P, seed=7)
+@pytest.mark.parametrize("n,pool", [(2500, 60000), (6000, 150000), (40, 1100000)])
+def test_many_sequences_and_large_pools(csa, n, pool):
+    """More than one block of the sums, every kind of change at once, over several steps; as many sequences and pages as
+    take the call's other way."""
+    r, P = np.random.default_rng(7), 16
+    x = make(csa, r.integers(0, 200, n).tolist(), 30, pool, P, seed=7)
     for step in range(3):
         target = np.where(r.random(n) < 0.3, -1, np.where(r.random(n) < 0.3, 0, r.integers(0, 480, n)))
         x.resize(target)
