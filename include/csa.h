@@ -667,10 +667,11 @@ csa_status csa_hca_layer_decode(const csa_params *p, int32_t B,
  * with such layers; the pages describe no model that mixes the two).  The calls
  * below serve such a layer: rotate queries and keys, attend over packed
  * prompts, append keys and values to a paged 8-bit cache, attend to it one
- * token or a chunk of tokens at a time, and keep its pages.  The layer calls above use none of them, and the cache and
- * both attentions stop at width 128; csa_rope also turns the compressed
- * layers' own rows (rope_dim 64, offset 448, CSA_ROPE_INTERLEAVED), which the
- * layer calls expect of their queries.  They take no csa_params.  Conventions are those at the top, with these
+ * token or a chunk of tokens at a time, and keep its pages.  The layer calls
+ * above use none of them, and the cache and the attentions stop at width 128;
+ * csa_rope also turns the compressed layers' own rows (rope_dim 64, offset 448,
+ * CSA_ROPE_INTERLEAVED), which the layer calls expect of their queries.  They
+ * take no csa_params.  Conventions are those at the top, with these
  * additions: rows are [rows][heads][head_dim] bf16 with strides in elements
  * for rows and heads (multiples of 8, at least head_dim; the channels are
  * contiguous), so views of a fused projection pass as they are; row pointers
@@ -889,7 +890,8 @@ csa_status csa_chunk_attn(const csa_paged_cache *c, int32_t B, int32_t n_heads,
  * lists the pair in src and dst (-1: none) for csa_pages_copy, once for each
  * layer's cache, before anything is appended to.  Lengths past the table count
  * up to it, and entries outside the pool are no pages; both record
- * CSA_ERR_INDEX_RANGE.
+ * CSA_ERR_INDEX_RANGE.  A call's arrays do not overlap, but for those of
+ * csa_pages_compact that it says may.
  * Workspace: csa_pages_workspace_size bytes, of the call's own while it runs.
  */
 typedef struct {

@@ -80,9 +80,13 @@ class Pages:
                 if taken > len(free):
                     self.refused = True
                     continue
-                src[b], dst[b] = self.table[a, L // P], free[taken - 1]
-                self.table[b, L // P] = dst[b]
-                refs[dst[b]] = 1
+                last = int(self.table[a, L // P])
+                self.table[b, L // P] = free[taken - 1]
+                refs[free[taken - 1]] = 1
+                if self.is_page(last):
+                    src[b], dst[b] = last, free[taken - 1]
+                else:
+                    self.refused = True
             for j in range(L // P):
                 p = int(self.table[a, j])
                 self.table[b, j] = p

@@ -225,6 +225,16 @@ def test_wrong_numbers(csa):
     assert (guard == 5).all()
 
 
+@pytest.mark.parametrize("last", [-1, -9, 8, 2 ** 31 - 1])
+def test_fork_of_a_last_page_that_is_none(csa, last):
+    """A parent whose partly filled page is outside the pool: reported; the child has a page and no pair to copy."""
+    table = np.array([[0, last, -1], [-1, -1, -1], [2, 3, -1], [-1, -1, -1]], np.int32)
+    x = Both(csa, table, [20, 0, 20, 0], [1, 0, 1, 1, 0, 0, 0, 0], 16)
+    src, dst = x.fork([-1, 0, -1, 2])
+    assert src.tolist() == [-1, -1, -1, 3] and dst.tolist() == [-1, -1, -1, 4]
+    assert x.host.table[1].tolist() == [0, 1, -1] and x.host.table[3].tolist() == [2, 4, -1]
+
+
 def test_streams_graphs_and_overlapping_calls(csa):
     """A captured growth replays on what is there then; two books' calls run at once with a workspace each."""
     P = 16
