@@ -48,6 +48,9 @@ constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kWalkWarp = 12, kMmaWarp = 13, kKeyWarp = 14, kValueWarp = 15;
 constexpr int kConvThreads = 128;
 constexpr int kOrders = 4;                  // tiles that the walking warp may be ahead
+// The walking warp waits for whole tiles (2^30 tokens: some 15 s), all others for a
+// block at most: what stops is theirs to report, and ends its wait too.
+constexpr int kTileWaits = 16;
 // A maximum may lag behind by this much (in log2) before the sums are rescaled:
 // weights are then at most 2^8 times 1, and as f16 they carry 2^7 more, so that
 // weights down to 2^-21 of the largest keep f16's full precision.
@@ -233,12 +236,17 @@ __device__ __forceinline__ uint32_t timer_low() {
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Watch* w) {
+// (limits: how many of them it waits for)
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Watch* w, int limits = 1) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint32_t t0 = timer_low();
+  uint32_t t0 = timer_low();
   while (w->abort == 0) {
     if (mbar_try_wait(bar, parity)) return true;
     if (timer_low() - t0 > w->limit) {
+      if (--limits > 0) {
+        t0 = timer_low();
+        continue;
+      }
       record_error(w->status, kErrTimeout);
       w->abort = 1;
     }
@@ -652,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
           if (item >= kOrders)
-            ok = await(order_empty + item % kOrders, (item / kOrders - 1) & 1, &watch);
+            ok = await(order_empty + item % kOrders, (item / kOrders - 1) & 1, &watch, kTileWaits);
           if (ok) {
             orders[item % kOrders] = o;
             mbar_arrive(order_full + item % kOrders);

@@ -389,6 +389,21 @@ def test_waits_give_up(csa):
         assert csa.csa_check_status() == 0
 
 
+def test_tiles_that_take_longer_than_a_wait(csa):
+    """Shares of six tiles, each longer than the limit of a wait: the warp that is tiles ahead waits for their ends."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n, L = sms * 32, 32768                   # of two key heads that four query heads share: sms tiles
+    x = make([(n, L)] * 6, 8, 2, 64, 128, seed=3)
+    good, _ = run(csa, x)
+    csa.csa_test_set_wait_fault(150, 0)      # (a tile takes some 400 us)
+    try:
+        out, _ = run(csa, x)
+        status = csa.csa_check_status()
+    finally:
+        csa.csa_test_set_wait_fault(0, 0)
+    assert status == 0 and torch.equal(out, good)
+
+
 def test_refusals(csa):
     x = make([(5, 9), (2, 3)], 4, 2, 64, 16)
     cache = csa.paged_cache(x["k"], x["v"], x["ks"], x["vs"], x["table"])
