@@ -236,20 +236,29 @@ __device__ __forceinline__ uint32_t timer_low() {
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-// (limits: how many of them it waits for)
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Watch* w, int limits = 1) {
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Watch* w) {
   if (mbar_try_wait(bar, parity)) return true;
-  uint32_t t0 = timer_low();
+  const uint32_t t0 = timer_low();
   while (w->abort == 0) {
     if (mbar_try_wait(bar, parity)) return true;
     if (timer_low() - t0 > w->limit) {
-      if (--limits > 0) {
-        t0 = timer_low();
-        continue;
-      }
       record_error(w->status, kErrTimeout);
       w->abort = 1;
     }
+  }
+  return false;
+}
+// The same for up to kTileWaits limits.
+__device__ __noinline__ bool await_tile(uint64_t* bar, uint32_t parity, Watch* w) {
+  uint32_t t0 = timer_low();
+  int limits = kTileWaits;
+  while (w->abort == 0) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (timer_low() - t0 <= w->limit) continue;
+    t0 = timer_low();
+    if (--limits > 0) continue;
+    record_error(w->status, kErrTimeout);
+    w->abort = 1;
   }
   return false;
 }
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
           if (item >= kOrders)
-            ok = await(order_empty + item % kOrders, (item / kOrders - 1) & 1, &watch, kTileWaits);
+            ok = await_tile(order_empty + item % kOrders, (item / kOrders - 1) & 1, &watch);
           if (ok) {
             orders[item % kOrders] = o;
             mbar_arrive(order_full + item % kOrders);
@@ -820,9 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int steps = static_cast<int>(uniform(orders[item % kOrders].blocks)) << (split ? 0 : 1);
         done(item);
 #pragma unroll 1
-        for (int t = 0; t < 2 && ok; ++t) {
+        for (int t = 0; t < min(steps, 2) && ok; ++t) {
           ok = wait(q_full + t, item & 1);
-          if (t >= steps) break;
+          // (before the queries are given up: the next ones would pass the phase)
+          if (ok && steps == 1) ok = wait(q_full + 1, item & 1);
           if (ok && (here(split) || t == 0)) ok = wait(k_full + k_slot, k_parity);
           tc_fence_after();
           if (ok && elect_one()) {

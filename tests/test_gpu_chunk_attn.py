@@ -389,6 +389,22 @@ def test_waits_give_up(csa):
         assert csa.csa_check_status() == 0
 
 
+def test_tiles_of_one_block_again_and_again(csa):
+    """Tiles of one block between longer ones, 300 calls on end of two books: no wait gives up, the bits stay."""
+    seqs = [[(1 + i % 3, 5 + i % 120 if i % 5 else 500 + 10 * i) for i in range(n)] for n in (20, 90)]
+    xs = [make(s, 16, 4, 64, 16, seed=i) for i, s in enumerate(seqs)]
+    good = [run(csa, x)[0] for x in xs]
+    cache = [csa.paged_cache(x["k"], x["v"], x["ks"], x["vs"], x["table"]) for x in xs]
+    ws = [csa.chunk_attn_workspace(c, 16) for c in cache]
+    outs = [torch.empty_like(g) for g in good]
+    for _ in range(300):
+        for x, c, w, o in zip(xs, cache, ws, outs):
+            csa.csa_chunk_attn(c, x["cu"], x["lens"], x["q"], 0.125, 0, None, o, None, w)
+    assert csa.csa_check_status() == 0
+    for o, g in zip(outs, good):
+        assert torch.equal(o, g)
+
+
 def test_tiles_that_take_longer_than_a_wait(csa):
     """Shares of six tiles, each longer than the limit of a wait: the warp that is tiles ahead waits for their ends."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
