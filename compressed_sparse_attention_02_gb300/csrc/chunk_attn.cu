@@ -25,6 +25,24 @@
 // f16 and read from there.  The softmax has one thread a row, so no value
 // crosses threads.
 //
+// Roles of a CTA's 16 warps: 0..7 the softmax of the two halves, 8..11 queries
+// into their two parts and values into f16, 12 the walk along the CTA's share, 13
+// the products, 14 keys and scales, 15 values.  The softmax has 200 registers a
+// thread (a row's 128 scores and what goes with them, no spills), the converting
+// warps 48, the others 64.
+//
+// What bounds it: at width 128 the products of a block for 256 rows take 2050 cycles
+// alone; a block takes some 3300, a half's scores, softmax and product one after the
+// other while the other half is half a turn away, and neither instructions (46 % of
+// the issue slots) nor memory (2 % of it) are short.  Most of the softmax's 1600
+// cycles a half are waits for instructions: code that is not run again at once is
+// fetched at some 3 cycles an instruction, so what runs once a tile is kept short
+// and in rolled loops.  (2048 tokens at 62000, 32 heads on 8 of width 128: 1604 us,
+// 1.35 PFLOP/s counting each product once, 71 % of what a 16-bit library product
+// reaches; 12 prompts of up to 1000 tokens behind up to 6000: 546 us; 48 mixed
+// sequences of width 64 under a window of 4096: 304 us; 5 tokens after 900: 17 us,
+// of which two launches and the chain of loads before the first product are 12.)
+//
 // A masked weight is 0, and 0 * NaN is NaN: in blocks that some row of the tile
 // masks, NaN codes of values are taken out as they become f16, and the rows that
 // do see such a key get its NaN at the end.
@@ -70,7 +88,9 @@ constexpr int kMaxMasked = 8;
 // warp, a row each, store neighbouring words.
 constexpr int kFewRows = 64;
 // What a tile costs, in the units of the shares: a block for two halves, for
-// one, and the tile itself.
+// one, and the tile itself: its queries, its outputs and the pipeline that runs
+// empty between it and the next, some 7500 cycles (12 prompts 632 us with 4 in
+// the place of 16, 588 so).
 constexpr int kCostTwo = 3, kCostOne = 2, kCostTile = 16;
 
 // Registers a thread: 512 threads are launched with 128 each.
@@ -527,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------- the CTA's share ----------------
   // Prefix sums of the sequences' costs; more than a block of sequences takes a
   // pass for the total first.  Up to kFewSeqs the walking warp finds it by itself
-  // (one sequence, 5 tokens after 900: 19.3 us, 18.4 so).
+  // (one sequence, 5 tokens after 900: 19.3 us, 18.1 so).
   if (a.B > kFewSeqs) {
     int64_t per = 1, total = 0;
 #pragma unroll 1
@@ -829,16 +849,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int steps = static_cast<int>(uniform(orders[item % kOrders].blocks)) << (split ? 0 : 1);
         done(item);
 #pragma unroll 1
-        for (int t = 0; t < min(steps, 2) && ok; ++t) {
+        for (int t = 0; t < 2 && ok; ++t) {
           ok = wait(q_full + t, item & 1);
-          // (before the queries are given up: the next ones would pass the phase)
-          if (ok && steps == 1) ok = wait(q_full + 1, item & 1);
+          if (t >= steps) {  // (only now: the next queries would pass the phase)
+            if (elect_one()) tc_commit(&q_empty);
+            break;
+          }
           if (ok && (here(split) || t == 0)) ok = wait(k_full + k_slot, k_parity);
           tc_fence_after();
           if (ok && elect_one()) {
             s_of(t, here(split) ? 0 : t, k_slot);
             if (here(split) || t == 1) tc_commit(k_empty + k_slot);
-            if (steps <= t + 1 || (t == 1 && steps == 2)) tc_commit(&q_empty);
+            if (t == 1 && steps == 2) tc_commit(&q_empty);
           }
           __syncwarp();
           if (here(split) || t == 1) next_k();
@@ -1080,24 +1102,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = kNone, mv = kNone, l = 0.f;
       const int step = split ? 2 : 1;
       bool began = false;
+      auto factor = [&](float ks) { return fmaxf(fac * ks, FLT_MIN); };  // (not 0: a masked score is -inf, and stays so under it)
 #pragma unroll 1
       for (int q = split ? t : 0; q < o.blocks; q += step) {
         const int n = n0 + q, j = o.j_top - q, meta = n % C::kMeta;
         ok = await(meta_full + meta, (n / C::kMeta) & 1, &watch);
-        float cf[kGroups], lv[kGroups];  // the groups' factors and value scales (log2)
-        {
-          const float4 x = *reinterpret_cast<const float4*>(&k_scale_s[meta][0]);
-          const float4 y = *reinterpret_cast<const float4*>(&k_scale_s[meta][4]);
-          const float4 z = *reinterpret_cast<const float4*>(&v_log_s[meta][0]);
-          const float4 w = *reinterpret_cast<const float4*>(&v_log_s[meta][4]);
-          const float ks[kGroups] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          const float vs[kGroups] = {z.x, z.y, z.z, z.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            cf[g] = fmaxf(fac * ks[g], FLT_MIN);  // (not 0: a masked score is -inf, and stays so under it)
-            lv[g] = vs[g];
-          }
-        }
         const float v_min = v_min_s[meta];
         const uint32_t bad = bad_s[meta];
         ok = ok && await(s_full + t, n_s & 1u, &watch);
@@ -1105,35 +1114,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++n_s;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, s[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) landed(s[c]);
-        if (o.masked(j) || bad) {  // this row's keys among the block's, as a bit each
+        // This row's keys alone, where a block has others: the scores of the rest
+        // become -inf where they lie, 32 at a time (for its 128 keys at once, in
+        // registers, the code is four times as long and in every block's way).
+        if (o.masked(j) || bad) {
           const int c_hi = last_key + 1 - j * kTile, c_lo = first_key - j * kTile;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(s_tmem + 32 * c, x);
             const int hi = max(0, min(32, c_hi - 32 * c)), lo = max(0, min(32, c_lo - 32 * c));
             uint32_t seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
             if (bad & (1u << (2 * c))) seen &= 0xFFFF0000u;
             if (bad & (2u << (2 * c))) seen &= 0x0000FFFFu;
+            tmem_wait_ld();
+            landed(x);
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (!((seen >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
+              if (!((seen >> k) & 1u)) x[k] = 0xFF800000u;
+            tmem_st32(s_tmem + 32 * c, x);
           }
+          tmem_wait_st();
         }
+        uint32_t x[4][32];
+        float ks[kGroups], vs[kGroups];
         float top = -INFINITY, topv = -INFINITY;
+        {
+          tmem_ld32(s_tmem, x[0]);
+          tmem_ld32(s_tmem + 32, x[1]);
+          tmem_ld32(s_tmem + 64, x[2]);
+          tmem_ld32(s_tmem + 96, x[3]);
+          const float4 k0 = *reinterpret_cast<const float4*>(&k_scale_s[meta][0]);
+          const float4 k1 = *reinterpret_cast<const float4*>(&k_scale_s[meta][4]);
+          const float4 v0 = *reinterpret_cast<const float4*>(&v_log_s[meta][0]);
+          const float4 v1 = *reinterpret_cast<const float4*>(&v_log_s[meta][4]);
+          const float ku[kGroups] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+          const float vu[kGroups] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t* y = s[g >> 1] + (g & 1) * 16;
-          float x = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+          for (int g = 0; g < kGroups; ++g) {
+            ks[g] = factor(ku[g]);
+            vs[g] = vu[g];
+          }
+          tmem_wait_ld();
+          landed(x[0]);
+          landed(x[1]);
+          landed(x[2]);
+          landed(x[3]);
 #pragma unroll
-          for (int k = 2; k < 16; k += 2) x = max3(x, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-          x *= cf[g];
-          top = fmaxf(top, x);
-          topv = fmaxf(topv, x + lv[g]);
+          for (int g = 0; g < kGroups; ++g) {
+            const uint32_t* u = x[g >> 1] + (g & 1) * 16;
+            float w = fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1]));
+#pragma unroll
+            for (int k = 2; k < 16; k += 2) w = max3(w, __uint_as_float(u[k]), __uint_as_float(u[k + 1]));
+            w *= ks[g];
+            top = fmaxf(top, w);
+            topv = fmaxf(topv, w + vs[g]);
+          }
         }
         // (a row whose own maximum has not grown keeps its reference, so that no bit
         // of it depends on what only the warp's other rows see)
@@ -1157,59 +1193,84 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         began = true;
-        // exponents in one rounding, factor s - m; where logits are so large that the
-        // rounding of m shows, the products first
-        const bool large = fmaxf(fabsf(m), fabsf(mv)) > kLarge && m > kNone;
-        float up = kWeightExp - mv, minus_m = -m;
         const float down = mv - kWeightExp - m;
-        if (__any_sync(0xffffffffu, large)) {
-          const float less = large ? m : 0.f;
-          if (large) {
-            up = kWeightExp + (m - mv);
-            minus_m = 0.f;
-          }
+        const bool large = fmaxf(fabsf(m), fabsf(mv)) > kLarge && m > kNone, far = v_min - down < kFar;
+        if (!__any_sync(0xffffffffu, large || far)) {
+          // 32 keys a turn, the scores behind them moved up in the registers: code for all
+          // 128 is faster where one long sequence keeps the loop in the instruction
+          // caches (2048 tokens at 62000 1535 us, 1604 so) and slower where tiles end
+          // often (12 prompts 584 us, 546 so; 48 mixed sequences 312, 304).  Reading the
+          // scores again from tensor memory instead takes 1690 and 564 us.
+          const float up = kWeightExp - mv;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[16];
+            uint64_t y[16];
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const float x = large ? cf[g] : 1.f;
-            if (large) cf[g] = 1.f;
+            for (int k = 0; k < 16; ++k)
+              y[k] = fma2(pair_of(x[0][2 * k], x[0][2 * k + 1]), pair_of(ks[k >> 3], ks[k >> 3]),
+                          pair_of(vs[k >> 3] + up, vs[k >> 3] + up));
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              uint32_t& w = s[g >> 1][(g & 1) * 16 + k];
-              w = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(w), x), less));
+            for (int g = 0; g < 2; ++g) {
+              uint64_t sum = 0ull;
+              float u, v;
+#pragma unroll
+              for (int k = 8 * g; k < 8 * g + 8; ++k) {
+                csa::split(y[k], &u, &v);
+                u = ex2(u);
+                v = ex2(v);
+                sum = add2(sum, pair_of(u, v));
+                p[k] = pack_f16(u, v);
+              }
+              csa::split(sum, &u, &v);
+              l = fmaf(u + v, ex2(down - vs[g]), l);
+            }
+            tmem_st16(s_tmem + 16 * c, p);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              x[0][k] = x[1][k];
+              x[1][k] = x[2][k];
+              x[2][k] = x[3][k];
+            }
+#pragma unroll
+            for (int g = 0; g < 6; ++g) {
+              ks[g] = ks[g + 2];
+              vs[g] = vs[g + 2];
             }
           }
-        }
-        const bool far = v_min - down < kFar;
-        if (__any_sync(0xffffffffu, far)) {
-          float sum = 0.f;
+        } else {
+          // Rare: exponents are one rounding, factor s - m, but where logits are so large
+          // that the rounding of m shows the products come first; where the weights' sum
+          // cannot be taken from the weights it has exponentials of its own.
+          const float less = large ? m : 0.f, up = large ? kWeightExp + (m - mv) : kWeightExp - mv;
+          const float minus_m = large ? 0.f : -m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32], p[16];
+            tmem_ld32(s_tmem + 32 * c, y);
+            tmem_wait_ld();
+            landed(y);
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g)
+            for (int h = 0; h < 2; ++h) {
+              float f = factor(k_scale_s[meta][2 * c + h]);
+              const float vs = v_log_s[meta][2 * c + h];
+              const float f_first = large ? f : 1.f;
+              if (large) f = 1.f;
+              float sum_u = 0.f, sum_v = 0.f, sum_far = 0.f;  // (in the order of the other way)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum += ex2(fmaf(__uint_as_float(s[g >> 1][(g & 1) * 16 + k]), cf[g], minus_m));
-          if (far) l += sum;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int g = 2 * c + h;
-            const uint64_t cf2 = pair_of(cf[g], cf[g]), up2 = pair_of(lv[g] + up, lv[g] + up);
-            uint64_t sum = 0ull;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float x, y;
-              csa::split(fma2(pair_of(s[c][16 * h + 2 * k], s[c][16 * h + 2 * k + 1]), cf2, up2), &x, &y);
-              x = ex2(x);
-              y = ex2(y);
-              sum = add2(sum, pair_of(x, y));
-              p[8 * h + k] = pack_f16(x, y);
+              for (int k = 0; k < 8; ++k) {
+                const float y0 = __fsub_rn(__fmul_rn(__uint_as_float(y[16 * h + 2 * k]), f_first), less);
+                const float y1 = __fsub_rn(__fmul_rn(__uint_as_float(y[16 * h + 2 * k + 1]), f_first), less);
+                const float u = ex2(fmaf(y0, f, vs + up)), v = ex2(fmaf(y1, f, vs + up));
+                sum_u += u;
+                sum_v += v;
+                sum_far += ex2(fmaf(y0, f, minus_m)) + ex2(fmaf(y1, f, minus_m));
+                p[8 * h + k] = pack_f16(u, v);
+              }
+              l = far ? l + sum_far : fmaf(sum_u + sum_v, ex2(down - vs), l);
             }
-            float sx, sy;
-            csa::split(sum, &sx, &sy);
-            if (!far) l = fmaf(sx + sy, ex2(down - lv[g]), l);
+            tmem_st16(s_tmem + 16 * c, p);
           }
-          tmem_st16(s_tmem + 16 * c, p);
         }
         tmem_wait_st();
         tc_fence_before();
