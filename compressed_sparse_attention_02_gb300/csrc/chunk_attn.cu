@@ -32,12 +32,12 @@
 // warps 48, the others 64.
 //
 // What bounds it: at width 128 the products of a block for 256 rows take 2050 cycles
-// alone; a block takes some 3300, a half's scores, softmax and product one after the
-// other while the other half is half a turn away, and neither instructions (46 % of
-// the issue slots) nor memory (2 % of it) are short.  Most of the softmax's 1600
-// cycles a half are waits for instructions: code that is not run again at once is
-// fetched at some 3 cycles an instruction, so what runs once a tile is kept short
-// and in rolled loops.  (2048 tokens at 62000, 32 heads on 8 of width 128: 1604 us,
+// alone; a block takes some 3400, a half's scores, softmax and product one after the
+// other while the other half is half a turn away (tensor pipe 59 % active, 63 % of
+// the issue slots used, memory 1 %).  A half's softmax is some 1600 of them, with one
+// warp a scheduler at a time.  Code that is not run again at once is fetched at some
+// 3 cycles an instruction, so the softmax is rolled where it can be, and so is all
+// that runs once a tile.  (2048 tokens at 62000, 32 heads on 4 of width 128: 1604 us,
 // 1.35 PFLOP/s counting each product once, 71 % of what a 16-bit library product
 // reaches; 12 prompts of up to 1000 tokens behind up to 6000: 546 us; 48 mixed
 // sequences of width 64 under a window of 4096: 304 us; 5 tokens after 900: 17 us,
