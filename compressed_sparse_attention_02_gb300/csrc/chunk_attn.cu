@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float v_min_s[C::kMeta];          // the least of the block's value scales, in log2
   __shared__ uint32_t bad_s[C::kMeta];         // groups whose page is outside the pool
   __shared__ float q_scale_s[2][kTile];
-  __shared__ float m_s[2][kTile], mv_s[2][kTile], l_s[2][kTile];
+  __shared__ float m_s[2][kTile], d_s[2][kTile], l_s[2][kTile];
   // keys of masked blocks whose values had NaN codes, as each converting warp
   // found them, of three tiles (who converts for tile n + 2 knows that every warp
   // has begun tile n): those of tile number n are valid if odd_item[n % 3] is n + 1
@@ -1099,7 +1099,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the row's keys [first_key, last_key]
       const int last_key = row < o.rows ? qi + o.shift : -1;
       const int first_key = a.window > 0 && last_key >= a.window ? last_key - a.window + 1 : 0;
-      float m = kNone, mv = kNone, l = 0.f;
+      // The sum l is in units of 2^m, m the largest logit so far; the weighted values
+      // are in units of 2^(m + d - kWeightExp), d the largest logit + log2(v_scale),
+      // seen from m.  (As a number of its own that would be a multiple of 16 where
+      // logits are of 2^28, and weights would leave f16.)
+      float m = kNone, d = 0.f, l = 0.f;
       const int step = split ? 2 : 1;
       bool began = false;
       auto factor = [&](float ks) { return fmaxf(fac * ks, FLT_MIN); };  // (not 0: a masked score is -inf, and stays so under it)
@@ -1138,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t x[4][32];
         float ks[kGroups], vs[kGroups];
-        float top = -INFINITY, topv = -INFINITY;
+        float top = -INFINITY, w[kGroups];
         {
           tmem_ld32(s_tmem, x[0]);
           tmem_ld32(s_tmem + 32, x[1]);
@@ -1163,23 +1167,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
             const uint32_t* u = x[g >> 1] + (g & 1) * 16;
-            float w = fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1]));
+            w[g] = fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1]));
 #pragma unroll
-            for (int k = 2; k < 16; k += 2) w = max3(w, __uint_as_float(u[k]), __uint_as_float(u[k + 1]));
-            w *= ks[g];
-            top = fmaxf(top, w);
-            topv = fmaxf(topv, w + vs[g]);
+            for (int k = 2; k < 16; k += 2) w[g] = max3(w[g], __uint_as_float(u[k]), __uint_as_float(u[k + 1]));
+            w[g] *= ks[g];
+            top = fmaxf(top, w[g]);
           }
         }
+        // d so far and of this block, both seen from the larger maximum
+        const float both = fmaxf(m, top), d_old = d + (m - both);
+        float d_new = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) d_new = fmaxf(d_new, w[g] - both + vs[g]);
         // (a row whose own maximum has not grown keeps its reference, so that no bit
         // of it depends on what only the warp's other rows see)
-        const bool grown = top - m > kLag || topv - mv > kLag;
+        const bool grown = top - m > kLag || d_new - d_old > kLag;
         if (__any_sync(0xffffffffu, grown)) {
-          const float m1 = grown ? fmaxf(m, top) : m, mv1 = grown ? fmaxf(mv, topv) : mv;
-          l *= ex2(m - m1);
-          const float f = ex2(mv - mv1);
-          m = m1;
-          mv = mv1;
+          float f = 1.f;
+          if (grown) {
+            const float d1 = fmaxf(d_old, d_new);
+            l *= ex2(m - both);
+            f = ex2(d_old - d1);
+            m = both;
+            d = d1;
+          }
           if (began) {  // (the half's products before have finished: these scores were issued after them)
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
@@ -1193,15 +1204,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         began = true;
-        const float down = mv - kWeightExp - m;
-        const bool large = fmaxf(fabsf(m), fabsf(mv)) > kLarge && m > kNone, far = v_min - down < kFar;
+        const float down = d - kWeightExp;
+        const bool large = fabsf(m) > kLarge && m > kNone, far = v_min - down < kFar;
         if (!__any_sync(0xffffffffu, large || far)) {
           // 32 keys a turn, the scores behind them moved up in the registers: code for all
           // 128 is faster where one long sequence keeps the loop in the instruction
           // caches (2048 tokens at 62000 1535 us, 1604 so) and slower where tiles end
           // often (12 prompts 584 us, 546 so; 48 mixed sequences 312, 304).  Reading the
           // scores again from tensor memory instead takes 1690 and 564 us.
-          const float up = kWeightExp - mv;
+          const float up = -down - m;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t p[16];
@@ -1242,7 +1253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Rare: exponents are one rounding, factor s - m, but where logits are so large
           // that the rounding of m shows the products come first; where the weights' sum
           // cannot be taken from the weights it has exponentials of its own.
-          const float less = large ? m : 0.f, up = large ? kWeightExp + (m - mv) : kWeightExp - mv;
+          const float less = large ? m : 0.f, up = large ? -down : -down - m;
           const float minus_m = large ? 0.f : -m;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -1282,7 +1293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool have[2] = {true, !split || o.blocks > 1};
       if (split) {
         m_s[t][r] = m;
-        mv_s[t][r] = mv;
+        d_s[t][r] = d;
         l_s[t][r] = l;
         mbar_arrive(&joined);
         ok = await(&joined, n_split & 1u, &watch) &&
@@ -1298,14 +1309,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       float f0 = 1.f, f1 = 0.f;  // of the halves' sums
       if (split) {
-        const float ma = m_s[0][r], mb = m_s[1][r], va = mv_s[0][r], vb = mv_s[1][r];
-        m = fmaxf(ma, mb);
-        mv = fmaxf(va, vb);
+        const float ma = m_s[0][r], mb = m_s[1][r], da = d_s[0][r], db = d_s[1][r];
+        m = ma;
+        d = da;
+        join_units(m, d, mb, db);
         l = l_s[0][r] * ex2(ma - m) + l_s[1][r] * ex2(mb - m);
-        f0 = ex2(va - mv);
-        f1 = ex2(vb - mv);
+        f0 = ex2(in_unit(ma, da, m, d));
+        f1 = ex2(in_unit(mb, db, m, d));
       }
-      const float unit = mv - kWeightExp;
+      const float unit = d - kWeightExp;
       const int64_t out_row = static_cast<int64_t>(o.q0 + qi) * a.n_heads + o.head0 + hd;
       float* part = a.part + gridDim.x * (sizeof(Cut) / sizeof(float)) + (blockIdx.x * 2 + max(o.record, 0)) * C::kRecord;
       float f = 1.f;
@@ -1442,12 +1454,11 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
   if (cut.rows > kFewRows) {
     const int r = blockIdx.y * kMergeRows + tid % kMergeRows;
     if (r >= cut.rows) return;
-    float m = kNone, unit = kNone;
+    float m = kNone, unit = 0.f;
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
       const float4 y = stats(k, r);
-      m = fmaxf(m, y.x);
-      unit = fmaxf(unit, y.z);
+      join_units(m, unit, y.x, y.z);
     }
     for (int c = tid / kMergeRows; c < D / 4; c += kMergeThreads / kMergeRows) {
       float l = 0.f;
@@ -1456,7 +1467,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
       for (int k = 0; k < n; ++k) {
         const float4 y = stats(k, r), x = *reinterpret_cast<const float4*>(record(k) + (c * kTileRows + r) * 4);
         l += y.y * ex2(y.x - m);
-        const float f = ex2(y.z - unit);
+        const float f = ex2(in_unit(y.x, y.z, m, unit));
         z.x = fmaf(x.x, f, z.x);
         z.y = fmaf(x.y, f, z.y);
         z.z = fmaf(x.z, f, z.z);
@@ -1473,25 +1484,20 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
   constexpr int kPer = D / 32;  // channels a lane, neighbours
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   for (int r = blockIdx.y; r < cut.rows; r += kMergeCtas) {
-    float m = kNone, unit = kNone, l = 0.f, z[kPer];
+    float m = kNone, unit = 0.f, l = 0.f, z[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) z[j] = 0.f;
     for (int k = lane; k < n; k += 32) {
       const float4 y = stats(k, r);
-      m = fmaxf(m, y.x);
-      unit = fmaxf(unit, y.z);
+      join_units(m, unit, y.x, y.z);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, off));
-    }
+    join_lanes(m, unit);
 #pragma unroll 4
     for (int k = warp; k < n; k += kMergeWarps) {
       const float4 y = stats(k, r);
       const Vec v = *reinterpret_cast<const Vec*>(record(k) + r * D + lane * kPer);
       l += y.y * ex2(y.x - m);
-      const float f = ex2(y.z - unit);
+      const float f = ex2(in_unit(y.x, y.z, m, unit));
       const float* x = reinterpret_cast<const float*>(&v);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) z[j] = fmaf(x[j], f, z[j]);

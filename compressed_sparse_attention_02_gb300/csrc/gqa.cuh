@@ -145,15 +145,41 @@ __device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
 }
 // From a row's sum of weights l in units of 2^m to the factor of its weighted
-// values, which are in units of 2^unit, and its lse, the sink's weight in.
+// values, which are in units of 2^(m + unit), and its lse, the sink's weight in.
+// (unit is kept apart from m: of a logit of 2^28 fp32 holds no more than its
+// multiples of 16, so that m + unit would lose what a value scale and f16's room
+// add to it.)
 __device__ __forceinline__ float finish_row(float m, float unit, float l, const float* sink, int head, float* lse) {
   if (sink) {
     const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
     l = l * ex2(m - m1) + ex2(s2 - m1);
+    unit += m - m1;
     m = m1;
   }
   *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  return l == 0.f ? 0.f : ex2(unit - m) / l;
+  return l == 0.f ? 0.f : ex2(unit) / l;
+}
+
+// The references of two parts of a row, sums of weights in units of 2^m and
+// weighted values in units of 2^(m + unit), become those of both: a part's sums
+// then count 2^(m' - m) and 2^in_unit(m', unit', m, unit) times.
+__device__ __forceinline__ void join_units(float& m, float& unit, float m2, float unit2) {
+  const float top = fmaxf(m, m2);
+  unit = fmaxf(unit + (m - top), unit2 + (m2 - top));
+  m = top;
+}
+// (those of a warp's lanes)
+__device__ __forceinline__ void join_lanes(float& m, float& unit) {
+  float top = m;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  unit += m - top;
+  m = top;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, off));
+}
+__device__ __forceinline__ float in_unit(float m2, float unit2, float m, float unit) {
+  return unit2 + (m2 - m) - unit;
 }
 
 // Finds the sequence that work item w belongs to, where sequence b has

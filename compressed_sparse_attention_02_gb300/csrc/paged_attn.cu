@@ -65,7 +65,7 @@ struct Cfg {
 
 template <int D>
 constexpr int kRecord = kRows * (D + 4);  // floats of a partial result: sums, and a float4 a row: m, the weights'
-                                          // sum (in units of 2^m), the sums' unit (log2), nothing
+                                          // sum (in units of 2^m), the sums' unit (log2, from m on), nothing
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -383,11 +383,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
     float o[kN][4];
 #pragma unroll
     for (int j = 0; j < kN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[H], mv[H], room = 0.f;  // room: the value scale up to which no weight is far
+    // the sums' reference 2^m; weighted values are in units of 2^(m + d - kWeightExp),
+    // d the largest logit + log2(v_scale) seen from m (see finish_row); room: the value
+    // scale up to which no weight is far
+    float m[H], d[H], room = 0.f;
     uint64_t l2[H];  // sums of weights, as pairs of partial sums
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      m[h] = mv[h] = kNone;
+      m[h] = kNone;
+      d[h] = 0.f;
       l2[h] = 0ull;
     }
 
@@ -442,15 +446,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
         }
         // maxima of the logits, and of logit + log2(v_scale), the weights' exponents
         const float lv[2] = {__log2f(sc.z), __log2f(sc.w)};
-        float top[H], topv[H];
+        float tops[2][H];
         bool grown = sc.z > room || sc.w > room;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          const float a0 = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
-          const float a1 = fmaxf(fmaxf(x[2][2 * h], x[2][2 * h + 1]), fmaxf(x[3][2 * h], x[3][2 * h + 1]));
-          top[h] = fmaxf(a0, a1);
-          topv[h] = fmaxf(a0 + lv[0], a1 + lv[1]);
-          grown |= top[h] > m[h] + kLag || topv[h] > mv[h] + kLag;
+          tops[0][h] = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+          tops[1][h] = fmaxf(fmaxf(x[2][2 * h], x[2][2 * h + 1]), fmaxf(x[3][2 * h], x[3][2 * h + 1]));
+#pragma unroll
+          for (int s = 0; s < 2; ++s) grown |= tops[s][h] - m[h] > fminf(kLag, d[h] + kLag - lv[s]);
         }
         uint32_t pf[2][2 * H];
         auto weights = [&](auto apart) {
@@ -465,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
               const uint64_t p01 = pair_of(ex2(p0), ex2(p1)), p23 = pair_of(ex2(p2), ex2(p3));
               l2[h] = add2(l2[h], add2(p01, p23));
               if constexpr (apart) {
-                const float up = lv[s] + kWeightExp;
-                p0 = ex2(x[2 * s][2 * h] - mv[h] + up);
-                p1 = ex2(x[2 * s][2 * h + 1] - mv[h] + up);
-                p2 = ex2(x[2 * s + 1][2 * h] - mv[h] + up);
-                p3 = ex2(x[2 * s + 1][2 * h + 1] - mv[h] + up);
+                const float up = lv[s] - d[h] + kWeightExp;
+                p0 = ex2(p0 + up);
+                p1 = ex2(p1 + up);
+                p2 = ex2(p2 + up);
+                p3 = ex2(p3 + up);
               } else {
-                const float w = ex2(lv[s] + (m[h] - mv[h]) + kWeightExp);
+                const float w = ex2(lv[s] - d[h] + kWeightExp);
                 const uint64_t ww = pair_of(w, w);
                 split(mul2(p01, ww), &p0, &p1);
                 split(mul2(p23, ww), &p2, &p3);
@@ -517,23 +520,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
           for (int h = 0; h < H; ++h) {
+            float m1 = fmaxf(m[h], fmaxf(tops[0][h], tops[1][h]));
 #pragma unroll
-            for (int off = 1; off < 4; off <<= 1) {
-              top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
-              topv[h] = fmaxf(topv[h], __shfl_xor_sync(0xffffffffu, topv[h], off));
-            }
-            const float m1 = fmaxf(m[h], top[h]), mv1 = fmaxf(mv[h], topv[h]);
+            for (int off = 1; off < 4; off <<= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
+            const float d0 = d[h] + (m[h] - m1);
+            float d1 = fmaxf(d0, fmaxf(tops[0][h] - m1 + lv[0], tops[1][h] - m1 + lv[1]));
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, off));
             const float fl = ex2(m[h] - m1);
             l2[h] = mul2(l2[h], pair_of(fl, fl));
-            const float f = ex2(mv[h] - mv1);
+            const float f = ex2(d0 - d1);
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
               o[j][2 * h] *= f;
               o[j][2 * h + 1] *= f;
             }
             m[h] = m1;
-            mv[h] = mv1;
-            room = h == 0 ? mv1 - m1 : fminf(room, mv1 - m1);
+            d[h] = d1;
+            room = h == 0 ? d1 : fminf(room, d1);
           }
           room = ex2(room + kFar);
           if (__any_sync(0xffffffffu, sc.z > room || sc.w > room)) {
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
       __syncwarp();
       issue();
     }
-    // The pair's rows, or this share's part of them in units of 2^mv / 2^kWeightExp
+    // The pair's rows, or this share's part of them in units of 2^(m + d) / 2^kWeightExp
     // (not of 2^m: the two can be further apart than fp32's exponents).
     // Accumulator tile j holds channels 2cq * D/8 + j and (2cq + 1) * D/8 + j.
     const bool whole = take == nt;
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, H>::kCtas) paged_attn_kernel(
       l += other;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const float unit = mv[h] - kWeightExp;
+      const float unit = d[h] - kWeightExp;
       if (r >= rows) continue;
       if (whole) {
         const int64_t row = static_cast<int64_t>(c.b) * a.n_heads + head0 + r;
@@ -643,25 +647,20 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
   };
   for (int r = SPLIT == 1 ? warp : blockIdx.y; r < rows; r += SPLIT == 1 ? kMergeWarps : gridDim.y) {
     const int part = SPLIT == 1 ? 0 : warp;
-    float m = kNone, unit = kNone, l = 0.f, n[kPer];
+    float m = kNone, unit = 0.f, l = 0.f, n[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) n[j] = 0.f;
     for (int k = part + lane * SPLIT; k < n_rec; k += 32 * SPLIT) {
       const float4 y = *reinterpret_cast<const float4*>(record(k) + kRows * D + 4 * r);
-      m = fmaxf(m, y.x);
-      unit = fmaxf(unit, y.z);
+      join_units(m, unit, y.x, y.z);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, off));
-    }
+    join_lanes(m, unit);
 #pragma unroll 4
     for (int k = part; k < n_rec; k += SPLIT) {
       const float* p = record(k);
       const float4 w = *reinterpret_cast<const float4*>(p + kRows * D + 4 * r);
       l += w.y * ex2(w.x - m);
-      const float f = ex2(w.z - unit);
+      const float f = ex2(in_unit(w.x, w.z, m, unit));
       const Vec v = *reinterpret_cast<const Vec*>(p + r * D + lane * kPer);
       const float* y = reinterpret_cast<const float*>(&v);
 #pragma unroll
@@ -679,17 +678,18 @@ __global__ void __launch_bounds__(32 * merge_warps(SPLIT))
       __syncthreads();
       if (part != 0) continue;
       const float m0 = m, unit0 = unit;
-      for (int w = 1; w < SPLIT; ++w) {
-        m = fmaxf(m, m_s[w]);
-        unit = fmaxf(unit, u_s[w]);
-      }
+#pragma unroll
+      for (int w = 1; w < SPLIT; ++w) m = fmaxf(m, m_s[w]);
+      unit += m0 - m;
+#pragma unroll
+      for (int w = 1; w < SPLIT; ++w) unit = fmaxf(unit, u_s[w] + (m_s[w] - m));
       l *= ex2(m0 - m);
-      const float f0 = ex2(unit0 - unit);
+      const float f0 = ex2(in_unit(m0, unit0, m, unit));
 #pragma unroll
       for (int j = 0; j < kPer; ++j) n[j] *= f0;
       for (int w = 1; w < SPLIT; ++w) {
         l += l_s[w] * ex2(m_s[w] - m);
-        const float f = ex2(u_s[w] - unit);
+        const float f = ex2(in_unit(m_s[w], u_s[w], m, unit));
 #pragma unroll
         for (int j = 0; j < kPer; ++j) n[j] += n_s[w][lane * kPer + j] * f;
       }

@@ -1,0 +1,98 @@
+"""The paged cache's attention and its pages at the edges of what the calls
+take: logits far past what fp32 resolves to one, next to value scales of any
+size."""
+import pytest
+import torch
+
+import _gqa as ref
+import test_gpu_chunk_attn as chunk
+import test_gpu_paged_attn as paged
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def csa():
+    import compressed_sparse_attention_02_gb300 as m
+    return m
+
+
+# ---- large logits ----------------------------------------------------------------------
+
+# Heads' logits are 2^(a - 3) times 1 or 2, or times -1 or -1/2.  From the second head on a
+# row's largest logit stands 2^9 and more above its other ones, whose weights are then 0 in
+# 64 bits as in 32, and keys of equal logits have equal ones in fp32 too: their products are
+# the same.  So no error of a logit has a part in the result, and the tolerance has none for
+# it.
+POWERS = (3, 13, 20, 25, 29, 31, 63, 99)
+
+
+def large(seqs, Hkv, D, P, scales, seed, sign):
+    """Sequences whose keys have 1 or (one in 37) 2 or 1/2 in the channel that the queries have; pages of value scale 2^e for
+    the e of `scales`, or (None) of zeros with the scale 2^-126 that the append gives them."""
+    x = chunk.make(seqs, Hkv * len(POWERS), Hkv, D, P, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    n = x["k"].shape[0]
+    codes = (torch.rand(n, Hkv, P, D, generator=g) * 7 + 1) * (torch.randint(0, 2, (n, Hkv, P, D), generator=g) * 2 - 1)
+    written = ~x["v"].float().isnan().cpu()
+    e = torch.randint(0, len(scales), (n,), generator=g)
+    for i, s in enumerate(scales):
+        x["vs"][e == i] = 2.0 ** (-126 if s is None else s)
+        if s is None:
+            codes[e == i] = 0.0
+    x["v"] = codes.where(written, float("nan")).to(torch.float8_e4m3fn).to(DEV)
+    k = x["k"].float().cpu()
+    k[..., 0] = 1.0
+    for b, L in enumerate(x["lens"].tolist()):
+        t = torch.arange(5, L, 37)
+        k[x["table"][b].cpu().long()[t // P], :, t % P, 0] = 2.0 if sign > 0 else 0.5
+    x["k"] = k.where(written, float("nan")).to(torch.float8_e4m3fn).to(DEV)
+    x["ks"].fill_(1.0)
+    x["q"].zero_()
+    x["q"][..., 0] = sign * torch.exp2(torch.tensor(POWERS * Hkv, device=DEV).float())
+    return x
+
+
+def exact(want, x, **kw):
+    """`want` without an allowance for logits' errors.  Past 2^53 a logit of 64 bits does not hold its sum's logarithm
+    either: such heads' weights are those of 2^29, their lse the largest logit."""
+    powers = torch.tensor(POWERS * (x["q"].shape[1] // len(POWERS)))
+    less = (powers - 29).clamp(min=0)
+    q = (x["q"].double() * torch.exp2(-less.double()).to(DEV)[:, None]).bfloat16()
+    out, lse, A, Q = want(dict(x, q=q), sm=0.125, **kw)
+    return out, lse * torch.exp2(less.double()), A, Q * (powers == POWERS[0])
+
+
+SCALES = [(0,), (20,), (-30,), (0, None), (0, 40), (-100, 30), (0, -60, 9), (100, None)]
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("scales", SCALES)
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+def test_chunk_attn_of_large_logits(csa, D, P, scales, sign):
+    """In tiles that a share holds whole, some of one block, and in tiles that many shares divide."""
+    for seqs, Hkv in (([(2, 300), (40, 130)] * 40 + [(1, 50)] * 60, 2), ([(3, 100), (4, 2500), (40, 2000)], 1)):
+        x = large(seqs, Hkv, D, P, scales, 17 + D, sign)
+        out, lse = chunk.run(csa, x, sm=0.125)
+        n = int(x["cu"][-1])
+        rows = list(range(0, n, 1 + n // 30))
+        w = exact(chunk.want, x, rows=rows)
+        ref.check_attention(out[rows], lse[rows], *w, chunk.STEP, "large logits")
+    assert csa.csa_check_status() == 0
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("scales", SCALES)
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+def test_paged_attn_of_large_logits(csa, D, P, scales, sign):
+    """The same for single tokens: pairs of a sequence and a key head that one warp has whole, and divided ones, whose
+    parts a warp or several join."""
+    for lens, Hkv in (([300, 40, 7] * 100, 2), ([250] * 50, 1), ([3000], 1)):
+        x = large([(1, L) for L in lens], Hkv, D, P, scales, 29 + D, sign)
+        out, lse = paged.run(csa, x, sm=0.125)
+        some = list(range(0, len(lens), 1 + len(lens) // 40))
+        y = dict(x, q=x["q"][some], lens=x["lens"][some], table=x["table"][some])
+        w = exact(paged.want, y)
+        ref.check_attention(out[some], lse[some], *w, paged.STEP, "large logits")
+    assert csa.csa_check_status() == 0
