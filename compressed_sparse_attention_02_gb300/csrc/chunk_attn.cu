@@ -79,7 +79,7 @@ constexpr float kWeightExp = 7.f;
 // pass fp32 while e^(l - m) counts: the sum then has exponentials of its own.
 constexpr float kFar = -64.f;
 constexpr float kLarge = 65536.f;           // a maximum whose half step, 2^-8, may show in a weight
-constexpr float kNone = -1e30f;             // running maximum before the first key
+constexpr float kNone = -1e31f;             // running maximum before the first key: below every logit times log2 e
 // Blocks that some row of a tile masks: the causal edge of 256 rows crosses at
 // most 3, the window's edge 3.
 constexpr int kMaxMasked = 8;

@@ -150,13 +150,15 @@ __device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
 // multiples of 16, so that m + unit would lose what a value scale and f16's room
 // add to it.)
 __device__ __forceinline__ float finish_row(float m, float unit, float l, const float* sink, int head, float* lse) {
+  float none = -INFINITY;  // lse where nothing has weight: the sink's, which may be below every m
   if (sink) {
-    const float s2 = __ldg(sink + head) * kLog2e, m1 = fmaxf(m, s2);
+    none = __ldg(sink + head);
+    const float s2 = none * kLog2e, m1 = fmaxf(m, s2);
     l = l * ex2(m - m1) + ex2(s2 - m1);
     unit += m - m1;
     m = m1;
   }
-  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  *lse = l == 0.f ? none : (m + log2f(l)) * kLn2;
   return l == 0.f ? 0.f : ex2(unit) / l;
 }
 

@@ -47,7 +47,7 @@ constexpr float kWeightExp = 11.f;
 // weight is one exponential instead: the factor could pass fp32, and up to
 // here no weight that f16 holds (2^-24 and more) has an e^(l - m) that fp32 flushes.
 constexpr float kFar = 64.f - kWeightExp;
-constexpr float kNone = -1e30f;           // running maximum before the first token
+constexpr float kNone = -1e31f;           // running maximum before the first token: below every logit times log2 e
 
 // H: halves of the 16 rows that hold query heads (1: groups of up to 8).
 template <int D, int H>

@@ -1,12 +1,13 @@
-"""The paged cache's attention and its pages at the edges of what the calls
-take: logits far past what fp32 resolves to one, next to value scales of any
-size."""
+"""The grouped-query attention calls and the cache's pages at the edges of what
+they take: logits far past what fp32 resolves to one, next to value scales of
+any size; logits near -1e30."""
 import pytest
 import torch
 
 import _gqa as ref
 import test_gpu_chunk_attn as chunk
 import test_gpu_paged_attn as paged
+import test_gpu_prompt_attn as prompt
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -95,4 +96,54 @@ def test_paged_attn_of_large_logits(csa, D, P, scales, sign):
         y = dict(x, q=x["q"][some], lens=x["lens"][some], table=x["table"][some])
         w = exact(paged.want, y)
         ref.check_attention(out[some], lse[some], *w, paged.STEP, "large logits")
+    assert csa.csa_check_status() == 0
+
+
+# ---- logits near the least that the calls take -----------------------------------------
+
+LEAST = -1.5 * 2.0 ** 99               # -9.5e29
+
+
+def lowest(make, seqs, Hq, D, c):
+    """make's book or prompts, every logit LEAST under a scale of 1/8 (from two factors that bf16 and the codes hold)."""
+    x = make(seqs, Hq, 1, D, *(() if c == "prompt" else (32,)), seed=D)
+    x["q"].zero_()
+    if c == "prompt":
+        x["q"][..., 0], x["k"][..., 0] = -1.5 * 2.0 ** 51, 2.0 ** 51
+    else:
+        x["q"][..., 0] = -1.5 * 2.0 ** 102
+        k = x["k"].float()
+        k[..., 0] = torch.where(k[..., 0].isnan(), k[..., 0], 1.0)
+        x["k"] = k.to(torch.float8_e4m3fn)
+        x["ks"].fill_(1.0)
+    x["sink"] = torch.tensor([LEAST / 2, LEAST * 0.75, LEAST, -3e38], device=DEV)
+    return x
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("call", ["chunk", "paged", "prompt"])
+def test_lowest_logits(csa, call, D):
+    """Rows all of whose logits are -9.5e29 have the mean of what they see, rows that see nothing their sink, however low
+    (a sink of -3e38 has no weight beside anything)."""
+    seqs = {"chunk": [(3, 100), (140, 400), (2, 0), (3, 1), (2, 5000)], "paged": [100, 0, 1, 5000],
+            "prompt": [(3, 100), (140, 400), (2, 0), (3, 1), (300, 300)]}[call]
+    of = {"chunk": chunk, "paged": paged, "prompt": prompt}[call]
+    x = lowest(of.make, seqs, 4, D, call)
+    same = dict(x, q=torch.zeros_like(x["q"]))      # (logits of 0: the same weights)
+    want, lse, A, Q = of.want(same, sm=0.125)
+    seen = ~torch.isinf(lse)
+    lse[seen] = LEAST
+    got = of.run(csa, x, sm=0.125)
+    ref.check_attention(*got, want, lse, A, Q, of.STEP, "lowest")
+    # beside a sink: all of the weight is the higher one's (LEAST itself: whose share is what follows from fp32 products)
+    sink = x["sink"].double().cpu()
+    got, got_lse = (y.double().cpu() for y in of.run(csa, x, sm=0.125, sink=True))
+    for h in range(4):
+        s = seen[:, h]
+        assert (got[~s, h] == 0).all() and ((got_lse[~s, h] - sink[h]).abs() <= 2.0 ** -20 * sink[h].abs()).all()
+        if h < 2:
+            assert (got[s, h] == 0).all() and ((got_lse[s, h] - sink[h]).abs() <= 2.0 ** -20 * sink[h].abs()).all()
+    s = seen[:, 3]
+    ref.check_attention(got[s][:, 3:], got_lse[s][:, 3:], want[s][:, 3:], lse[s][:, 3:], A[s][:, 3:], Q[s][:, 3:], of.STEP,
+                        "a sink without weight")
     assert csa.csa_check_status() == 0
