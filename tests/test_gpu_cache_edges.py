@@ -1,12 +1,14 @@
 """The grouped-query attention calls and the cache's pages at the edges of what
 they take: logits far past what fp32 resolves to one, next to value scales of
-any size; logits near -1e30."""
+any size; logits near -1e30; arrays beside which nothing else may be written."""
+import numpy as np
 import pytest
 import torch
 
 import _gqa as ref
 import test_gpu_chunk_attn as chunk
 import test_gpu_paged_attn as paged
+import test_gpu_pages as pages
 import test_gpu_prompt_attn as prompt
 
 pytestmark = pytest.mark.gpu
@@ -147,3 +149,121 @@ def test_lowest_logits(csa, call, D):
     ref.check_attention(got[s][:, 3:], got_lse[s][:, 3:], want[s][:, 3:], lse[s][:, 3:], A[s][:, 3:], Q[s][:, 3:], of.STEP,
                         "a sink without weight")
     assert csa.csa_check_status() == 0
+
+
+# ---- nothing is written outside what a call is given -----------------------------------
+
+GUARD, MARGIN = 0x5A5A5A5A, 256
+
+
+class Margins:
+    """Arrays with filled memory directly before and behind them."""
+
+    def __init__(self):
+        self.whole = []
+
+    def take(self, shape, dtype=torch.int32):
+        n = -(-torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size() // 16) * 4
+        w = torch.full((n + 2 * MARGIN,), GUARD, dtype=torch.int32, device=DEV)
+        self.whole.append((w, MARGIN + n))
+        x = w[MARGIN:MARGIN + n].view(dtype)
+        return x[:torch.Size(shape).numel()].view(shape)
+
+    def like(self, x):
+        x = torch.as_tensor(x, dtype=None if torch.is_tensor(x) else torch.int32, device=DEV)
+        y = self.take(x.shape, x.dtype)
+        y.copy_(x)
+        return y
+
+    def check(self):
+        for w, end in self.whole:
+            assert (w[:MARGIN] == GUARD).all() and (w[end:] == GUARD).all()
+
+
+def guarded_book(csa, monkeypatch, m, table, lens, refs, page):
+    """A book of test_gpu_pages, every array of which, and the workspace, is in margins."""
+    monkeypatch.setattr(pages, "i32", lambda x: m.like(torch.tensor(np.asarray(x), dtype=torch.int32)))
+    monkeypatch.setattr(pages.Both, "outs", lambda self, n, k: [m.take((k,)).fill_(77) for _ in range(n)])
+    x = pages.Both(csa, table, lens, refs, page)
+    x.ws = m.take((x.ws.numel(),), torch.uint8).fill_(0xA5)
+    return x
+
+
+def compacted(csa, m, x):
+    """Out of place and then in place."""
+    src, dst = x.outs(2, len(x.host.refs) // 2)
+    used, = x.outs(1, 1)
+    csa.csa_pages_compact(x.book, src, dst, used, m.take(x.table.shape), m.take(x.refs.shape), x.ws)
+    csa.csa_check_status()
+    x.compact(in_place=True)
+
+
+def test_page_calls_write_in_their_arrays_alone(csa, monkeypatch):
+    """Lengths past the table and below 0, entries outside the pool, counts that do not fit, targets past the table,
+    parents that are none, pools that run out, tables of one entry."""
+    table = np.array([[0, 1, 2], [3, -7, 99], [5, 6, 2 ** 31 - 1], [-1, -1, -1]], np.int32)
+    refs = np.array([1, 1, 1, 1, 0, 1, 0, -4], np.int32)
+    m = Margins()
+    for lens, call in (([100, 40, 48, -3], lambda x: x.resize([48, 41, 2 ** 31 - 1, 17])),
+                       ([100, 40, 48, -3], lambda x: x.resize([0, 0, 1, 0])),
+                       ([48, 48, 48, 48], lambda x: x.resize([0, 0, 0, 0])),
+                       ([2 ** 31 - 1, -2 ** 31, 48, 0], lambda x: x.resize([-2 ** 31, 2 ** 31 - 1, 49, 48])),
+                       ([48, 40, 48, -3], lambda x: x.fork([-1, -1, -1, 1])),
+                       ([48, 0, 40, 0], lambda x: x.fork([4, 2 ** 31 - 1, -2 ** 31, 2])),
+                       ([2 ** 31 - 1, 0, 0, 0], lambda x: x.fork([-1, 0, 0, 3])),
+                       ([100, 40, 48, -3], lambda x: compacted(csa, m, x))):
+        x = guarded_book(csa, monkeypatch, m, table, lens, refs, 16)
+        x.host.refused = max(lens) > 48      # (reported, as the header has it; the host's steps only cut such lengths)
+        call(x)
+        m.check()
+    for pool in (1, 31, 33, 4097):
+        x = guarded_book(csa, monkeypatch, m, np.full((5, 1), -1, np.int32), [0] * 5, np.zeros(pool, np.int32), 128)
+        x.resize([1, 128, 129, 0, 2 ** 31 - 1])
+        x.fork([-1, -1, -1, 0, 0])
+        x.resize([0, -1, -1, -1, -1])
+        compacted(csa, m, x)
+        x.resize([128] * 5)
+        compacted(csa, m, x)
+        m.check()
+
+
+def test_page_copies_write_in_their_pages_alone(csa):
+    H, P, D, n = 3, 32, 64, 9
+    m = Margins()
+    g = torch.Generator(DEV).manual_seed(1)
+    k, v = (m.like(torch.randint(0, 256, (n, H, P, D), device=DEV, generator=g, dtype=torch.uint8)) for _ in range(2))
+    ks, vs = (m.like(torch.rand(n, H, device=DEV, generator=g)) for _ in range(2))
+    cache = csa.paged_cache(k, v, ks, vs, m.take((1, 1)))
+    before = [x.clone() for x in (k, v, ks, vs)]
+    src = m.like([0, 3, -1, 8, 9, 2, 2 ** 31 - 1, -2 ** 31, 5])
+    dst = m.like([1, 9, 4, 8, 7, 2 ** 31 - 1, 6, 3, -1])
+    csa.csa_pages_copy(cache, src, dst)
+    assert csa.csa_check_status() == 5
+    for x, y in zip((k, v, ks, vs), before):
+        y[1] = y[0]
+        assert torch.equal(x, y)
+    m.check()
+
+
+def test_chunk_attn_writes_in_its_outputs_alone(csa):
+    """Whole tiles, divided ones and their records, offsets and tables that are wrong among them."""
+    for D, seqs in ((64, [(5, 300), (260, 700), (0, 9), (40, 90)]), (128, [(70, 3000), (1, 2000), (3, 5)])):
+        x = chunk.make(seqs, 8, 2, D, 32, seed=D)
+        n = x["q"].shape[0]
+        cache = csa.paged_cache(x["k"], x["v"], x["ks"], x["vs"], x["table"])
+        for cu, page, length in (([], None, None), ([(1, 2 ** 31 - 1)], 5, None), ([(2, -2 ** 31), (3, n + 1)], -1, 2 ** 31 - 1),
+                                 ([(0, 3), (2, 1)], 2 ** 31 - 1, -2 ** 31)):
+            y = dict(x, cu=x["cu"].clone(), table=x["table"].clone(), lens=x["lens"].clone())
+            for i, value in cu:
+                y["cu"][i] = value
+            if page is not None:
+                y["table"][0, 1] = page
+            if length is not None:
+                y["lens"][1] = length
+            m = Margins()
+            out, lse = m.take((n, 8, D), torch.bfloat16), m.take((n, 8), torch.float32)
+            ws = m.take((csa.chunk_attn_workspace(cache, 8).numel(),), torch.uint8)
+            bad = csa.paged_cache(x["k"], x["v"], x["ks"], x["vs"], y["table"])
+            csa.csa_chunk_attn(bad, y["cu"], y["lens"], x["q"], D ** -0.5, 0, x["sink"], out, lse, ws)
+            assert csa.csa_check_status() == (5 if cu else 0)
+            m.check()
