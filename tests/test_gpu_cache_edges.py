@@ -267,3 +267,24 @@ def test_chunk_attn_writes_in_its_outputs_alone(csa):
             csa.csa_chunk_attn(bad, y["cu"], y["lens"], x["q"], D ** -0.5, 0, x["sink"], out, lse, ws)
             assert csa.csa_check_status() == (5 if cu else 0)
             m.check()
+
+
+# ---- a chunk far into a sequence -------------------------------------------------------
+
+def test_chunk_far_into_a_long_sequence(csa):
+    """2048 tokens behind 60000 of 32 query heads on 4: rows at the tiles' and the chunk's ends against 64 bits."""
+    D, P, n, L, heads = 128, 128, 2048, 62048, (0, 13, 31)
+    x = chunk.make([(n, L)], 32, 4, D, P, seed=62)
+    rows = [0, 31, 32, 33, 1000, 2015, 2016, 2047]
+    out, lse = chunk.run(csa, x)
+    assert csa.csa_check_status() == 0
+    pages_of = x["table"][0].long()
+    for h in heads:
+        k, v = ((x[c][pages_of, h // 8].double() * x[c + "s"][pages_of, h // 8].double()[:, None, None])
+                .reshape(-1, D)[:L].cpu() for c in "kv")
+        q = x["q"][rows, h].double().cpu()
+        seen = torch.arange(L) <= torch.tensor(rows)[:, None] + L - n
+        want, want_lse, A, Q = ref.attend(q, k, v, D ** -0.5, seen)
+        # (what a query's two parts leave out, as test_gpu_chunk_attn.want has it)
+        Q += 0.5 * q.abs().amax(1) * k.abs().sum(1).max() * D ** -0.5
+        ref.check_attention(out[rows, h], lse[rows, h], want, want_lse, A, Q, chunk.STEP, "far into a sequence")
