@@ -183,20 +183,9 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t 
                "r"(c2)
                : "memory");
 }
-// Two fp32 values as f16, the first in the low half.
-__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Four E4M3 codes (low byte first) as two pairs of f16, exact.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
 }
 // The nearest E4M3 codes of four f16 values, the first in the low byte.
 __device__ __forceinline__ uint32_t f16x4_to_e4m3(uint32_t xy, uint32_t zw) {

@@ -3,6 +3,7 @@
 // sequences of different lengths.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "kernels.h"
@@ -143,6 +144,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
 }
 __device__ __forceinline__ void split(uint64_t p, float* x, float* y) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
+}
+// Four E4M3 codes (low byte first) as two pairs of f16, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+// Two fp32 values as f16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // From a row's sum of weights l in units of 2^m to the factor of its weighted
 // values, which are in units of 2^(m + unit), and its lse, the sink's weight in.

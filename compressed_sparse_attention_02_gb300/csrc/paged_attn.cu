@@ -89,13 +89,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-// Four E4M3 codes (low byte first) as two pairs of f16, exact.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
-}
-
 // c += a b; a of the halves that hold heads (the other half's rows are zero,
 // and so stay its sums).
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -107,11 +100,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)
 }
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
   mma_f16_16816(c, {a[0], 0u, a[1], 0u}, b0, b1);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Where 16-byte chunk c of row r of a 32-row tile lies: rows of 128 bytes

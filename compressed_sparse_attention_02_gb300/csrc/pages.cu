@@ -114,39 +114,38 @@ __device__ __forceinline__ T sum_before(T n, T* sh, T* all) {
 }
 
 // Looks at a stretch of the counts: a bit a page and the free pages' number.  Every
-// thread of the CTA calls it; sh holds THREADS / 32 values.
-template <int THREADS>
+// thread of the CTA calls it; sh holds kSumThreads / 32 values.
 __device__ __forceinline__ void scan_stretch(const PageBook& k, const Work& w, int shift, int s, int64_t* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = static_cast<int64_t>(s) << shift, end = min(first + (int64_t(1) << shift), k.n_pages);
   int n = 0;
   constexpr int kFlight = 4;  // words a warp
-  for (int64_t p0 = first + warp * 32; p0 < end; p0 += kFlight * THREADS) {
+  for (int64_t p0 = first + warp * 32; p0 < end; p0 += kFlight * kSumThreads) {
     int32_t r[kFlight];
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
-      const int64_t p = p0 + i * THREADS + lane;
+      const int64_t p = p0 + i * kSumThreads + lane;
       r[i] = p < end ? k.refs[p] : 1;
     }
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
       const uint32_t word = __ballot_sync(0xffffffffu, r[i] <= 0);
-      const int64_t p = p0 + i * THREADS;
+      const int64_t p = p0 + i * kSumThreads;
       if (lane == 0 && p < end) w.bits[p >> 5] = word;
       n += __popc(word);
     }
   }
   int64_t all;
-  sum_before<THREADS, int64_t>(lane == 0 ? n : 0, sh, &all);
+  sum_before<kSumThreads, int64_t>(lane == 0 ? n : 0, sh, &all);
   if (threadIdx.x == 0) w.free_of[s] = static_cast<int32_t>(all);
 }
 
 // Sums up what the sequences need, by one CTA.
-template <int OP, int THREADS>
+template <int OP>
 __device__ __forceinline__ void sum_needs(const PageBook& k, const Work& w, const int32_t* want, unsigned* status,
                                           int64_t* sh) {
   int64_t base = 0;
-  for (int b0 = 0; b0 < k.n_seqs; b0 += THREADS) {
+  for (int b0 = 0; b0 < k.n_seqs; b0 += kSumThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     int64_t n = 0;
     if (b < k.n_seqs) {
@@ -168,7 +167,7 @@ __device__ __forceinline__ void sum_needs(const PageBook& k, const Work& w, cons
       w.lens[b] = L;
     }
     int64_t all;
-    const int64_t before = base + sum_before<THREADS, int64_t>(n, sh, &all);
+    const int64_t before = base + sum_before<kSumThreads, int64_t>(n, sh, &all);
     if (b < k.n_seqs) w.before[b] = before;
     base += all;
   }
@@ -382,67 +381,69 @@ __global__ void __launch_bounds__(kSumThreads)
   pdl_wait();
   __shared__ int64_t sh[kSumThreads / 32];
   if (static_cast<int>(blockIdx.x) < stretches)
-    scan_stretch<kSumThreads>(k, w, shift, blockIdx.x, sh);
+    scan_stretch(k, w, shift, blockIdx.x, sh);
   else if (OP != kCompact)
-    sum_needs<OP, kSumThreads>(k, w, want, status, sh);
+    sum_needs<OP>(k, w, want, status, sh);
 }
 
 // Lists of a compaction: with U used pages, the used ones from U on (src) and
 // the free ones below U (dst), as many, both in order; rank: each one's place.
-template <int THREADS>
-__device__ __forceinline__ void list_moves(const PageBook& k, const Work& w, int shift, int stretches, int cta,
-                                           int ctas, int32_t* src, int32_t* dst, int32_t* used, int32_t* before,
-                                           int64_t* sh) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t U = k.n_pages - free_before<THREADS>(w, stretches, before, sh);
-  if (cta == 0 && tid == 0) *used = static_cast<int32_t>(U);
+// A CTA a stretch.
+__global__ void __launch_bounds__(kScanThreads)
+    pages_list_kernel(const PageBook k, const Work w, const int shift, const int stretches, int32_t* src, int32_t* dst,
+                      int32_t* used) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int32_t before[kMaxStretches + 1];
+  __shared__ int64_t sh[kScanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, stretch = blockIdx.x;
+  const int64_t U = k.n_pages - free_before<kScanThreads>(w, stretches, before, sh);
+  if (stretch == 0 && tid == 0) *used = static_cast<int32_t>(U);
   const int64_t words = (k.n_pages + 31) >> 5, per = int64_t(1) << (shift - 5);
   // free pages below U
   int64_t holes = 0;
   if (U < k.n_pages) {
     const int s = static_cast<int>(U >> shift);
     int32_t n = 0;
-    for (int64_t i = s * per + tid; i <= U >> 5; i += THREADS) {
+    for (int64_t i = s * per + tid; i <= U >> 5; i += kScanThreads) {
       uint32_t u = w.bits[i];
       if (i == U >> 5) u &= (1u << (U & 31)) - 1u;
       n += __popc(u);
     }
     int64_t all;
-    sum_before<THREADS, int64_t>(n, sh, &all);
+    sum_before<kScanThreads, int64_t>(n, sh, &all);
     holes = before[s] + all;
   }
-  for (int s = cta; s < stretches; s += ctas) {
-    int64_t rank = before[s];
-    const int64_t end = min((s + 1) * per, words);
-    for (int64_t i0 = s * per; i0 < end; i0 += THREADS) {
-      const int64_t i = i0 + tid;
-      const uint32_t word = i < end ? w.bits[i] : 0u;
-      int64_t all;
-      const int32_t mine = static_cast<int32_t>(rank + sum_before<THREADS, int64_t>(__popc(word), sh, &all));
-      rank += all;
-      // a warp takes its lanes' words in turn, a lane a page
-      const int here = static_cast<int>(min(end - (i - lane), static_cast<int64_t>(32)));
+  int64_t rank = before[stretch];
+  const int64_t end = min((stretch + 1) * per, words);
+  for (int64_t i0 = stretch * per; i0 < end; i0 += kScanThreads) {
+    const int64_t i = i0 + tid;
+    const uint32_t word = i < end ? w.bits[i] : 0u;
+    int64_t all;
+    const int32_t mine = static_cast<int32_t>(rank + sum_before<kScanThreads, int64_t>(__popc(word), sh, &all));
+    rank += all;
+    // a warp takes its lanes' words in turn, a lane a page
+    const int here = static_cast<int>(min(end - (i - lane), static_cast<int64_t>(32)));
 #pragma unroll 4
-      for (int l = 0; l < here; ++l) {
-        const uint32_t u = __shfl_sync(0xffffffffu, word, l);
-        const int32_t free_here = __shfl_sync(0xffffffffu, mine, l);
-        const int64_t p = (i - lane + l) * 32 + lane;
-        if (p >= k.n_pages) continue;
-        const int32_t f = free_here + __popc(u & ((1u << lane) - 1u));  // free pages before p
-        const bool is_free = (u >> lane) & 1u;
-        if (is_free && p < U) {
-          dst[f] = static_cast<int32_t>(p);
-          w.rank[p] = f;
-        } else if (!is_free && p >= U) {
-          const int32_t r = static_cast<int32_t>(p - f - (U - holes));  // used pages before p, less those below U
-          src[r] = static_cast<int32_t>(p);
-          w.rank[p] = r;
-        }
+    for (int l = 0; l < here; ++l) {
+      const uint32_t u = __shfl_sync(0xffffffffu, word, l);
+      const int32_t free_here = __shfl_sync(0xffffffffu, mine, l);
+      const int64_t p = (i - lane + l) * 32 + lane;
+      if (p >= k.n_pages) continue;
+      const int32_t f = free_here + __popc(u & ((1u << lane) - 1u));  // free pages before p
+      const bool is_free = (u >> lane) & 1u;
+      if (is_free && p < U) {
+        dst[f] = static_cast<int32_t>(p);
+        w.rank[p] = f;
+      } else if (!is_free && p >= U) {
+        const int32_t r = static_cast<int32_t>(p - f - (U - holes));  // used pages before p, less those below U
+        src[r] = static_cast<int32_t>(p);
+        w.rank[p] = r;
       }
     }
   }
-  for (int64_t r = holes + static_cast<int64_t>(cta) * THREADS + tid; r < k.n_pages / 2;
-       r += static_cast<int64_t>(ctas) * THREADS) {
+  for (int64_t r = holes + static_cast<int64_t>(stretch) * kScanThreads + tid; r < k.n_pages / 2;
+       r += static_cast<int64_t>(stretches) * kScanThreads) {
     src[r] = -1;
     dst[r] = -1;
   }
@@ -501,16 +502,6 @@ __device__ __forceinline__ void renumber_table(const PageBook& k, const Work& w,
       table[b * k.table_stride + j] = page[q];
     }
   }
-}
-
-__global__ void __launch_bounds__(kScanThreads)
-    pages_list_kernel(const PageBook k, const Work w, const int shift, const int stretches, int32_t* src, int32_t* dst,
-                      int32_t* used) {
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ int32_t before[kMaxStretches + 1];
-  __shared__ int64_t sh[kScanThreads / 32];
-  list_moves<kScanThreads>(k, w, shift, stretches, blockIdx.x, gridDim.x, src, dst, used, before, sh);
 }
 
 __global__ void __launch_bounds__(kScanThreads)
