@@ -32,16 +32,19 @@
 // warps 48, the others 64.
 //
 // What bounds it: at width 128 the products of a block for 256 rows take 2050 cycles
-// alone; a block takes some 3400, a half's scores, softmax and product one after the
-// other while the other half is half a turn away (tensor pipe 59 % active, 63 % of
+// alone; a block takes some 3500, a half's scores, softmax and product one after the
+// other while the other half is half a turn away (tensor pipe 58 % active, 62 % of
 // the issue slots used, memory 1 %).  A half's softmax is some 1600 of them, with one
 // warp a scheduler at a time.  Code that is not run again at once is fetched at some
 // 3 cycles an instruction, so the softmax is rolled where it can be, and so is all
-// that runs once a tile.  (2048 tokens at 62000, 32 heads on 4 of width 128: 1604 us,
-// 1.35 PFLOP/s counting each product once, 71 % of what a 16-bit library product
-// reaches; 12 prompts of up to 1000 tokens behind up to 6000: 546 us; 48 mixed
-// sequences of width 64 under a window of 4096: 304 us; 5 tokens after 900: 17 us,
+// that runs once a tile.  (2048 tokens at 62000, 32 heads on 4 of width 128: 1638 us,
+// 1.32 PFLOP/s counting each product once, 70 % of what a 16-bit library product
+// reaches; 12 prompts of up to 1000 tokens behind up to 6000: 554 us; 48 mixed
+// sequences of width 64 under a window of 4096: 307 us; 5 tokens after 900: 17 us,
 // of which two launches and the chain of loads before the first product are 12.)
+// A block of few rows costs what one of 128 does, some 2000 to 2900 cycles: 64
+// sequences of 4096 with 64 heads on 8 take 147 us at width 64 and 163 at 128 with
+// four new tokens each, 141 and 154 with one (csa_paged_attn 58 and 92).
 //
 // A masked weight is 0, and 0 * NaN is NaN: in blocks that some row of the tile
 // masks, NaN codes of values are taken out as they become f16, and the rows that
@@ -89,8 +92,11 @@ constexpr int kMaxMasked = 8;
 constexpr int kFewRows = 64;
 // What a tile costs, in the units of the shares: a block for two halves, for
 // one, and the tile itself: its queries, its outputs and the pipeline that runs
-// empty between it and the next, some 7500 cycles (12 prompts 632 us with 4 in
-// the place of 16, 588 so).
+// empty between it and the next.  The tile's 16 were found by timing, not from its
+// some 7500 cycles, which are 6 or 7 units: with 4, 8, 12, 16 and 24, 12 prompts of
+// width 128 take 636, 581, 552, 555 and 561 us, of width 64 479, 475, 477, 482 and
+// 491; 48 mixed sequences of width 64 299, 301, 303, 306 and 312, of width 128 361,
+// 351, 350, 353 and 357; 30 prompts of up to 300 111, 105, 104, 103 and 105.
 constexpr int kCostTwo = 3, kCostOne = 2, kCostTile = 16;
 
 // Registers a thread: 512 threads are launched with 128 each.
@@ -1090,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first_key = a.window > 0 && last_key >= a.window ? last_key - a.window + 1 : 0;
       // The sum l is in units of 2^m, m the largest logit so far; the weighted values
       // are in units of 2^(m + d - kWeightExp), d the largest logit + log2(v_scale),
-      // seen from m.  (As a number of its own that would be a multiple of 16 where
+      // seen from m.  (As a number of its own that would be a multiple of 32 where
       // logits are of 2^28, and weights would leave f16.)
       float m = kNone, d = 0.f, l = 0.f;
       const int step = split ? 2 : 1;
@@ -1200,7 +1206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 128 is faster where one long sequence keeps the loop in the instruction
           // caches (2048 tokens at 62000 1535 us, 1604 so) and slower where tiles end
           // often (12 prompts 584 us, 546 so; 48 mixed sequences 312, 304).  Reading the
-          // scores again from tensor memory instead takes 1690 and 564 us.
+          // scores again from tensor memory instead takes 1690 and 564 us.  (All with m
+          // and d as one sum; d apart takes 2 % on the first, 1 % on the others, and as
+          // much with the exact form of d_new for rows of large logits alone: 1616, 564
+          // and 312 us against 1636, 554 and 307.)
           const float up = -down - m;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -1411,8 +1420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // first share's second one, the later shares' first.  CTAs (x, 0..) take the rows
 // of the tile that begins in share x and goes on: with few rows one at a time,
 // each warp a part of the records; else 16 at a time, a thread four channels.
-// (8 tokens at 60000 53.7 us with the second way alone, 47.5 so; 64 tokens at 1000
-// 23.9 us, 27.6 with a warp a row.)
+// (8 tokens at 60000 53.7 us with the second way alone, 48.5 so; 64 tokens at 1000
+// 22.7 us, 27.6 with a warp a row.)
 constexpr int kMergeWarps = 8, kMergeThreads = 32 * kMergeWarps, kMergeRows = 16;
 constexpr int kMergeCtas = kTileRows / kMergeRows;  // a tile
 

@@ -159,7 +159,7 @@ __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
 // From a row's sum of weights l in units of 2^m to the factor of its weighted
 // values, which are in units of 2^(m + unit), and its lse, the sink's weight in.
 // (unit is kept apart from m: of a logit of 2^28 fp32 holds no more than its
-// multiples of 16, so that m + unit would lose what a value scale and f16's room
+// multiples of 32, so that m + unit would lose what a value scale and f16's room
 // add to it.)
 __device__ __forceinline__ float finish_row(float m, float unit, float l, const float* sink, int head, float* lse) {
   float none = -INFINITY;  // lse where nothing has weight: the sink's, which may be below every m

@@ -8,9 +8,10 @@
 // need; in the second a CTA a sequence finds its pages by their rank: the
 // stretch from the stretches' sums, the page from its bits.  Bound by the two
 // launches and the handful of dependent loads in each, some 3 us a launch: 64
-// sequences given 8 tokens and taken back 11.3 us (two calls), 1024 that grow by up
-// to 500 tokens in a pool of 2^20 pages and back 25 us.  One launch of a cluster of
-// 8 CTAs with the cluster's barrier between the steps took 14 and 149 us: eight SMs
+// sequences given 8 tokens and taken back 11.7 us replayed from a graph (two calls;
+// 15 to 16 as eager ones, which the host's side bounds), 1024 that grow by up to 500
+// tokens in a pool of 2^20 pages and back 25.5 us.  One launch of a cluster of 8 CTAs
+// with the cluster's barrier between the steps took 14 (eager) and 149 us: eight SMs
 // read the counts no faster.
 #include "gqa.cuh"
 #include "ptx.cuh"

@@ -733,8 +733,8 @@ csa_status csa_rope(const csa_rope_params *r, const uint64_t *turns,
  * scale * code.  Sequence b's token t lies in page table[b][t / page_size],
  * row t % page_size.  A host struct of device pointers, read during the call.
  *   k, v             [n_pages][n_kv_heads][page_size][head_dim] codes
- *   k_scale, v_scale [n_pages][n_kv_heads], positive (csa_kv_append writes
- *                    powers of two; csa_paged_attn reads any)
+ *   k_scale, v_scale [n_pages][n_kv_heads], positive and finite (csa_kv_append
+ *                    writes powers of two; the attentions read any)
  *   table            [sequences][table_stride] page numbers; table_stride *
  *                    page_size at most 2^30
  * head_dim: 64 or 128.
